@@ -18,7 +18,8 @@ CSRC = os.path.join(PKG, "csrc")
 ROOT = os.path.dirname(PKG)
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libconv2d_gb300.so")
-SOURCES = ["api.cu", "transforms.cu", "conv_fp32.cu", "conv_tc.cu", "winograd.cu", "static_workspace.cu"]
+SOURCES = ["api.cu", "transforms.cu", "conv_fp32.cu", "conv_tc.cu", "winograd.cu", "static_workspace.cu",
+           "head_api.cu", "layernorm.cu", "layernorm_planes.cu", "dropout.cu", "linear_ce.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -36,6 +37,7 @@ def _flags(extra=()):
 
 def _deps_mtime():
     paths = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(ROOT, "include", "conv2d.h"),
+                                                                  os.path.join(ROOT, "include", "head.h"),
                                                                   os.path.abspath(__file__)]
     return max(os.path.getmtime(p) for p in paths)
 

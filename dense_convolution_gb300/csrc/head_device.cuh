@@ -1,0 +1,106 @@
+// Element types and 16-byte vectors of the training-head kernels: values are
+// widened to fp32 on load and rounded to nearest even once on store.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace conv2d_gb300 {
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename T> __device__ __forceinline__ T from_f32(float v);
+template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <> __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// V adjacent elements as they lie in memory; aligned so that a full 16-byte
+// vector is one load.
+template <typename T, int V> struct alignas(sizeof(T) * V) Vec { T v[V]; };
+
+template <typename T, int V> __device__ __forceinline__ void widen(const Vec<T, V>& a, float (&f)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = to_f32(a.v[i]);
+}
+template <typename T, int V> __device__ __forceinline__ Vec<T, V> narrow(const float (&f)[V]) {
+    Vec<T, V> a;
+#pragma unroll
+    for (int i = 0; i < V; ++i) a.v[i] = from_f32<T>(f[i]);
+    return a;
+}
+
+// Elements [lo, hi) of a vector whose first element is p[0]: one load when it
+// is whole, else one by one with zeros outside (nothing outside is read).
+template <typename T, int V> __device__ __forceinline__ Vec<T, V> load_part(const T* p, int lo, int hi) {
+    Vec<T, V> a;
+    if (lo == 0 && hi == V) {
+        a = *reinterpret_cast<const Vec<T, V>*>(p);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) a.v[i] = i >= lo && i < hi ? p[i] : from_f32<T>(0.f);
+    }
+    return a;
+}
+template <typename T, int V> __device__ __forceinline__ void store_part(T* p, const Vec<T, V>& a, int lo, int hi) {
+    if (lo == 0 && hi == V) {
+        *reinterpret_cast<Vec<T, V>*>(p) = a;
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (i >= lo && i < hi) p[i] = a.v[i];
+    }
+}
+
+// Elements [lo, hi) of the V parameters from column e0 on, of type T or fp32
+// (`f32`); `fill` outside, and everywhere when there are none (null).  `vec`
+// says that a whole vector may be read with 16-byte loads.
+template <typename T, int V>
+__device__ __forceinline__ void load_params(const void* p, bool f32, int64_t e0, int lo, int hi, bool vec, float fill,
+                                            float (&f)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = fill;
+    if (!p) return;
+    const bool whole = vec && V > 1 && lo == 0 && hi == V;
+    if (f32) {
+        const float* q = static_cast<const float*>(p) + e0;
+        if (whole) {
+            if constexpr (V >= 4) {
+#pragma unroll
+                for (int i = 0; i < V; i += 4) {
+                    const float4 t = *reinterpret_cast<const float4*>(q + i);
+                    f[i] = t.x; f[i + 1] = t.y; f[i + 2] = t.z; f[i + 3] = t.w;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (i >= lo && i < hi) f[i] = q[i];
+        }
+    } else {
+        const T* q = static_cast<const T*>(p) + e0;
+        if (whole) {
+            widen<T, V>(*reinterpret_cast<const Vec<T, V>*>(q), f);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (i >= lo && i < hi) f[i] = to_f32(q[i]);
+        }
+    }
+}
+
+__device__ __forceinline__ void store_param(void* p, bool f32, bool bf16, int64_t i, float v) {
+    if (f32) static_cast<float*>(p)[i] = v;
+    else if (bf16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+    else static_cast<__half*>(p)[i] = __float2half_rn(v);
+}
+
+// Sum over aligned groups of `width` lanes (a power of two), in every lane.
+__device__ __forceinline__ float lane_sum(float v, int width) {
+    for (int o = width >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+}  // namespace conv2d_gb300

@@ -131,6 +131,8 @@ bool halo_plan_fits(const conv2d_desc& d);
 void* driver_entry(const char* name);
 cudaError_t status_read_clear_tc(cudaStream_t st, uint32_t* out);
 cudaError_t status_read_clear_fp32(cudaStream_t st, uint32_t* out);
+cudaError_t status_read_clear_ce(cudaStream_t st, uint32_t* out);   // linear_ce.cu
+cudaError_t wait_limit_set_ce(cudaStream_t st, uint64_t ns);
 cudaError_t wait_limit_set_tc(cudaStream_t st, uint64_t ns);
 cudaError_t wait_limit_set_fp32(cudaStream_t st, uint64_t ns);
 

@@ -1,0 +1,679 @@
+// Layer norm over rows of adjacent elements, forward and backward.
+//
+// Forward: a row belongs to `tpr` threads of one block (a power of two up to a
+// warp, or whole warps), or to a cluster of up to eight blocks.  Each thread
+// keeps its part of the row in registers, so x is read once: the mean is
+// summed first and the squares of x - mean second (no cancellation between
+// large sums), then y is written.
+//
+// Backward: dx needs two sums over the row, sum a and sum a z (a = dy gamma,
+// z = (x - mean) rstd); dgamma and dbeta are sums over rows.  Rows are dealt
+// out to a fixed grid, every thread keeps the same columns for all of its
+// rows and adds dy z and dy into registers; the blocks' sums go through the
+// workspace to a second kernel that adds them in a fixed order.  Rows longer
+// than a block's registers hold take two passes over x and dy instead.
+//
+// Rows are cut into 16-byte vectors at the memory's own 16-byte boundaries, so
+// rows that start off a boundary (odd strides) still move in full vectors,
+// with single elements only at the two ends.  That needs all tensors of a call
+// to sit alike against the boundary; otherwise elements move one by one.
+#include <cooperative_groups.h>
+
+#include "head_device.cuh"
+#include "head_internal.h"
+#include "ptx.cuh"
+
+namespace conv2d_gb300 {
+
+namespace cg = cooperative_groups;
+
+namespace {
+
+struct LnParams {
+    int64_t rows, xs, ys;
+    int cols;
+    int tpr;             // threads per row: a power of two below 32, or a multiple of 32
+    int cs;              // blocks (one cluster) per row; above 1: tpr = the block's threads
+    int per_block;       // vector slots of a row per block of the cluster
+    int groups;          // backward: row groups of the grid (rows in flight)
+    int param_f32;
+    int vec_params;      // gamma and beta rows are 16-byte aligned like the data's vectors
+    float eps, inv_cols;
+    const void *x, *dy, *gamma, *beta;
+    void *y, *dx;        // y may be x: no __restrict__
+    float *mean, *rstd;
+    const float *mean_in, *rstd_in;
+    float *part;         // backward: [parts][2][cols] sums of dy z and dy
+    int want_params;
+};
+
+template <typename T> __host__ __device__ constexpr int vec_of(bool scalar) { return scalar ? 1 : 16 / (int)sizeof(T); }
+
+// Sum over the tpr threads of each row group (red: 32 floats, one per warp).
+__device__ __forceinline__ float row_sum(float v, int tpr, float* red) {
+    v = lane_sum(v, tpr < 32 ? tpr : 32);
+    if (tpr <= 32) return v;
+    const int wpr = tpr >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (lane == 0) red[warp] = v;
+    __syncthreads();
+    const int first = warp / wpr * wpr;
+    return lane_sum(lane < wpr ? red[first + lane] : 0.f, 32);
+}
+
+template <typename T, bool SCALAR, int NV>
+__global__ void __launch_bounds__(1024) layernorm_fwd_kernel(const LnParams p) {
+    constexpr int V = vec_of<T>(SCALAR);
+    __shared__ float red[2][32];
+    __shared__ float cl[2];
+    pdl_wait();
+    const int rpb = blockDim.x / p.tpr, sub = threadIdx.x / p.tpr, t = threadIdx.x - sub * p.tpr;
+    const int rank = p.cs > 1 ? (int)(blockIdx.x % p.cs) : 0;
+    const int64_t row = (int64_t)(blockIdx.x / p.cs) * rpb + sub;
+    const bool live = row < p.rows;
+    const T* x = static_cast<const T*>(p.x) + (live ? row : 0) * p.xs;
+    T* y = static_cast<T*>(p.y) + (live ? row : 0) * p.ys;
+    const int shift = SCALAR ? 0 : (int)((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
+    const int slots = live ? (p.cols + shift + V - 1) / V : 0;
+    const int s0 = rank * p.per_block, s1 = min(slots, s0 + p.per_block);
+    const bool vec = p.vec_params && shift == 0;
+
+    Vec<T, V> raw[NV];
+    float sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int s = s0 + j * p.tpr + t, e0 = s * V - shift;
+        if (s < s1) raw[j] = load_part<T, V>(x + e0, max(0, -e0), min(V, p.cols - e0));
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        if (s0 + j * p.tpr + t < s1) {                 // elements outside the row are zero
+            float f[V];
+            widen(raw[j], f);
+#pragma unroll
+            for (int i = 0; i < V; ++i) sum += f[i];
+        }
+    }
+    float mean = row_sum(sum, p.tpr, red[0]);
+    if (p.cs > 1) {
+        cg::cluster_group cl_g = cg::this_cluster();
+        if (threadIdx.x == 0) cl[0] = mean;
+        cl_g.sync();
+        const int lane = threadIdx.x & 31;
+        mean = lane_sum(lane < p.cs ? *cl_g.map_shared_rank(&cl[0], lane) : 0.f, 32);
+    }
+    mean *= p.inv_cols;
+
+    float sq = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int s = s0 + j * p.tpr + t, e0 = s * V - shift;
+        if (s < s1) {
+            float f[V];
+            widen(raw[j], f);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float c = f[i] - mean;
+                if (V == 1 || (e0 + i >= 0 && e0 + i < p.cols)) sq += c * c;
+            }
+        }
+    }
+    sq = row_sum(sq, p.tpr, red[1]);
+    if (p.cs > 1) {
+        cg::cluster_group cl_g = cg::this_cluster();
+        if (threadIdx.x == 0) cl[1] = sq;
+        cl_g.sync();
+        const int lane = threadIdx.x & 31;
+        sq = lane_sum(lane < p.cs ? *cl_g.map_shared_rank(&cl[1], lane) : 0.f, 32);
+        cl_g.sync();                                   // no block leaves while another reads its sums
+    }
+    const float rstd = 1.0f / sqrtf(sq * p.inv_cols + p.eps);
+    if (live && t == 0 && rank == 0) {
+        if (p.mean) p.mean[row] = mean;
+        if (p.rstd) p.rstd[row] = rstd;
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int s = s0 + j * p.tpr + t, e0 = s * V - shift;
+        if (s < s1) {
+            const int lo = max(0, -e0), hi = min(V, p.cols - e0);
+            float f[V], g[V], b[V];
+            widen(raw[j], f);
+            load_params<T, V>(p.gamma, p.param_f32, e0, lo, hi, vec, 1.f, g);
+            load_params<T, V>(p.beta, p.param_f32, e0, lo, hi, vec, 0.f, b);
+#pragma unroll
+            for (int i = 0; i < V; ++i) f[i] = (f[i] - mean) * rstd * g[i] + b[i];
+            store_part<T, V>(y + e0, narrow<T, V>(f), lo, hi);
+        }
+    }
+}
+
+// Rows beyond a cluster's registers: the same three steps, re-reading x.
+template <typename T, bool SCALAR>
+__global__ void __launch_bounds__(1024) layernorm_fwd_long_kernel(const LnParams p) {
+    constexpr int V = vec_of<T>(SCALAR);
+    __shared__ float red[2][32];
+    __shared__ float cl[2];
+    pdl_wait();
+    cg::cluster_group cl_g = cg::this_cluster();
+    const int rank = (int)(blockIdx.x % p.cs), lane = threadIdx.x & 31;
+    const int64_t row = blockIdx.x / p.cs;
+    const T* x = static_cast<const T*>(p.x) + row * p.xs;
+    T* y = static_cast<T*>(p.y) + row * p.ys;
+    const int shift = SCALAR ? 0 : (int)((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
+    const int slots = (int)(((int64_t)p.cols + shift + V - 1) / V);
+    const int64_t s0 = (int64_t)rank * p.per_block;
+    const int64_t s1 = min((int64_t)slots, s0 + p.per_block);
+    const bool vec = p.vec_params && shift == 0;
+    float sum = 0.f;
+    for (int64_t s = s0 + threadIdx.x; s < s1; s += blockDim.x) {
+        const int64_t e0 = s * V - shift;
+        float f[V];
+        widen(load_part<T, V>(x + e0, e0 < 0 ? (int)-e0 : 0, (int)min((int64_t)V, p.cols - e0)), f);
+        float u = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) u += f[i];
+        sum += u;
+    }
+    float mean = row_sum(sum, p.tpr, red[0]);
+    if (threadIdx.x == 0) cl[0] = mean;
+    cl_g.sync();
+    mean = lane_sum(lane < p.cs ? *cl_g.map_shared_rank(&cl[0], lane) : 0.f, 32) * p.inv_cols;
+    float sq = 0.f;
+    for (int64_t s = s0 + threadIdx.x; s < s1; s += blockDim.x) {
+        const int64_t e0 = s * V - shift;
+        const int lo = e0 < 0 ? (int)-e0 : 0, hi = (int)min((int64_t)V, p.cols - e0);
+        float f[V];
+        widen(load_part<T, V>(x + e0, lo, hi), f);
+        float u = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const float c = f[i] - mean;
+            if (i >= lo && i < hi) u += c * c;
+        }
+        sq += u;
+    }
+    sq = row_sum(sq, p.tpr, red[1]);
+    if (threadIdx.x == 0) cl[1] = sq;
+    cl_g.sync();
+    sq = lane_sum(lane < p.cs ? *cl_g.map_shared_rank(&cl[1], lane) : 0.f, 32);
+    cl_g.sync();
+    const float rstd = 1.0f / sqrtf(sq * p.inv_cols + p.eps);
+    if (threadIdx.x == 0 && rank == 0) {
+        if (p.mean) p.mean[row] = mean;
+        if (p.rstd) p.rstd[row] = rstd;
+    }
+    for (int64_t s = s0 + threadIdx.x; s < s1; s += blockDim.x) {
+        const int64_t e0 = s * V - shift;
+        const int lo = e0 < 0 ? (int)-e0 : 0, hi = (int)min((int64_t)V, p.cols - e0);
+        float f[V], g[V], b[V];
+        widen(load_part<T, V>(x + e0, lo, hi), f);
+        load_params<T, V>(p.gamma, p.param_f32, e0, lo, hi, vec, 1.f, g);
+        load_params<T, V>(p.beta, p.param_f32, e0, lo, hi, vec, 0.f, b);
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] = (f[i] - mean) * rstd * g[i] + b[i];
+        store_part<T, V>(y + e0, narrow<T, V>(f), lo, hi);
+    }
+}
+
+// Backward of rows that a block's registers hold.  Group k of the grid takes
+// rows k, k + groups, ...; groups is a multiple of the vector length when rows
+// start off the 16-byte boundary, so that all rows of a group are cut alike
+// and a thread's registers keep the same columns.
+template <typename T, bool SCALAR, int NV>
+__global__ void __launch_bounds__(512) layernorm_bwd_kernel(const LnParams p) {
+    constexpr int V = vec_of<T>(SCALAR);
+    __shared__ float red[2][2][32];
+    extern __shared__ float acc_s[];                   // [2][cols] when several groups share the block
+    pdl_wait();
+    const int rpb = blockDim.x / p.tpr, sub = threadIdx.x / p.tpr, t = threadIdx.x - sub * p.tpr;
+    const int group = blockIdx.x * rpb + sub;
+    const T* x0 = static_cast<const T*>(p.x);
+    const int shift =
+        SCALAR ? 0 : (int)((reinterpret_cast<uintptr_t>(x0 + (int64_t)group * p.xs) & 15u) / sizeof(T));
+    const int slots = (p.cols + shift + V - 1) / V;
+    const bool vec = p.vec_params && shift == 0;
+
+    float g[NV][V], dg[NV][V], db[NV][V];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int s = j * p.tpr + t, e0 = s * V - shift;
+        const bool in = s < slots;
+        load_params<T, V>(p.gamma, p.param_f32, e0, in ? max(0, -e0) : V, in ? min(V, p.cols - e0) : 0, vec && in, 1.f,
+                          g[j]);
+#pragma unroll
+        for (int i = 0; i < V; ++i) dg[j][i] = db[j][i] = 0.f;
+    }
+    // Every group of the block runs the same number of turns (they meet at barriers).
+    const int64_t turns = (p.rows - (int64_t)blockIdx.x * rpb + p.groups - 1) / p.groups;
+    Vec<T, V> rx[NV], rd[NV];
+    float mean = 0.f, rstd = 0.f;
+    auto fetch = [&](int64_t row) {
+        if (row < p.rows) {
+            const T* x = x0 + row * p.xs;
+            const T* dy = static_cast<const T*>(p.dy) + row * p.ys;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int s = j * p.tpr + t, e0 = s * V - shift;
+                if (s < slots) {
+                    const int lo = max(0, -e0), hi = min(V, p.cols - e0);
+                    rx[j] = load_part<T, V>(x + e0, lo, hi);
+                    rd[j] = load_part<T, V>(dy + e0, lo, hi);
+                }
+            }
+            mean = p.mean_in[row];
+            rstd = p.rstd_in[row];
+        }
+    };
+    fetch(group);
+    for (int64_t it = 0; it < turns; ++it) {
+        const int64_t row = group + it * p.groups;
+        const bool live = row < p.rows;
+        const float mu = mean, r = rstd;
+        float z[NV][V], a[NV][V];
+        float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int s = j * p.tpr + t, e0 = s * V - shift;
+            if (live && s < slots) {
+                float fx[V], fd[V];
+                widen(rx[j], fx);
+                widen(rd[j], fd);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    // Outside the row dy is zero; z must be too (it is finite, but has no column).
+                    const bool in = V == 1 || (e0 + i >= 0 && e0 + i < p.cols);
+                    z[j][i] = in ? (fx[i] - mu) * r : 0.f;
+                    a[j][i] = fd[i] * g[j][i];
+                    s1 += a[j][i];
+                    s2 += a[j][i] * z[j][i];
+                    dg[j][i] += fd[i] * z[j][i];
+                    db[j][i] += fd[i];
+                }
+            }
+        }
+        fetch(row + p.groups);                         // the next row's loads run under the sums
+        if (!p.dx) continue;
+        const int tpr = p.tpr;
+        s1 = lane_sum(s1, tpr < 32 ? tpr : 32);
+        s2 = lane_sum(s2, tpr < 32 ? tpr : 32);
+        if (tpr > 32) {
+            // Two buffers in turn: a warp that is a row ahead writes the other one.
+            const int wpr = tpr >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = (int)(it & 1);
+            if (lane == 0) { red[b][0][warp] = s1; red[b][1][warp] = s2; }
+            __syncthreads();
+            const int first = warp / wpr * wpr;
+            s1 = lane_sum(lane < wpr ? red[b][0][first + lane] : 0.f, 32);
+            s2 = lane_sum(lane < wpr ? red[b][1][first + lane] : 0.f, 32);
+        }
+        s1 *= p.inv_cols;
+        s2 *= p.inv_cols;
+        if (live) {
+            T* dx = static_cast<T*>(p.dx) + row * p.xs;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int s = j * p.tpr + t, e0 = s * V - shift;
+                if (s < slots) {
+                    float f[V];
+#pragma unroll
+                    for (int i = 0; i < V; ++i) f[i] = r * (a[j][i] - s1 - z[j][i] * s2);
+                    store_part<T, V>(dx + e0, narrow<T, V>(f), max(0, -e0), min(V, p.cols - e0));
+                }
+            }
+        }
+    }
+    if (!p.want_params) return;
+    float* out = p.part + (int64_t)blockIdx.x * 2 * p.cols;
+    for (int k = 0; k < rpb; ++k) {
+        if (k > 0) __syncthreads();
+        if (sub == k) {
+            float* dst = k + 1 < rpb ? acc_s : out;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int s = j * p.tpr + t, e0 = s * V - shift;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const int c = e0 + i;
+                    if (s < slots && c >= 0 && c < p.cols) {
+                        dst[c] = dg[j][i] + (k ? acc_s[c] : 0.f);
+                        dst[p.cols + c] = db[j][i] + (k ? acc_s[p.cols + c] : 0.f);
+                    }
+                }
+            }
+        }
+    }
+}
+
+// Long rows, pass 1: sum a and sum a z of one row's share of columns.
+template <typename T, bool SCALAR>
+__global__ void __launch_bounds__(256) layernorm_bwd_sums_kernel(const LnParams p, float2* sums) {
+    constexpr int V = vec_of<T>(SCALAR);
+    __shared__ float red[2][32];
+    pdl_wait();
+    const int64_t row = blockIdx.x;
+    const T* x = static_cast<const T*>(p.x) + row * p.xs;
+    const T* dy = static_cast<const T*>(p.dy) + row * p.ys;
+    const int shift = SCALAR ? 0 : (int)((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
+    const int64_t slots = ((int64_t)p.cols + shift + V - 1) / V;
+    const int64_t per = (slots + gridDim.y - 1) / gridDim.y;
+    const int64_t s0 = blockIdx.y * per, s1 = min(slots, s0 + per);
+    const bool vec = p.vec_params && shift == 0;
+    const float mu = p.mean_in[row], r = p.rstd_in[row];
+    float a1 = 0.f, a2 = 0.f;
+    for (int64_t s = s0 + threadIdx.x; s < s1; s += blockDim.x) {
+        const int64_t e0 = s * V - shift;
+        const int lo = e0 < 0 ? (int)-e0 : 0, hi = (int)min((int64_t)V, p.cols - e0);
+        float fx[V], fd[V], g[V];
+        widen(load_part<T, V>(x + e0, lo, hi), fx);
+        widen(load_part<T, V>(dy + e0, lo, hi), fd);
+        load_params<T, V>(p.gamma, p.param_f32, e0, lo, hi, vec, 1.f, g);
+        float u1 = 0.f, u2 = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if (i >= lo && i < hi) {
+                const float a = fd[i] * g[i];
+                u1 += a;
+                u2 += a * ((fx[i] - mu) * r);
+            }
+        }
+        a1 += u1;
+        a2 += u2;
+    }
+    a1 = row_sum(a1, blockDim.x, red[0]);
+    a2 = row_sum(a2, blockDim.x, red[1]);
+    if (threadIdx.x == 0) sums[row * gridDim.y + blockIdx.y] = make_float2(a1, a2);
+}
+
+// Long rows, pass 2: a thread owns one vector of columns and runs down every
+// gridDim.y-th row (a multiple of the vector length when rows are cut
+// differently, as above), writing dx and adding dgamma and dbeta.
+template <typename T, bool SCALAR>
+__global__ void __launch_bounds__(128) layernorm_bwd_cols_kernel(const LnParams p, const float2* sums, int shares) {
+    constexpr int V = vec_of<T>(SCALAR);
+    pdl_wait();
+    const T* x0 = static_cast<const T*>(p.x) + (int64_t)blockIdx.y * p.xs;
+    const int shift = SCALAR ? 0 : (int)((reinterpret_cast<uintptr_t>(x0) & 15u) / sizeof(T));
+    const int64_t s = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, e0 = s * V - shift;
+    if (e0 >= p.cols) return;
+    const int lo = e0 < 0 ? (int)-e0 : 0, hi = (int)min((int64_t)V, p.cols - e0);
+    const bool vec = p.vec_params && shift == 0;
+    float g[V], dg[V], db[V];
+    load_params<T, V>(p.gamma, p.param_f32, e0, lo, hi, vec, 1.f, g);
+#pragma unroll
+    for (int i = 0; i < V; ++i) dg[i] = db[i] = 0.f;
+    for (int64_t row = blockIdx.y; row < p.rows; row += gridDim.y) {
+        float s1 = 0.f, s2 = 0.f;
+        for (int k = 0; k < shares; ++k) {
+            const float2 u = sums[row * shares + k];
+            s1 += u.x;
+            s2 += u.y;
+        }
+        s1 *= p.inv_cols;
+        s2 *= p.inv_cols;
+        const float mu = p.mean_in[row], r = p.rstd_in[row];
+        float fx[V], fd[V], f[V];
+        widen(load_part<T, V>(static_cast<const T*>(p.x) + row * p.xs + e0, lo, hi), fx);
+        widen(load_part<T, V>(static_cast<const T*>(p.dy) + row * p.ys + e0, lo, hi), fd);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const float z = (fx[i] - mu) * r;
+            f[i] = r * (fd[i] * g[i] - s1 - z * s2);
+            dg[i] += fd[i] * z;                        // (outside the row nothing is stored)
+            db[i] += fd[i];
+        }
+        if (p.dx)
+            store_part<T, V>(static_cast<T*>(p.dx) + row * p.xs + e0, narrow<T, V>(f), lo, hi);
+    }
+    if (!p.want_params) return;
+    float* out = p.part + (int64_t)blockIdx.y * 2 * p.cols + e0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        if (i >= lo && i < hi) {
+            out[i] = dg[i];
+            out[p.cols + i] = db[i];
+        }
+    }
+}
+
+// dgamma and dbeta: the parts' columns added in order, 32 columns by 8 shares
+// of the parts per block (blockIdx.y: dgamma or dbeta).
+__global__ void __launch_bounds__(256) layernorm_params_kernel(const float* part, int parts, int cols, void* dgamma,
+                                                               void* dbeta, int f32, int bf16) {
+    __shared__ float sh[8][33];
+    pdl_wait();
+    void* out = blockIdx.y ? dbeta : dgamma;
+    if (!out) return;
+    const int lane = threadIdx.x & 31, k = threadIdx.x >> 5;
+    const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+    float v = 0.f;
+    if (c < cols) {
+        const float* q = part + (int64_t)blockIdx.y * cols + c;
+        const int64_t pitch = 2 * (int64_t)cols;
+        int i = k;
+        for (; i + 24 < parts; i += 32) {              // four loads in flight
+            const float a0 = q[i * pitch], a1 = q[(i + 8) * pitch], a2 = q[(i + 16) * pitch], a3 = q[(i + 24) * pitch];
+            v += (a0 + a1) + (a2 + a3);
+        }
+        for (; i < parts; i += 8) v += q[i * pitch];
+    }
+    sh[k][lane] = v;
+    __syncthreads();
+    if (k == 0 && c < cols) {
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += sh[i][lane];
+        store_param(out, f32, bf16, c, s);
+    }
+}
+
+// ------------------------------------------------------------------ host side
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Threads for `slots` vectors of a row at nv vectors per thread: a power of
+// two below a warp, else whole warps.
+int threads_for(int64_t slots, int nv) {
+    const int64_t t = ceil_div(slots, nv);
+    if (t >= 32) return (int)(ceil_div(t, 32) * 32);
+    int p = 1;
+    while (p < t) p <<= 1;
+    return p;
+}
+
+constexpr int kBwdElems = 16;         // backward: elements of a row per thread at most (registers)
+constexpr int kBwdThreads = 512;      // and threads per row
+
+bool bwd_in_block(const layernorm_desc& d) { return d.cols <= (int64_t)(kBwdElems - 1) * kBwdThreads; }
+
+int bwd_grid() { return device_sm_count() * 2; }
+
+// Blocks per row of the long form's sums at most: eight blocks per SM in all.
+int64_t long_shares(int64_t rows) {
+    const int64_t s = rows ? ceil_div(8 * device_sm_count(), rows) : 1;
+    return s > 64 ? 64 : s;
+}
+
+// Whether a call's tensors can move in 16-byte vectors: every row of all of
+// them sits alike against the 16-byte boundary.
+bool same_phase(const void* a, int64_t sa, const void* b, int64_t sb, size_t e) {
+    return (reinterpret_cast<uintptr_t>(a) & 15) == (reinterpret_cast<uintptr_t>(b) & 15) &&
+           ((sa - sb) * (int64_t)e) % 16 == 0;
+}
+
+template <typename T> cudaError_t fwd_typed(const layernorm_desc& d, LnParams p, cudaStream_t st) {
+    const bool scalar = !same_phase(p.x, p.xs, p.y, p.ys, sizeof(T));
+    const int V = scalar ? 1 : 16 / (int)sizeof(T);
+    const int64_t slots = ceil_div(p.cols + V - 1, V);      // with the widest cut
+    // Vectors per thread: as few as keep every row's threads resident at once
+    // (64 warps an SM), so that small calls spread over the GPU and large
+    // ones keep several loads per thread in flight.
+    const int64_t room = (int64_t)device_sm_count() * 2048;
+    int nv = 1;
+    while (nv < 4 && p.rows * threads_for(slots, nv) > room) nv *= 2;
+    while (nv < 8 && threads_for(slots, nv) > 1024) nv *= 2;
+    int64_t threads = threads_for(slots, nv), grid;
+    bool is_long = false;
+    p.cs = 1;
+    if (threads > 1024 || (slots >= 2048 && p.rows * 2 <= device_sm_count())) {
+        // One row over a cluster: the fewest blocks that hold it, then more
+        // while the GPU has SMs to spare and a thread would keep a vector.
+        while (p.cs < 8 && (threads_for(ceil_div(slots, p.cs), 8) > 1024 ||
+                            (p.rows * p.cs * 2 <= device_sm_count() && ceil_div(slots, p.cs * 2) >= 256)))
+            p.cs *= 2;
+        p.per_block = (int)ceil_div(slots, p.cs);
+        nv = 1;
+        while (nv < 8 && threads_for(p.per_block, nv) > (nv < 4 ? 512 : 1024)) nv *= 2;
+        threads = threads_for(p.per_block, nv);
+        is_long = threads > 1024;
+        if (is_long) threads = 1024;
+        grid = p.rows * p.cs;
+        p.tpr = (int)threads;
+    } else {
+        p.per_block = (int)slots;
+        p.tpr = (int)threads;
+        const int64_t rpb = threads >= 256 ? 1 : 256 / threads;
+        threads *= rpb;
+        grid = ceil_div(p.rows, rpb);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)p.cs;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (is_long)
+        return scalar ? cudaLaunchKernelEx(&cfg, layernorm_fwd_long_kernel<T, true>, p)
+                      : cudaLaunchKernelEx(&cfg, layernorm_fwd_long_kernel<T, false>, p);
+#define LN_FWD(NV)                                                                    \
+    (scalar ? cudaLaunchKernelEx(&cfg, layernorm_fwd_kernel<T, true, NV>, p)          \
+            : cudaLaunchKernelEx(&cfg, layernorm_fwd_kernel<T, false, NV>, p))
+    switch (nv) {
+        case 1: return LN_FWD(1);
+        case 2: return LN_FWD(2);
+        case 4: return LN_FWD(4);
+        default: return LN_FWD(8);
+    }
+#undef LN_FWD
+}
+
+template <typename T> cudaError_t bwd_typed(const layernorm_desc& d, LnParams p, float* ws, int* parts, cudaStream_t st) {
+    const bool scalar = !same_phase(p.x, p.xs, p.dy, p.ys, sizeof(T)) ||
+                        (p.dx && !same_phase(p.x, p.xs, p.dx, p.xs, sizeof(T)));
+    const int V = scalar ? 1 : 16 / (int)sizeof(T);
+    const bool cut_alike = scalar || (p.xs * (int64_t)sizeof(T)) % 16 == 0;
+    const int64_t slots = ceil_div(p.cols + V - 1, V);
+    const int sms = device_sm_count();
+    if (bwd_in_block(d)) {
+        int nv = 1;
+        const int64_t room = (int64_t)sms * 512;
+        while (nv * V < kBwdElems && (threads_for(slots, nv) > kBwdThreads || p.rows * threads_for(slots, nv) > room))
+            nv *= 2;
+        p.tpr = threads_for(slots, nv);
+        const int rpb = p.tpr >= 256 ? 1 : 256 / p.tpr;
+        int64_t grid = ceil_div(p.rows, rpb);
+        if (grid > bwd_grid()) grid = bwd_grid();
+        if (!cut_alike) grid = ceil_div(grid, V) * V;
+        p.groups = (int)grid * rpb;
+        *parts = (int)grid;
+        const size_t smem = rpb > 1 && p.want_params ? 2 * (size_t)p.cols * sizeof(float) : 0;
+#define LN_BWD(NV)                                                                                               \
+    launch_after(scalar ? layernorm_bwd_kernel<T, true, NV> : layernorm_bwd_kernel<T, false, (NV * 16 / (int)sizeof(T) <= kBwdElems ? NV : 1)>, \
+                 dim3((unsigned)grid), dim3(p.tpr * rpb), smem, st, p)
+        switch (nv) {
+            case 1: return LN_BWD(1);
+            case 2: return LN_BWD(2);
+            case 4: return LN_BWD(4);
+            case 8: return LN_BWD(8);
+            default: return LN_BWD(16);
+        }
+#undef LN_BWD
+    }
+    // Two passes: row sums, then columns.  Enough shares of the columns, and
+    // of the rows, to fill the GPU.
+    int64_t shares = long_shares(p.rows);
+    if (shares > ceil_div(slots, 1024)) shares = ceil_div(slots, 1024);
+    float2* sums = reinterpret_cast<float2*>(ws);
+    cudaError_t e = cudaSuccess;
+    if (p.dx) {
+        e = launch_after(scalar ? layernorm_bwd_sums_kernel<T, true> : layernorm_bwd_sums_kernel<T, false>,
+                         dim3((unsigned)p.rows, (unsigned)shares), dim3(256), 0, st, p, sums);
+        if (e != cudaSuccess) return e;
+    }
+    const int64_t gx = ceil_div(slots, 128);
+    int64_t gy = ceil_div(8 * sms, gx);
+    if (gy > 64) gy = 64;
+    if (gy > p.rows) gy = p.rows;
+    if (!cut_alike) gy = ceil_div(gy, V) * V;
+    if (gy > 64) gy = 64;
+    *parts = (int)gy;
+    return launch_after(scalar ? layernorm_bwd_cols_kernel<T, true> : layernorm_bwd_cols_kernel<T, false>,
+                        dim3((unsigned)gx, (unsigned)gy), dim3(128), 0, st, p, static_cast<const float2*>(sums),
+                        p.dx ? (int)shares : 0);
+}
+
+}  // namespace
+
+cudaError_t launch_layernorm_fwd(const layernorm_desc& d, const void* x, const void* gamma, const void* beta, void* y,
+                                 float* mean, float* rstd, cudaStream_t st) {
+    if (d.pixels) return launch_layernorm_planes_fwd(d, x, gamma, beta, y, mean, rstd, st);
+    LnParams p{};
+    p.rows = d.rows; p.xs = d.xs; p.ys = d.ys; p.cols = (int)d.cols;
+    p.param_f32 = d.param == CONV2D_F32;
+    p.vec_params = aligned_to(gamma, 16) && aligned_to(beta, 16);
+    p.eps = d.eps;
+    p.inv_cols = 1.0f / (float)d.cols;
+    p.x = x; p.gamma = gamma; p.beta = beta; p.y = y; p.mean = mean; p.rstd = rstd;
+    switch (d.dtype) {
+        case CONV2D_F32: return fwd_typed<float>(d, p, st);
+        case CONV2D_F16: return fwd_typed<__half>(d, p, st);
+        default: return fwd_typed<__nv_bfloat16>(d, p, st);
+    }
+}
+
+// Row sums of the long form (rows x shares pairs), then the parts of dgamma
+// and dbeta (blocks of the in-block form, or row shares of the long one).
+static size_t bwd_sums_bytes(const layernorm_desc& d) {
+    return bwd_in_block(d) ? 0 : align_up((size_t)(d.rows * long_shares(d.rows)) * sizeof(float2), 256);
+}
+
+size_t layernorm_bwd_workspace(const layernorm_desc& d) {
+    if (d.pixels) return layernorm_planes_bwd_workspace(d);
+    const size_t parts = bwd_in_block(d) ? (size_t)bwd_grid() + 8 : 64;
+    return bwd_sums_bytes(d) + parts * 2 * (size_t)d.cols * sizeof(float);
+}
+
+cudaError_t launch_layernorm_params(const float* part, int parts, const layernorm_desc& d, void* dgamma, void* dbeta,
+                                    cudaStream_t st) {
+    return launch_after(layernorm_params_kernel, dim3((unsigned)((d.cols + 31) / 32), 2), dim3(256), 0, st, part, parts,
+                        (int)d.cols, dgamma, dbeta, d.param == CONV2D_F32 ? 1 : 0, d.param == CONV2D_BF16 ? 1 : 0);
+}
+
+cudaError_t launch_layernorm_bwd(const layernorm_desc& d, const void* dy, const void* x, const void* gamma,
+                                 const float* mean, const float* rstd, void* dx, void* dgamma, void* dbeta, void* ws,
+                                 cudaStream_t st) {
+    if (d.pixels) return launch_layernorm_planes_bwd(d, dy, x, gamma, mean, rstd, dx, dgamma, dbeta, ws, st);
+    LnParams p{};
+    p.rows = d.rows; p.xs = d.xs; p.ys = d.ys; p.cols = (int)d.cols;
+    p.param_f32 = d.param == CONV2D_F32;
+    p.vec_params = aligned_to(gamma, 16);
+    p.inv_cols = 1.0f / (float)d.cols;
+    p.x = x; p.dy = dy; p.gamma = gamma; p.dx = dx; p.mean_in = mean; p.rstd_in = rstd;
+    p.want_params = dgamma || dbeta;
+    float* sums = static_cast<float*>(ws);
+    p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + bwd_sums_bytes(d));
+    int parts = 0;
+    cudaError_t e;
+    switch (d.dtype) {
+        case CONV2D_F32: e = bwd_typed<float>(d, p, sums, &parts, st); break;
+        case CONV2D_F16: e = bwd_typed<__half>(d, p, sums, &parts, st); break;
+        default: e = bwd_typed<__nv_bfloat16>(d, p, sums, &parts, st);
+    }
+    if (e != cudaSuccess || !p.want_params) return e;
+    return launch_layernorm_params(p.part, parts, d, dgamma, dbeta, st);
+}
+
+}  // namespace conv2d_gb300

@@ -20,10 +20,10 @@ namespace {
 
 struct DropParams {
     int64_t rows, cols, xs, rs, ys;
-    int64_t blocks;              // blocks of eight elements of the whole tensor
+    int64_t blocks, whole;       // blocks of eight elements of the whole tensor, and those moved as vectors
     uint32_t k0, k1, off0, off1;
-    uint32_t hi, lo;             // halves of the threshold
-    int all, none;               // threshold 2^32 and 0
+    uint32_t threshold;          // dropped below it
+    int all;                     // threshold 2^32: nothing is kept
     float scale;
     const void *x, *r;
     void* y;
@@ -41,93 +41,115 @@ __device__ __forceinline__ void philox(uint32_t (&c)[4], uint32_t k0, uint32_t k
     }
 }
 
-// Bit i: element i of block b is kept.
-__device__ __forceinline__ uint32_t keep_bits(const DropParams& p, int64_t b) {
-    if (p.none) return 0xffu;
-    if (p.all) return 0u;
+// The 32-bit numbers of block b's eight elements.  Their high halves come from
+// one Philox call; what stands below a high half is meaningless unless it ties
+// with the threshold's, and then the second call fills the low halves in.
+__device__ __forceinline__ void numbers(const DropParams& p, int64_t b, uint32_t (&n)[8]) {
     uint32_t c[4] = {(uint32_t)b, (uint32_t)((uint64_t)b >> 32), p.off0, p.off1};
     philox(c, p.k0, p.k1);
-    uint32_t keep = 0, tie = 0;
+    const uint32_t base = p.threshold & 0xffff0000u;
+    uint32_t nearest = 0xffffffffu;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const uint32_t h = i & 1 ? c[i >> 1] >> 16 : c[i >> 1] & 0xffffu;
-        keep |= h > p.hi ? 1u << i : 0u;
-        tie |= h == p.hi ? 1u << i : 0u;
+        n[i] = i & 1 ? c[i >> 1] : c[i >> 1] << 16;
+        nearest = min(nearest, n[i] - base);           // below 2^16: the high halves are equal
     }
-    if (tie) {
+    if (nearest < 0x10000u) {
         uint32_t l[4] = {(uint32_t)b, (uint32_t)((uint64_t)b >> 32), p.off0, p.off1 | 0x80000000u};
         philox(l, p.k0, p.k1);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t w = i & 1 ? l[i >> 1] >> 16 : l[i >> 1] & 0xffffu;
-            if ((tie >> i & 1) && w >= p.lo) keep |= 1u << i;
-        }
+        for (int i = 0; i < 8; ++i)
+            n[i] = (n[i] & 0xffff0000u) | (i & 1 ? l[i >> 1] >> 16 : l[i >> 1] & 0xffffu);
     }
-    return keep;
 }
 
-// VECTOR: blocks of eight are whole, adjacent and 16-byte aligned in every
-// tensor (rows a multiple of eight long, or one row, whose last block may be
-// short).  Otherwise each element finds its own row and column.
-template <typename T, bool VECTOR>
-__global__ void __launch_bounds__(256) dropout_kernel(const DropParams p) {
+// VECTOR: blocks of eight are adjacent and 16-byte aligned in every tensor
+// (rows a multiple of eight long, or one row, whose last block may be short).
+// Otherwise each element finds its own row and column.
+// A thread takes two blocks a grid's length apart, so that both blocks' loads
+// are under way during the generator's arithmetic.
+template <typename T, bool VECTOR, bool RESIDUAL>
+__global__ void __launch_bounds__(256, 4) dropout_kernel(const DropParams p) {
+    constexpr int V = 16 / (int)sizeof(T), L = 8 / V;  // a block is one load of 16-bit values, two of fp32
     pdl_wait();
     const T* x = static_cast<const T*>(p.x);
     const T* r = static_cast<const T*>(p.r);
     T* y = static_cast<T*>(p.y);
-    const int64_t total = p.rows * p.cols;
-    for (int64_t b = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; b < p.blocks; b += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t e0 = b * 8;
-        const int n = (int)min((int64_t)8, total - e0);
-        if (VECTOR && n == 8) {
-            constexpr int V = 16 / (int)sizeof(T), L = 8 / V;      // one load of 16-bit values, two of fp32
-            int64_t row = 0, col = e0;
-            if (p.rows > 1) {
-                row = e0 / p.cols;
-                col = e0 - row * p.cols;
-            }
-            const T* xr = x + row * p.xs + col;
-            T* yr = y + row * p.ys + col;
-            Vec<T, V> vx[L], vr[L];
+    const int64_t step = (int64_t)gridDim.x * blockDim.x;
+    int64_t b = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if constexpr (VECTOR) {
+        for (; b < p.whole; b += 2 * step) {
+            Vec<T, V> vx[2][L], vr[2][L];
+            int64_t yo[2];
 #pragma unroll
-            for (int l = 0; l < L; ++l) vx[l] = *reinterpret_cast<const Vec<T, V>*>(xr + l * V);
-            if (r) {
-#pragma unroll
-                for (int l = 0; l < L; ++l)
-                    vr[l] = *reinterpret_cast<const Vec<T, V>*>(r + row * p.rs + col + l * V);
-            }
-            const uint32_t keep = keep_bits(p, b);
-#pragma unroll
-            for (int l = 0; l < L; ++l) {
-                float f[V], g[V];
-                widen(vx[l], f);
-                if (r) widen(vr[l], g);
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    f[i] = keep >> (l * V + i) & 1 ? f[i] * p.scale : 0.f;
-                    if (r) f[i] += g[i];
+            for (int u = 0; u < 2; ++u) {
+                const int64_t e0 = (b + u * step) * 8;
+                int64_t xo = e0, ro = e0;
+                yo[u] = e0;
+                if (p.rows > 1) {
+                    const int64_t row = e0 / p.cols, col = e0 - row * p.cols;
+                    xo = row * p.xs + col;
+                    ro = row * p.rs + col;
+                    yo[u] = row * p.ys + col;
                 }
-                *reinterpret_cast<Vec<T, V>*>(yr + l * V) = narrow<T, V>(f);
+                if (b + u * step < p.whole) {
+#pragma unroll
+                    for (int l = 0; l < L; ++l) {
+                        vx[u][l] = *reinterpret_cast<const Vec<T, V>*>(x + xo + l * V);
+                        if (RESIDUAL) vr[u][l] = *reinterpret_cast<const Vec<T, V>*>(r + ro + l * V);
+                    }
+                }
             }
-        } else {
-            const uint32_t keep = keep_bits(p, b);
-            int64_t row = e0 / p.cols, col = e0 - row * p.cols;
-            for (int i = 0; i < n; ++i) {
-                float f = keep >> i & 1 ? to_f32(x[row * p.xs + col]) * p.scale : 0.f;
-                if (r) f += to_f32(r[row * p.rs + col]);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                if (b + u * step < p.whole) {
+                    uint32_t n[8];
+                    numbers(p, b + u * step, n);
+#pragma unroll
+                    for (int l = 0; l < L; ++l) {
+                        float f[V], g[V];
+                        widen(vx[u][l], f);
+                        if (RESIDUAL) widen(vr[u][l], g);
+#pragma unroll
+                        for (int i = 0; i < V; ++i) {
+                            f[i] = n[l * V + i] >= p.threshold && !p.all ? f[i] * p.scale : 0.f;
+                            if (RESIDUAL) f[i] += g[i];
+                        }
+                        *reinterpret_cast<Vec<T, V>*>(y + yo[u] + l * V) = narrow<T, V>(f);
+                    }
+                }
+            }
+        }
+        // The short last block, if any.
+        b = p.whole + (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    }
+    const int64_t total = p.rows * p.cols;
+    for (; b < p.blocks; b += step) {
+        uint32_t n[8];
+        numbers(p, b, n);
+        const int64_t e0 = b * 8, row0 = e0 / p.cols, col0 = e0 - row0 * p.cols;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (e0 + i < total) {
+                int64_t row = row0, col = col0 + i;
+                while (col >= p.cols) { col -= p.cols; ++row; }
+                float f = n[i] >= p.threshold && !p.all ? to_f32(x[row * p.xs + col]) * p.scale : 0.f;
+                if (RESIDUAL) f += to_f32(r[row * p.rs + col]);
                 y[row * p.ys + col] = from_f32<T>(f);
-                if (++col == p.cols) { col = 0; ++row; }
             }
         }
     }
 }
 
-template <typename T> cudaError_t run(const DropParams& p, bool vector, cudaStream_t st) {
-    const int64_t most = (int64_t)device_sm_count() * 8 * 16;      // sixteen turns at most keep the tail short
-    int64_t grid = (p.blocks + 255) / 256;
+template <typename T> cudaError_t run(DropParams p, bool vector, cudaStream_t st) {
+    p.whole = vector ? p.rows * p.cols / 8 : 0;
+    // Two blocks of eight a thread; sixteen turns at most keep the tail short.
+    const int64_t most = (int64_t)device_sm_count() * 4 * 16;
+    int64_t grid = (p.blocks + 511) / 512;
     if (grid > most) grid = most;
-    return launch_after(vector ? dropout_kernel<T, true> : dropout_kernel<T, false>, dim3((unsigned)grid), dim3(256), 0,
-                        st, p);
+    auto kern = vector ? (p.r ? dropout_kernel<T, true, true> : dropout_kernel<T, true, false>)
+                       : (p.r ? dropout_kernel<T, false, true> : dropout_kernel<T, false, false>);
+    return launch_after(kern, dim3((unsigned)grid), dim3(256), 0, st, p);
 }
 
 }  // namespace
@@ -146,9 +168,7 @@ cudaError_t launch_dropout(const dropout_desc& d, const void* x, int64_t xs, con
     p.off0 = (uint32_t)offset; p.off1 = (uint32_t)(offset >> 32);
     const uint64_t threshold = (uint64_t)nearbyint(d.p * 4294967296.0);
     p.all = threshold >> 32 != 0;
-    p.none = threshold == 0;
-    p.hi = (uint32_t)(threshold >> 16) & 0xffffu;
-    p.lo = (uint32_t)threshold & 0xffffu;
+    p.threshold = (uint32_t)threshold;
     p.scale = d.p < 1.0 ? (float)(1.0 / (1.0 - d.p)) : 0.f;
     p.x = x; p.r = residual; p.y = y;
     const int64_t e = (int64_t)elem_bytes(d.dtype);

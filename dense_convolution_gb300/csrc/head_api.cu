@@ -176,6 +176,7 @@ CONV2D_API conv2d_status linear_ce_desc_create(linear_ce_desc_t* out, int64_t to
     d.tokens = tokens; d.hidden = hidden; d.vocab = vocab; d.dtype = dtype;
     d.reduction = reduction; d.ignore_index = ignore_index;
     d.hs = d.ws = hidden;
+    linear_ce_plan(d);
     return give(out, d);
 }
 
@@ -187,6 +188,7 @@ CONV2D_API conv2d_status linear_ce_desc_set_row_strides(linear_ce_desc_t d, int6
         return CONV2D_ERR_BAD_PARAM;
     d->hs = h_stride;
     d->ws = w_stride;
+    linear_ce_plan(*d);
     return CONV2D_OK;
 }
 
@@ -194,6 +196,7 @@ CONV2D_API conv2d_status linear_ce_desc_set_piece(linear_ce_desc_t d, int64_t vo
     if (!d) return CONV2D_ERR_NULL_PTR;
     if (vocab_rows < 0 || vocab_rows > kMaxGemmSide) return CONV2D_ERR_BAD_PARAM;
     d->piece = vocab_rows;
+    linear_ce_plan(*d);
     return CONV2D_OK;
 }
 
@@ -204,10 +207,8 @@ CONV2D_API conv2d_status linear_ce_desc_destroy(linear_ce_desc_t d) {
 
 CONV2D_API conv2d_status linear_ce_workspace_size(linear_ce_desc_t d, size_t* fwd_bytes, size_t* bwd_bytes) {
     if (!d || (!fwd_bytes && !bwd_bytes)) return CONV2D_ERR_NULL_PTR;
-    size_t f = 0, b = 0;
-    linear_ce_workspace(*d, &f, &b);
-    if (fwd_bytes) *fwd_bytes = f;
-    if (bwd_bytes) *bwd_bytes = b;
+    if (fwd_bytes) *fwd_bytes = d->fwd.total;
+    if (bwd_bytes) *bwd_bytes = d->bwd.total;
     return CONV2D_OK;
 }
 
@@ -233,13 +234,11 @@ CONV2D_API conv2d_status linear_ce_fwd(linear_ce_desc_t dp, const void* h, const
         if (!loss) return CONV2D_ERR_NULL_PTR;
         return of(cudaMemsetAsync(loss, 0, sizeof(float), st));
     }
-    size_t need = 0;
-    linear_ce_workspace(d, &need, nullptr);
     if (!h || !w || !target || !loss || !lse || !workspace) return CONV2D_ERR_NULL_PTR;
     if (!ce_operand_ok(d, h, d.hs) || !ce_operand_ok(d, w, d.ws) || !aligned_to(target, 8) || !aligned_to(loss, 4) ||
         !aligned_to(lse, 4) || !aligned_to(workspace, 16))
         return CONV2D_ERR_MISALIGNED;
-    if (workspace_bytes < need) return CONV2D_ERR_WORKSPACE_TOO_SMALL;
+    if (workspace_bytes < d.fwd.total) return CONV2D_ERR_WORKSPACE_TOO_SMALL;
     return launch_linear_ce_fwd(d, h, w, target, loss, lse, workspace, st);
 }
 
@@ -254,12 +253,10 @@ CONV2D_API conv2d_status linear_ce_bwd(linear_ce_desc_t dp, const void* h, const
     if (!aligned_to(dh, e) || !aligned_to(dw, e)) return CONV2D_ERR_MISALIGNED;
     if (d.tokens == 0)
         return dw ? of(cudaMemsetAsync(dw, 0, (size_t)d.vocab * d.hidden * e, st)) : CONV2D_OK;
-    size_t need = 0;
-    linear_ce_workspace(d, nullptr, &need);
     if (!h || !w || !target || !lse || !dloss || !workspace) return CONV2D_ERR_NULL_PTR;
     if (!ce_operand_ok(d, h, d.hs) || !ce_operand_ok(d, w, d.ws) || !aligned_to(target, 8) || !aligned_to(lse, 4) ||
         !aligned_to(dloss, 4) || !aligned_to(workspace, 16))
         return CONV2D_ERR_MISALIGNED;
-    if (workspace_bytes < need) return CONV2D_ERR_WORKSPACE_TOO_SMALL;
+    if (workspace_bytes < d.bwd.total) return CONV2D_ERR_WORKSPACE_TOO_SMALL;
     return launch_linear_ce_bwd(d, h, w, target, lse, dloss, dh, dw, workspace, st);
 }

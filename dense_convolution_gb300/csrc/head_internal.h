@@ -24,6 +24,23 @@ struct dropout_desc {
     int64_t xs, rs, ys;  // row strides of x and dx, residual, y and dy
 };
 
+namespace conv2d_gb300 {
+
+// Tile width and K splits of one product (linear_ce.cu, plan_gemm).
+struct GemmPlan { int BN, splits; };
+
+// Sizes and workspace offsets of one pass of the linear cross entropy.
+struct CePlan {
+    bool bf16, pack_w, pack_h;
+    int parts, pairs;              // bf16 parts per value (1, or 3 for fp32) and their products (1 or 6)
+    int64_t dp;                    // packed row pitch of one part
+    int64_t piece, pieces;         // vocabulary rows per piece
+    GemmPlan z, dh, dw;
+    size_t part, z_target, row_loss, coef, common, hp, wp, dz, acc, sums, total;
+};
+
+}  // namespace conv2d_gb300
+
 struct linear_ce_desc {
     int64_t tokens, hidden, vocab;
     conv2d_dtype dtype;
@@ -31,6 +48,7 @@ struct linear_ce_desc {
     int64_t ignore_index;
     int64_t hs, ws;      // row strides of h and w
     int64_t piece;       // vocabulary rows per backward piece; 0 = automatic
+    conv2d_gb300::CePlan fwd, bwd;
 };
 
 namespace conv2d_gb300 {
@@ -63,7 +81,7 @@ cudaError_t launch_dropout(const dropout_desc& d, const void* x, int64_t xs, con
                            int64_t ys, uint64_t seed, uint64_t offset, cudaStream_t st);
 
 // linear_ce.cu
-void linear_ce_workspace(const linear_ce_desc& d, size_t* fwd, size_t* bwd);
+void linear_ce_plan(linear_ce_desc& d);      // sets fwd and bwd from the rest
 conv2d_status launch_linear_ce_fwd(const linear_ce_desc& d, const void* h, const void* w, const int64_t* target,
                                    float* loss, float* lse, void* ws, cudaStream_t st);
 conv2d_status launch_linear_ce_bwd(const linear_ce_desc& d, const void* h, const void* w, const int64_t* target,

@@ -47,7 +47,40 @@ struct LnParams {
     int want_params;
 };
 
-template <typename T> __host__ __device__ constexpr int vec_of(bool scalar) { return scalar ? 1 : 16 / (int)sizeof(T); }
+// How a call's rows are cut: whole 16-byte vectors only; vectors with single
+// elements at a row's ends; single elements.  (Whole rows get kernels of their
+// own: the code for the ends costs the backward kernel its registers.)
+enum Cut { WHOLE = 0, ENDS = 1, SINGLE = 2 };
+template <typename T, int CUT> __host__ __device__ constexpr int vec_of() { return CUT == SINGLE ? 1 : 16 / (int)sizeof(T); }
+
+// Vector slot s of a row that starts `shift` elements after a 16-byte boundary
+// covers elements [s V - shift, s V - shift + V); only the row's first and
+// last slot can stick out of it.
+template <int V> __device__ __forceinline__ bool slot_whole(int64_t e0, int cols) { return e0 >= 0 && e0 + V <= cols; }
+
+// A slot's elements that lie in the row: [first, last).
+template <int CUT> __device__ __forceinline__ int slot_first(int64_t e0) { return CUT == ENDS && e0 < 0 ? (int)-e0 : 0; }
+template <int CUT, int V> __device__ __forceinline__ int slot_last(int64_t e0, int cols) {
+    return CUT == ENDS && e0 + V > cols ? (int)(cols - e0) : V;
+}
+
+// NV slots s0 + j * step of a row, those below s1.  The whole ones first, so
+// that all of their loads are issued before the rare partial ones branch.
+template <typename T, int CUT, int V, int NV>
+__device__ __forceinline__ void load_row(const T* x, int cols, int shift, int s0, int step, int s1, Vec<T, V> (&raw)[NV]) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int s = s0 + j * step, e0 = s * V - shift;
+        if (s < s1 && (CUT != ENDS || slot_whole<V>(e0, cols))) raw[j] = *reinterpret_cast<const Vec<T, V>*>(x + e0);
+    }
+    if (CUT == ENDS) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int s = s0 + j * step, e0 = s * V - shift;
+            if (s < s1 && !slot_whole<V>(e0, cols)) raw[j] = load_part<T, V>(x + e0, slot_first<CUT>(e0), slot_last<CUT, V>(e0, cols));
+        }
+    }
+}
 
 // Sum over the tpr threads of each row group (red: 32 floats, one per warp).
 __device__ __forceinline__ float row_sum(float v, int tpr, float* red) {
@@ -60,9 +93,9 @@ __device__ __forceinline__ float row_sum(float v, int tpr, float* red) {
     return lane_sum(lane < wpr ? red[first + lane] : 0.f, 32);
 }
 
-template <typename T, bool SCALAR, int NV>
+template <typename T, int CUT, int NV>
 __global__ void __launch_bounds__(1024) layernorm_fwd_kernel(const LnParams p) {
-    constexpr int V = vec_of<T>(SCALAR);
+    constexpr int V = vec_of<T, CUT>();
     __shared__ float red[2][32];
     __shared__ float cl[2];
     pdl_wait();
@@ -72,18 +105,14 @@ __global__ void __launch_bounds__(1024) layernorm_fwd_kernel(const LnParams p) {
     const bool live = row < p.rows;
     const T* x = static_cast<const T*>(p.x) + (live ? row : 0) * p.xs;
     T* y = static_cast<T*>(p.y) + (live ? row : 0) * p.ys;
-    const int shift = SCALAR ? 0 : (int)((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
+    const int shift = CUT != ENDS ? 0 : (int)((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
     const int slots = live ? (p.cols + shift + V - 1) / V : 0;
     const int s0 = rank * p.per_block, s1 = min(slots, s0 + p.per_block);
     const bool vec = p.vec_params && shift == 0;
 
     Vec<T, V> raw[NV];
     float sum = 0.f;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int s = s0 + j * p.tpr + t, e0 = s * V - shift;
-        if (s < s1) raw[j] = load_part<T, V>(x + e0, max(0, -e0), min(V, p.cols - e0));
-    }
+    load_row<T, CUT, V, NV>(x, p.cols, shift, s0 + t, p.tpr, s1, raw);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         if (s0 + j * p.tpr + t < s1) {                 // elements outside the row are zero
@@ -113,7 +142,7 @@ __global__ void __launch_bounds__(1024) layernorm_fwd_kernel(const LnParams p) {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const float c = f[i] - mean;
-                if (V == 1 || (e0 + i >= 0 && e0 + i < p.cols)) sq += c * c;
+                if (CUT != ENDS || (e0 + i >= 0 && e0 + i < p.cols)) sq += c * c;
             }
         }
     }
@@ -135,7 +164,7 @@ __global__ void __launch_bounds__(1024) layernorm_fwd_kernel(const LnParams p) {
     for (int j = 0; j < NV; ++j) {
         const int s = s0 + j * p.tpr + t, e0 = s * V - shift;
         if (s < s1) {
-            const int lo = max(0, -e0), hi = min(V, p.cols - e0);
+            const int lo = slot_first<CUT>(e0), hi = slot_last<CUT, V>(e0, p.cols);
             float f[V], g[V], b[V];
             widen(raw[j], f);
             load_params<T, V>(p.gamma, p.param_f32, e0, lo, hi, vec, 1.f, g);
@@ -148,9 +177,9 @@ __global__ void __launch_bounds__(1024) layernorm_fwd_kernel(const LnParams p) {
 }
 
 // Rows beyond a cluster's registers: the same three steps, re-reading x.
-template <typename T, bool SCALAR>
+template <typename T, int CUT>
 __global__ void __launch_bounds__(1024) layernorm_fwd_long_kernel(const LnParams p) {
-    constexpr int V = vec_of<T>(SCALAR);
+    constexpr int V = vec_of<T, CUT>();
     __shared__ float red[2][32];
     __shared__ float cl[2];
     pdl_wait();
@@ -159,7 +188,7 @@ __global__ void __launch_bounds__(1024) layernorm_fwd_long_kernel(const LnParams
     const int64_t row = blockIdx.x / p.cs;
     const T* x = static_cast<const T*>(p.x) + row * p.xs;
     T* y = static_cast<T*>(p.y) + row * p.ys;
-    const int shift = SCALAR ? 0 : (int)((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
+    const int shift = CUT != ENDS ? 0 : (int)((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
     const int slots = (int)(((int64_t)p.cols + shift + V - 1) / V);
     const int64_t s0 = (int64_t)rank * p.per_block;
     const int64_t s1 = min((int64_t)slots, s0 + p.per_block);
@@ -168,7 +197,7 @@ __global__ void __launch_bounds__(1024) layernorm_fwd_long_kernel(const LnParams
     for (int64_t s = s0 + threadIdx.x; s < s1; s += blockDim.x) {
         const int64_t e0 = s * V - shift;
         float f[V];
-        widen(load_part<T, V>(x + e0, e0 < 0 ? (int)-e0 : 0, (int)min((int64_t)V, p.cols - e0)), f);
+        widen(load_part<T, V>(x + e0, slot_first<CUT>(e0), slot_last<CUT, V>(e0, p.cols)), f);
         float u = 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i) u += f[i];
@@ -181,7 +210,7 @@ __global__ void __launch_bounds__(1024) layernorm_fwd_long_kernel(const LnParams
     float sq = 0.f;
     for (int64_t s = s0 + threadIdx.x; s < s1; s += blockDim.x) {
         const int64_t e0 = s * V - shift;
-        const int lo = e0 < 0 ? (int)-e0 : 0, hi = (int)min((int64_t)V, p.cols - e0);
+        const int lo = slot_first<CUT>(e0), hi = slot_last<CUT, V>(e0, p.cols);
         float f[V];
         widen(load_part<T, V>(x + e0, lo, hi), f);
         float u = 0.f;
@@ -204,7 +233,7 @@ __global__ void __launch_bounds__(1024) layernorm_fwd_long_kernel(const LnParams
     }
     for (int64_t s = s0 + threadIdx.x; s < s1; s += blockDim.x) {
         const int64_t e0 = s * V - shift;
-        const int lo = e0 < 0 ? (int)-e0 : 0, hi = (int)min((int64_t)V, p.cols - e0);
+        const int lo = slot_first<CUT>(e0), hi = slot_last<CUT, V>(e0, p.cols);
         float f[V], g[V], b[V];
         widen(load_part<T, V>(x + e0, lo, hi), f);
         load_params<T, V>(p.gamma, p.param_f32, e0, lo, hi, vec, 1.f, g);
@@ -218,108 +247,114 @@ __global__ void __launch_bounds__(1024) layernorm_fwd_long_kernel(const LnParams
 // Backward of rows that a block's registers hold.  Group k of the grid takes
 // rows k, k + groups, ...; groups is a multiple of the vector length when rows
 // start off the 16-byte boundary, so that all rows of a group are cut alike
-// and a thread's registers keep the same columns.
-template <typename T, bool SCALAR, int NV>
-__global__ void __launch_bounds__(512) layernorm_bwd_kernel(const LnParams p) {
-    constexpr int V = vec_of<T>(SCALAR);
-    __shared__ float red[2][2][32];
+// and a thread's registers keep the same columns.  Eight elements of a row per
+// thread: sums, gamma and two rows in flight fit 64 registers, so 32 warps an
+// SM keep the memory busy; a group meets at a barrier of its own.
+template <typename T, int CUT, int NV, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) layernorm_bwd_kernel(const LnParams p) {
+    constexpr int V = vec_of<T, CUT>();
+    __shared__ float2 red[2][32];
     extern __shared__ float acc_s[];                   // [2][cols] when several groups share the block
     pdl_wait();
-    const int rpb = blockDim.x / p.tpr, sub = threadIdx.x / p.tpr, t = threadIdx.x - sub * p.tpr;
+    const int tpr = p.tpr, rpb = blockDim.x / tpr, sub = threadIdx.x / tpr, t = threadIdx.x - sub * tpr;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int group = blockIdx.x * rpb + sub;
     const T* x0 = static_cast<const T*>(p.x);
+    const T* d0 = static_cast<const T*>(p.dy);
     const int shift =
-        SCALAR ? 0 : (int)((reinterpret_cast<uintptr_t>(x0 + (int64_t)group * p.xs) & 15u) / sizeof(T));
+        CUT != ENDS ? 0 : (int)((reinterpret_cast<uintptr_t>(x0 + (int64_t)group * p.xs) & 15u) / sizeof(T));
     const int slots = (p.cols + shift + V - 1) / V;
     const bool vec = p.vec_params && shift == 0;
 
     float g[NV][V], dg[NV][V], db[NV][V];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        const int s = j * p.tpr + t, e0 = s * V - shift;
+        const int s = j * tpr + t, e0 = s * V - shift;
         const bool in = s < slots;
-        load_params<T, V>(p.gamma, p.param_f32, e0, in ? max(0, -e0) : V, in ? min(V, p.cols - e0) : 0, vec && in, 1.f,
+        load_params<T, V>(p.gamma, p.param_f32, e0, in ? slot_first<CUT>(e0) : V, in ? slot_last<CUT, V>(e0, p.cols) : 0, vec && in, 1.f,
                           g[j]);
 #pragma unroll
         for (int i = 0; i < V; ++i) dg[j][i] = db[j][i] = 0.f;
     }
-    // Every group of the block runs the same number of turns (they meet at barriers).
-    const int64_t turns = (p.rows - (int64_t)blockIdx.x * rpb + p.groups - 1) / p.groups;
+    // Every group of the block runs the same number of turns.
+    const int rows = (int)p.rows, turns = (int)((p.rows - (int64_t)blockIdx.x * rpb + p.groups - 1) / p.groups);
     Vec<T, V> rx[NV], rd[NV];
-    float mean = 0.f, rstd = 0.f;
-    auto fetch = [&](int64_t row) {
-        if (row < p.rows) {
-            const T* x = x0 + row * p.xs;
-            const T* dy = static_cast<const T*>(p.dy) + row * p.ys;
-#pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int s = j * p.tpr + t, e0 = s * V - shift;
-                if (s < slots) {
-                    const int lo = max(0, -e0), hi = min(V, p.cols - e0);
-                    rx[j] = load_part<T, V>(x + e0, lo, hi);
-                    rd[j] = load_part<T, V>(dy + e0, lo, hi);
-                }
-            }
-            mean = p.mean_in[row];
-            rstd = p.rstd_in[row];
+    float mu = 0.f, r = 0.f;
+    if (group < p.rows) {
+        load_row<T, CUT, V, NV>(x0 + (int64_t)group * p.xs, p.cols, shift, t, tpr, slots, rx);
+        load_row<T, CUT, V, NV>(d0 + (int64_t)group * p.ys, p.cols, shift, t, tpr, slots, rd);
+        mu = p.mean_in[group];
+        r = p.rstd_in[group];
+    }
+    // Number of lanes that hold the warps' sums of a row, a power of two.
+    const int wpr = tpr >> 5;
+    int width = 1;
+    while (width < wpr) width <<= 1;
+    int64_t row = group;
+    for (int it = 0; it < turns; ++it, row += p.groups) {
+        const int64_t next = row + p.groups;
+        const bool live = row < rows;
+        Vec<T, V> nx[NV], nd[NV];
+        float nmu = 0.f, nr = 0.f;
+        if (next < rows) {                             // under this row's arithmetic
+            load_row<T, CUT, V, NV>(x0 + next * p.xs, p.cols, shift, t, tpr, slots, nx);
+            load_row<T, CUT, V, NV>(d0 + next * p.ys, p.cols, shift, t, tpr, slots, nd);
+            nmu = p.mean_in[next];
+            nr = p.rstd_in[next];
         }
-    };
-    fetch(group);
-    for (int64_t it = 0; it < turns; ++it) {
-        const int64_t row = group + it * p.groups;
-        const bool live = row < p.rows;
-        const float mu = mean, r = rstd;
-        float z[NV][V], a[NV][V];
         float s1 = 0.f, s2 = 0.f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int s = j * p.tpr + t, e0 = s * V - shift;
+            const int s = j * tpr + t;
             if (live && s < slots) {
                 float fx[V], fd[V];
                 widen(rx[j], fx);
                 widen(rd[j], fd);
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    // Outside the row dy is zero; z must be too (it is finite, but has no column).
-                    const bool in = V == 1 || (e0 + i >= 0 && e0 + i < p.cols);
-                    z[j][i] = in ? (fx[i] - mu) * r : 0.f;
-                    a[j][i] = fd[i] * g[j][i];
-                    s1 += a[j][i];
-                    s2 += a[j][i] * z[j][i];
-                    dg[j][i] += fd[i] * z[j][i];
+                for (int i = 0; i < V; ++i) {          // outside the row dy, and so every term, is zero
+                    const float z = (fx[i] - mu) * r, a = fd[i] * g[j][i];
+                    s1 += a;
+                    s2 += a * z;
+                    dg[j][i] += fd[i] * z;
                     db[j][i] += fd[i];
                 }
             }
         }
-        fetch(row + p.groups);                         // the next row's loads run under the sums
-        if (!p.dx) continue;
-        const int tpr = p.tpr;
-        s1 = lane_sum(s1, tpr < 32 ? tpr : 32);
-        s2 = lane_sum(s2, tpr < 32 ? tpr : 32);
-        if (tpr > 32) {
-            // Two buffers in turn: a warp that is a row ahead writes the other one.
-            const int wpr = tpr >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = (int)(it & 1);
-            if (lane == 0) { red[b][0][warp] = s1; red[b][1][warp] = s2; }
-            __syncthreads();
-            const int first = warp / wpr * wpr;
-            s1 = lane_sum(lane < wpr ? red[b][0][first + lane] : 0.f, 32);
-            s2 = lane_sum(lane < wpr ? red[b][1][first + lane] : 0.f, 32);
-        }
-        s1 *= p.inv_cols;
-        s2 *= p.inv_cols;
-        if (live) {
-            T* dx = static_cast<T*>(p.dx) + row * p.xs;
+        if (p.dx) {
+            s1 = lane_sum(s1, tpr < 32 ? tpr : 32);
+            s2 = lane_sum(s2, tpr < 32 ? tpr : 32);
+            if (tpr > 32) {
+                // Two buffers in turn: a warp that is a row ahead writes the other one.
+                float2* buf = red[it & 1];
+                if (lane == 0) buf[warp] = make_float2(s1, s2);
+                named_bar_sync(1 + sub, tpr);
+                const int k = lane & (width - 1);
+                const float2 v = k < wpr ? buf[sub * wpr + k] : make_float2(0.f, 0.f);
+                s1 = lane_sum(v.x, width);
+                s2 = lane_sum(v.y, width);
+            }
+            s1 *= p.inv_cols;
+            s2 *= p.inv_cols;
+            if (live) {
+                T* dx = static_cast<T*>(p.dx) + row * p.xs;
 #pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int s = j * p.tpr + t, e0 = s * V - shift;
-                if (s < slots) {
-                    float f[V];
+                for (int j = 0; j < NV; ++j) {
+                    const int s = j * tpr + t, e0 = s * V - shift;
+                    if (s < slots) {
+                        float fx[V], f[V];
+                        widen(rx[j], fx);
+                        widen(rd[j], f);
 #pragma unroll
-                    for (int i = 0; i < V; ++i) f[i] = r * (a[j][i] - s1 - z[j][i] * s2);
-                    store_part<T, V>(dx + e0, narrow<T, V>(f), max(0, -e0), min(V, p.cols - e0));
+                        for (int i = 0; i < V; ++i) f[i] = r * (f[i] * g[j][i] - s1 - (fx[i] - mu) * r * s2);
+                        store_part<T, V>(dx + e0, narrow<T, V>(f), slot_first<CUT>(e0), slot_last<CUT, V>(e0, p.cols));
+                    }
                 }
             }
         }
+#pragma unroll
+        for (int j = 0; j < NV; ++j) { rx[j] = nx[j]; rd[j] = nd[j]; }
+        mu = nmu;
+        r = nr;
     }
     if (!p.want_params) return;
     float* out = p.part + (int64_t)blockIdx.x * 2 * p.cols;
@@ -329,11 +364,11 @@ __global__ void __launch_bounds__(512) layernorm_bwd_kernel(const LnParams p) {
             float* dst = k + 1 < rpb ? acc_s : out;
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                const int s = j * p.tpr + t, e0 = s * V - shift;
+                const int s = j * tpr + t, e0 = s * V - shift;
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     const int c = e0 + i;
-                    if (s < slots && c >= 0 && c < p.cols) {
+                    if (s < slots && (CUT != ENDS || (c >= 0 && c < p.cols))) {
                         dst[c] = dg[j][i] + (k ? acc_s[c] : 0.f);
                         dst[p.cols + c] = db[j][i] + (k ? acc_s[p.cols + c] : 0.f);
                     }
@@ -344,15 +379,15 @@ __global__ void __launch_bounds__(512) layernorm_bwd_kernel(const LnParams p) {
 }
 
 // Long rows, pass 1: sum a and sum a z of one row's share of columns.
-template <typename T, bool SCALAR>
+template <typename T, int CUT>
 __global__ void __launch_bounds__(256) layernorm_bwd_sums_kernel(const LnParams p, float2* sums) {
-    constexpr int V = vec_of<T>(SCALAR);
+    constexpr int V = vec_of<T, CUT>();
     __shared__ float red[2][32];
     pdl_wait();
     const int64_t row = blockIdx.x;
     const T* x = static_cast<const T*>(p.x) + row * p.xs;
     const T* dy = static_cast<const T*>(p.dy) + row * p.ys;
-    const int shift = SCALAR ? 0 : (int)((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
+    const int shift = CUT != ENDS ? 0 : (int)((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
     const int64_t slots = ((int64_t)p.cols + shift + V - 1) / V;
     const int64_t per = (slots + gridDim.y - 1) / gridDim.y;
     const int64_t s0 = blockIdx.y * per, s1 = min(slots, s0 + per);
@@ -361,7 +396,7 @@ __global__ void __launch_bounds__(256) layernorm_bwd_sums_kernel(const LnParams 
     float a1 = 0.f, a2 = 0.f;
     for (int64_t s = s0 + threadIdx.x; s < s1; s += blockDim.x) {
         const int64_t e0 = s * V - shift;
-        const int lo = e0 < 0 ? (int)-e0 : 0, hi = (int)min((int64_t)V, p.cols - e0);
+        const int lo = slot_first<CUT>(e0), hi = slot_last<CUT, V>(e0, p.cols);
         float fx[V], fd[V], g[V];
         widen(load_part<T, V>(x + e0, lo, hi), fx);
         widen(load_part<T, V>(dy + e0, lo, hi), fd);
@@ -386,15 +421,15 @@ __global__ void __launch_bounds__(256) layernorm_bwd_sums_kernel(const LnParams 
 // Long rows, pass 2: a thread owns one vector of columns and runs down every
 // gridDim.y-th row (a multiple of the vector length when rows are cut
 // differently, as above), writing dx and adding dgamma and dbeta.
-template <typename T, bool SCALAR>
+template <typename T, int CUT>
 __global__ void __launch_bounds__(128) layernorm_bwd_cols_kernel(const LnParams p, const float2* sums, int shares) {
-    constexpr int V = vec_of<T>(SCALAR);
+    constexpr int V = vec_of<T, CUT>();
     pdl_wait();
     const T* x0 = static_cast<const T*>(p.x) + (int64_t)blockIdx.y * p.xs;
-    const int shift = SCALAR ? 0 : (int)((reinterpret_cast<uintptr_t>(x0) & 15u) / sizeof(T));
+    const int shift = CUT != ENDS ? 0 : (int)((reinterpret_cast<uintptr_t>(x0) & 15u) / sizeof(T));
     const int64_t s = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, e0 = s * V - shift;
     if (e0 >= p.cols) return;
-    const int lo = e0 < 0 ? (int)-e0 : 0, hi = (int)min((int64_t)V, p.cols - e0);
+    const int lo = slot_first<CUT>(e0), hi = slot_last<CUT, V>(e0, p.cols);
     const bool vec = p.vec_params && shift == 0;
     float g[V], dg[V], db[V];
     load_params<T, V>(p.gamma, p.param_f32, e0, lo, hi, vec, 1.f, g);
@@ -434,11 +469,12 @@ __global__ void __launch_bounds__(128) layernorm_bwd_cols_kernel(const LnParams 
     }
 }
 
-// dgamma and dbeta: the parts' columns added in order, 32 columns by 8 shares
-// of the parts per block (blockIdx.y: dgamma or dbeta).
-__global__ void __launch_bounds__(256) layernorm_params_kernel(const float* part, int parts, int cols, void* dgamma,
-                                                               void* dbeta, int f32, int bf16) {
-    __shared__ float sh[8][33];
+// dgamma and dbeta: the parts' columns added in order, 32 columns by 32 shares
+// of the parts per block (blockIdx.y: dgamma or dbeta).  A few hundred parts:
+// one round of about ten loads per thread, all in flight.
+__global__ void __launch_bounds__(1024) layernorm_params_kernel(const float* part, int parts, int cols, void* dgamma,
+                                                                void* dbeta, int f32, int bf16) {
+    __shared__ float sh[32][33];
     pdl_wait();
     void* out = blockIdx.y ? dbeta : dgamma;
     if (!out) return;
@@ -448,21 +484,15 @@ __global__ void __launch_bounds__(256) layernorm_params_kernel(const float* part
     if (c < cols) {
         const float* q = part + (int64_t)blockIdx.y * cols + c;
         const int64_t pitch = 2 * (int64_t)cols;
-        int i = k;
-        for (; i + 24 < parts; i += 32) {              // four loads in flight
-            const float a0 = q[i * pitch], a1 = q[(i + 8) * pitch], a2 = q[(i + 16) * pitch], a3 = q[(i + 24) * pitch];
-            v += (a0 + a1) + (a2 + a3);
-        }
-        for (; i < parts; i += 8) v += q[i * pitch];
+#pragma unroll 10
+        for (int i = k; i < parts; i += 32) v += q[i * pitch];
     }
     sh[k][lane] = v;
     __syncthreads();
-    if (k == 0 && c < cols) {
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s += sh[i][lane];
-        store_param(out, f32, bf16, c, s);
-    }
+    // Warp k adds column k's 32 shares.
+    v = lane_sum(sh[lane][k], 32);
+    const int64_t col = (int64_t)blockIdx.x * 32 + k;
+    if (lane == 0 && col < cols) store_param(out, f32, bf16, col, v);
 }
 
 // ------------------------------------------------------------------ host side
@@ -478,12 +508,12 @@ int threads_for(int64_t slots, int nv) {
     return p;
 }
 
-constexpr int kBwdElems = 16;         // backward: elements of a row per thread at most (registers)
-constexpr int kBwdThreads = 512;      // and threads per row
+constexpr int kBwdElems = 8;          // backward: elements of a row per thread at most (registers)
+constexpr int kBwdCols = kBwdElems * 1024;
 
-bool bwd_in_block(const layernorm_desc& d) { return d.cols <= (int64_t)(kBwdElems - 1) * kBwdThreads; }
-
-int bwd_grid() { return device_sm_count() * 2; }
+// Blocks of the in-block form at most: 1024 threads an SM, in blocks of 512 or
+// one of 1024; rounded up to whole vectors of groups.
+int bwd_grid(int tpr) { return device_sm_count() * (tpr > 512 ? 1 : 2); }
 
 // Blocks per row of the long form's sums at most: eight blocks per SM in all.
 int64_t long_shares(int64_t rows) {
@@ -498,10 +528,21 @@ bool same_phase(const void* a, int64_t sa, const void* b, int64_t sb, size_t e) 
            ((sa - sb) * (int64_t)e) % 16 == 0;
 }
 
+// The cut of a call that moves vectors.
+int cut_of(const void* x, int64_t xs, int64_t cols, size_t e) {
+    const bool whole = aligned_to(x, 16) && xs * (int64_t)e % 16 == 0 && cols * (int64_t)e % 16 == 0;
+    return whole ? WHOLE : ENDS;
+}
+
 template <typename T> cudaError_t fwd_typed(const layernorm_desc& d, LnParams p, cudaStream_t st) {
     const bool scalar = !same_phase(p.x, p.xs, p.y, p.ys, sizeof(T));
+    const int cut = scalar ? SINGLE : cut_of(p.x, p.xs, p.cols, sizeof(T));
     const int V = scalar ? 1 : 16 / (int)sizeof(T);
-    const int64_t slots = ceil_div(p.cols + V - 1, V);      // with the widest cut
+    // Vectors of the most unevenly cut row.
+    const int shift = scalar                                  ? 0
+                      : (p.xs * (int64_t)sizeof(T)) % 16 == 0 ? (int)((reinterpret_cast<uintptr_t>(p.x) & 15u) / sizeof(T))
+                                                              : V - 1;
+    const int64_t slots = ceil_div((int64_t)p.cols + shift, V);
     // Vectors per thread: as few as keep every row's threads resident at once
     // (64 warps an SM), so that small calls spread over the GPU and large
     // ones keep several loads per thread in flight.
@@ -546,11 +587,13 @@ template <typename T> cudaError_t fwd_typed(const layernorm_desc& d, LnParams p,
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     if (is_long)
-        return scalar ? cudaLaunchKernelEx(&cfg, layernorm_fwd_long_kernel<T, true>, p)
-                      : cudaLaunchKernelEx(&cfg, layernorm_fwd_long_kernel<T, false>, p);
-#define LN_FWD(NV)                                                                    \
-    (scalar ? cudaLaunchKernelEx(&cfg, layernorm_fwd_kernel<T, true, NV>, p)          \
-            : cudaLaunchKernelEx(&cfg, layernorm_fwd_kernel<T, false, NV>, p))
+        return cudaLaunchKernelEx(&cfg, cut == SINGLE ? layernorm_fwd_long_kernel<T, SINGLE>
+                                        : cut == ENDS ? layernorm_fwd_long_kernel<T, ENDS>
+                                                      : layernorm_fwd_long_kernel<T, WHOLE>, p);
+#define LN_FWD(NV)                                                              \
+    cudaLaunchKernelEx(&cfg, cut == SINGLE ? layernorm_fwd_kernel<T, SINGLE, NV> \
+                             : cut == ENDS ? layernorm_fwd_kernel<T, ENDS, NV>   \
+                                           : layernorm_fwd_kernel<T, WHOLE, NV>, p)
     switch (nv) {
         case 1: return LN_FWD(1);
         case 2: return LN_FWD(2);
@@ -563,34 +606,44 @@ template <typename T> cudaError_t fwd_typed(const layernorm_desc& d, LnParams p,
 template <typename T> cudaError_t bwd_typed(const layernorm_desc& d, LnParams p, float* ws, int* parts, cudaStream_t st) {
     const bool scalar = !same_phase(p.x, p.xs, p.dy, p.ys, sizeof(T)) ||
                         (p.dx && !same_phase(p.x, p.xs, p.dx, p.xs, sizeof(T)));
+    const int cut = scalar ? SINGLE : cut_of(p.x, p.xs, p.cols, sizeof(T));
     const int V = scalar ? 1 : 16 / (int)sizeof(T);
     const bool cut_alike = scalar || (p.xs * (int64_t)sizeof(T)) % 16 == 0;
-    const int64_t slots = ceil_div(p.cols + V - 1, V);
+    const int most_shift = scalar     ? 0
+                           : cut_alike ? (int)((reinterpret_cast<uintptr_t>(p.x) & 15u) / sizeof(T))
+                                       : V - 1;
+    const int64_t slots = ceil_div((int64_t)p.cols + most_shift, V);
     const int sms = device_sm_count();
-    if (bwd_in_block(d)) {
+    if (slots * V <= kBwdCols) {
+        // As many threads a row as keep one vector each, or eight elements.
         int nv = 1;
-        const int64_t room = (int64_t)sms * 512;
-        while (nv * V < kBwdElems && (threads_for(slots, nv) > kBwdThreads || p.rows * threads_for(slots, nv) > room))
-            nv *= 2;
+        const int64_t room = (int64_t)sms * 1024;
+        while (nv * V < kBwdElems && (threads_for(slots, nv) > 1024 || p.rows * threads_for(slots, nv) > room)) nv *= 2;
         p.tpr = threads_for(slots, nv);
-        const int rpb = p.tpr >= 256 ? 1 : 256 / p.tpr;
+        const int block = p.tpr > 512 ? p.tpr : 512 / p.tpr * p.tpr;
+        const int rpb = block / p.tpr;
         int64_t grid = ceil_div(p.rows, rpb);
-        if (grid > bwd_grid()) grid = bwd_grid();
+        if (grid > bwd_grid(p.tpr)) grid = bwd_grid(p.tpr);
         if (!cut_alike) grid = ceil_div(grid, V) * V;
         p.groups = (int)grid * rpb;
         *parts = (int)grid;
         const size_t smem = rpb > 1 && p.want_params ? 2 * (size_t)p.cols * sizeof(float) : 0;
-#define LN_BWD(NV)                                                                                               \
-    launch_after(scalar ? layernorm_bwd_kernel<T, true, NV> : layernorm_bwd_kernel<T, false, (NV * 16 / (int)sizeof(T) <= kBwdElems ? NV : 1)>, \
-                 dim3((unsigned)grid), dim3(p.tpr * rpb), smem, st, p)
-        switch (nv) {
-            case 1: return LN_BWD(1);
-            case 2: return LN_BWD(2);
-            case 4: return LN_BWD(4);
-            case 8: return LN_BWD(8);
-            default: return LN_BWD(16);
+#define LN_BWD_AT(CUT, NV, TH) launch_after(layernorm_bwd_kernel<T, CUT, NV, TH>, dim3((unsigned)grid), dim3(block), smem, st, p)
+#define LN_BWD(CUT, NV) (block > 512 ? LN_BWD_AT(CUT, NV, 1024) : LN_BWD_AT(CUT, NV, 512))
+        if (cut == SINGLE) {
+            switch (nv) {
+                case 1: return LN_BWD(SINGLE, 1);
+                case 2: return LN_BWD(SINGLE, 2);
+                case 4: return LN_BWD(SINGLE, 4);
+                default: return LN_BWD(SINGLE, 8);
+            }
         }
+        if constexpr (sizeof(T) == 4) {
+            if (nv == 2) return cut == ENDS ? LN_BWD(ENDS, 2) : LN_BWD(WHOLE, 2);
+        }
+        return cut == ENDS ? LN_BWD(ENDS, 1) : LN_BWD(WHOLE, 1);
 #undef LN_BWD
+#undef LN_BWD_AT
     }
     // Two passes: row sums, then columns.  Enough shares of the columns, and
     // of the rows, to fill the GPU.
@@ -599,7 +652,7 @@ template <typename T> cudaError_t bwd_typed(const layernorm_desc& d, LnParams p,
     float2* sums = reinterpret_cast<float2*>(ws);
     cudaError_t e = cudaSuccess;
     if (p.dx) {
-        e = launch_after(scalar ? layernorm_bwd_sums_kernel<T, true> : layernorm_bwd_sums_kernel<T, false>,
+        e = launch_after(cut == SINGLE ? layernorm_bwd_sums_kernel<T, SINGLE> : layernorm_bwd_sums_kernel<T, ENDS>,
                          dim3((unsigned)p.rows, (unsigned)shares), dim3(256), 0, st, p, sums);
         if (e != cudaSuccess) return e;
     }
@@ -610,7 +663,7 @@ template <typename T> cudaError_t bwd_typed(const layernorm_desc& d, LnParams p,
     if (!cut_alike) gy = ceil_div(gy, V) * V;
     if (gy > 64) gy = 64;
     *parts = (int)gy;
-    return launch_after(scalar ? layernorm_bwd_cols_kernel<T, true> : layernorm_bwd_cols_kernel<T, false>,
+    return launch_after(cut == SINGLE ? layernorm_bwd_cols_kernel<T, SINGLE> : layernorm_bwd_cols_kernel<T, ENDS>,
                         dim3((unsigned)gx, (unsigned)gy), dim3(128), 0, st, p, static_cast<const float2*>(sums),
                         p.dx ? (int)shares : 0);
 }
@@ -636,19 +689,22 @@ cudaError_t launch_layernorm_fwd(const layernorm_desc& d, const void* x, const v
 
 // Row sums of the long form (rows x shares pairs), then the parts of dgamma
 // and dbeta (blocks of the in-block form, or row shares of the long one).
+// Which form runs depends on the tensors' alignment when a vector more or
+// less decides, so the sizes allow for both.
 static size_t bwd_sums_bytes(const layernorm_desc& d) {
-    return bwd_in_block(d) ? 0 : align_up((size_t)(d.rows * long_shares(d.rows)) * sizeof(float2), 256);
+    if (d.cols <= kBwdCols - 8) return 0;
+    return align_up((size_t)(d.rows * long_shares(d.rows)) * sizeof(float2), 256);
 }
 
 size_t layernorm_bwd_workspace(const layernorm_desc& d) {
     if (d.pixels) return layernorm_planes_bwd_workspace(d);
-    const size_t parts = bwd_in_block(d) ? (size_t)bwd_grid() + 8 : 64;
+    const size_t parts = d.cols <= kBwdCols ? (size_t)bwd_grid(1) + 8 : 64;
     return bwd_sums_bytes(d) + parts * 2 * (size_t)d.cols * sizeof(float);
 }
 
 cudaError_t launch_layernorm_params(const float* part, int parts, const layernorm_desc& d, void* dgamma, void* dbeta,
                                     cudaStream_t st) {
-    return launch_after(layernorm_params_kernel, dim3((unsigned)((d.cols + 31) / 32), 2), dim3(256), 0, st, part, parts,
+    return launch_after(layernorm_params_kernel, dim3((unsigned)((d.cols + 31) / 32), 2), dim3(1024), 0, st, part, parts,
                         (int)d.cols, dgamma, dbeta, d.param == CONV2D_F32 ? 1 : 0, d.param == CONV2D_BF16 ? 1 : 0);
 }
 

@@ -36,6 +36,10 @@
 #include <cuda.h>
 #include <math.h>
 
+#include <mutex>
+#include <set>
+#include <utility>
+
 #include "head_device.cuh"
 #include "head_internal.h"
 #include "ptx.cuh"
@@ -710,7 +714,6 @@ bool make_map(CUtensorMap* map, const void* base, bool bf16, int64_t rows, int64
 
 constexpr int64_t kMostPiece = 1LL << 28;      // three parts of a piece keep 32-bit column numbers
 
-struct GemmPlan { int BN, splits; };
 
 // Tile width and K splits by an estimate in SM cycles.  An item (one tile of
 // one split) takes its MMAs (2 BN cycles per 64-wide chunk), a fixed cost per
@@ -739,6 +742,19 @@ GemmPlan plan_gemm(int64_t M, int64_t N, int64_t chunks, int step, bool may_spli
 // (32 columns in about 100 cycles a warp) stay under those chunks' MMAs.
 constexpr int kSegment = 4;
 
+// Lift a kernel's shared-memory limit, once per device and kernel.
+bool allow_smem(const void* kern) {
+    static std::mutex lock;
+    static std::set<std::pair<int, const void*>> done;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    std::lock_guard<std::mutex> hold(lock);
+    if (done.count({dev, kern})) return true;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost) != cudaSuccess) return false;
+    done.insert({dev, kern});
+    return true;
+}
+
 template <int EPI, bool A_MN, bool B_MN>
 conv2d_status launch_gemm(bool bf16, const CUtensorMap& a, const CUtensorMap& b, GemmParams p, cudaStream_t st) {
     // fp32 operands (six products) are bf16 parts; their results stay in fp32.
@@ -751,8 +767,7 @@ conv2d_status launch_gemm(bool bf16, const CUtensorMap& a, const CUtensorMap& b,
     p.stages = (kSmemMost - fixed) / stage_bytes;
     if (p.stages > kMaxRing) p.stages = kMaxRing;
     const int smem = fixed + p.stages * stage_bytes;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-        return CONV2D_ERR_CUDA;
+    if (!allow_smem(reinterpret_cast<const void*>(kern))) return CONV2D_ERR_CUDA;
     p.n_m = (int)ceil_div(p.M, kBM);
     p.n_n = (int)ceil_div(p.N, p.BN);
     const int64_t items = (int64_t)p.n_m * p.n_n * p.splits;
@@ -765,16 +780,6 @@ conv2d_status launch_gemm(bool bf16, const CUtensorMap& a, const CUtensorMap& b,
     return launch_after(kern, dim3(grid), dim3(kThreads), smem, st, a, b, p) == cudaSuccess ? CONV2D_OK
                                                                                             : CONV2D_ERR_CUDA;
 }
-
-// Sizes and workspace offsets of both passes.
-struct CePlan {
-    bool bf16, pack_w, pack_h;
-    int parts, pairs;
-    int64_t dp;                    // packed row pitch of one part
-    int64_t piece, pieces;         // vocabulary rows per piece
-    GemmPlan z, dh, dw;
-    size_t part, z_target, row_loss, coef, common, hp, wp, dz, acc, sums, total;
-};
 
 void take(size_t& at, size_t& off, size_t bytes) {
     off = at;
@@ -919,14 +924,16 @@ const void* at_row(const void* base, int64_t row, int64_t stride, size_t e) {
 
 }  // namespace
 
-void linear_ce_workspace(const linear_ce_desc& d, size_t* fwd, size_t* bwd) {
-    if (fwd) *fwd = d.tokens ? plan_ce(d, false).total : 0;
-    if (bwd) *bwd = d.tokens ? plan_ce(d, true).total : 0;
+void linear_ce_plan(linear_ce_desc& d) {
+    d.fwd = d.bwd = CePlan{};
+    if (d.tokens == 0) return;
+    d.fwd = plan_ce(d, false);
+    d.bwd = plan_ce(d, true);
 }
 
 conv2d_status launch_linear_ce_fwd(const linear_ce_desc& d, const void* h, const void* w, const int64_t* target,
                                    float* loss, float* lse, void* ws, cudaStream_t st) {
-    const CePlan c = plan_ce(d, false);
+    const CePlan& c = d.fwd;
     uint8_t* base = static_cast<uint8_t*>(ws);
     const size_t e = elem_bytes(d.dtype);
     Operand ho{h, d.hidden, d.hs};
@@ -972,7 +979,7 @@ conv2d_status launch_linear_ce_fwd(const linear_ce_desc& d, const void* h, const
 conv2d_status launch_linear_ce_bwd(const linear_ce_desc& d, const void* h, const void* w, const int64_t* target,
                                    const float* lse, const float* dloss, void* dh, void* dw, void* ws,
                                    cudaStream_t st) {
-    const CePlan c = plan_ce(d, true);
+    const CePlan& c = d.bwd;
     uint8_t* base = static_cast<uint8_t*>(ws);
     const size_t e = elem_bytes(d.dtype);
     float* coef = reinterpret_cast<float*>(base + c.coef);

@@ -17,8 +17,11 @@ from . import head_capi
 from .conv import _NAME, _TORCH_DTYPE
 
 
-def _stream(device):
-    return torch.cuda.current_stream(device).cuda_stream
+_raw_stream = torch._C._cuda_getCurrentRawStream      # the current stream's handle by device index
+
+
+def _stream(t):
+    return _raw_stream(t.device.index)
 
 
 def _on_stream(f):
@@ -36,23 +39,29 @@ def _ptr(t):
     return t.data_ptr() if t is not None else 0
 
 
-def _check_rows(name, t, rows, cols, stride, dtype):
-    """A (rows, cols) tensor whose rows are `stride` elements apart."""
-    if (t.dtype != _TORCH_DTYPE[dtype] or t.shape != (rows, cols)
-            or not (t.stride() == (stride, 1) or _same_rows(t, rows, cols, stride))):
-        raise ValueError(f"{name} must be a {dtype} tensor of shape {(rows, cols)} with rows {stride} elements apart")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
+class _Rows:
+    """The (rows, cols) tensors of one type whose rows are `stride` elements apart."""
 
+    def __init__(self, rows, cols, stride, dtype):
+        self.shape, self.strides, self.name, self.dtype = (rows, cols), (stride, 1), dtype, _TORCH_DTYPE[dtype]
 
-def _same_rows(t, rows, cols, stride):
-    # Strides of dimensions of size one (or of empty tensors) mean nothing.
-    return (cols <= 1 or t.stride(1) == 1) and (rows <= 1 or t.stride(0) == stride)
+    def check(self, name, t):
+        if t.dtype is self.dtype and t.shape == self.shape and t.is_cuda:
+            s = t.stride()
+            # The stride of a dimension of size one (or of an empty tensor) means nothing.
+            if s == self.strides or ((self.shape[0] <= 1 or s[0] == self.strides[0])
+                                     and (self.shape[1] <= 1 or s[1] == 1)) or t.numel() == 0:
+                return
+        raise ValueError(f"{name} must be a CUDA {self.name} tensor of shape {self.shape} with rows "
+                         f"{self.strides[0]} elements apart")
+
+    def new(self, device):
+        return torch.empty_strided(self.shape, self.strides, dtype=self.dtype, device=device)
 
 
 def _check_flat(name, t, shape, dtype):
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError(f"{name} must be a contiguous CUDA tensor of {dtype} and shape {tuple(shape)}")
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{name} must be a contiguous CUDA tensor of {dtype} and shape {shape}")
 
 
 class _Op:
@@ -89,62 +98,60 @@ class LayerNorm(_Op):
         if pixels:
             head_capi.layernorm_desc_set_planes(self.desc, pixels)
         self.workspace_bytes = head_capi.layernorm_workspace_size(self.desc)
+        self._x, self._y = _Rows(rows, cols, self.x_stride, dtype), _Rows(rows, cols, self.y_stride, dtype)
+        self._param = _TORCH_DTYPE[self.param_dtype]
 
-    def _check_x(self, name, x):
+    def _check_x(self, x):
         if not self.pixels:
-            _check_rows(name, x, self.rows, self.cols, self.x_stride, self.dtype)
+            self._x.check("x", x)
             return
         want = (self.rows // self.pixels, self.cols)
-        if (x.dim() < 3 or tuple(x.shape[:2]) != want or x[0, 0].numel() != self.pixels if x.numel() else False) \
-                or x.numel() != self.rows * self.cols or x.dtype != _TORCH_DTYPE[self.dtype] \
-                or not x.is_contiguous() or not x.is_cuda:
-            raise ValueError(f"{name} must be contiguous {self.dtype} planes of shape {want} + pixels, "
-                             f"{self.pixels} pixels each")
+        if x.dtype is not self._x.dtype or x.dim() < 3 or x.shape[:2] != want \
+                or x.numel() != self.rows * self.cols or not x.is_contiguous() or not x.is_cuda:
+            raise ValueError(f"x must be contiguous CUDA {self.dtype} planes of shape {want} and {self.pixels} pixels")
 
-    def _check_params(self, *named):
-        for name, t in named:
-            if t is not None:
-                _check_flat(name, t, (self.cols,), _TORCH_DTYPE[self.param_dtype])
-
-    def _like_x(self, x):
-        if self.pixels:
-            return torch.empty_like(x)
-        return torch.empty_strided((self.rows, self.cols), (self.x_stride, 1), dtype=x.dtype, device=x.device)
+    def _check_param(self, name, t):
+        if t is not None:
+            _check_flat(name, t, (self.cols,), self._param)
 
     @_on_stream
     def __call__(self, x, gamma=None, beta=None, y=None, stats=False):
         """y, or (y, mean, rstd) with `stats` (what `backward` needs)."""
-        self._check_x("x", x)
-        self._check_params(("gamma", gamma), ("beta", beta))
+        self._check_x(x)
+        self._check_param("gamma", gamma)
+        self._check_param("beta", beta)
         if y is None:
-            y = torch.empty_strided((self.rows, self.cols), (self.y_stride, 1), dtype=x.dtype, device=x.device)
+            y = self._y.new(x.device)
         else:
-            _check_rows("y", y, self.rows, self.cols, self.y_stride, self.dtype)
+            self._y.check("y", y)
         mean = rstd = None
         if stats:
-            mean, rstd = torch.empty((2, self.rows), dtype=torch.float32, device=x.device).unbind(0)
-        head_capi.layernorm_fwd(self.desc, _ptr(x), _ptr(gamma), _ptr(beta), _ptr(y), _ptr(mean), _ptr(rstd),
-                                _stream(x.device))
+            mean = torch.empty(self.rows, dtype=torch.float32, device=x.device)
+            rstd = torch.empty(self.rows, dtype=torch.float32, device=x.device)
+        head_capi.layernorm_fwd(self.desc, x.data_ptr(), _ptr(gamma), _ptr(beta), y.data_ptr(), _ptr(mean), _ptr(rstd),
+                                _stream(x))
         return (y, mean, rstd) if stats else y
 
     @_on_stream
     def backward(self, dy, x, gamma, mean, rstd, need_dx=True, need_params=True, workspace=None):
         """(dx, dgamma, dbeta); None in the place of what is not needed."""
-        self._check_x("x", x)
-        _check_rows("dy", dy, self.rows, self.cols, self.y_stride, self.dtype)
-        self._check_params(("gamma", gamma))
+        self._check_x(x)
+        self._y.check("dy", dy)
+        self._check_param("gamma", gamma)
         _check_flat("mean", mean, (self.rows,), torch.float32)
         _check_flat("rstd", rstd, (self.rows,), torch.float32)
-        dx = self._like_x(x) if need_dx else None
-        dgamma = dbeta = None
+        dev = x.device
+        dx = dgamma = dbeta = None
+        if need_dx:
+            dx = torch.empty_like(x) if self.pixels else self._x.new(dev)
         if need_params:
-            dgamma, dbeta = torch.empty((2, self.cols), dtype=_TORCH_DTYPE[self.param_dtype],
-                                        device=x.device).unbind(0)
+            dgamma = torch.empty(self.cols, dtype=self._param, device=dev)
+            dbeta = torch.empty(self.cols, dtype=self._param, device=dev)
         if workspace is None:
-            workspace = torch.empty(max(self.workspace_bytes, 1), dtype=torch.uint8, device=x.device)
-        head_capi.layernorm_bwd(self.desc, _ptr(dy), _ptr(x), _ptr(gamma), _ptr(mean), _ptr(rstd), _ptr(dx),
-                                _ptr(dgamma), _ptr(dbeta), _ptr(workspace), workspace.numel(),
-                                _stream(x.device))
+            workspace = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=dev)
+        head_capi.layernorm_bwd(self.desc, dy.data_ptr(), x.data_ptr(), _ptr(gamma), mean.data_ptr(), rstd.data_ptr(),
+                                _ptr(dx), _ptr(dgamma), _ptr(dbeta), workspace.data_ptr(), workspace.numel(),
+                                _stream(x))
         return dx, dgamma, dbeta
 
 
@@ -159,29 +166,31 @@ class Dropout(_Op):
         self.desc = head_capi.dropout_desc_create(rows, cols, dtype, p)
         if (self.x_stride, self.residual_stride, self.y_stride) != (cols, cols, cols):
             head_capi.dropout_desc_set_row_strides(self.desc, self.x_stride, self.residual_stride, self.y_stride)
+        self._x, self._y = _Rows(rows, cols, self.x_stride, dtype), _Rows(rows, cols, self.y_stride, dtype)
+        self._residual = _Rows(rows, cols, self.residual_stride, dtype)
 
     @_on_stream
     def __call__(self, x, seed, offset=0, residual=None, y=None):
         """residual + dropped x (y may be x or residual)."""
-        _check_rows("x", x, self.rows, self.cols, self.x_stride, self.dtype)
+        self._x.check("x", x)
         if residual is not None:
-            _check_rows("residual", residual, self.rows, self.cols, self.residual_stride, self.dtype)
+            self._residual.check("residual", residual)
         if y is None:
-            y = torch.empty_strided((self.rows, self.cols), (self.y_stride, 1), dtype=x.dtype, device=x.device)
+            y = self._y.new(x.device)
         else:
-            _check_rows("y", y, self.rows, self.cols, self.y_stride, self.dtype)
-        head_capi.dropout_fwd(self.desc, _ptr(x), _ptr(residual), _ptr(y), seed, offset, _stream(x.device))
+            self._y.check("y", y)
+        head_capi.dropout_fwd(self.desc, x.data_ptr(), _ptr(residual), y.data_ptr(), seed, offset, _stream(x))
         return y
 
     @_on_stream
     def backward(self, dy, seed, offset=0, dx=None):
         """dx under the mask of the forward call with the same seed and offset."""
-        _check_rows("dy", dy, self.rows, self.cols, self.y_stride, self.dtype)
+        self._y.check("dy", dy)
         if dx is None:
-            dx = torch.empty_strided((self.rows, self.cols), (self.x_stride, 1), dtype=dy.dtype, device=dy.device)
+            dx = self._x.new(dy.device)
         else:
-            _check_rows("dx", dx, self.rows, self.cols, self.x_stride, self.dtype)
-        head_capi.dropout_bwd(self.desc, _ptr(dy), _ptr(dx), seed, offset, _stream(dy.device))
+            self._x.check("dx", dx)
+        head_capi.dropout_bwd(self.desc, dy.data_ptr(), dx.data_ptr(), seed, offset, _stream(dy))
         return dx
 
 
@@ -204,26 +213,25 @@ class LinearCrossEntropy(_Op):
         if piece:
             head_capi.linear_ce_desc_set_piece(self.desc, piece)
         self.workspace_bytes, self.backward_workspace_bytes = head_capi.linear_ce_workspace_size(self.desc)
-
-    @property
-    def loss_shape(self):
-        return (self.tokens,) if self.reduction == "none" else ()
+        self.loss_shape = (tokens,) if reduction == "none" else ()
+        self._h, self._w = _Rows(tokens, hidden, self.h_stride, dtype), _Rows(vocab, hidden, self.w_stride, dtype)
 
     def _check(self, h, w, target):
-        _check_rows("h", h, self.tokens, self.hidden, self.h_stride, self.dtype)
-        _check_rows("w", w, self.vocab, self.hidden, self.w_stride, self.dtype)
+        self._h.check("h", h)
+        self._w.check("w", w)
         _check_flat("target", target, (self.tokens,), torch.int64)
 
     @_on_stream
     def __call__(self, h, w, target, workspace=None):
         """(loss, lse): lse (log-sum-exp per token) is what `backward` needs."""
         self._check(h, w, target)
-        loss = torch.empty(self.loss_shape, dtype=torch.float32, device=h.device)
-        lse = torch.empty((self.tokens,), dtype=torch.float32, device=h.device)
+        dev = h.device
+        loss = torch.empty(self.loss_shape, dtype=torch.float32, device=dev)
+        lse = torch.empty(self.tokens, dtype=torch.float32, device=dev)
         if workspace is None:
-            workspace = torch.empty(max(self.workspace_bytes, 1), dtype=torch.uint8, device=h.device)
-        head_capi.linear_ce_fwd(self.desc, _ptr(h), _ptr(w), _ptr(target), _ptr(loss), _ptr(lse), _ptr(workspace),
-                                workspace.numel(), _stream(h.device))
+            workspace = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=dev)
+        head_capi.linear_ce_fwd(self.desc, h.data_ptr(), w.data_ptr(), target.data_ptr(), loss.data_ptr(),
+                                lse.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream(h))
         return loss, lse
 
     @_on_stream
@@ -232,12 +240,14 @@ class LinearCrossEntropy(_Op):
         self._check(h, w, target)
         _check_flat("lse", lse, (self.tokens,), torch.float32)
         _check_flat("dloss", dloss, self.loss_shape, torch.float32)
-        dh = torch.empty((self.tokens, self.hidden), dtype=h.dtype, device=h.device) if need_dh else None
-        dw = torch.empty((self.vocab, self.hidden), dtype=w.dtype, device=w.device) if need_dw else None
+        dev = h.device
+        dh = torch.empty((self.tokens, self.hidden), dtype=h.dtype, device=dev) if need_dh else None
+        dw = torch.empty((self.vocab, self.hidden), dtype=w.dtype, device=dev) if need_dw else None
         if workspace is None:
-            workspace = torch.empty(max(self.backward_workspace_bytes, 1), dtype=torch.uint8, device=h.device)
-        head_capi.linear_ce_bwd(self.desc, _ptr(h), _ptr(w), _ptr(target), _ptr(lse), _ptr(dloss), _ptr(dh), _ptr(dw),
-                                _ptr(workspace), workspace.numel(), _stream(h.device))
+            workspace = torch.empty(self.backward_workspace_bytes, dtype=torch.uint8, device=dev)
+        head_capi.linear_ce_bwd(self.desc, h.data_ptr(), w.data_ptr(), target.data_ptr(), lse.data_ptr(),
+                                dloss.data_ptr(), _ptr(dh), _ptr(dw), workspace.data_ptr(), workspace.numel(),
+                                _stream(h))
         return dh, dw
 
 

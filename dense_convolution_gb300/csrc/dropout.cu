@@ -20,7 +20,7 @@ namespace {
 
 struct DropParams {
     int64_t rows, cols, xs, rs, ys;
-    int64_t blocks, whole;       // blocks of eight elements of the whole tensor, and those moved as vectors
+    int64_t blocks;              // blocks of eight elements of the whole tensor
     uint32_t k0, k1, off0, off1;
     uint32_t threshold;          // dropped below it
     int all;                     // threshold 2^32: nothing is kept
@@ -45,6 +45,11 @@ __device__ __forceinline__ void philox(uint32_t (&c)[4], uint32_t k0, uint32_t k
 // one Philox call; what stands below a high half is meaningless unless it ties
 // with the threshold's, and then the second call fills the low halves in.
 __device__ __forceinline__ void numbers(const DropParams& p, int64_t b, uint32_t (&n)[8]) {
+    if (p.all) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) n[i] = 0u;         // below the threshold, 2^32 - 1 here
+        return;
+    }
     uint32_t c[4] = {(uint32_t)b, (uint32_t)((uint64_t)b >> 32), p.off0, p.off1};
     philox(c, p.k0, p.k1);
     const uint32_t base = p.threshold & 0xffff0000u;
@@ -63,92 +68,75 @@ __device__ __forceinline__ void numbers(const DropParams& p, int64_t b, uint32_t
     }
 }
 
-// VECTOR: blocks of eight are adjacent and 16-byte aligned in every tensor
-// (rows a multiple of eight long, or one row, whose last block may be short).
-// Otherwise each element finds its own row and column.
-// A thread takes two blocks a grid's length apart, so that both blocks' loads
-// are under way during the generator's arithmetic.
-template <typename T, bool VECTOR, bool RESIDUAL>
-__global__ void __launch_bounds__(256, 4) dropout_kernel(const DropParams p) {
+// How a call's blocks of eight lie: FLAT, adjacent in every tensor; ROWS,
+// inside rows a multiple of eight long; both 16-byte aligned.  SINGLE: each
+// element finds its own row and column.
+enum Lie { FLAT = 0, ROWS = 1, SINGLE = 2 };
+
+// One block a thread; six blocks of threads an SM (40 registers) cover the
+// loads of some with the generator's arithmetic of others.
+template <typename T, int LIE, bool RESIDUAL>
+__global__ void __launch_bounds__(256, 6) dropout_kernel(const DropParams p) {
     constexpr int V = 16 / (int)sizeof(T), L = 8 / V;  // a block is one load of 16-bit values, two of fp32
     pdl_wait();
     const T* x = static_cast<const T*>(p.x);
     const T* r = static_cast<const T*>(p.r);
     T* y = static_cast<T*>(p.y);
-    const int64_t step = (int64_t)gridDim.x * blockDim.x;
-    int64_t b = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if constexpr (VECTOR) {
-        for (; b < p.whole; b += 2 * step) {
-            Vec<T, V> vx[2][L], vr[2][L];
-            int64_t yo[2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int64_t e0 = (b + u * step) * 8;
-                int64_t xo = e0, ro = e0;
-                yo[u] = e0;
-                if (p.rows > 1) {
-                    const int64_t row = e0 / p.cols, col = e0 - row * p.cols;
-                    xo = row * p.xs + col;
-                    ro = row * p.rs + col;
-                    yo[u] = row * p.ys + col;
-                }
-                if (b + u * step < p.whole) {
-#pragma unroll
-                    for (int l = 0; l < L; ++l) {
-                        vx[u][l] = *reinterpret_cast<const Vec<T, V>*>(x + xo + l * V);
-                        if (RESIDUAL) vr[u][l] = *reinterpret_cast<const Vec<T, V>*>(r + ro + l * V);
-                    }
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                if (b + u * step < p.whole) {
-                    uint32_t n[8];
-                    numbers(p, b + u * step, n);
-#pragma unroll
-                    for (int l = 0; l < L; ++l) {
-                        float f[V], g[V];
-                        widen(vx[u][l], f);
-                        if (RESIDUAL) widen(vr[u][l], g);
-#pragma unroll
-                        for (int i = 0; i < V; ++i) {
-                            f[i] = n[l * V + i] >= p.threshold && !p.all ? f[i] * p.scale : 0.f;
-                            if (RESIDUAL) f[i] += g[i];
-                        }
-                        *reinterpret_cast<Vec<T, V>*>(y + yo[u] + l * V) = narrow<T, V>(f);
-                    }
-                }
-            }
-        }
-        // The short last block, if any.
-        b = p.whole + (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    }
+    const int64_t b = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (b >= p.blocks) return;
     const int64_t total = p.rows * p.cols;
-    for (; b < p.blocks; b += step) {
+    int64_t e0 = b * 8, row = 0, col = e0;
+    if constexpr (LIE != FLAT) {
+        row = e0 / p.cols;
+        col = e0 - row * p.cols;
+    }
+    if (LIE != SINGLE && e0 + 8 <= total) {
+        Vec<T, V> vx[L], vr[L];
+#pragma unroll
+        for (int l = 0; l < L; ++l) {
+            vx[l] = *reinterpret_cast<const Vec<T, V>*>(x + row * p.xs + col + l * V);
+            if (RESIDUAL) vr[l] = *reinterpret_cast<const Vec<T, V>*>(r + row * p.rs + col + l * V);
+        }
         uint32_t n[8];
         numbers(p, b, n);
-        const int64_t e0 = b * 8, row0 = e0 / p.cols, col0 = e0 - row0 * p.cols;
+#pragma unroll
+        for (int l = 0; l < L; ++l) {
+            float f[V], g[V];
+            widen(vx[l], f);
+            if (RESIDUAL) widen(vr[l], g);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                f[i] = n[l * V + i] >= p.threshold ? f[i] * p.scale : 0.f;
+                if (RESIDUAL) f[i] += g[i];
+            }
+            *reinterpret_cast<Vec<T, V>*>(y + row * p.ys + col + l * V) = narrow<T, V>(f);
+        }
+    } else {
+        uint32_t n[8];
+        numbers(p, b, n);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             if (e0 + i < total) {
-                int64_t row = row0, col = col0 + i;
-                while (col >= p.cols) { col -= p.cols; ++row; }
-                float f = n[i] >= p.threshold && !p.all ? to_f32(x[row * p.xs + col]) * p.scale : 0.f;
+                float f = n[i] >= p.threshold ? to_f32(x[row * p.xs + col]) * p.scale : 0.f;
                 if (RESIDUAL) f += to_f32(r[row * p.rs + col]);
                 y[row * p.ys + col] = from_f32<T>(f);
+                if (LIE == FLAT) {
+                    ++col;
+                } else if (++col == p.cols) {
+                    col = 0;
+                    ++row;
+                }
             }
         }
     }
 }
 
-template <typename T> cudaError_t run(DropParams p, bool vector, cudaStream_t st) {
-    p.whole = vector ? p.rows * p.cols / 8 : 0;
-    // Two blocks of eight a thread; sixteen turns at most keep the tail short.
-    const int64_t most = (int64_t)device_sm_count() * 4 * 16;
-    int64_t grid = (p.blocks + 511) / 512;
-    if (grid > most) grid = most;
-    auto kern = vector ? (p.r ? dropout_kernel<T, true, true> : dropout_kernel<T, true, false>)
-                       : (p.r ? dropout_kernel<T, false, true> : dropout_kernel<T, false, false>);
+template <typename T> cudaError_t run(const DropParams& p, int lie, cudaStream_t st) {
+    const int64_t grid = (p.blocks + 255) / 256;
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;      // 2^42 elements
+#define DROP(LIE) (p.r ? dropout_kernel<T, LIE, true> : dropout_kernel<T, LIE, false>)
+    auto kern = lie == FLAT ? DROP(FLAT) : lie == ROWS ? DROP(ROWS) : DROP(SINGLE);
+#undef DROP
     return launch_after(kern, dim3((unsigned)grid), dim3(256), 0, st, p);
 }
 
@@ -168,17 +156,17 @@ cudaError_t launch_dropout(const dropout_desc& d, const void* x, int64_t xs, con
     p.off0 = (uint32_t)offset; p.off1 = (uint32_t)(offset >> 32);
     const uint64_t threshold = (uint64_t)nearbyint(d.p * 4294967296.0);
     p.all = threshold >> 32 != 0;
-    p.threshold = (uint32_t)threshold;
+    p.threshold = p.all ? 0xffffffffu : (uint32_t)threshold;
     p.scale = d.p < 1.0 ? (float)(1.0 / (1.0 - d.p)) : 0.f;
     p.x = x; p.r = residual; p.y = y;
     const int64_t e = (int64_t)elem_bytes(d.dtype);
-    const bool vector = aligned_to(x, 16) && aligned_to(y, 16) && aligned_to(residual, 16) &&
-                        (flat || (d.cols % 8 == 0 && xs * e % 16 == 0 && ys * e % 16 == 0 &&
-                                  (!residual || rs * e % 16 == 0)));
+    const bool aligned = aligned_to(x, 16) && aligned_to(y, 16) && aligned_to(residual, 16);
+    const bool rows = d.cols % 8 == 0 && xs * e % 16 == 0 && ys * e % 16 == 0 && (!residual || rs * e % 16 == 0);
+    const int lie = !aligned ? SINGLE : flat ? FLAT : rows ? ROWS : SINGLE;
     switch (d.dtype) {
-        case CONV2D_F32: return run<float>(p, vector, st);
-        case CONV2D_F16: return run<__half>(p, vector, st);
-        default: return run<__nv_bfloat16>(p, vector, st);
+        case CONV2D_F32: return run<float>(p, lie, st);
+        case CONV2D_F16: return run<__half>(p, lie, st);
+        default: return run<__nv_bfloat16>(p, lie, st);
     }
 }
 

@@ -378,6 +378,157 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) layernorm_bwd_kernel(
     }
 }
 
+// The same for whole 16-byte aligned rows of at least kBulkBytes, which bulk
+// copies bring into a ring in shared memory: the reach of the loads no longer
+// depends on registers, and x and dy are read from shared memory twice (sums,
+// then dx) instead of being kept.  So a thread can take sixteen elements,
+// which halves its share of the row's fixed work (exchanges, barrier, waits):
+// with eight, 46 instructions an element bound the kernel, not the memory.
+constexpr int kBulkBytes = 1024, kBulkThreads = 512, kBulkElems = 16, kRingBytes = 192 * 1024, kRingMost = 8;
+
+template <typename T>
+__global__ void __launch_bounds__(kBulkThreads, 1) layernorm_bwd_bulk_kernel(const LnParams p, const int ring_rows) {
+    constexpr int V = vec_of<T, WHOLE>(), NV = kBulkElems / V;
+    __shared__ float red[2][2][16];
+    __shared__ uint64_t bars[8][kRingMost];                    // a group is at least two warps
+    __shared__ int abort_word;
+    extern __shared__ __align__(128) uint8_t ring_s[];  // [group][ring_rows][x row, dy row]; then sums [2][cols]
+    volatile int* abort_flag = &abort_word;
+    const int tpr = p.tpr, rpb = blockDim.x / tpr, sub = threadIdx.x / tpr, t = threadIdx.x - sub * tpr;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int group = blockIdx.x * rpb + sub;
+    const uint32_t row_bytes = (uint32_t)p.cols * sizeof(T);
+    if (t == 0)
+        for (int i = 0; i < ring_rows; ++i) mbar_init(smem_addr(&bars[sub][i]), 1);
+    if (threadIdx.x == 0) abort_word = 0;
+    mbar_fence_init();
+    __syncthreads();
+    pdl_wait();
+    const T* x0 = static_cast<const T*>(p.x);
+    const T* d0 = static_cast<const T*>(p.dy);
+    uint8_t* ring = ring_s + (size_t)sub * ring_rows * 2 * row_bytes;
+    const int slots = p.cols / V;
+
+    float g[NV][V], dg[NV][V], db[NV][V];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int s = j * tpr + t;
+        const bool in = s < slots;
+        load_params<T, V>(p.gamma, p.param_f32, s * V, 0, in ? V : 0, p.vec_params && in, 1.f, g[j]);
+#pragma unroll
+        for (int i = 0; i < V; ++i) dg[j][i] = db[j][i] = 0.f;
+    }
+    const int turns = group < p.rows ? (int)((p.rows - group + p.groups - 1) / p.groups) : 0;
+    auto issue = [&](int it, int slot) {                   // row `it` of this group
+        const int64_t row = group + (int64_t)it * p.groups;
+        const uint32_t bar = smem_addr(&bars[sub][slot]);
+        const uint32_t dst = smem_addr(ring + (size_t)slot * 2 * row_bytes);
+        mbar_arrive_expect_tx(bar, 2 * row_bytes);
+        bulk_load(dst, x0 + row * p.xs, row_bytes, bar);
+        bulk_load(dst + row_bytes, d0 + row * p.ys, row_bytes, bar);
+    };
+    int issued = 0;                                        // (of thread 0 of the group)
+    if (t == 0)
+        for (; issued < ring_rows - 1 && issued < turns; ++issued) issue(issued, issued);
+    const int wpr = tpr >> 5;                              // 2 to 16
+    int slot = 0;
+    uint32_t phase = 0;
+    int64_t row = group;
+    float mu = 0.f, r = 0.f;
+    if (turns > 0) { mu = p.mean_in[row]; r = p.rstd_in[row]; }
+    bool ok = true;
+    for (int it = 0; it < turns; ++it, row += p.groups) {
+        float nmu = 0.f, nr = 0.f;
+        if (it + 1 < turns) { nmu = p.mean_in[row + p.groups]; nr = p.rstd_in[row + p.groups]; }
+        const T* xs = reinterpret_cast<const T*>(ring + (size_t)slot * 2 * row_bytes);
+        const T* ds = xs + p.cols;
+        const bool landed = mbar_wait(smem_addr(&bars[sub][slot]), phase, abort_flag);
+        float s1 = 0.f, s2 = 0.f;
+        if (landed) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int s = j * tpr + t;
+                if (s < slots) {
+                    float fx[V], fd[V];
+                    widen(*reinterpret_cast<const Vec<T, V>*>(xs + s * V), fx);
+                    widen(*reinterpret_cast<const Vec<T, V>*>(ds + s * V), fd);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        const float z = (fx[i] - mu) * r, a = fd[i] * g[j][i];
+                        s1 += a;
+                        s2 += a * z;
+                        dg[j][i] += fd[i] * z;
+                        db[j][i] += fd[i];
+                    }
+                }
+            }
+        }
+        // Both sums in five exchanges: lanes below 16 go on with s1, the others with s2.
+        const bool up = lane & 16;
+        float v = (up ? s2 : s1) + __shfl_xor_sync(0xffffffffu, up ? s1 : s2, 16);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        float(*buf)[16] = red[it & 1];
+        if ((lane & 15) == 0) buf[lane >> 4][warp] = v;
+        // The group meets once a row: the sums are there, a wait that ran out
+        // stops all of the group, and the previous row's slot is free.
+        ok = named_bar_and(1 + sub, tpr, landed);
+        if (!ok) break;
+        if (t == 0 && issued < turns) {
+            issue(issued, slot == 0 ? ring_rows - 1 : slot - 1);
+            ++issued;
+        }
+        if (++slot == ring_rows) { slot = 0; phase ^= 1; }
+        const float cmu = mu, cr = r;
+        mu = nmu;
+        r = nr;
+        if (!p.dx) continue;
+        v = (lane & 15) < wpr ? buf[lane >> 4][sub * wpr + (lane & 15)] : 0.f;
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        v *= p.inv_cols * cr;
+        const float rs1 = __shfl_sync(0xffffffffu, v, 0), rs2 = __shfl_sync(0xffffffffu, v, 16) * cr;
+        T* dx = static_cast<T*>(p.dx) + row * p.xs;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int s = j * tpr + t;
+            if (s < slots) {
+                float fx[V], f[V];
+                widen(*reinterpret_cast<const Vec<T, V>*>(xs + s * V), fx);
+                widen(*reinterpret_cast<const Vec<T, V>*>(ds + s * V), f);
+#pragma unroll
+                for (int i = 0; i < V; ++i) f[i] = fmaf(f[i] * g[j][i], cr, -fmaf(fx[i] - cmu, rs2, rs1));
+                *reinterpret_cast<Vec<T, V>*>(dx + s * V) = narrow<T, V>(f);
+            }
+        }
+    }
+    // Copies still in flight after a wait that ran out land before the block leaves.
+    if (t == 0 && !ok)
+        for (int i = issued > ring_rows ? issued - ring_rows : 0; i < issued; ++i)
+            mbar_drain_wait(smem_addr(&bars[sub][i % ring_rows]), (uint32_t)(i / ring_rows) & 1u);
+    if (!p.want_params) return;
+    float* acc_s = reinterpret_cast<float*>(ring_s);       // the ring is done with
+    float* out = p.part + (int64_t)blockIdx.x * 2 * p.cols;
+    for (int k = 0; k < rpb; ++k) {
+        __syncthreads();
+        if (sub == k) {
+            float* dst = k + 1 < rpb ? acc_s : out;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int s = j * tpr + t;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const int c = s * V + i;
+                    if (s < slots) {
+                        dst[c] = dg[j][i] + (k ? acc_s[c] : 0.f);
+                        dst[p.cols + c] = db[j][i] + (k ? acc_s[p.cols + c] : 0.f);
+                    }
+                }
+            }
+        }
+    }
+}
+
 // Long rows, pass 1: sum a and sum a z of one row's share of columns.
 template <typename T, int CUT>
 __global__ void __launch_bounds__(256) layernorm_bwd_sums_kernel(const LnParams p, float2* sums) {
@@ -614,6 +765,25 @@ template <typename T> cudaError_t bwd_typed(const layernorm_desc& d, LnParams p,
                                        : V - 1;
     const int64_t slots = ceil_div((int64_t)p.cols + most_shift, V);
     const int sms = device_sm_count();
+    const int64_t row_bytes = (int64_t)p.cols * sizeof(T);
+    if (slots * V <= kBwdCols && cut == WHOLE && row_bytes >= kBulkBytes) {
+        // Bulk copies from two rows a group on (one hides nothing).
+        const int tpr = threads_for(slots, kBulkElems / V) < 64 ? 64 : threads_for(slots, kBulkElems / V);
+        const int rpb = kBulkThreads / tpr;
+        if (p.rows >= 2 * (int64_t)sms * rpb) {
+            p.tpr = tpr;
+            p.groups = sms * rpb;
+            *parts = sms;
+            int rows = (int)(kRingBytes / (rpb * 2 * row_bytes));
+            rows = rows > kRingMost ? kRingMost : rows;
+            const size_t ring = (size_t)rpb * rows * 2 * row_bytes, sums = 2 * (size_t)p.cols * sizeof(float);
+            const size_t smem = ring > sums ? ring : sums;
+            const cudaError_t e = cudaFuncSetAttribute(layernorm_bwd_bulk_kernel<T>,
+                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (e != cudaSuccess) return e;
+            return launch_after(layernorm_bwd_bulk_kernel<T>, dim3((unsigned)sms), dim3(rpb * tpr), smem, st, p, rows);
+        }
+    }
     if (slots * V <= kBwdCols) {
         // As many threads a row as keep one vector each, or eight elements.
         int nv = 1;
@@ -701,6 +871,9 @@ size_t layernorm_bwd_workspace(const layernorm_desc& d) {
     const size_t parts = d.cols <= kBwdCols ? (size_t)bwd_grid(1) + 8 : 64;
     return bwd_sums_bytes(d) + parts * 2 * (size_t)d.cols * sizeof(float);
 }
+
+cudaError_t status_read_clear_ln(cudaStream_t st, uint32_t* out) { return status_read_clear(st, out); }
+cudaError_t wait_limit_set_ln(cudaStream_t st, uint64_t ns) { return wait_limit_set(st, ns); }
 
 cudaError_t launch_layernorm_params(const float* part, int parts, const layernorm_desc& d, void* dgamma, void* dbeta,
                                     cudaStream_t st) {

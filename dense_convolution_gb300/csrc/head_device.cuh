@@ -97,6 +97,86 @@ __device__ __forceinline__ void store_param(void* p, bool f32, bool bf16, int64_
     else static_cast<__half*>(p)[i] = __float2half_rn(v);
 }
 
+// Two fp32 values in a 64-bit register pair: one instruction does both (the
+// packed fp32 arithmetic of sm_100 and later; each half rounds as usual).
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pack2f(float a, float b) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 both(float a) { return pack2f(a, a); }
+__device__ __forceinline__ void unpack2f(f32x2 v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ float sum_halves(f32x2 v) {
+    float a, b;
+    unpack2f(v, a, b);
+    return a + b;
+}
+
+// A packed pair of 16-bit values to and from a pair of fp32 ones.
+template <typename T> __device__ __forceinline__ f32x2 widen_pair(uint32_t w);
+template <> __device__ __forceinline__ f32x2 widen_pair<__nv_bfloat16>(uint32_t w) {
+    return pack2f(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <> __device__ __forceinline__ f32x2 widen_pair<__half>(uint32_t w) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    return pack2f(f.x, f.y);
+}
+template <typename T> __device__ __forceinline__ uint32_t narrow_pair(f32x2 v);
+template <> __device__ __forceinline__ uint32_t narrow_pair<__nv_bfloat16>(f32x2 v) {
+    float a, b;
+    unpack2f(v, a, b);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <> __device__ __forceinline__ uint32_t narrow_pair<__half>(f32x2 v) {
+    float a, b;
+    unpack2f(v, a, b);
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// A 16-byte vector as pairs of fp32 values, and back.
+template <typename T> struct Pairs {
+    static constexpr int N = 4;
+    static __device__ __forceinline__ void widen(const uint4& w, f32x2 (&f)[4]) {
+        f[0] = widen_pair<T>(w.x); f[1] = widen_pair<T>(w.y); f[2] = widen_pair<T>(w.z); f[3] = widen_pair<T>(w.w);
+    }
+    static __device__ __forceinline__ uint4 narrow(const f32x2 (&f)[4]) {
+        return make_uint4(narrow_pair<T>(f[0]), narrow_pair<T>(f[1]), narrow_pair<T>(f[2]), narrow_pair<T>(f[3]));
+    }
+};
+template <> struct Pairs<float> {
+    static constexpr int N = 2;
+    static __device__ __forceinline__ void widen(const uint4& w, f32x2 (&f)[2]) {
+        f[0] = pack2f(__uint_as_float(w.x), __uint_as_float(w.y));
+        f[1] = pack2f(__uint_as_float(w.z), __uint_as_float(w.w));
+    }
+    static __device__ __forceinline__ uint4 narrow(const f32x2 (&f)[2]) {
+        float a, b, c, d;
+        unpack2f(f[0], a, b);
+        unpack2f(f[1], c, d);
+        return make_uint4(__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d));
+    }
+};
+
 // Sum over aligned groups of `width` lanes (a power of two), in every lane.
 __device__ __forceinline__ float lane_sum(float v, int width) {
     for (int o = width >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);

@@ -135,6 +135,8 @@ cudaError_t status_read_clear_ce(cudaStream_t st, uint32_t* out);   // linear_ce
 cudaError_t wait_limit_set_ce(cudaStream_t st, uint64_t ns);
 cudaError_t status_read_clear_ln(cudaStream_t st, uint32_t* out);   // layernorm.cu
 cudaError_t wait_limit_set_ln(cudaStream_t st, uint64_t ns);
+cudaError_t status_read_clear_lp(cudaStream_t st, uint32_t* out);   // layernorm_planes.cu
+cudaError_t wait_limit_set_lp(cudaStream_t st, uint64_t ns);
 cudaError_t wait_limit_set_tc(cudaStream_t st, uint64_t ns);
 cudaError_t wait_limit_set_fp32(cudaStream_t st, uint64_t ns);
 

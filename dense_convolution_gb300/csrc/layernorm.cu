@@ -37,6 +37,7 @@ struct LnParams {
     int per_block;       // vector slots of a row per block of the cluster
     int groups;          // backward: row groups of the grid (rows in flight)
     int param_f32;
+    int cut_alike;       // backward: every row starts at the same place after a 16-byte boundary
     int vec_params;      // gamma and beta rows are 16-byte aligned like the data's vectors
     float eps, inv_cols;
     const void *x, *dy, *gamma, *beta;
@@ -93,9 +94,68 @@ __device__ __forceinline__ float row_sum(float v, int tpr, float* red) {
     return lane_sum(lane < wpr ? red[first + lane] : 0.f, 32);
 }
 
+// H pairs or single values of a vector slot, as the arithmetic takes them.
+template <typename T, int V> struct Values {
+    static constexpr int H = V / 2;
+    f32x2 v[H];
+    __device__ __forceinline__ void widen(const Vec<T, V>& a) {
+        Pairs<T>::widen(*reinterpret_cast<const uint4*>(&a), v);
+    }
+    __device__ __forceinline__ void set(const float (&f)[V]) {
+#pragma unroll
+        for (int i = 0; i < H; ++i) v[i] = pack2f(f[2 * i], f[2 * i + 1]);
+    }
+    __device__ __forceinline__ void keep(int lo, int hi) {         // zero outside [lo, hi)
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            float a, b;
+            unpack2f(v[i], a, b);
+            v[i] = pack2f(2 * i >= lo && 2 * i < hi ? a : 0.f, 2 * i + 1 >= lo && 2 * i + 1 < hi ? b : 0.f);
+        }
+    }
+    __device__ __forceinline__ void minus(float m) {
+#pragma unroll
+        for (int i = 0; i < H; ++i) v[i] = add2(v[i], both(-m));
+    }
+    __device__ __forceinline__ float sum() const {
+        f32x2 s = v[0];
+#pragma unroll
+        for (int i = 1; i < H; ++i) s = add2(s, v[i]);
+        return sum_halves(s);
+    }
+    __device__ __forceinline__ float squares() const {
+        f32x2 s = mul2(v[0], v[0]);
+#pragma unroll
+        for (int i = 1; i < H; ++i) s = fma2(v[i], v[i], s);
+        return sum_halves(s);
+    }
+    __device__ __forceinline__ Vec<T, V> affine(float r, const Values& g, const Values& b) const {
+        f32x2 o[H];
+#pragma unroll
+        for (int i = 0; i < H; ++i) o[i] = fma2(mul2(v[i], both(r)), g.v[i], b.v[i]);
+        const uint4 w = Pairs<T>::narrow(o);
+        return *reinterpret_cast<const Vec<T, V>*>(&w);
+    }
+};
+template <typename T> struct Values<T, 1> {
+    float v;
+    __device__ __forceinline__ void widen(const Vec<T, 1>& a) { v = to_f32(a.v[0]); }
+    __device__ __forceinline__ void set(const float (&f)[1]) { v = f[0]; }
+    __device__ __forceinline__ void keep(int, int) {}
+    __device__ __forceinline__ void minus(float m) { v -= m; }
+    __device__ __forceinline__ float sum() const { return v; }
+    __device__ __forceinline__ float squares() const { return v * v; }
+    __device__ __forceinline__ Vec<T, 1> affine(float r, const Values& g, const Values& b) const {
+        Vec<T, 1> o;
+        o.v[0] = from_f32<T>(fmaf(v * r, g.v, b.v));
+        return o;
+    }
+};
+
 template <typename T, int CUT, int NV>
 __global__ void __launch_bounds__(1024) layernorm_fwd_kernel(const LnParams p) {
     constexpr int V = vec_of<T, CUT>();
+    constexpr bool EARLY = NV == 1;                    // one vector a thread: gamma and beta ride with x's latency
     __shared__ float red[2][32];
     __shared__ float cl[2];
     pdl_wait();
@@ -107,19 +167,28 @@ __global__ void __launch_bounds__(1024) layernorm_fwd_kernel(const LnParams p) {
     T* y = static_cast<T*>(p.y) + (live ? row : 0) * p.ys;
     const int shift = CUT != ENDS ? 0 : (int)((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
     const int slots = live ? (p.cols + shift + V - 1) / V : 0;
-    const int s0 = rank * p.per_block, s1 = min(slots, s0 + p.per_block);
+    const int s0 = rank * p.per_block + t, s1 = min(slots, rank * p.per_block + p.per_block);
     const bool vec = p.vec_params && shift == 0;
 
     Vec<T, V> raw[NV];
+    load_row<T, CUT, V, NV>(x, p.cols, shift, s0, p.tpr, s1, raw);
+    Values<T, V> g, b;
+    auto params = [&](int e0) {
+        const int lo = slot_first<CUT>(e0), hi = slot_last<CUT, V>(e0, p.cols);
+        float f[V];
+        load_params<T, V>(p.gamma, p.param_f32, e0, lo, hi, vec, 1.f, f);
+        g.set(f);
+        load_params<T, V>(p.beta, p.param_f32, e0, lo, hi, vec, 0.f, f);
+        b.set(f);
+    };
+    if (EARLY && s0 < s1) params(s0 * V - shift);
     float sum = 0.f;
-    load_row<T, CUT, V, NV>(x, p.cols, shift, s0 + t, p.tpr, s1, raw);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        if (s0 + j * p.tpr + t < s1) {                 // elements outside the row are zero
-            float f[V];
-            widen(raw[j], f);
-#pragma unroll
-            for (int i = 0; i < V; ++i) sum += f[i];
+        if (s0 + j * p.tpr < s1) {                     // elements outside the row are zero
+            Values<T, V> f;
+            f.widen(raw[j]);
+            sum += f.sum();
         }
     }
     float mean = row_sum(sum, p.tpr, red[0]);
@@ -135,15 +204,13 @@ __global__ void __launch_bounds__(1024) layernorm_fwd_kernel(const LnParams p) {
     float sq = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        const int s = s0 + j * p.tpr + t, e0 = s * V - shift;
+        const int s = s0 + j * p.tpr, e0 = s * V - shift;
         if (s < s1) {
-            float f[V];
-            widen(raw[j], f);
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float c = f[i] - mean;
-                if (CUT != ENDS || (e0 + i >= 0 && e0 + i < p.cols)) sq += c * c;
-            }
+            Values<T, V> f;
+            f.widen(raw[j]);
+            f.minus(mean);
+            if (CUT == ENDS && !slot_whole<V>(e0, p.cols)) f.keep(slot_first<CUT>(e0), slot_last<CUT, V>(e0, p.cols));
+            sq += f.squares();
         }
     }
     sq = row_sum(sq, p.tpr, red[1]);
@@ -155,23 +222,20 @@ __global__ void __launch_bounds__(1024) layernorm_fwd_kernel(const LnParams p) {
         sq = lane_sum(lane < p.cs ? *cl_g.map_shared_rank(&cl[1], lane) : 0.f, 32);
         cl_g.sync();                                   // no block leaves while another reads its sums
     }
-    const float rstd = 1.0f / sqrtf(sq * p.inv_cols + p.eps);
+    const float rstd = rsqrtf(sq * p.inv_cols + p.eps);
     if (live && t == 0 && rank == 0) {
         if (p.mean) p.mean[row] = mean;
         if (p.rstd) p.rstd[row] = rstd;
     }
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        const int s = s0 + j * p.tpr + t, e0 = s * V - shift;
+        const int s = s0 + j * p.tpr, e0 = s * V - shift;
         if (s < s1) {
-            const int lo = slot_first<CUT>(e0), hi = slot_last<CUT, V>(e0, p.cols);
-            float f[V], g[V], b[V];
-            widen(raw[j], f);
-            load_params<T, V>(p.gamma, p.param_f32, e0, lo, hi, vec, 1.f, g);
-            load_params<T, V>(p.beta, p.param_f32, e0, lo, hi, vec, 0.f, b);
-#pragma unroll
-            for (int i = 0; i < V; ++i) f[i] = (f[i] - mean) * rstd * g[i] + b[i];
-            store_part<T, V>(y + e0, narrow<T, V>(f), lo, hi);
+            if (!EARLY) params(e0);
+            Values<T, V> f;
+            f.widen(raw[j]);
+            f.minus(mean);
+            store_part<T, V>(y + e0, f.affine(rstd, g, b), slot_first<CUT>(e0), slot_last<CUT, V>(e0, p.cols));
         }
     }
 }
@@ -226,7 +290,7 @@ __global__ void __launch_bounds__(1024) layernorm_fwd_long_kernel(const LnParams
     cl_g.sync();
     sq = lane_sum(lane < p.cs ? *cl_g.map_shared_rank(&cl[1], lane) : 0.f, 32);
     cl_g.sync();
-    const float rstd = 1.0f / sqrtf(sq * p.inv_cols + p.eps);
+    const float rstd = rsqrtf(sq * p.inv_cols + p.eps);
     if (threadIdx.x == 0 && rank == 0) {
         if (p.mean) p.mean[row] = mean;
         if (p.rstd) p.rstd[row] = rstd;
@@ -256,6 +320,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) layernorm_bwd_kernel(
     __shared__ float2 red[2][32];
     extern __shared__ float acc_s[];                   // [2][cols] when several groups share the block
     pdl_wait();
+    pdl_launch_dependents();                           // one wave: the reduction's blocks wait beside it
     const int tpr = p.tpr, rpb = blockDim.x / tpr, sub = threadIdx.x / tpr, t = threadIdx.x - sub * tpr;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int group = blockIdx.x * rpb + sub;
@@ -358,10 +423,24 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) layernorm_bwd_kernel(
     }
     if (!p.want_params) return;
     float* out = p.part + (int64_t)blockIdx.x * 2 * p.cols;
-    for (int k = 0; k < rpb; ++k) {
+    // Groups that share a warp and its cut are added there first.
+    int steps = rpb, mine = sub;
+    if (tpr < 32 && p.cut_alike) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                for (int o = tpr; o < 32; o <<= 1) {
+                    dg[j][i] += __shfl_xor_sync(0xffffffffu, dg[j][i], o);
+                    db[j][i] += __shfl_xor_sync(0xffffffffu, db[j][i], o);
+                }
+        steps = blockDim.x >> 5;
+        mine = lane < tpr ? warp : -1;
+    }
+    for (int k = 0; k < steps; ++k) {
         if (k > 0) __syncthreads();
-        if (sub == k) {
-            float* dst = k + 1 < rpb ? acc_s : out;
+        if (mine == k) {
+            float* dst = k + 1 < steps ? acc_s : out;
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 const int s = j * tpr + t, e0 = s * V - shift;
@@ -381,18 +460,23 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) layernorm_bwd_kernel(
 // The same for whole 16-byte aligned rows of at least kBulkBytes, which bulk
 // copies bring into a ring in shared memory: the reach of the loads no longer
 // depends on registers, and x and dy are read from shared memory twice (sums,
-// then dx) instead of being kept.  So a thread can take sixteen elements,
-// which halves its share of the row's fixed work (exchanges, barrier, waits):
-// with eight, 46 instructions an element bound the kernel, not the memory.
+// then dx) instead of being kept.  What bounds this kernel is instructions (46
+// an element with eight elements a thread and one row a turn), so a thread
+// takes sixteen elements, a turn ROWS rows whose four sums share their
+// exchanges and barrier, and the arithmetic is packed two by two.
 constexpr int kBulkBytes = 1024, kBulkThreads = 512, kBulkElems = 16, kRingBytes = 192 * 1024, kRingMost = 8;
 
-template <typename T>
+// The lane group that value k of 2 ROWS ends up in when every exchange keeps
+// the lower half of the values in the lower lanes: bit by bit, k itself.
+template <int ROWS> __device__ __forceinline__ constexpr int sum_lane(int k) { return k * (32 / (2 * ROWS)); }
+
+template <typename T, int ROWS>
 __global__ void __launch_bounds__(kBulkThreads, 1) layernorm_bwd_bulk_kernel(const LnParams p, const int ring_rows) {
-    constexpr int V = vec_of<T, WHOLE>(), NV = kBulkElems / V;
-    __shared__ float red[2][2][16];
-    __shared__ uint64_t bars[8][kRingMost];                    // a group is at least two warps
+    constexpr int V = vec_of<T, WHOLE>(), NV = kBulkElems / V, H = Pairs<T>::N;
+    __shared__ float red[2][2 * ROWS][16];
+    __shared__ uint64_t bars[8][kRingMost];                // a group is at least two warps
     __shared__ int abort_word;
-    extern __shared__ __align__(128) uint8_t ring_s[];  // [group][ring_rows][x row, dy row]; then sums [2][cols]
+    extern __shared__ __align__(128) uint8_t ring_s[];     // [group][ring_rows][x row, dy row]; then sums [2][cols]
     volatile int* abort_flag = &abort_word;
     const int tpr = p.tpr, rpb = blockDim.x / tpr, sub = threadIdx.x / tpr, t = threadIdx.x - sub * tpr;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -404,108 +488,152 @@ __global__ void __launch_bounds__(kBulkThreads, 1) layernorm_bwd_bulk_kernel(con
     mbar_fence_init();
     __syncthreads();
     pdl_wait();
-    const T* x0 = static_cast<const T*>(p.x);
-    const T* d0 = static_cast<const T*>(p.dy);
+    pdl_launch_dependents();                               // one wave: the reduction's blocks wait beside it
     uint8_t* ring = ring_s + (size_t)sub * ring_rows * 2 * row_bytes;
     const int slots = p.cols / V;
 
-    float g[NV][V], dg[NV][V], db[NV][V];
+    f32x2 g[NV][H], dg[NV][H], db[NV][H];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int s = j * tpr + t;
         const bool in = s < slots;
-        load_params<T, V>(p.gamma, p.param_f32, s * V, 0, in ? V : 0, p.vec_params && in, 1.f, g[j]);
+        float f[V];
+        load_params<T, V>(p.gamma, p.param_f32, s * V, 0, in ? V : 0, p.vec_params && in, 1.f, f);
 #pragma unroll
-        for (int i = 0; i < V; ++i) dg[j][i] = db[j][i] = 0.f;
+        for (int i = 0; i < H; ++i) {
+            g[j][i] = pack2f(f[2 * i], f[2 * i + 1]);
+            dg[j][i] = db[j][i] = 0ull;
+        }
     }
-    const int turns = group < p.rows ? (int)((p.rows - group + p.groups - 1) / p.groups) : 0;
-    auto issue = [&](int it, int slot) {                   // row `it` of this group
-        const int64_t row = group + (int64_t)it * p.groups;
-        const uint32_t bar = smem_addr(&bars[sub][slot]);
-        const uint32_t dst = smem_addr(ring + (size_t)slot * 2 * row_bytes);
+    const int mine = group < p.rows ? (int)((p.rows - group + p.groups - 1) / p.groups) : 0;   // this group's rows
+    const uint32_t bar0 = smem_addr(&bars[sub][0]), ring0 = smem_addr(ring);
+    const int64_t x_step = (int64_t)p.groups * p.xs, d_step = (int64_t)p.groups * p.ys;
+    const T* x_next = static_cast<const T*>(p.x) + (int64_t)group * p.xs;
+    const T* d_next = static_cast<const T*>(p.dy) + (int64_t)group * p.ys;
+    auto issue = [&](int slot) {                           // the next row into its slot (thread 0 of the group)
+        const uint32_t bar = bar0 + slot * 8, dst = ring0 + (uint32_t)slot * 2 * row_bytes;
         mbar_arrive_expect_tx(bar, 2 * row_bytes);
-        bulk_load(dst, x0 + row * p.xs, row_bytes, bar);
-        bulk_load(dst + row_bytes, d0 + row * p.ys, row_bytes, bar);
+        bulk_load(dst, x_next, row_bytes, bar);
+        bulk_load(dst + row_bytes, d_next, row_bytes, bar);
+        x_next += x_step;
+        d_next += d_step;
     };
-    int issued = 0;                                        // (of thread 0 of the group)
+    int issued = 0;
     if (t == 0)
-        for (; issued < ring_rows - 1 && issued < turns; ++issued) issue(issued, issued);
+        for (; issued < ring_rows - ROWS && issued < mine; ++issued) issue(issued);
     const int wpr = tpr >> 5;                              // 2 to 16
-    int slot = 0;
+    int slot = 0, fill = ring_rows - ROWS;                 // the slots to read and to fill next
     uint32_t phase = 0;
-    int64_t row = group;
-    float mu = 0.f, r = 0.f;
-    if (turns > 0) { mu = p.mean_in[row]; r = p.rstd_in[row]; }
+    float mu[ROWS], r[ROWS];
+    const float *mean = p.mean_in + group, *rstd = p.rstd_in + group;
+#pragma unroll
+    for (int q = 0; q < ROWS; ++q) {
+        mu[q] = q < mine ? mean[(int64_t)q * p.groups] : 0.f;
+        r[q] = q < mine ? rstd[(int64_t)q * p.groups] : 0.f;
+    }
+    T* dx = static_cast<T*>(p.dx) + (p.dx ? (int64_t)group * p.xs + t * V : 0);
     bool ok = true;
-    for (int it = 0; it < turns; ++it, row += p.groups) {
-        float nmu = 0.f, nr = 0.f;
-        if (it + 1 < turns) { nmu = p.mean_in[row + p.groups]; nr = p.rstd_in[row + p.groups]; }
-        const T* xs = reinterpret_cast<const T*>(ring + (size_t)slot * 2 * row_bytes);
-        const T* ds = xs + p.cols;
-        const bool landed = mbar_wait(smem_addr(&bars[sub][slot]), phase, abort_flag);
-        float s1 = 0.f, s2 = 0.f;
-        if (landed) {
+    for (int it = 0, turn = 0; it < mine; it += ROWS, ++turn) {
+        float nmu[ROWS], nr[ROWS];
+        const uint8_t* src[ROWS];
+        f32x2 s1[ROWS], s2[ROWS];
+        bool landed = true;
 #pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int s = j * tpr + t;
-                if (s < slots) {
-                    float fx[V], fd[V];
-                    widen(*reinterpret_cast<const Vec<T, V>*>(xs + s * V), fx);
-                    widen(*reinterpret_cast<const Vec<T, V>*>(ds + s * V), fd);
+        for (int q = 0; q < ROWS; ++q) {
+            const int64_t at = (int64_t)(it + ROWS + q) * p.groups;
+            nmu[q] = it + ROWS + q < mine ? mean[at] : 0.f;
+            nr[q] = it + ROWS + q < mine ? rstd[at] : 0.f;
+            s1[q] = s2[q] = 0ull;
+            src[q] = ring + (size_t)(slot + q) * 2 * row_bytes + t * 16;
+            if (it + q < mine) {
+                const uint32_t bar = bar0 + (slot + q) * 8;
+                const bool here = mbar_try_wait(bar, phase) || mbar_wait(bar, phase, abort_flag);
+                landed = landed && here;
+                if (here) {
+                    const f32x2 nmean = both(-mu[q]), rr = both(r[q]);
 #pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        const float z = (fx[i] - mu) * r, a = fd[i] * g[j][i];
-                        s1 += a;
-                        s2 += a * z;
-                        dg[j][i] += fd[i] * z;
-                        db[j][i] += fd[i];
+                    for (int j = 0; j < NV; ++j) {
+                        if (j * tpr + t < slots) {
+                            f32x2 fx[H], fd[H];
+                            Pairs<T>::widen(*reinterpret_cast<const uint4*>(src[q] + j * tpr * 16), fx);
+                            Pairs<T>::widen(*reinterpret_cast<const uint4*>(src[q] + row_bytes + j * tpr * 16), fd);
+#pragma unroll
+                            for (int i = 0; i < H; ++i) {  // with u = dy (x - mean): a z = gamma u r, dy z = u r
+                                const f32x2 u = mul2(fd[i], add2(fx[i], nmean));
+                                s1[q] = fma2(fd[i], g[j][i], s1[q]);
+                                s2[q] = fma2(u, g[j][i], s2[q]);
+                                dg[j][i] = fma2(u, rr, dg[j][i]);
+                                db[j][i] = add2(db[j][i], fd[i]);
+                            }
+                        }
                     }
                 }
             }
         }
-        // Both sums in five exchanges: lanes below 16 go on with s1, the others with s2.
-        const bool up = lane & 16;
-        float v = (up ? s2 : s1) + __shfl_xor_sync(0xffffffffu, up ? s1 : s2, 16);
+        // 2 ROWS sums over the warp at once: each exchange also halves the
+        // values a lane carries, until lane group k holds sum k.
+        float v[2 * ROWS];
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        float(*buf)[16] = red[it & 1];
-        if ((lane & 15) == 0) buf[lane >> 4][warp] = v;
-        // The group meets once a row: the sums are there, a wait that ran out
-        // stops all of the group, and the previous row's slot is free.
+        for (int q = 0; q < ROWS; ++q) { v[2 * q] = sum_halves(s1[q]); v[2 * q + 1] = sum_halves(s2[q]); }
+        int o = 16;
+#pragma unroll
+        for (int n = ROWS; n > 0; n >>= 1, o >>= 1) {
+            const bool up = lane & o;
+#pragma unroll
+            for (int k = 0; k < n; ++k)
+                v[k] = (up ? v[k + n] : v[k]) + __shfl_xor_sync(0xffffffffu, up ? v[k] : v[k + n], o);
+        }
+#pragma unroll
+        for (; o > 0; o >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+        constexpr int kSpan = 32 / (2 * ROWS);             // lanes per sum
+        float(*buf)[16] = red[turn & 1];                   // two buffers in turn: one barrier a turn is enough
+        if (lane % kSpan == 0) buf[lane / kSpan][warp] = v[0];
+        // The group meets once a turn: the sums are there, a wait that ran out
+        // stops all of the group, and the previous turn's slots are free.
         ok = named_bar_and(1 + sub, tpr, landed);
         if (!ok) break;
-        if (t == 0 && issued < turns) {
-            issue(issued, slot == 0 ? ring_rows - 1 : slot - 1);
-            ++issued;
-        }
-        if (++slot == ring_rows) { slot = 0; phase ^= 1; }
-        const float cmu = mu, cr = r;
-        mu = nmu;
-        r = nr;
-        if (!p.dx) continue;
-        v = (lane & 15) < wpr ? buf[lane >> 4][sub * wpr + (lane & 15)] : 0.f;
+        if (t == 0)
+            for (int q = 0; q < ROWS && issued < mine; ++q, ++issued) issue(fill + q);
+        fill = fill + ROWS == ring_rows ? 0 : fill + ROWS;
+        slot += ROWS;
+        if (slot == ring_rows) { slot = 0; phase ^= 1; }
+        if (p.dx) {
+            const int k = lane % kSpan;
+            float w = 0.f;
+            for (int i = k; i < wpr; i += kSpan) w += buf[lane / kSpan][sub * wpr + i];
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        v *= p.inv_cols * cr;
-        const float rs1 = __shfl_sync(0xffffffffu, v, 0), rs2 = __shfl_sync(0xffffffffu, v, 16) * cr;
-        T* dx = static_cast<T*>(p.dx) + row * p.xs;
+            for (int d = kSpan / 2; d > 0; d >>= 1) w += __shfl_xor_sync(0xffffffffu, w, d);
+            w *= p.inv_cols;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int s = j * tpr + t;
-            if (s < slots) {
-                float fx[V], f[V];
-                widen(*reinterpret_cast<const Vec<T, V>*>(xs + s * V), fx);
-                widen(*reinterpret_cast<const Vec<T, V>*>(ds + s * V), f);
+            for (int q = 0; q < ROWS; ++q) {
+                const float t1 = __shfl_sync(0xffffffffu, w, sum_lane<ROWS>(2 * q)) * r[q];
+                const float t2 = __shfl_sync(0xffffffffu, w, sum_lane<ROWS>(2 * q + 1)) * r[q] * r[q] * r[q];
+                if (it + q < mine) {
+                    // dx = r a - r mean(a) - (x - mean) r^3 mean(gamma u)
+                    const f32x2 nmean = both(-mu[q]), rr = both(r[q]), n1 = both(-t1), n2 = both(-t2);
 #pragma unroll
-                for (int i = 0; i < V; ++i) f[i] = fmaf(f[i] * g[j][i], cr, -fmaf(fx[i] - cmu, rs2, rs1));
-                *reinterpret_cast<Vec<T, V>*>(dx + s * V) = narrow<T, V>(f);
+                    for (int j = 0; j < NV; ++j) {
+                        if (j * tpr + t < slots) {
+                            f32x2 fx[H], fd[H];
+                            Pairs<T>::widen(*reinterpret_cast<const uint4*>(src[q] + j * tpr * 16), fx);
+                            Pairs<T>::widen(*reinterpret_cast<const uint4*>(src[q] + row_bytes + j * tpr * 16), fd);
+#pragma unroll
+                            for (int i = 0; i < H; ++i)
+                                fd[i] = fma2(mul2(fd[i], g[j][i]), rr, fma2(add2(fx[i], nmean), n2, n1));
+                            *reinterpret_cast<uint4*>(dx + j * tpr * V) = Pairs<T>::narrow(fd);
+                        }
+                    }
+                    dx += x_step;
+                }
             }
         }
+#pragma unroll
+        for (int q = 0; q < ROWS; ++q) { mu[q] = nmu[q]; r[q] = nr[q]; }
     }
     // Copies still in flight after a wait that ran out land before the block leaves.
     if (t == 0 && !ok)
         for (int i = issued > ring_rows ? issued - ring_rows : 0; i < issued; ++i)
-            mbar_drain_wait(smem_addr(&bars[sub][i % ring_rows]), (uint32_t)(i / ring_rows) & 1u);
+            mbar_drain_wait(bar0 + (i % ring_rows) * 8, (uint32_t)(i / ring_rows) & 1u);
     if (!p.want_params) return;
     float* acc_s = reinterpret_cast<float*>(ring_s);       // the ring is done with
     float* out = p.part + (int64_t)blockIdx.x * 2 * p.cols;
@@ -515,13 +643,17 @@ __global__ void __launch_bounds__(kBulkThreads, 1) layernorm_bwd_bulk_kernel(con
             float* dst = k + 1 < rpb ? acc_s : out;
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                const int s = j * tpr + t;
+                if (j * tpr + t < slots) {
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const int c = s * V + i;
-                    if (s < slots) {
-                        dst[c] = dg[j][i] + (k ? acc_s[c] : 0.f);
-                        dst[p.cols + c] = db[j][i] + (k ? acc_s[p.cols + c] : 0.f);
+                    for (int i = 0; i < H; ++i) {
+                        const int c = (j * tpr + t) * V + 2 * i;
+                        float a0, a1, b0, b1;
+                        unpack2f(dg[j][i], a0, a1);
+                        unpack2f(db[j][i], b0, b1);
+                        dst[c] = a0 + (k ? acc_s[c] : 0.f);
+                        dst[c + 1] = a1 + (k ? acc_s[c + 1] : 0.f);
+                        dst[p.cols + c] = b0 + (k ? acc_s[p.cols + c] : 0.f);
+                        dst[p.cols + c + 1] = b1 + (k ? acc_s[p.cols + c + 1] : 0.f);
                     }
                 }
             }
@@ -620,30 +752,37 @@ __global__ void __launch_bounds__(128) layernorm_bwd_cols_kernel(const LnParams 
     }
 }
 
-// dgamma and dbeta: the parts' columns added in order, 32 columns by 32 shares
-// of the parts per block (blockIdx.y: dgamma or dbeta).  A few hundred parts:
-// one round of about ten loads per thread, all in flight.
+// dgamma and dbeta: the parts' columns added in order, SPAN columns by 1024 /
+// SPAN shares of the parts per block (blockIdx.y: dgamma or dbeta).  A few
+// hundred parts of a normal row: 32 shares, about ten loads per thread, all in
+// flight.  A few parts of a long row: one share.
+template <int SPAN>
 __global__ void __launch_bounds__(1024) layernorm_params_kernel(const float* part, int parts, int cols, void* dgamma,
                                                                 void* dbeta, int f32, int bf16) {
-    __shared__ float sh[32][33];
+    constexpr int SHARES = 1024 / SPAN;
     pdl_wait();
     void* out = blockIdx.y ? dbeta : dgamma;
     if (!out) return;
-    const int lane = threadIdx.x & 31, k = threadIdx.x >> 5;
-    const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+    const int at = threadIdx.x % SPAN, k = threadIdx.x / SPAN;
+    const int64_t c = (int64_t)blockIdx.x * SPAN + at;
     float v = 0.f;
     if (c < cols) {
         const float* q = part + (int64_t)blockIdx.y * cols + c;
         const int64_t pitch = 2 * (int64_t)cols;
 #pragma unroll 10
-        for (int i = k; i < parts; i += 32) v += q[i * pitch];
+        for (int i = k; i < parts; i += SHARES) v += q[i * pitch];
     }
-    sh[k][lane] = v;
-    __syncthreads();
-    // Warp k adds column k's 32 shares.
-    v = lane_sum(sh[lane][k], 32);
-    const int64_t col = (int64_t)blockIdx.x * 32 + k;
-    if (lane == 0 && col < cols) store_param(out, f32, bf16, col, v);
+    if constexpr (SHARES == 1) {
+        if (c < cols) store_param(out, f32, bf16, c, v);
+    } else {
+        static_assert(SPAN == 32, "a warp per column");
+        __shared__ float sh[32][33];
+        sh[k][at] = v;
+        __syncthreads();
+        v = lane_sum(sh[at][k], 32);                   // warp k adds column k's shares
+        const int64_t col = (int64_t)blockIdx.x * 32 + k;
+        if (at == 0 && col < cols) store_param(out, f32, bf16, col, v);
+    }
 }
 
 // ------------------------------------------------------------------ host side
@@ -765,6 +904,7 @@ template <typename T> cudaError_t bwd_typed(const layernorm_desc& d, LnParams p,
                                        : V - 1;
     const int64_t slots = ceil_div((int64_t)p.cols + most_shift, V);
     const int sms = device_sm_count();
+    p.cut_alike = cut_alike;
     const int64_t row_bytes = (int64_t)p.cols * sizeof(T);
     if (slots * V <= kBwdCols && cut == WHOLE && row_bytes >= kBulkBytes) {
         // Bulk copies from two rows a group on (one hides nothing).
@@ -776,12 +916,14 @@ template <typename T> cudaError_t bwd_typed(const layernorm_desc& d, LnParams p,
             *parts = sms;
             int rows = (int)(kRingBytes / (rpb * 2 * row_bytes));
             rows = rows > kRingMost ? kRingMost : rows;
+            const bool twice = rows >= 4;              // two rows a turn, and two on their way
+            if (twice) rows &= ~1;
             const size_t ring = (size_t)rpb * rows * 2 * row_bytes, sums = 2 * (size_t)p.cols * sizeof(float);
             const size_t smem = ring > sums ? ring : sums;
-            const cudaError_t e = cudaFuncSetAttribute(layernorm_bwd_bulk_kernel<T>,
-                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            auto kern = twice ? layernorm_bwd_bulk_kernel<T, 2> : layernorm_bwd_bulk_kernel<T, 1>;
+            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
             if (e != cudaSuccess) return e;
-            return launch_after(layernorm_bwd_bulk_kernel<T>, dim3((unsigned)sms), dim3(rpb * tpr), smem, st, p, rows);
+            return launch_after(kern, dim3((unsigned)sms), dim3(rpb * tpr), smem, st, p, rows);
         }
     }
     if (slots * V <= kBwdCols) {
@@ -877,8 +1019,10 @@ cudaError_t wait_limit_set_ln(cudaStream_t st, uint64_t ns) { return wait_limit_
 
 cudaError_t launch_layernorm_params(const float* part, int parts, const layernorm_desc& d, void* dgamma, void* dbeta,
                                     cudaStream_t st) {
-    return launch_after(layernorm_params_kernel, dim3((unsigned)((d.cols + 31) / 32), 2), dim3(1024), 0, st, part, parts,
-                        (int)d.cols, dgamma, dbeta, d.param == CONV2D_F32 ? 1 : 0, d.param == CONV2D_BF16 ? 1 : 0);
+    const int span = parts > 64 || d.cols < 1024 ? 32 : 1024;
+    return launch_after(span == 32 ? layernorm_params_kernel<32> : layernorm_params_kernel<1024>,
+                        dim3((unsigned)((d.cols + span - 1) / span), 2), dim3(1024), 0, st, part, parts, (int)d.cols,
+                        dgamma, dbeta, d.param == CONV2D_F32 ? 1 : 0, d.param == CONV2D_BF16 ? 1 : 0);
 }
 
 cudaError_t launch_layernorm_bwd(const layernorm_desc& d, const void* dy, const void* x, const void* gamma,

@@ -17,12 +17,14 @@
 // tile's words are transposed-and-added across the half-warp, so one lane ends
 // up with one channel, and collect in shared memory over the block's tiles.
 //
-// Planes of a 16-bit type with a multiple of four pixels and of eight channels
-// (every 16-bit layer of this library's workloads) take a faster form
-// (planes16_*): a thread holds two channels by four pixels, so a load or store
-// moves four pixels (or, in shared memory, a channel pair) and the index
-// arithmetic is shared by eight elements.  The general form spends 37
-// instructions an element forward and 68 backward, which bounds it.
+// Planes of a 16-bit type with a multiple of eight pixels and of eight channels
+// take a faster form (planes16_*): TMA moves tiles in and out on both sides,
+// and the matrix loads and stores of shared memory (8 x 8 blocks, transposed on
+// the way) hand every thread channel pairs of one pixel from either side, for
+// packed arithmetic.  What bounds the general form is instructions (37 an
+// element forward, 68 backward), most of them addresses.
+#include <cuda.h>
+
 #include "head_device.cuh"
 #include "head_internal.h"
 #include "ptx.cuh"
@@ -155,7 +157,7 @@ __global__ void __launch_bounds__(kFwdThreads, 4) planes_fwd_kernel(const PlaneP
 #pragma unroll
             for (int i = 0; i < PP; ++i) {
                 if (pass == 0) mean[i] = v[i] * p.inv_c;
-                else rstd[i] = 1.0f / sqrtf(v[i] * p.inv_c + p.eps);
+                else rstd[i] = rsqrtf(v[i] * p.inv_c + p.eps);
             }
         }
         if (half == 0) {
@@ -369,316 +371,424 @@ __global__ void __launch_bounds__(kBwdThreads, 2) planes_bwd_kernel(const PlaneP
         for (int c = threadIdx.x; c < 2 * p.C; c += kBwdThreads) p.part[(int64_t)blockIdx.x * 2 * p.C + c] = acc[c];
 }
 
-// ------------------------------------------------------------------ 16-bit, four pixels a thread
-// A tile is 32 pixels by all channels.  Lane l & 7 of a warp holds pixels
-// 4 l .. 4 l + 3, lane >> 3 (and the warp) the channel pair.  The [pixel]
-// [channel] side of the tile sits in shared memory in 16-byte chunks of eight
-// channels, chunk k of pixel q at k ^ (q / 4 % 8): eight lanes of different
-// pixels then meet different banks, and so do a row's consecutive chunks.
-constexpr int kTile = 32;
+// ------------------------------------------------------------------ 16-bit, 8 x 8 blocks
+// A tile is 8 PG pixels of one image by all channels, worked on by 16 warps: a
+// warp takes G neighbouring groups of eight pixels of every kShares-th
+// 32-channel block (NB at most), so that a channel's gamma is read once for G
+// pixels.  In a block thread t has pixel t / 4 and the channel pairs
+// 8 m + 2 (t % 4), m = 0..3.
+//   x side   [channel][8 PG pixels]: rows of 64 or 32 bytes, as TMA writes them
+//            with a swizzle of that width
+//   y side   [64 channels][8 PG pixels][128 bytes], 128-byte swizzle
+// so that the eight rows of a matrix lie in different banks on both sides.
+constexpr int kThreads16 = 512;
 
-__device__ __forceinline__ uint32_t chunk_at(int pixel, int chunk, int pitch) {
-    return (uint32_t)(pixel * pitch * 2 + ((chunk ^ (pixel >> 2 & 7)) << 4));
+template <int PG> __device__ __forceinline__ uint32_t x_at(int c, int group) {
+    return (uint32_t)(c * PG * 16 + ((group ^ (c / (8 / PG) & (PG - 1))) << 4));
 }
-template <typename T> __device__ __forceinline__ void widen2(uint32_t w, float& a, float& b) {
-    float f[2];
-    Word<T, 2>::widen(w, f);
-    a = f[0];
-    b = f[1];
-}
-template <typename T> __device__ __forceinline__ void widen4(uint2 w, float (&f)[4]) {
-    widen2<T>(w.x, f[0], f[1]);
-    widen2<T>(w.y, f[2], f[3]);
-}
-template <typename T> __device__ __forceinline__ uint32_t pair(float a, float b) {
-    const float f[2] = {a, b};
-    return Word<T, 2>::narrow(f);
+template <int PG> __device__ __forceinline__ uint32_t y_at(int pixel, int chunk) {
+    return (uint32_t)((chunk >> 3) * PG * 1024 + pixel * 128 + (((chunk ^ pixel) & 7) << 4));
 }
 
-template <typename T, int NP, int THREADS>
-__global__ void __launch_bounds__(THREADS, 1024 / THREADS) planes16_fwd_kernel(const PlaneParams p) {
-    extern __shared__ __align__(16) uint8_t tile_b[];
-    __shared__ float4 red[2][THREADS / 32][8];
-    pdl_wait();
-    const int l = threadIdx.x & 7, k0 = threadIdx.x >> 3, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int pitch = (p.C + 63) / 64 * 64;
-    const int64_t tile = blockIdx.x, row0 = tile * kTile + 4 * l;
-    const bool live = row0 < p.rows;
-    const int64_t n = live ? row0 / p.pixels : 0, off = live ? n * p.C * p.pixels + (row0 - n * p.pixels) : 0;
-    const T* x = static_cast<const T*>(p.x) + off;
-    uint2 raw[NP][2];
-#pragma unroll
-    for (int j = 0; j < NP; ++j) {
-        const int c = 2 * (k0 + j * (THREADS / 8));
-        raw[j][0] = raw[j][1] = make_uint2(0, 0);
-        if (live && c < p.C) {
-            raw[j][0] = *reinterpret_cast<const uint2*>(x + c * p.pixels);
-            raw[j][1] = *reinterpret_cast<const uint2*>(x + (c + 1) * p.pixels);
-        }
+// How the 16 warps of a tile of 8 PG pixels share it, G groups of pixels each.
+template <int PG, int G> struct Share {
+    static constexpr int kShares = 16 * G / PG;            // warps along the channels
+    int group, share;                                      // first pixel group; which share of the channel blocks
+    __device__ __forceinline__ Share() {
+        const int warp = threadIdx.x >> 5;
+        group = warp % (PG / G) * G;
+        share = warp / (PG / G);
     }
-    // Sum over the channels: this thread's, the warp's four pairs, the warps.
-    auto total = [&](float (&v)[4], int which) {
+    // Pixel of group j of this thread.
+    __device__ __forceinline__ int pixel(int j) const { return (group + j) * 8 + ((threadIdx.x & 31) >> 2); }
+};
+
+// N sums over a pixel's channels for each of the thread's G pixels, complete in
+// every thread of the pixel: the thread's, its neighbours', then the warps'.
+template <int PG, int G, int N>
+__device__ __forceinline__ void pixel_sums(float (&v)[G][N], float (*red)[8 * PG][Share<PG, G>::kShares],
+                                           const Share<PG, G>& sh) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[i] += __shfl_xor_sync(0xffffffffu, v[i], 8);
-            v[i] += __shfl_xor_sync(0xffffffffu, v[i], 16);
-        }
-        if (lane < 8) red[which][warp][l] = make_float4(v[0], v[1], v[2], v[3]);
-        __syncthreads();
+    for (int j = 0; j < G; ++j) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = 0.f;
-#pragma unroll
-        for (int w = 0; w < THREADS / 32; ++w) {
-            const float4 t = red[which][w][l];
-            v[0] += t.x; v[1] += t.y; v[2] += t.z; v[3] += t.w;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] *= p.inv_c;
-    };
-    float mean[4] = {0.f, 0.f, 0.f, 0.f}, rstd[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int j = 0; j < NP; ++j) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            float f[4];
-            widen4<T>(raw[j][e], f);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) mean[i] += f[i];
-        }
-    }
-    total(mean, 0);
-#pragma unroll
-    for (int j = 0; j < NP; ++j) {
-        if (2 * (k0 + j * (THREADS / 8)) < p.C) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float f[4];
-                widen4<T>(raw[j][e], f);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) rstd[i] += (f[i] - mean[i]) * (f[i] - mean[i]);
-            }
-        }
-    }
-    total(rstd, 1);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) rstd[i] = 1.0f / sqrtf(rstd[i] + p.eps);
-    if (threadIdx.x < 8 && live) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (p.mean) p.mean[row0 + i] = mean[i];
-            if (p.rstd) p.rstd[row0 + i] = rstd[i];
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < NP; ++j) {
-        const int c = 2 * (k0 + j * (THREADS / 8));
-        if (c < p.C) {
-            const float g0 = param_at(p.gamma, p.param_f32, is_bf16<T>, c, 1.f);
-            const float g1 = param_at(p.gamma, p.param_f32, is_bf16<T>, c + 1, 1.f);
-            const float b0 = param_at(p.beta, p.param_f32, is_bf16<T>, c, 0.f);
-            const float b1 = param_at(p.beta, p.param_f32, is_bf16<T>, c + 1, 0.f);
-            float f0[4], f1[4];
-            widen4<T>(raw[j][0], f0);
-            widen4<T>(raw[j][1], f1);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<uint32_t*>(tile_b + chunk_at(4 * l + i, c >> 3, pitch) + (c & 7) * 2) =
-                    pair<T>((f0[i] - mean[i]) * rstd[i] * g0 + b0, (f1[i] - mean[i]) * rstd[i] * g1 + b1);
+        for (int k = 0; k < N; ++k) {
+            v[j][k] += __shfl_xor_sync(0xffffffffu, v[j][k], 1);
+            v[j][k] += __shfl_xor_sync(0xffffffffu, v[j][k], 2);
+            if ((threadIdx.x & 3) == 0) red[k][sh.pixel(j)][sh.share] = v[j][k];
         }
     }
     __syncthreads();
-    for (int q = warp; q < kTile; q += THREADS / 32) {
-        const int64_t row = tile * kTile + q;
-        if (row >= p.rows) break;
-        T* y = static_cast<T*>(p.y) + row * p.ys;
-        for (int k = lane; k < p.C / 8; k += 32)
-            *reinterpret_cast<uint4*>(y + k * 8) = *reinterpret_cast<const uint4*>(tile_b + chunk_at(q, k, pitch));
+#pragma unroll
+    for (int j = 0; j < G; ++j) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const float4* q = reinterpret_cast<const float4*>(red[k][sh.pixel(j)]);
+            v[j][k] = 0.f;
+#pragma unroll
+            for (int w = 0; w < Share<PG, G>::kShares / 4; ++w) v[j][k] += (q[w].x + q[w].y) + (q[w].z + q[w].w);
+        }
     }
 }
 
-__device__ __forceinline__ void copy_async8(uint32_t dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// Geometry of a launch: TMA boxes of `xbox` channels by 8 PG pixels on the x
+// side, 64 channels by 8 PG pixels on the y side.
+struct Boxes {
+    int tpi;                 // tiles per image
+    int xbox, xboxes, yboxes;
+    int x_bytes, y_bytes;    // of a tile, whole boxes
+};
+
+template <int PG> __device__ __forceinline__ void load_x(const CUtensorMap* map, const Boxes& bx, int n, int px,
+                                                         uint32_t dst, uint32_t bar) {
+    for (int i = 0; i < bx.xboxes; ++i) tma_load_3d(dst + i * bx.xbox * PG * 16, map, bar, px, i * bx.xbox, n);
 }
 
-// One block of 512 threads per SM (two for few channels) over many tiles.
-// Asynchronous copies bring later tiles in while this one is worked on: x into
-// the thread's own words, dy into the swizzled tile.  dgamma and dbeta of the
-// thread's channels stay in registers until the end.
-template <typename T, int NP>
-__global__ void __launch_bounds__(512, NP <= 2 ? 2 : 1) planes16_bwd_kernel(const PlaneParams p) {
-    constexpr int STAGES = NP == 8 ? 1 : 3, XBYTES = NP * 8192;
-    extern __shared__ __align__(16) uint8_t smem_b[];
-    __shared__ float4 red[2][16][8];
+template <typename T, int PG, int G, int NB>
+__global__ void __launch_bounds__(kThreads16, 2)
+planes16_fwd_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap ymap,
+                    const PlaneParams p, const Boxes bx) {
+    using S = Share<PG, G>;
+    extern __shared__ uint8_t smem_raw[];                  // x side [2], y side, gamma, beta
+    __shared__ __align__(16) float red[2][1][8 * PG][S::kShares];
+    __shared__ uint64_t full[2];
+    __shared__ int abort_word;
+    volatile int* abort_flag = &abort_word;
+    const uint32_t xs = (smem_addr(smem_raw) + 1023u) & ~1023u, ys = xs + 2 * bx.x_bytes;
+    float* gam = reinterpret_cast<float*>(smem_raw + (ys - smem_addr(smem_raw)) + bx.y_bytes);
+    float* bet = gam + p.C;
+    if (threadIdx.x == 0) {
+        mbar_init(smem_addr(&full[0]), 1);
+        mbar_init(smem_addr(&full[1]), 1);
+        abort_word = 0;
+        mbar_fence_init();
+        tma_prefetch_desc(&xmap);
+        tma_prefetch_desc(&ymap);
+    }
+    __syncthreads();
     pdl_wait();
-    const int l = threadIdx.x & 7, k0 = threadIdx.x >> 3, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int pitch = (p.C + 63) / 64 * 64, stage_bytes = XBYTES + kTile * pitch * 2;
-    float* gam = reinterpret_cast<float*>(smem_b + STAGES * stage_bytes);
-    for (int c = threadIdx.x; c < p.C; c += 512) gam[c] = param_at(p.gamma, p.param_f32, is_bf16<T>, c, 1.f);
-
-    auto place = [&](int64_t tile, int64_t& row0) {        // offset of this thread's pixels, or -1
-        row0 = tile * kTile + 4 * l;
-        if (row0 >= p.rows) return (int64_t)-1;
-        const int64_t n = row0 / p.pixels;
-        return n * p.C * p.pixels + (row0 - n * p.pixels);
+    const S sh;
+    const int lane = threadIdx.x & 31, blocks = (p.C + 31) / 32, tiles = (int)p.tiles, pixels = (int)p.pixels;
+    for (int c = threadIdx.x; c < p.C; c += kThreads16) {
+        gam[c] = param_at(p.gamma, p.param_f32, is_bf16<T>, c, 1.f);
+        bet[c] = param_at(p.beta, p.param_f32, is_bf16<T>, c, 0.f);
+    }
+    auto fetch = [&](int tile, int stage) {                // (thread 0)
+        const int n = (unsigned)tile / (unsigned)bx.tpi;
+        mbar_arrive_expect_tx(smem_addr(&full[stage]), bx.x_bytes);
+        load_x<PG>(&xmap, bx, n, (tile - n * bx.tpi) * 8 * PG, xs + stage * bx.x_bytes, smem_addr(&full[stage]));
     };
-    auto issue = [&](int64_t tile, int stage) {
-        int64_t row0;
-        const int64_t off = tile < p.tiles ? place(tile, row0) : -1;
-        const uint32_t xd = smem_addr(smem_b + stage * stage_bytes) + threadIdx.x * 8;
-        if (off >= 0) {
-            const T* x = static_cast<const T*>(p.x) + off;
+    uint32_t x_off[G][NB], y_off[G][NB];
 #pragma unroll
-            for (int j = 0; j < NP; ++j) {
-                const int c = 2 * (k0 + j * 64);
-                if (c < p.C) {
-                    copy_async8(xd + j * 8192, x + c * p.pixels);
-                    copy_async8(xd + j * 8192 + 4096, x + (c + 1) * p.pixels);
+    for (int j = 0; j < G; ++j) {
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            const int b = sh.share + i * S::kShares;
+            x_off[j][i] = xs + x_at<PG>(b * 32 + lane, sh.group + j);
+            y_off[j][i] = ys + y_at<PG>((sh.group + j) * 8 + (lane & 7), b * 4 + (lane >> 3));
+        }
+    }
+    int stage = 0, fetched = 0;
+    uint32_t phase = 0;
+    if (threadIdx.x == 0 && blockIdx.x < tiles) { fetch(blockIdx.x, 0); fetched = 1; }
+    bool ok = true;
+    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        // The tile is here, and everyone is done with the other stage.
+        ok = __syncthreads_and(mbar_wait(smem_addr(&full[stage]), phase, abort_flag));
+        if (!ok) break;
+        if (threadIdx.x == 0 && tile + (int)gridDim.x < tiles) { fetch(tile + gridDim.x, stage ^ 1); ++fetched; }
+        const uint32_t x_stage = stage * bx.x_bytes;
+        f32x2 f[G][NB][4];
+        float v[G][1];
+#pragma unroll
+        for (int j = 0; j < G; ++j) {
+            f32x2 sum = 0ull;
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                const int b = sh.share + i * S::kShares;
+                if (b < blocks) {
+                    uint32_t r[4];
+                    ldsm_x4_trans(x_off[j][i] + x_stage, r);
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {          // (channels past C read as zero)
+                        f[j][i][m] = widen_pair<T>(r[m]);
+                        sum = add2(sum, f[j][i][m]);
+                    }
                 }
             }
+            v[j][0] = sum_halves(sum);
         }
-        if (tile < p.tiles) {
-            const uint32_t dd = smem_addr(smem_b + stage * stage_bytes) + XBYTES;
+        pixel_sums<PG, G, 1>(v, red[0], sh);
+        float mean[G], rstd[G];
 #pragma unroll
-            for (int q = warp; q < kTile; q += 16) {
-                const int64_t row = tile * kTile + q;
-                if (row < p.rows) {
-                    const T* dy = static_cast<const T*>(p.dy) + row * p.ys;
-                    for (int k = lane; k < p.C / 8; k += 32) copy_async16(dd + chunk_at(q, k, pitch), dy + k * 8);
+        for (int j = 0; j < G; ++j) {
+            mean[j] = v[j][0] * p.inv_c;
+            f32x2 sq = 0ull;
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                const int b = sh.share + i * S::kShares;
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    if (b * 32 + m * 8 < p.C) {
+                        f[j][i][m] = add2(f[j][i][m], both(-mean[j]));
+                        sq = fma2(f[j][i][m], f[j][i][m], sq);
+                    }
                 }
             }
+            v[j][0] = sum_halves(sq);
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-
-    float ag[NP][2], ab[NP][2];
+        if (threadIdx.x == 0) bulk_wait_read_all();        // the last tile's y side has been copied out
+        pixel_sums<PG, G, 1>(v, red[1], sh);
+        const int n = (unsigned)tile / (unsigned)bx.tpi, px = (tile - n * bx.tpi) * 8 * PG;
 #pragma unroll
-    for (int j = 0; j < NP; ++j) ag[j][0] = ag[j][1] = ab[j][0] = ab[j][1] = 0.f;
-    float nmu[4], nr[4];
-    auto stats = [&](int64_t tile) {
-        int64_t row0;
-        const bool live = tile < p.tiles && place(tile, row0) >= 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            nmu[i] = live ? p.mean_in[row0 + i] : 0.f;
-            nr[i] = live ? p.rstd_in[row0 + i] : 0.f;
+        for (int j = 0; j < G; ++j) {
+            rstd[j] = rsqrtf(v[j][0] * p.inv_c + p.eps);
+            if (sh.share == 0 && (lane & 3) == 0 && px + sh.pixel(j) < pixels) {
+                const int64_t row = (int64_t)n * pixels + px + sh.pixel(j);
+                if (p.mean) p.mean[row] = mean[j];
+                if (p.rstd) p.rstd[row] = rstd[j];
+            }
         }
-    };
 #pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s) issue(blockIdx.x + (int64_t)s * gridDim.x, s);
-    stats(blockIdx.x);
-    int stage = 0;
-    for (int64_t tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
-        const int ahead = STAGES == 1 ? 0 : (stage == 0 ? STAGES - 1 : stage - 1);
-        issue(tile + (int64_t)(STAGES - 1) * gridDim.x, ahead);
-        float mu[4], r[4];
+        for (int i = 0; i < NB; ++i) {
+            const int b = sh.share + i * S::kShares;
+            if (b < blocks) {
+                uint32_t r[G][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) { mu[i] = nmu[i]; r[i] = nr[i]; }
-        stats(tile + gridDim.x);
-        asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
+                for (int m = 0; m < 4; ++m) {
+                    const int c = b * 32 + m * 8 + 2 * (lane & 3);
+                    if (b * 32 + m * 8 < p.C) {
+                        const f32x2 g = *reinterpret_cast<const f32x2*>(gam + c);
+                        const f32x2 be = *reinterpret_cast<const f32x2*>(bet + c);
+#pragma unroll
+                        for (int j = 0; j < G; ++j)
+                            r[j][m] = narrow_pair<T>(fma2(mul2(f[j][i][m], both(rstd[j])), g, be));
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < G; ++j) r[j][m] = 0;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < G; ++j) stsm_x4(y_off[j][i], r[j]);
+            }
+        }
+        fence_proxy_async_smem();
         __syncthreads();
-        int64_t row0;
-        const int64_t off = place(tile, row0);
-        const uint8_t* xs = smem_b + stage * stage_bytes + threadIdx.x * 8;
-        const uint8_t* ds = smem_b + stage * stage_bytes + XBYTES;
-        float s1[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
-        if (off >= 0) {
+        if (threadIdx.x == 0) {
+            for (int i = 0; i < bx.yboxes; ++i) tma_store_3d(&ymap, ys + i * PG * 1024, i * 64, px, n);
+            bulk_commit_group();
+        }
+        stage ^= 1;
+        if (stage == 0) phase ^= 1;
+    }
+    if (threadIdx.x == 0) {
+        if (!ok)                                           // copies in flight land before the block leaves
+            for (int i = fetched > 2 ? fetched - 2 : 0; i < fetched; ++i)
+                mbar_drain_wait(smem_addr(&full[i & 1]), (uint32_t)(i >> 1) & 1u);
+        bulk_wait_all();
+    }
+}
+
+// dgamma and dbeta of the thread's channel pairs stay in registers over the
+// block's tiles; dx goes back through the x side, whose words the same warp read.
+template <typename T, int PG, int G, int NB>
+__global__ void __launch_bounds__(kThreads16, NB == 1 ? 2 : 1)
+planes16_bwd_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap dmap,
+                    const __grid_constant__ CUtensorMap omap, const PlaneParams p, const Boxes bx) {
+    using S = Share<PG, G>;
+    constexpr int STAGES = 3;
+    extern __shared__ uint8_t smem_raw[];                  // stages of (y side, x side), gamma
+    __shared__ __align__(16) float red[2][8 * PG][S::kShares];
+    __shared__ uint64_t full[STAGES];
+    __shared__ int abort_word;
+    volatile int* abort_flag = &abort_word;
+    const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u, stage_bytes = bx.y_bytes + bx.x_bytes;
+    uint8_t* smem = smem_raw + (base - smem_addr(smem_raw));
+    float* gam = reinterpret_cast<float*>(smem + STAGES * stage_bytes);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < STAGES; ++i) mbar_init(smem_addr(&full[i]), 1);
+        abort_word = 0;
+        mbar_fence_init();
+        tma_prefetch_desc(&xmap);
+        tma_prefetch_desc(&dmap);
+    }
+    __syncthreads();
+    pdl_wait();
+    const S sh;
+    const int lane = threadIdx.x & 31, blocks = (p.C + 31) / 32, tiles = (int)p.tiles, pixels = (int)p.pixels;
+    for (int c = threadIdx.x; c < p.C; c += kThreads16) gam[c] = param_at(p.gamma, p.param_f32, is_bf16<T>, c, 1.f);
+    auto fetch = [&](int tile, int stage) {                // (thread 0)
+        const uint32_t bar = smem_addr(&full[stage]), dst = base + stage * stage_bytes;
+        const int n = (unsigned)tile / (unsigned)bx.tpi, px = (tile - n * bx.tpi) * 8 * PG;
+        mbar_arrive_expect_tx(bar, stage_bytes);
+        for (int i = 0; i < bx.yboxes; ++i) tma_load_3d(dst + i * PG * 1024, &dmap, bar, i * 64, px, n);
+        load_x<PG>(&xmap, bx, n, px, dst + bx.y_bytes, bar);
+    };
+    uint32_t x_off[G][NB], d_off[G][NB];
 #pragma unroll
-            for (int j = 0; j < NP; ++j) {
-                const int c = 2 * (k0 + j * 64);
-                if (c < p.C) {
-                    float x0[4], x1[4];
-                    widen4<T>(*reinterpret_cast<const uint2*>(xs + j * 8192), x0);
-                    widen4<T>(*reinterpret_cast<const uint2*>(xs + j * 8192 + 4096), x1);
-                    const float2 g = *reinterpret_cast<const float2*>(gam + c);
+    for (int j = 0; j < G; ++j) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float d0, d1;
-                        widen2<T>(*reinterpret_cast<const uint32_t*>(ds + chunk_at(4 * l + i, c >> 3, pitch) + (c & 7) * 2),
-                                  d0, d1);
-                        const float z0 = (x0[i] - mu[i]) * r[i], z1 = (x1[i] - mu[i]) * r[i];
-                        const float a0 = d0 * g.x, a1 = d1 * g.y;
-                        s1[i] += a0 + a1;
-                        s2[i] = fmaf(a0, z0, fmaf(a1, z1, s2[i]));
-                        ag[j][0] = fmaf(d0, z0, ag[j][0]);
-                        ag[j][1] = fmaf(d1, z1, ag[j][1]);
-                        ab[j][0] += d0;
-                        ab[j][1] += d1;
+        for (int i = 0; i < NB; ++i) {
+            const int b = sh.share + i * S::kShares;
+            d_off[j][i] = base + y_at<PG>((sh.group + j) * 8 + (lane & 7), b * 4 + (lane >> 3));
+            x_off[j][i] = base + bx.y_bytes + x_at<PG>(b * 32 + lane, sh.group + j);
+        }
+    }
+    f32x2 dg[NB][4], db[NB][4];
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int m = 0; m < 4; ++m) dg[i][m] = db[i][m] = 0ull;
+    int fetched = 0, stage = 0;
+    uint32_t phase = 0;
+    if (threadIdx.x == 0)
+        for (int t = blockIdx.x; fetched < STAGES - 1 && t < tiles; t += gridDim.x, ++fetched) fetch(t, fetched);
+    // Statistics of the thread's pixels; past the image both are zero, which
+    // makes every term of the tile's empty pixels zero (their x and dy are).
+    float nmu[G], nr[G];
+    auto stats = [&](int tile) {
+        const int n = (unsigned)tile / (unsigned)bx.tpi, px = (tile - n * bx.tpi) * 8 * PG;
+#pragma unroll
+        for (int j = 0; j < G; ++j) {
+            nmu[j] = nr[j] = 0.f;
+            if (tile < tiles && px + sh.pixel(j) < pixels) {
+                nmu[j] = p.mean_in[(int64_t)n * pixels + px + sh.pixel(j)];
+                nr[j] = p.rstd_in[(int64_t)n * pixels + px + sh.pixel(j)];
+            }
+        }
+    };
+    stats(blockIdx.x);
+    bool ok = true;
+    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        float mu[G], r[G];
+#pragma unroll
+        for (int j = 0; j < G; ++j) { mu[j] = nmu[j]; r[j] = nr[j]; }
+        stats(tile + gridDim.x);
+        // The tile is here; the last one's dx, whose stage is next, has been copied out.
+        bool landed = mbar_wait(smem_addr(&full[stage]), phase, abort_flag);
+        if (threadIdx.x == 0) bulk_wait_read_all();
+        ok = __syncthreads_and(landed);
+        if (!ok) break;
+        if (threadIdx.x == 0 && tile + (STAGES - 1) * (int)gridDim.x < tiles) {
+            fetch(tile + (STAGES - 1) * gridDim.x, stage == 0 ? STAGES - 1 : stage - 1);
+            ++fetched;
+        }
+        const uint32_t at = stage * stage_bytes;
+        f32x2 s1[G], s2[G];
+#pragma unroll
+        for (int j = 0; j < G; ++j) s1[j] = s2[j] = 0ull;
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            const int b = sh.share + i * S::kShares;
+            if (b < blocks) {
+                uint32_t rx[G][4], rd[G][4];
+#pragma unroll
+                for (int j = 0; j < G; ++j) {
+                    ldsm_x4_trans(x_off[j][i] + at, rx[j]);
+                    ldsm_x4(d_off[j][i] + at, rd[j]);
+                }
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    if (b * 32 + m * 8 < p.C) {            // with u = dy (x - mean): a z = gamma u r, dy z = u r
+                        const f32x2 g = *reinterpret_cast<const f32x2*>(gam + b * 32 + m * 8 + 2 * (lane & 3));
+#pragma unroll
+                        for (int j = 0; j < G; ++j) {
+                            const f32x2 d = widen_pair<T>(rd[j][m]);
+                            const f32x2 u = mul2(d, add2(widen_pair<T>(rx[j][m]), both(-mu[j])));
+                            s1[j] = fma2(d, g, s1[j]);
+                            s2[j] = fma2(u, g, s2[j]);
+                            dg[i][m] = fma2(u, both(r[j]), dg[i][m]);
+                            db[i][m] = add2(db[i][m], d);
+                        }
                     }
                 }
             }
         }
         if (p.dx) {
+            float v[G][2];
+            f32x2 n1[G], n2[G];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                s1[i] += __shfl_xor_sync(0xffffffffu, s1[i], 8);
-                s2[i] += __shfl_xor_sync(0xffffffffu, s2[i], 8);
-                s1[i] += __shfl_xor_sync(0xffffffffu, s1[i], 16);
-                s2[i] += __shfl_xor_sync(0xffffffffu, s2[i], 16);
+            for (int j = 0; j < G; ++j) { v[j][0] = sum_halves(s1[j]); v[j][1] = sum_halves(s2[j]); }
+            pixel_sums<PG, G, 2>(v, red, sh);
+#pragma unroll
+            for (int j = 0; j < G; ++j) {                  // dx = r a - r mean(a) - (x - mean) r^3 mean(gamma u)
+                n1[j] = both(-v[j][0] * p.inv_c * r[j]);
+                n2[j] = both(-v[j][1] * p.inv_c * r[j] * r[j] * r[j]);
             }
-            if (lane < 8) {
-                red[0][warp][l] = make_float4(s1[0], s1[1], s1[2], s1[3]);
-                red[1][warp][l] = make_float4(s2[0], s2[1], s2[2], s2[3]);
-            }
-            __syncthreads();
-            if (off >= 0) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s1[i] = s2[i] = 0.f;
+            for (int i = 0; i < NB; ++i) {
+                const int b = sh.share + i * S::kShares;
+                if (b < blocks) {
+                    uint32_t rx[G][4], rd[G][4];
 #pragma unroll
-                for (int w = 0; w < 16; ++w) {
-                    const float4 a = red[0][w][l], b = red[1][w][l];
-                    s1[0] += a.x; s1[1] += a.y; s1[2] += a.z; s1[3] += a.w;
-                    s2[0] += b.x; s2[1] += b.y; s2[2] += b.z; s2[3] += b.w;
-                }
+                    for (int j = 0; j < G; ++j) {
+                        ldsm_x4_trans(x_off[j][i] + at, rx[j]);
+                        ldsm_x4(d_off[j][i] + at, rd[j]);
+                    }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {              // dx = r a - r s1 - (x - mu) r r s2
-                    s1[i] *= p.inv_c * r[i];
-                    s2[i] *= p.inv_c * r[i] * r[i];
-                }
-                T* dx = static_cast<T*>(p.dx) + off;
+                    for (int m = 0; m < 4; ++m) {
+                        if (b * 32 + m * 8 < p.C) {
+                            const f32x2 g = *reinterpret_cast<const f32x2*>(gam + b * 32 + m * 8 + 2 * (lane & 3));
 #pragma unroll
-                for (int j = 0; j < NP; ++j) {
-                    const int c = 2 * (k0 + j * 64);
-                    if (c < p.C) {
-                        float x0[4], x1[4];
-                        widen4<T>(*reinterpret_cast<const uint2*>(xs + j * 8192), x0);
-                        widen4<T>(*reinterpret_cast<const uint2*>(xs + j * 8192 + 4096), x1);
-                        const float2 g = *reinterpret_cast<const float2*>(gam + c);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            float d0, d1;
-                            widen2<T>(*reinterpret_cast<const uint32_t*>(ds + chunk_at(4 * l + i, c >> 3, pitch) +
-                                                                         (c & 7) * 2), d0, d1);
-                            x0[i] = fmaf(d0 * g.x, r[i], -fmaf(x0[i] - mu[i], s2[i], s1[i]));
-                            x1[i] = fmaf(d1 * g.y, r[i], -fmaf(x1[i] - mu[i], s2[i], s1[i]));
+                            for (int j = 0; j < G; ++j)
+                                rx[j][m] = narrow_pair<T>(
+                                    fma2(mul2(widen_pair<T>(rd[j][m]), g), both(r[j]),
+                                         fma2(add2(widen_pair<T>(rx[j][m]), both(-mu[j])), n2[j], n1[j])));
                         }
-                        *reinterpret_cast<uint2*>(dx + c * p.pixels) =
-                            make_uint2(pair<T>(x0[0], x0[1]), pair<T>(x0[2], x0[3]));
-                        *reinterpret_cast<uint2*>(dx + (c + 1) * p.pixels) =
-                            make_uint2(pair<T>(x1[0], x1[1]), pair<T>(x1[2], x1[3]));
+                    }
+#pragma unroll
+                    for (int j = 0; j < G; ++j) stsm_x4_trans(x_off[j][i] + at, rx[j]);
+                }
+            }
+            fence_proxy_async_smem();
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                const int n = (unsigned)tile / (unsigned)bx.tpi, px = (tile - n * bx.tpi) * 8 * PG;
+                for (int i = 0; i < bx.xboxes; ++i)
+                    tma_store_3d(&omap, base + at + bx.y_bytes + i * bx.xbox * PG * 16, px, i * bx.xbox, n);
+                bulk_commit_group();
+            }
+        }
+        if (++stage == STAGES) { stage = 0; phase ^= 1; }
+    }
+    if (threadIdx.x == 0) {
+        if (!ok)                                           // copies in flight land before the block leaves
+            for (int i = fetched > STAGES ? fetched - STAGES : 0; i < fetched; ++i)
+                mbar_drain_wait(smem_addr(&full[i % STAGES]), (uint32_t)(i / STAGES) & 1u);
+        bulk_wait_all();
+    }
+    if (!p.want_params) return;
+    // Add the eight pixels of a matrix, then the warps that share a channel block.
+    __syncthreads();
+    float* acc = reinterpret_cast<float*>(smem);           // [2][channels of the blocks]
+    for (int q = 0; q < PG; q += G) {
+        if (q > 0) __syncthreads();
+        if (sh.group == q) {
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                const int b = sh.share + i * S::kShares;
+                if (b < blocks) {
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        float v[4];
+                        unpack2f(dg[i][m], v[0], v[1]);
+                        unpack2f(db[i][m], v[2], v[3]);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+#pragma unroll
+                            for (int o = 4; o < 32; o <<= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+                            const int c = (k >> 1) * blocks * 32 + b * 32 + m * 8 + 2 * (lane & 3) + (k & 1);
+                            if (lane < 4) acc[c] = v[k] + (q ? acc[c] : 0.f);
+                        }
                     }
                 }
             }
         }
-        __syncthreads();                                   // the stage (and red) may be written again
-        if (++stage == STAGES) stage = 0;
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    if (!p.want_params) return;
+    __syncthreads();
     float* out = p.part + (int64_t)blockIdx.x * 2 * p.C;
-#pragma unroll
-    for (int j = 0; j < NP; ++j) {
-        const int c = 2 * (k0 + j * 64);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const float vg = lane_sum(ag[j][e], 8), vb = lane_sum(ab[j][e], 8);
-            if (l == 0 && c < p.C) {
-                out[c + e] = vg;
-                out[p.C + c + e] = vb;
-            }
-        }
+    for (int c = threadIdx.x; c < p.C; c += kThreads16) {
+        out[c] = acc[c];
+        out[p.C + c] = acc[blocks * 32 + c];
     }
 }
 
@@ -716,47 +826,94 @@ cudaError_t bwd_planes(PlaneParams p, int* parts, cudaStream_t st) {
     return launch_after(planes_bwd_kernel<T, PP>, dim3((unsigned)grid), dim3(kBwdThreads), smem, st, p);
 }
 
-// Whether the 16-bit form serves the call: a plane is whole groups of four
-// pixels, rows whole 16-byte vectors, and a thread holds all of its channels.
+// Whether the 16-bit form serves the call: what TMA moves starts and repeats at
+// 16-byte boundaries, and 16 warps hold all channels.
 bool fast16(const layernorm_desc& d, const void* x, const void* dx, const void* rows) {
-    return d.dtype != CONV2D_F32 && d.pixels % 4 == 0 && d.cols % 8 == 0 && d.cols <= 1024 && d.ys % 8 == 0 &&
-           aligned_to(x, 8) && aligned_to(dx, 8) && aligned_to(rows, 16);
+    return d.dtype != CONV2D_F32 && d.pixels % 8 == 0 && d.cols % 8 == 0 && d.cols <= 1024 && d.ys % 8 == 0 &&
+           aligned_to(x, 16) && aligned_to(dx, 16) && aligned_to(rows, 16) && d.ys < (1LL << 38);
 }
 
-template <typename T> cudaError_t fwd_fast(PlaneParams p, cudaStream_t st) {
-    const int64_t tiles = (p.rows + kTile - 1) / kTile;
-    const size_t smem = (size_t)kTile * ((p.C + 63) / 64 * 64) * 2;
-    const dim3 grid((unsigned)tiles);
-    const int pairs = (p.C / 2 + 31) / 32;                 // per thread of 256
-    if (pairs <= 1) return launch_after(planes16_fwd_kernel<T, 1, 256>, grid, dim3(256), smem, st, p);
-    if (pairs <= 2) return launch_after(planes16_fwd_kernel<T, 2, 256>, grid, dim3(256), smem, st, p);
-    if (pairs <= 4) return launch_after(planes16_fwd_kernel<T, 4, 256>, grid, dim3(256), smem, st, p);
-    if (pairs <= 8) return launch_after(planes16_fwd_kernel<T, 8, 256>, grid, dim3(256), smem, st, p);
-    const cudaError_t e = cudaFuncSetAttribute(planes16_fwd_kernel<T, 8, 512>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    return launch_after(planes16_fwd_kernel<T, 8, 512>, grid, dim3(512), smem, st, p);
+typedef CUresult (*PFN_encode_t)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// A 3-D 16-bit tensor (innermost first), boxes of b0 x b1 x 1, zeros outside.
+bool map3(CUtensorMap* m, const void* base, bool bf16, int64_t d0, int64_t d1, int64_t d2, int64_t s1, int64_t s2,
+          int b0, int b1, CUtensorMapSwizzle swizzle) {
+    static PFN_encode_t enc = reinterpret_cast<PFN_encode_t>(driver_entry("cuTensorMapEncodeTiled"));
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)d0, (cuuint64_t)d1, (cuuint64_t)d2};
+    cuuint64_t str[2] = {(cuuint64_t)s1 * 2, (cuuint64_t)s2 * 2};
+    cuuint32_t box[3] = {(cuuint32_t)b0, (cuuint32_t)b1, 1}, es[3] = {1, 1, 1};
+    return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+               const_cast<void*>(base), dims, str, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, int NP> cudaError_t bwd_fast_np(PlaneParams p, int* parts, cudaStream_t st) {
-    p.tiles = (p.rows + kTile - 1) / kTile;
-    const size_t stage = (size_t)NP * 8192 + (size_t)kTile * ((p.C + 63) / 64 * 64) * 2;
-    const size_t smem = (NP == 8 ? 1 : 3) * stage + (size_t)p.C * 4;
-    const cudaError_t e = cudaFuncSetAttribute(planes16_bwd_kernel<T, NP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)smem);
+template <int PG> Boxes boxes_of(PlaneParams& p) {
+    Boxes b;
+    b.tpi = (int)((p.pixels + 8 * PG - 1) / (8 * PG));
+    p.tiles = p.rows / p.pixels * b.tpi;
+    const int c32 = (p.C + 31) / 32 * 32;
+    b.xbox = c32 < 256 ? c32 : 256;
+    b.xboxes = (p.C + b.xbox - 1) / b.xbox;
+    b.yboxes = (p.C + 63) / 64;
+    b.x_bytes = (b.xboxes * b.xbox * PG * 16 + 1023) / 1024 * 1024;
+    b.y_bytes = b.yboxes * PG * 1024;
+    return b;
+}
+template <int PG> bool x_map(CUtensorMap* m, const PlaneParams& p, const Boxes& b, const void* x, bool bf16) {
+    return map3(m, x, bf16, p.pixels, p.C, p.rows / p.pixels, p.pixels, p.pixels * p.C, 8 * PG, b.xbox,
+                PG == 4 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B);
+}
+template <int PG> bool y_map(CUtensorMap* m, const PlaneParams& p, const void* y, bool bf16) {
+    return map3(m, y, bf16, p.C, p.pixels, p.rows / p.pixels, p.ys, p.ys * p.pixels, 64, 8 * PG,
+                CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <typename T, int PG, int G, int NB> cudaError_t fwd_fast(PlaneParams p, cudaStream_t st) {
+    const Boxes b = boxes_of<PG>(p);
+    CUtensorMap xm, ym;
+    if (!x_map<PG>(&xm, p, b, p.x, is_bf16<T>) || !y_map<PG>(&ym, p, p.y, is_bf16<T>)) return cudaErrorInvalidValue;
+    const int smem = 1024 + 2 * b.x_bytes + b.y_bytes + 2 * p.C * 4;
+    const cudaError_t e =
+        cudaFuncSetAttribute(planes16_fwd_kernel<T, PG, G, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    int64_t grid = (int64_t)device_sm_count() * (NP <= 2 ? 2 : 1);
+    int64_t grid = 2 * device_sm_count();
+    if (grid > p.tiles) grid = p.tiles;
+    return launch_after(planes16_fwd_kernel<T, PG, G, NB>, dim3((unsigned)grid), dim3(kThreads16), smem, st, xm, ym, p,
+                        b);
+}
+
+template <typename T, int PG, int G, int NB> cudaError_t bwd_fast(PlaneParams p, int* parts, cudaStream_t st) {
+    const Boxes b = boxes_of<PG>(p);
+    CUtensorMap xm, dm, om;
+    if (!x_map<PG>(&xm, p, b, p.x, is_bf16<T>) || !y_map<PG>(&dm, p, p.dy, is_bf16<T>) ||
+        !x_map<PG>(&om, p, b, p.dx ? p.dx : p.x, is_bf16<T>))
+        return cudaErrorInvalidValue;
+    const int smem = 1024 + 3 * (b.x_bytes + b.y_bytes) + p.C * 4;
+    const cudaError_t e =
+        cudaFuncSetAttribute(planes16_bwd_kernel<T, PG, G, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    int64_t grid = device_sm_count() * (NB == 1 ? 2 : 1);
     if (grid > p.tiles) grid = p.tiles;
     *parts = (int)grid;
-    return launch_after(planes16_bwd_kernel<T, NP>, dim3((unsigned)grid), dim3(512), smem, st, p);
+    return launch_after(planes16_bwd_kernel<T, PG, G, NB>, dim3((unsigned)grid), dim3(kThreads16), smem, st, xm, dm, om,
+                        p, b);
 }
 
-template <typename T> cudaError_t bwd_fast(const PlaneParams& p, int* parts, cudaStream_t st) {
-    const int pairs = (p.C / 2 + 63) / 64;                 // per thread of 512
-    if (pairs <= 1) return bwd_fast_np<T, 1>(p, parts, st);
-    if (pairs <= 2) return bwd_fast_np<T, 2>(p, parts, st);
-    if (pairs <= 4) return bwd_fast_np<T, 4>(p, parts, st);
-    return bwd_fast_np<T, 8>(p, parts, st);
+// Tiles of 32 pixels up to 512 channels (64-byte runs of a plane), 16 beyond.
+template <typename T> cudaError_t fwd_16(const PlaneParams& p, cudaStream_t st) {
+    if (p.C <= 128) return fwd_fast<T, 4, 1, 1>(p, st);
+    if (p.C <= 256) return fwd_fast<T, 4, 2, 1>(p, st);
+    if (p.C <= 512) return fwd_fast<T, 4, 2, 2>(p, st);
+    return fwd_fast<T, 2, 2, 2>(p, st);
+}
+template <typename T> cudaError_t bwd_16(const PlaneParams& p, int* parts, cudaStream_t st) {
+    if (p.C <= 128) return bwd_fast<T, 4, 1, 1>(p, parts, st);
+    if (p.C <= 256) return bwd_fast<T, 4, 2, 1>(p, parts, st);
+    if (p.C <= 512) return bwd_fast<T, 4, 2, 2>(p, parts, st);
+    return bwd_fast<T, 2, 2, 2>(p, parts, st);
 }
 
 PlaneParams params_of(const layernorm_desc& d) {
@@ -778,12 +935,15 @@ bool pair_channels(const layernorm_desc& d, const void* r) {
 
 }  // namespace
 
+cudaError_t status_read_clear_lp(cudaStream_t st, uint32_t* out) { return status_read_clear(st, out); }
+cudaError_t wait_limit_set_lp(cudaStream_t st, uint64_t ns) { return wait_limit_set(st, ns); }
+
 cudaError_t launch_layernorm_planes_fwd(const layernorm_desc& d, const void* x, const void* gamma, const void* beta,
                                         void* y, float* mean, float* rstd, cudaStream_t st) {
     PlaneParams p = params_of(d);
     p.x = x; p.gamma = gamma; p.beta = beta; p.y = y; p.mean = mean; p.rstd = rstd;
     if (fast16(d, x, nullptr, y))
-        return d.dtype == CONV2D_F16 ? fwd_fast<__half>(p, st) : fwd_fast<__nv_bfloat16>(p, st);
+        return d.dtype == CONV2D_F16 ? fwd_16<__half>(p, st) : fwd_16<__nv_bfloat16>(p, st);
     p.pair_c = pair_channels(d, y);
     const bool pair = pair_pixels(d, x, x);
     switch (d.dtype) {
@@ -809,7 +969,7 @@ cudaError_t launch_layernorm_planes_bwd(const layernorm_desc& d, const void* dy,
     int parts = 0;
     cudaError_t e;
     if (fast16(d, x, dx, dy)) {
-        e = d.dtype == CONV2D_F16 ? bwd_fast<__half>(p, &parts, st) : bwd_fast<__nv_bfloat16>(p, &parts, st);
+        e = d.dtype == CONV2D_F16 ? bwd_16<__half>(p, &parts, st) : bwd_16<__nv_bfloat16>(p, &parts, st);
     } else switch (d.dtype) {
         case CONV2D_F32: e = bwd_planes<float, 1>(p, &parts, st); break;
         case CONV2D_F16: e = pair ? bwd_planes<__half, 2>(p, &parts, st) : bwd_planes<__half, 1>(p, &parts, st); break;

@@ -26,8 +26,8 @@ struct dropout_desc {
 
 namespace conv2d_gb300 {
 
-// Tile width and K splits of one product (linear_ce.cu, plan_gemm).
-struct GemmPlan { int BN, splits; };
+// Tile width, CTA pairs and K splits of a launch's products (linear_ce.cu, plan_gemm).
+struct LaunchPlan { int BN; bool pair; int splits[2]; };
 
 // Sizes and workspace offsets of one pass of the linear cross entropy.
 struct CePlan {
@@ -35,8 +35,8 @@ struct CePlan {
     int parts, pairs;              // bf16 parts per value (1, or 3 for fp32) and their products (1 or 6)
     int64_t dp;                    // packed row pitch of one part
     int64_t piece, pieces;         // vocabulary rows per piece
-    GemmPlan z, dh, dw;
-    size_t part, z_target, row_loss, coef, common, hp, wp, dz, acc, sums, total;
+    LaunchPlan z, out;             // the logits; dh and dw together
+    size_t part, z_target, row_loss, coef, common, hp, wp, dz, acc, sums_h, sums_w, total;
 };
 
 }  // namespace conv2d_gb300

@@ -31,6 +31,11 @@
 // partial sums in registers, rounded to nearest, while the next ones are
 // computed (PROMOTE).
 //
+// Large products run on CTA pairs (PAIR): the tile is 256 rows by BN columns,
+// each CTA keeps half of the rows of A and half of the columns of B in its
+// shared memory and the accumulators of its rows, and one MMA reads both, so a
+// CTA's copies and shared-memory reads per product are a third less.
+//
 // Few rows by many columns (or a long K by a small output) is split over K and
 // joined by a second kernel in a fixed order, so that all SMs have work.
 #include <cuda.h>
@@ -51,7 +56,9 @@ namespace {
 constexpr int kBM = 128, kBK = 64;            // MMA rows; K elements per stage (128 bytes)
 constexpr int kABytes = kBM * kBK * 2;
 constexpr int kMaxRing = 8;
-constexpr int kEpiWarps = 8, kThreads = 32 * (2 + kEpiWarps);
+// Epilogue warps.  PROMOTE: sixteen, so that a segment's sums are out of tensor
+// memory well within the next segment's MMAs (eight took 2400 cycles for 2048).
+__host__ __device__ constexpr int epi_warps(bool promote) { return promote ? 16 : 8; }
 constexpr int kStageWarpBytes = 32 * 17 * 4;  // epilogue staging per warp: 32 rows of 17 words
 constexpr int kSmemMost = 227 * 1024;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -60,19 +67,18 @@ enum Epilogue { EPI_LSE = 0, EPI_DZ = 1, EPI_OUT = 2 };
 
 struct GemmParams {
     int M, N;                // valid extents of C
-    int BN, n_m, n_n;        // tile width, tiles
+    int a_mn;                // A is MN-major
+    int n_m, n_n;            // tiles
     int group;               // row tiles that share each column tile before the next one is taken
     int nk, pairs;           // K chunks of one product of parts, and such products (1 or 6)
     int a_part, b_part;      // column offset from one part to the next
     int splits;
-    int stages;
-    int seg;                 // PROMOTE: chunks per accumulation in tensor memory
     // EPI_LSE and EPI_DZ
     int col0;                // first vocabulary row of this piece
     int vocab;
     int64_t ignore;
     const int64_t* target;
-    float2* lse_part;        // [(column tile, half)][M]
+    float2* lse_part;        // [(column tile, column group)][M]
     float* z_target;         // [M]
     const float *lse, *coef; // [M]
     void* dz;                // [M][parts * dz_part]
@@ -86,6 +92,17 @@ struct GemmParams {
     float* acc;              // [M][N]
     const float* scale;      // null: 1
 };
+
+// A launch: one product, or two that share the machine (dh and dw: the items of
+// the first, longer ones come first, those of the second fill its last wave).
+struct GemmJobs {
+    GemmParams job[2];
+    int items0, items;       // items of the first product, and of both
+    int BN;                  // tile width
+    int stages, seg;         // ring depth; PROMOTE: chunks per accumulation in tensor memory
+    int epi_bytes;           // epilogue staging in shared memory (0: none needed)
+};
+struct GemmMaps { CUtensorMap a[2], b[2]; };
 
 __device__ __constant__ int kPartA[6] = {2, 0, 1, 1, 0, 0};
 __device__ __constant__ int kPartB[6] = {0, 2, 1, 0, 1, 0};
@@ -214,14 +231,19 @@ __device__ __forceinline__ void store_out(const GemmParams& p, float (&v)[32], i
     }
 }
 
-template <bool BF16, int EPI, bool A_MN, bool B_MN, bool PROMOTE>
-__global__ void __launch_bounds__(kThreads, 1)
-ce_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap, const GemmParams p) {
+template <bool BF16, int EPI, bool PROMOTE, bool PAIR>
+__global__ void __launch_bounds__(32 * (2 + epi_warps(PROMOTE)), 1)
+ce_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ GemmJobs jobs) {
+    constexpr bool B_MN = EPI == EPI_OUT;
+    constexpr int kEpiWarps = epi_warps(PROMOTE), kGroups = kEpiWarps / 4;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-    const int stage_bytes = kABytes + p.BN * kBK * 2;
-    uint32_t* epi_stage = reinterpret_cast<uint32_t*>(smem + p.stages * stage_bytes);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + p.stages * stage_bytes + kEpiWarps * kStageWarpBytes);
+    constexpr int kTileM = PAIR ? 2 * kBM : kBM, kCtas = PAIR ? 2 : 1;
+    const int rank = PAIR ? (int)cluster_rank() : 0;       // 0 issues the pair's MMAs
+    const int bn = PAIR ? jobs.BN / 2 : jobs.BN;           // columns of B in this CTA
+    const int stages = jobs.stages, stage_bytes = kABytes + bn * kBK * 2;
+    uint32_t* epi_stage = reinterpret_cast<uint32_t*>(smem + stages * stage_bytes);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + stages * stage_bytes + jobs.epi_bytes);
     // full[stages], empty[stages], accumulator full[2], empty[2], drain
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kMaxRing + 5);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -233,26 +255,37 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (warp == 0 && lane == 0) {
-        for (int i = 0; i < p.stages; ++i) { mbar_init(full_bar(i), 1); mbar_init(empty_bar(i), 1); }
-        for (int a = 0; a < 2; ++a) { mbar_init(accf_bar(a), 1); mbar_init(acce_bar(a), kEpiWarps); }
+        for (int i = 0; i < stages; ++i) { mbar_init(full_bar(i), 1); mbar_init(empty_bar(i), 1); }
+        for (int a = 0; a < 2; ++a) { mbar_init(accf_bar(a), 1); mbar_init(acce_bar(a), kCtas * kEpiWarps); }
         mbar_init(drain_bar, 1);
         *abort_flag = 0;
         mbar_fence_init();
-        tma_prefetch_desc(&amap);
-        tma_prefetch_desc(&bmap);
+        tma_prefetch_desc(&maps.a[0]);
+        tma_prefetch_desc(&maps.b[0]);
     }
     if (warp == 1) {
-        tmem_alloc(smem_addr(tmem_slot), 512);
-        tmem_relinquish();
+        if constexpr (PAIR) {
+            tmem_alloc_pair(smem_addr(tmem_slot), 512);
+        } else {
+            tmem_alloc(smem_addr(tmem_slot), 512);
+            tmem_relinquish();
+        }
     }
     tc_fence_before();
     __syncthreads();
+    if constexpr (PAIR) cluster_sync();                    // the other CTA's barriers are ready
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     pdl_wait();
     pdl_launch_dependents();
 
-    const int items = p.n_m * p.n_n * p.splits, chunks = p.nk * p.pairs;
+    // Items are dealt out in turn; every role walks them alike.
+    const int first = blockIdx.x / kCtas, step = gridDim.x / kCtas;
+    auto job_of = [&](int& i) {                            // product of item i, which becomes its number there
+        if (EPI != EPI_OUT || i < jobs.items0) return 0;
+        i -= jobs.items0;
+        return 1;
+    };
     if (warp == 0) {
         // ------------------------------------------------------------ producer
         if (lane == 0) {
@@ -260,58 +293,86 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
             int stage = 0;
             uint32_t phase = 0;
             long long issued = 0;
-            for (int i = blockIdx.x; i < items && ok; i += gridDim.x) {
+            for (int n_item = first; n_item < jobs.items && ok; n_item += step) {
+                int i = n_item;
+                const int j = job_of(i);
+                const GemmParams& p = jobs.job[j];
+                const CUtensorMap *amap = &maps.a[j], *bmap = &maps.b[j];
                 const Item it = item_of(p, i);
+                const int chunks = p.nk * p.pairs;
                 const int k0 = (int)((long long)chunks * it.split / p.splits);
                 const int k1 = (int)((long long)chunks * (it.split + 1) / p.splits);
-                const int m0 = it.m * kBM, n0 = it.n * p.BN;
-                int pair = k0 / p.nk, k = k0 - pair * p.nk;
+                const int m0 = it.m * kTileM + rank * kBM, n0 = it.n * jobs.BN + rank * bn;
+                const int nk = p.nk, a_mn = p.a_mn, pairs = p.pairs;
+                int pair = k0 / nk, k = k0 - pair * nk;
                 for (int q = k0; q < k1; ++q) {
                     if (!mbar_wait(empty_bar(stage), phase ^ 1, abort_flag)) { ok = false; break; }
-                    mbar_arrive_expect_tx(full_bar(stage), (uint32_t)stage_bytes);
+                    // A pair's copies all count on the issuing CTA's barrier.
+                    if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), (uint32_t)(kCtas * stage_bytes));
+                    const uint32_t bar = PAIR ? cluster_addr(full_bar(stage), 0) : full_bar(stage);
                     const uint32_t a_dst = smem_addr(smem + stage * stage_bytes), b_dst = a_dst + kABytes;
-                    const int ao = p.pairs > 1 ? kPartA[pair] * p.a_part : 0;
-                    const int bo = p.pairs > 1 ? kPartB[pair] * p.b_part : 0;
-                    if constexpr (A_MN) {
+                    const int ao = pairs > 1 ? kPartA[pair] * p.a_part : 0;
+                    const int bo = pairs > 1 ? kPartB[pair] * p.b_part : 0;
+                    auto load = [&](uint32_t dst, const CUtensorMap* map, int c0, int c1) {
+                        if constexpr (PAIR) tma_load_2d_pair(dst, map, bar, c0, c1);
+                        else                tma_load_2d(dst, map, bar, c0, c1);
+                    };
+                    if (EPI == EPI_OUT && a_mn) {
 #pragma unroll
-                        for (int j = 0; j < kBM / 64; ++j)
-                            tma_load_2d(a_dst + j * 8192, &amap, full_bar(stage), ao + m0 + 64 * j, k * kBK);
+                        for (int l = 0; l < kBM / 64; ++l) load(a_dst + l * 8192, amap, ao + m0 + 64 * l, k * kBK);
                     } else {
-                        tma_load_2d(a_dst, &amap, full_bar(stage), ao + k * kBK, m0);
+                        load(a_dst, amap, ao + k * kBK, m0);
                     }
                     if constexpr (B_MN) {
-                        for (int j = 0; j < p.BN / 64; ++j)
-                            tma_load_2d(b_dst + j * 8192, &bmap, full_bar(stage), bo + n0 + 64 * j, k * kBK);
+                        for (int l = 0; l < bn / 64; ++l) load(b_dst + l * 8192, bmap, bo + n0 + 64 * l, k * kBK);
                     } else {
-                        tma_load_2d(b_dst, &bmap, full_bar(stage), bo + k * kBK, n0);
+                        load(b_dst, bmap, bo + k * kBK, n0);
                     }
                     ++issued;
-                    if (++stage == p.stages) { stage = 0; phase ^= 1; }
-                    if (++k == p.nk) { k = 0; ++pair; }
+                    if (++stage == stages) { stage = 0; phase ^= 1; }
+                    if (++k == nk) { k = 0; ++pair; }
                 }
             }
             if (!ok) {
                 // Let every copy already issued land before the CTA can exit.
-                for (int i = 0; i < p.stages && i < issued; ++i) {
-                    if (--stage < 0) { stage = p.stages - 1; phase ^= 1; }
-                    mbar_drain_wait(full_bar(stage), phase);
+                // (A pair's first CTA waits for both; the other one meets it at
+                // the end.  If the other has given up too, one limit covers all.)
+                for (int i = 0; i < stages && i < issued && rank == 0; ++i) {
+                    if (--stage < 0) { stage = stages - 1; phase ^= 1; }
+                    if (!mbar_drain_wait(full_bar(stage), phase)) break;
+                }
+            } else if (PAIR) {
+                // Every commit's arrival is in before either CTA can exit.
+                for (int i = 0; i < stages; ++i) {
+                    if (!mbar_wait(empty_bar(stage), phase ^ 1, abort_flag)) break;
+                    if (++stage == stages) { stage = 0; phase ^= 1; }
                 }
             }
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            const uint32_t idesc =
-                umma_idesc_f16(BF16, kBM, p.BN) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
+        if (lane == 0 && rank == 0) {
+            auto commit = [&](uint32_t bar) {
+                if constexpr (PAIR) umma_commit_pair(bar);
+                else                umma_commit(bar);
+            };
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
             bool ok = true, issued_any = false;
-            for (int i = blockIdx.x; i < items && ok; i += gridDim.x) {
-                const int split = i / (p.n_m * p.n_n);
+            for (int n_item = first; n_item < jobs.items && ok; n_item += step) {
+                int i = n_item;
+                const GemmParams& p = jobs.job[job_of(i)];
+                const int split = i / (p.n_m * p.n_n), chunks = p.nk * p.pairs;
                 const int k0 = (int)((long long)chunks * split / p.splits);
                 const int k1 = (int)((long long)chunks * (split + 1) / p.splits);
+                const bool a_mn = EPI == EPI_OUT && p.a_mn;
+                const uint32_t idesc =
+                    umma_idesc_f16(BF16, kTileM, jobs.BN) | (a_mn ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
+                // A K step of 16 elements: 32 bytes along a K-major row, 16
+                // rows of 128 bytes of an MN-major block.
+                const uint32_t a_step = a_mn ? 128 : 2, b_step = B_MN ? 128 : 2;
                 for (int q0 = k0; q0 < k1 && ok;) {
-                    const int q1 = PROMOTE ? min(k1, q0 + p.seg) : k1;
+                    const int q1 = PROMOTE ? min(k1, q0 + jobs.seg) : k1;
                     if (!mbar_wait(acce_bar(acc), acc_phase ^ 1, abort_flag)) { ok = false; break; }
                     tc_fence_after();
                     const uint32_t d_tmem = tmem_base + (uint32_t)(acc * 256);
@@ -319,41 +380,49 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
                         if (!mbar_wait(full_bar(stage), phase, abort_flag)) { ok = false; break; }
                         tc_fence_after();
                         const uint32_t a_addr = smem_addr(smem + stage * stage_bytes), b_addr = a_addr + kABytes;
-                        // A K step of 16 elements: 32 bytes along a K-major row,
-                        // 16 rows of 128 bytes of an MN-major block.
-                        const uint64_t a_desc = A_MN ? sw128_mnmajor_desc(a_addr, 8192u) : sw128_kmajor_desc(a_addr);
+                        const uint64_t a_desc = a_mn ? sw128_mnmajor_desc(a_addr, 8192u) : sw128_kmajor_desc(a_addr);
                         const uint64_t b_desc = B_MN ? sw128_mnmajor_desc(b_addr, 8192u) : sw128_kmajor_desc(b_addr);
 #pragma unroll
-                        for (int k = 0; k < kBK / 16; ++k)
-                            umma_f16(d_tmem, a_desc + (uint64_t)(k * (A_MN ? 128 : 2)),
-                                     b_desc + (uint64_t)(k * (B_MN ? 128 : 2)), idesc, (q > q0 || k > 0) ? 1u : 0u);
+                        for (int k = 0; k < kBK / 16; ++k) {
+                            const uint64_t ad = a_desc + (uint64_t)(k * a_step), bd = b_desc + (uint64_t)(k * b_step);
+                            const uint32_t add = (q > q0 || k > 0) ? 1u : 0u;
+                            if constexpr (PAIR) umma_f16_pair(d_tmem, ad, bd, idesc, add);
+                            else                umma_f16(d_tmem, ad, bd, idesc, add);
+                        }
                         issued_any = true;
-                        umma_commit(empty_bar(stage));
-                        if (++stage == p.stages) { stage = 0; phase ^= 1; }
+                        commit(empty_bar(stage));
+                        if (++stage == stages) { stage = 0; phase ^= 1; }
                     }
                     if (!ok) break;
-                    umma_commit(accf_bar(acc));
+                    commit(accf_bar(acc));
                     if (++acc == 2) { acc = 0; acc_phase ^= 1; }
                     q0 = q1;
                 }
             }
             if (!ok && issued_any) {
-                umma_commit(drain_bar);
+                commit(drain_bar);
                 mbar_drain_wait(drain_bar, 0);
             }
         }
     } else {
         // ------------------------------------------------------------ epilogue
-        // Two groups of four warps share an accumulator's columns by halves;
-        // warp q (mod 4) reads TMEM lanes 32 (q mod 4)..: one output row a lane.
-        const int ew = warp - 2, half = ew >> 2, quarter = warp & 3;
+        // Groups of four warps share an accumulator's columns; warp q (mod 4)
+        // reads TMEM lanes 32 (q mod 4)..: one output row a lane.
+        const int ew = warp - 2, group = ew >> 2, quarter = warp & 3;
         uint32_t* stage = epi_stage + ew * (kStageWarpBytes / 4);
-        const int nch = p.BN / 32, c_lo = half ? (nch + 1) / 2 : 0, c_hi = half ? nch : (nch + 1) / 2;
+        const int nch = jobs.BN / 32, c_lo = nch * group / kGroups, c_hi = nch * (group + 1) / kGroups;
+        // An emptied accumulator is reported to the CTA that issues the MMAs.
+        auto emptied = [&](int a) {
+            if constexpr (PAIR) mbar_arrive_cluster(cluster_addr(acce_bar(a), 0));
+            else                mbar_arrive(acce_bar(a));
+        };
         int acc = 0;
         uint32_t acc_phase = 0;
-        for (int i = blockIdx.x; i < items; i += gridDim.x) {
+        for (int n_item = first; n_item < jobs.items; n_item += step) {
+            int i = n_item;
+            const GemmParams& p = jobs.job[job_of(i)];
             const Item it = item_of(p, i);
-            const int row0 = it.m * kBM + quarter * 32, row = row0 + lane, n0 = it.n * p.BN;
+            const int row0 = it.m * kTileM + rank * kBM + quarter * 32, row = row0 + lane, n0 = it.n * jobs.BN;
             const bool live = row < p.M;
             float m_run = -INFINITY, s_run = 0.f;              // EPI_LSE
             float lse = 0.f, coef = 0.f;                       // EPI_DZ
@@ -369,9 +438,10 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
                 }
             }
             // PROMOTE: this warp's share of the tile's sums, in registers.
-            constexpr int kKept = PROMOTE ? 4 : 1;             // 32-column chunks per warp at most
+            constexpr int kKept = PROMOTE ? 8 / kGroups : 1;   // 32-column chunks per warp at most
             float sum[kKept][32];
             if constexpr (PROMOTE) {
+                const int chunks = p.nk * p.pairs;
                 const int k0 = (int)((long long)chunks * it.split / p.splits);
                 const int k1 = (int)((long long)chunks * (it.split + 1) / p.splits);
 #pragma unroll
@@ -379,7 +449,7 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
 #pragma unroll
                     for (int j = 0; j < 32; ++j) sum[c][j] = 0.f;
                 bool got = true;
-                for (int q0 = k0; q0 < k1; q0 += p.seg) {
+                for (int q0 = k0; q0 < k1; q0 += jobs.seg) {
                     got = __all_sync(0xffffffffu, mbar_wait(accf_bar(acc), acc_phase, abort_flag));
                     if (!got) break;
                     tc_fence_after();
@@ -388,7 +458,7 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
                     for (int c = 0; c < kKept; ++c) {
                         if (c_lo + c < c_hi) {
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {      // 16 at a time: 128 sums leave few registers
+                            for (int e = 0; e < 2; ++e) {      // 16 at a time: the sums leave few registers
                                 uint32_t u[16];
                                 tmem_ld_32x32b_x16(t_row + (c_lo + c) * 32 + e * 16, u);
                                 tmem_ld_wait();
@@ -399,7 +469,7 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
                     }
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(acce_bar(acc));
+                    if (lane == 0) emptied(acc);
                     if (++acc == 2) { acc = 0; acc_phase ^= 1; }
                 }
                 if (!got) break;
@@ -487,22 +557,26 @@ ce_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(acce_bar(acc));
+                if (lane == 0) emptied(acc);
                 if (++acc == 2) { acc = 0; acc_phase ^= 1; }
             }
             if constexpr (EPI == EPI_LSE) {
-                if (live && c_lo < c_hi)
-                    p.lse_part[(int64_t)(2 * it.n + half) * p.M + row] = make_float2(m_run, s_run);
+                if (live) p.lse_part[(int64_t)(kGroups * it.n + group) * p.M + row] = make_float2(m_run, s_run);
             }
         }
     }
 
     tc_fence_before();
     __syncthreads();
+    if constexpr (PAIR) {                                  // both CTAs are done with each other's memory
+        __syncwarp();
+        cluster_sync();
+    }
     if (warp == 1) {
         __syncwarp();
         tc_fence_after();
-        tmem_dealloc(tmem_base, 512);
+        if constexpr (PAIR) tmem_dealloc_pair(tmem_base, 512);
+        else                tmem_dealloc(tmem_base, 512);
     }
 }
 
@@ -712,34 +786,65 @@ bool make_map(CUtensorMap* map, const void* base, bool bf16, int64_t rows, int64
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// (max, sum) pairs per column tile: one per group of the sixteen epilogue warps.
+constexpr int kPartsPerTile = epi_warps(true) / 4;
 constexpr int64_t kMostPiece = 1LL << 28;      // three parts of a piece keep 32-bit column numbers
 
 
-// Tile width and K splits by an estimate in SM cycles.  An item (one tile of
-// one split) takes its MMAs (2 BN cycles per 64-wide chunk), a fixed cost per
-// chunk (barriers; more of it shows with narrow tiles) and a fixed cost per
-// item (pipeline fill, the last epilogue); items run in waves over the SMs;
-// splits add the write and read of their fp32 sums and one launch.
-GemmPlan plan_gemm(int64_t M, int64_t N, int64_t chunks, int step, bool may_split) {
-    const int sms = device_sm_count();
-    GemmPlan best{256, 1};
+// CTA pairs that run at once (SMs pair up within their cluster hardware).
+int pair_count();
+
+// One product of a launch, for the estimate.
+struct Product { int64_t M, N, chunks; bool may_split; };
+
+// Tile width, CTA pairs and K splits of a launch's products by an estimate in SM
+// cycles.  A 64-wide chunk takes its MMAs (2 BN cycles) or its operands' way
+// from the L2 (measured 75 bytes a cycle and SM: it is what holds single CTAs
+// at 78 % of the MMA rate, and any tile narrower than 256), and a fixed cost;
+// an item (one tile of one split) adds pipeline fill and its last epilogue;
+// items run in turn over the SMs or pairs, the first product's before the
+// second's; splits add the write and read of their fp32 sums and one launch.
+LaunchPlan plan_gemm(const Product* pr, int n, int step) {
+    LaunchPlan best{256, false, {1, 1}};
     double best_t = -1;
-    for (int bn = 256; bn >= 64; bn -= step) {
-        if (bn > 64 && bn - step >= N) continue;             // wider than the output needs
-        const int64_t tiles = ceil_div(M, kBM) * ceil_div(N, bn);
-        for (int s = 1; s <= 64 && s <= chunks; s = s < 4 ? s + 1 : s + s / 2) {
-            if (s > 1 && !may_split) break;
-            const double waves = (double)ceil_div(tiles * s, sms);
-            double t = waves * ((double)ceil_div(chunks, s) * (2.0 * bn + 64.0) + 3000.0);
-            if (s > 1) t += 4000.0 + (double)s * M * N * 8.0 / 3500.0;
-            if (best_t < 0 || t < best_t * 0.999) { best_t = t; best = GemmPlan{bn, s}; }
+    for (int pair = 0; pair < 2; ++pair) {
+        if (pair && pr[0].M <= kBM && (n == 1 || pr[1].M <= kBM)) break;
+        const int units = pair ? pair_count() : device_sm_count(), rows = pair ? 2 * kBM : kBM;
+        const int down = pair && step == 64 ? 128 : step;    // half a tile is whole 64-wide boxes
+        for (int bn = 256; bn >= (pair ? 128 : 64); bn -= down) {
+            if (bn - down >= pr[0].N && bn - down >= (pair ? 128 : 64)) continue;      // wider than the output needs
+            const double bytes = kABytes + (pair ? bn / 2 : bn) * kBK * 2;
+            const double chunk = (2.0 * bn > bytes / 75.0 ? 2.0 * bn : bytes / 75.0) + 24.0;
+            for (int s0 = 1; s0 <= 64; s0 = s0 < 4 ? s0 + 1 : s0 + s0 / 2) {
+                if (s0 > 1 && (!pr[0].may_split || s0 > pr[0].chunks)) break;
+                for (int s1 = 1; s1 <= 64; s1 = s1 < 4 ? s1 + 1 : s1 + s1 / 2) {
+                    if (s1 > 1 && (n == 1 || !pr[1].may_split || s1 > pr[1].chunks)) break;
+                    const int s[2] = {s0, s1};
+                    int64_t items[2] = {0, 0};
+                    double each[2] = {0, 0}, t = 0;
+                    for (int j = 0; j < n; ++j) {
+                        items[j] = ceil_div(pr[j].M, rows) * ceil_div(pr[j].N, bn) * s[j];
+                        each[j] = (double)ceil_div(pr[j].chunks, s[j]) * chunk + 3000.0;
+                        if (s[j] > 1) t += 4000.0 + (double)s[j] * pr[j].M * pr[j].N * 8.0 / 3500.0;
+                    }
+                    const int64_t turns = ceil_div(items[0] + items[1], units), turns0 = ceil_div(items[0], units);
+                    t += turns0 * each[0] + (turns - turns0) * each[1];
+                    // (A unit with a turn less of the first product may be the longest.)
+                    const double other = (turns0 - 1) * each[0] + (turns - turns0 + 1) * each[1];
+                    if (n > 1 && items[0] % units && other > turns0 * each[0] + (turns - turns0) * each[1])
+                        t += other - (turns0 * each[0] + (turns - turns0) * each[1]);
+                    if (best_t < 0 || t < best_t * 0.999) {
+                        best_t = t;
+                        best = LaunchPlan{bn, pair != 0, {s0, s1}};
+                    }
+                }
+            }
         }
     }
     return best;
 }
 
-// Chunks per accumulation: 256 K elements, 16 steps.  The epilogue's additions
-// (32 columns in about 100 cycles a warp) stay under those chunks' MMAs.
+// Chunks per accumulation: 256 K elements, 16 steps of the tensor core.
 constexpr int kSegment = 4;
 
 // Lift a kernel's shared-memory limit, once per device and kernel.
@@ -755,30 +860,94 @@ bool allow_smem(const void* kern) {
     return true;
 }
 
-template <int EPI, bool A_MN, bool B_MN>
-conv2d_status launch_gemm(bool bf16, const CUtensorMap& a, const CUtensorMap& b, GemmParams p, cudaStream_t st) {
+constexpr int kFixedSmem = 1024 + (2 * kMaxRing + 5) * 8 + 16;
+
+cudaError_t launch_clusters(const void* kern, int grid, int threads, int ctas, int smem, cudaStream_t st, void** args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)ctas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = ctas > 1 ? 2 : 1;
+    return cudaLaunchKernelExC(&cfg, kern, args);
+}
+
+int pair_count() {
+    static int cached[64] = {0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return device_sm_count() / 2;
+    if (dev >= 0 && dev < 64 && cached[dev]) return cached[dev];
+    const void* kern = reinterpret_cast<const void*>(&ce_gemm_kernel<true, EPI_OUT, false, true>);
+    int n = 0;
+    if (allow_smem(kern)) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(device_sm_count() / 2 * 2));
+        cfg.blockDim = dim3(32 * (2 + epi_warps(false)));
+        cfg.dynamicSmemBytes = kSmemMost;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) n = 0;
+    }
+    (void)cudaGetLastError();                              // without a GPU: the default below
+    if (n < 1) n = device_sm_count() / 2;
+    if (dev >= 0 && dev < 64) cached[dev] = n;
+    return n;
+}
+
+template <int EPI, bool PAIR> const void* gemm_kernel(bool bf16, bool f32) {
     // fp32 operands (six products) are bf16 parts; their results stay in fp32.
-    auto kern = p.pairs > 1 ? ce_gemm_kernel<true, EPI, A_MN, B_MN, true>
-                : bf16      ? ce_gemm_kernel<true, EPI, A_MN, B_MN, EPI == EPI_LSE>
-                            : ce_gemm_kernel<false, EPI, A_MN, B_MN, EPI == EPI_LSE>;
-    p.seg = kSegment;
-    const int stage_bytes = kABytes + p.BN * kBK * 2;
-    const int fixed = 1024 + kEpiWarps * kStageWarpBytes + (2 * kMaxRing + 5) * 8 + 16;
-    p.stages = (kSmemMost - fixed) / stage_bytes;
-    if (p.stages > kMaxRing) p.stages = kMaxRing;
-    const int smem = fixed + p.stages * stage_bytes;
-    if (!allow_smem(reinterpret_cast<const void*>(kern))) return CONV2D_ERR_CUDA;
-    p.n_m = (int)ceil_div(p.M, kBM);
-    p.n_n = (int)ceil_div(p.N, p.BN);
-    const int64_t items = (int64_t)p.n_m * p.n_n * p.splits;
-    const int sms = device_sm_count();
-    const int grid = items < sms ? (int)items : sms;
-    // Row tiles whose A (read again for every column tile) stays in the L2 beside the streams.
-    const int64_t a_tile = (int64_t)kBM * p.nk * kBK * 2 * (p.pairs > 1 ? 3 : 1);
-    int64_t g = (24 << 20) / a_tile;
-    p.group = (int)(g < 1 ? 1 : (g > p.n_m ? p.n_m : g));
-    return launch_after(kern, dim3(grid), dim3(kThreads), smem, st, a, b, p) == cudaSuccess ? CONV2D_OK
-                                                                                            : CONV2D_ERR_CUDA;
+    return f32    ? reinterpret_cast<const void*>(&ce_gemm_kernel<true, EPI, true, PAIR>)
+           : bf16 ? reinterpret_cast<const void*>(&ce_gemm_kernel<true, EPI, EPI == EPI_LSE, PAIR>)
+                  : reinterpret_cast<const void*>(&ce_gemm_kernel<false, EPI, EPI == EPI_LSE, PAIR>);
+}
+
+template <int EPI>
+conv2d_status launch_gemm(bool bf16, const LaunchPlan& g, const GemmMaps& maps, GemmJobs& jobs, int n, cudaStream_t st) {
+    const bool f32 = jobs.job[0].pairs > 1, promote = f32 || EPI == EPI_LSE;
+    const void* kern = g.pair ? gemm_kernel<EPI, true>(bf16, f32) : gemm_kernel<EPI, false>(bf16, f32);
+    if (!allow_smem(kern)) return CONV2D_ERR_CUDA;
+    const int ctas = g.pair ? 2 : 1;
+    jobs.BN = g.BN;
+    jobs.seg = kSegment;
+    jobs.epi_bytes = 0;
+    jobs.items0 = jobs.items = 0;
+    for (int j = 0; j < n; ++j) {
+        GemmParams& p = jobs.job[j];
+        p.n_m = (int)ceil_div(p.M, ctas * kBM);
+        p.n_n = (int)ceil_div(p.N, g.BN);
+        // Row tiles whose A (read again for every column tile) stays in the L2 beside the streams.
+        const int64_t a_tile = (int64_t)ctas * kBM * p.nk * kBK * 2 * (p.pairs > 1 ? 3 : 1);
+        const int64_t rows = (24 << 20) / a_tile;
+        p.group = (int)(rows < 1 ? 1 : (rows > p.n_m ? p.n_m : rows));
+        const int64_t items = (int64_t)p.n_m * p.n_n * p.splits;
+        if (jobs.items + items > 0x7fffffffLL) return CONV2D_ERR_UNSUPPORTED;
+        jobs.items += (int)items;
+        if (j == 0) jobs.items0 = (int)items;
+        // Rows that cannot take 16-byte stores, and ragged last columns, go through shared memory.
+        if (EPI == EPI_OUT && p.splits == 1 && !p.to_acc && (!p.out_vec || p.N % 32 != 0))
+            jobs.epi_bytes = epi_warps(promote) * kStageWarpBytes;
+    }
+    const int stage_bytes = kABytes + g.BN / ctas * kBK * 2;
+    jobs.stages = (kSmemMost - kFixedSmem - jobs.epi_bytes) / stage_bytes;
+    if (jobs.stages > kMaxRing) jobs.stages = kMaxRing;
+    const int smem = kFixedSmem + jobs.epi_bytes + jobs.stages * stage_bytes;
+    const int units = g.pair ? pair_count() : device_sm_count();
+    const int grid = (jobs.items < units ? jobs.items : units) * ctas;
+    void* args[2] = {const_cast<GemmMaps*>(&maps), &jobs};
+    return launch_clusters(kern, grid, 32 * (2 + epi_warps(promote)), ctas, smem, st, args) == cudaSuccess
+               ? CONV2D_OK
+               : CONV2D_ERR_CUDA;
 }
 
 void take(size_t& at, size_t& off, size_t bytes) {
@@ -814,24 +983,23 @@ CePlan plan_ce(const linear_ce_desc& d, bool backward) {
     const int64_t nk = c.dp / 64;
     const int64_t v = d.vocab < piece ? d.vocab : piece;
     // dz is read in 64-column chunks, so its tiles write whole ones (zeros past the vocabulary).
-    c.z = plan_gemm(d.tokens, v, nk * c.pairs, backward ? 64 : 32, false);
+    const Product z{d.tokens, v, nk * c.pairs, false};
+    c.z = plan_gemm(&z, 1, backward ? 64 : 32);
     size_t at = 0;
     if (!backward) {
-        take(at, c.part, (size_t)d.tokens * 2 * (size_t)(c.pieces * ceil_div(v, c.z.BN)) * sizeof(float2));
+        take(at, c.part, (size_t)d.tokens * kPartsPerTile * (size_t)(c.pieces * ceil_div(v, c.z.BN)) * sizeof(float2));
         take(at, c.z_target, (size_t)d.tokens * 4);
         take(at, c.row_loss, (size_t)d.tokens * 4);
     } else {
-        c.dh = plan_gemm(d.tokens, d.hidden, ceil_div(v, 64) * c.pairs, 64, true);
-        c.dw = plan_gemm(v, d.hidden, ceil_div(d.tokens, 64) * c.pairs, 64, true);
+        const Product out[2] = {{d.tokens, d.hidden, ceil_div(v, 64) * c.pairs, true},
+                                {v, d.hidden, ceil_div(d.tokens, 64) * c.pairs, true}};
+        c.out = plan_gemm(out, 2, 64);
         take(at, c.coef, (size_t)d.tokens * 4);
         take(at, c.common, 4);
         take(at, c.dz, (size_t)d.tokens * (size_t)piece * 2 * c.parts);
         if (c.pieces > 1) take(at, c.acc, (size_t)d.tokens * d.hidden * 4);
-        size_t sums = 0;
-        if (c.dh.splits > 1) sums = (size_t)c.dh.splits * d.tokens * d.hidden * 4;
-        if (c.dw.splits > 1 && (size_t)c.dw.splits * v * d.hidden * 4 > sums)
-            sums = (size_t)c.dw.splits * v * d.hidden * 4;
-        take(at, c.sums, sums);
+        if (c.out.splits[0] > 1) take(at, c.sums_h, (size_t)c.out.splits[0] * d.tokens * d.hidden * 4);
+        if (c.out.splits[1] > 1) take(at, c.sums_w, (size_t)c.out.splits[1] * v * d.hidden * 4);
     }
     if (c.pack_h) take(at, c.hp, (size_t)d.tokens * c.dp * 2 * c.parts);
     if (c.pack_w) take(at, c.wp, (size_t)v * c.dp * 2 * c.parts);
@@ -860,19 +1028,23 @@ conv2d_status gemm_z(const CePlan& c, const linear_ce_desc& d, int epi, const Op
                      GemmParams p, cudaStream_t st) {
     p.M = (int)d.tokens;
     p.N = (int)rows_w;
-    p.BN = c.z.BN;
+    p.a_mn = 0;
     p.nk = (int)(c.dp / 64);
     p.pairs = c.pairs;
     p.a_part = p.b_part = (int)c.dp;
     p.splits = 1;
     p.vocab = (int)d.vocab;
     p.ignore = d.ignore_index;
-    CUtensorMap a, b;
-    if (!make_map(&a, h.base, c.bf16, d.tokens, h.cols, h.pitch, kBM) ||
-        !make_map(&b, w.base, c.bf16, rows_w, w.cols, w.pitch, p.BN))
+    GemmMaps maps;
+    if (!make_map(&maps.a[0], h.base, c.bf16, d.tokens, h.cols, h.pitch, kBM) ||
+        !make_map(&maps.b[0], w.base, c.bf16, rows_w, w.cols, w.pitch, c.z.BN / (c.z.pair ? 2 : 1)))
         return CONV2D_ERR_CUDA;
-    return epi == EPI_LSE ? launch_gemm<EPI_LSE, false, false>(c.bf16, a, b, p, st)
-                          : launch_gemm<EPI_DZ, false, false>(c.bf16, a, b, p, st);
+    maps.a[1] = maps.a[0];
+    maps.b[1] = maps.b[0];
+    GemmJobs jobs{};
+    jobs.job[0] = p;
+    return epi == EPI_LSE ? launch_gemm<EPI_LSE>(c.bf16, c.z, maps, jobs, 1, st)
+                          : launch_gemm<EPI_DZ>(c.bf16, c.z, maps, jobs, 1, st);
 }
 
 template <typename T>
@@ -883,21 +1055,19 @@ cudaError_t join_splits(const float* part, int splits, int64_t count, float* acc
                         count, acc, add, to_acc, scale, static_cast<T*>(out));
 }
 
-// out = scale (acc + A B^T), split over K when planned; A is K-major (dz for
-// dh) or MN-major (dz for dw), B is MN-major.
-template <bool A_MN>
-conv2d_status gemm_out(const CePlan& c, const linear_ce_desc& d, const GemmPlan& g, const CUtensorMap& a,
-                       const CUtensorMap& b, int64_t M, int64_t K, int a_part, int b_part, void* out, float* acc,
-                       int add, int to_acc, const float* scale, float* sums, cudaStream_t st) {
+// One of the backward products: out = scale (acc + A B^T), split over K when
+// planned; A is dz, K-major (for dh) or MN-major (for dw), B is MN-major.
+GemmParams out_job(const CePlan& c, const linear_ce_desc& d, int splits, bool a_mn, int64_t M, int64_t K, int64_t b_part,
+                   void* out, float* acc, int add, int to_acc, const float* scale, float* sums) {
     GemmParams p{};
     p.M = (int)M;
     p.N = (int)d.hidden;
-    p.BN = g.BN;
+    p.a_mn = a_mn;
     p.nk = (int)ceil_div(K, 64);
     p.pairs = c.pairs;
-    p.a_part = a_part;
-    p.b_part = b_part;
-    p.splits = g.splits < p.nk * p.pairs ? g.splits : p.nk * p.pairs;
+    p.a_part = (int)c.piece;
+    p.b_part = (int)b_part;
+    p.splits = splits < p.nk * p.pairs ? splits : p.nk * p.pairs;
     p.ldo = d.hidden;
     p.out_f32 = d.dtype == CONV2D_F32;
     p.out_vec = d.hidden * (p.out_f32 ? 4 : 2) % 16 == 0 && aligned_to(out, 16);
@@ -906,16 +1076,17 @@ conv2d_status gemm_out(const CePlan& c, const linear_ce_desc& d, const GemmPlan&
     p.acc = acc;
     p.scale = scale;
     p.out = p.splits > 1 ? sums : out;
-    const conv2d_status s = launch_gemm<EPI_OUT, A_MN, true>(c.bf16, a, b, p, st);
-    if (s != CONV2D_OK || p.splits == 1) return s;
-    cudaError_t e;
+    return p;
+}
+
+cudaError_t join_job(const linear_ce_desc& d, const GemmParams& p, const float* sums, void* out, cudaStream_t st) {
+    if (p.splits == 1) return cudaSuccess;
+    const int64_t count = (int64_t)p.M * d.hidden;
     switch (d.dtype) {
-        case CONV2D_F32: e = join_splits<float>(sums, p.splits, M * d.hidden, acc, add, to_acc, scale, out, st); break;
-        case CONV2D_F16: e = join_splits<__half>(sums, p.splits, M * d.hidden, acc, add, to_acc, scale, out, st); break;
-        default:
-            e = join_splits<__nv_bfloat16>(sums, p.splits, M * d.hidden, acc, add, to_acc, scale, out, st);
+        case CONV2D_F32: return join_splits<float>(sums, p.splits, count, p.acc, p.add, p.to_acc, p.scale, out, st);
+        case CONV2D_F16: return join_splits<__half>(sums, p.splits, count, p.acc, p.add, p.to_acc, p.scale, out, st);
+        default: return join_splits<__nv_bfloat16>(sums, p.splits, count, p.acc, p.add, p.to_acc, p.scale, out, st);
     }
-    return e == cudaSuccess ? CONV2D_OK : CONV2D_ERR_CUDA;
 }
 
 const void* at_row(const void* base, int64_t row, int64_t stride, size_t e) {
@@ -957,7 +1128,7 @@ conv2d_status launch_linear_ce_fwd(const linear_ce_desc& d, const void* h, const
         p.lse_part = part + (size_t)tiles * d.tokens;
         const conv2d_status s = gemm_z(c, d, EPI_LSE, ho, wo, rows, p, st);
         if (s != CONV2D_OK) return s;
-        tiles += 2 * (int)ceil_div(rows, c.z.BN);
+        tiles += kPartsPerTile * (int)ceil_div(rows, c.z.BN);
     }
     float* row_loss = d.reduction == HEAD_REDUCE_NONE ? loss : reinterpret_cast<float*>(base + c.row_loss);
     float* total = d.reduction == HEAD_REDUCE_NONE ? nullptr : loss;
@@ -985,7 +1156,7 @@ conv2d_status launch_linear_ce_bwd(const linear_ce_desc& d, const void* h, const
     float* coef = reinterpret_cast<float*>(base + c.coef);
     float* common = reinterpret_cast<float*>(base + c.common);
     float* acc = c.pieces > 1 ? reinterpret_cast<float*>(base + c.acc) : nullptr;
-    float* sums = reinterpret_cast<float*>(base + c.sums);
+    float *sums_h = reinterpret_cast<float*>(base + c.sums_h), *sums_w = reinterpret_cast<float*>(base + c.sums_w);
     if (launch_after(ce_coef_kernel, dim3(1), dim3(1024), 0, st, dloss, target, (int)d.tokens, (int)d.vocab,
                      d.ignore_index, d.reduction == HEAD_REDUCE_NONE ? 1 : 0, d.reduction == HEAD_REDUCE_MEAN ? 1 : 0,
                      coef, common) != cudaSuccess)
@@ -1010,24 +1181,31 @@ conv2d_status launch_linear_ce_bwd(const linear_ce_desc& d, const void* h, const
         p.col0 = (int)v0;
         conv2d_status s = gemm_z(c, d, EPI_DZ, ho, wo, rows, p, st);
         if (s != CONV2D_OK) return s;
-        CUtensorMap a, b;
+        // dh and dw of the piece in one launch.
         const int64_t dz_pitch = c.piece * c.parts;
+        GemmMaps maps;
+        GemmJobs jobs{};
+        int n = 0;
+        void* dw_out = dw ? static_cast<uint8_t*>(dw) + (size_t)v0 * d.hidden * e : nullptr;
         if (dh) {
-            if (!make_map(&a, p.dz, c.bf16, d.tokens, dz_pitch, dz_pitch, kBM) ||
-                !make_map(&b, wo.base, c.bf16, rows, wo.cols, wo.pitch, 64))
+            if (!make_map(&maps.a[n], p.dz, c.bf16, d.tokens, dz_pitch, dz_pitch, kBM) ||
+                !make_map(&maps.b[n], wo.base, c.bf16, rows, wo.cols, wo.pitch, 64))
                 return CONV2D_ERR_CUDA;
-            s = gemm_out<false>(c, d, c.dh, a, b, d.tokens, rows, (int)c.piece, (int)c.dp, dh, acc, !first, !last, common,
-                                sums, st);
-            if (s != CONV2D_OK) return s;
+            jobs.job[n++] = out_job(c, d, c.out.splits[0], false, d.tokens, rows, c.dp, dh, acc, !first, !last, common,
+                                    sums_h);
         }
         if (dw) {
-            if (!make_map(&a, p.dz, c.bf16, d.tokens, dz_pitch, dz_pitch, 64) ||
-                !make_map(&b, ho.base, c.bf16, d.tokens, ho.cols, ho.pitch, 64))
+            if (!make_map(&maps.a[n], p.dz, c.bf16, d.tokens, dz_pitch, dz_pitch, 64) ||
+                !make_map(&maps.b[n], ho.base, c.bf16, d.tokens, ho.cols, ho.pitch, 64))
                 return CONV2D_ERR_CUDA;
-            s = gemm_out<true>(c, d, c.dw, a, b, rows, d.tokens, (int)c.piece, (int)c.dp,
-                               static_cast<uint8_t*>(dw) + (size_t)v0 * d.hidden * e, nullptr, 0, 0, common, sums, st);
-            if (s != CONV2D_OK) return s;
+            jobs.job[n++] = out_job(c, d, c.out.splits[1], true, rows, d.tokens, c.dp, dw_out, nullptr, 0, 0, common,
+                                    sums_w);
         }
+        if (n == 1) { maps.a[1] = maps.a[0]; maps.b[1] = maps.b[0]; }
+        s = launch_gemm<EPI_OUT>(c.bf16, c.out, maps, jobs, n, st);
+        if (s != CONV2D_OK) return s;
+        if (dh && join_job(d, jobs.job[0], sums_h, dh, st) != cudaSuccess) return CONV2D_ERR_CUDA;
+        if (dw && join_job(d, jobs.job[n - 1], sums_w, dw_out, st) != cudaSuccess) return CONV2D_ERR_CUDA;
     }
     return CONV2D_OK;
 }

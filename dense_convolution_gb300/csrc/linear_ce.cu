@@ -78,18 +78,19 @@ struct GemmParams {
     int vocab;
     int64_t ignore;
     const int64_t* target;
-    float2* lse_part;        // [(column tile, column group)][M]
+    float2* lse_part;        // [column tile][M]
     float* z_target;         // [M]
     const float *lse, *coef; // [M]
     void* dz;                // [M][parts * dz_part]
     int dz_part, parts;
     // EPI_OUT
-    void* out;               // final element type, or the fp32 partial sums [split][M][N]
+    void* out;               // final element type, or the fp32 partial sums [split][M][lds]
     int64_t ldo;
-    int out_f32, out_vec;    // out_vec: rows of out take 16-byte stores
+    int out_f32, out_vec;    // out_vec: rows of out take 32-byte (2), 16-byte (1) or no wide stores (0)
+    int64_t lds;             // row pitch of the fp32 sums: a multiple of 64, so they always move whole
     int add;                 // acc holds earlier pieces' sums
     int to_acc;              // store into acc rather than out
-    float* acc;              // [M][N]
+    float* acc;              // [M][lds]
     const float* scale;      // null: 1
 };
 
@@ -111,6 +112,14 @@ __device__ __forceinline__ float exp2_approx(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// Join two (max, sum of exp(z - max)) pairs.
+__device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
+    const float top = fmaxf(m, m2);
+    const float base = top == -INFINITY ? 0.f : top;
+    s = s * exp2_approx((m - base) * kLog2e) + s2 * exp2_approx((m2 - base) * kLog2e);
+    m = top;
 }
 
 struct Item { int m, n, split; };
@@ -138,14 +147,19 @@ template <bool BF16> __device__ __forceinline__ uint32_t pack2(float a, float b)
     }
 }
 
-// A value as the sum of three bf16 parts.
-__device__ __forceinline__ void split3(float x, float (&p)[3]) {
+// The bf16 nearest to x (toward zero where that would overflow), and what is
+// left for the next part: three parts hold all 24 bits of a float.
+__device__ __forceinline__ float part_of(float x) {
     __nv_bfloat16 a = __float2bfloat16_rn(x);
     if (__hisinf(a) && !isinf(x)) a = __float2bfloat16_rz(x);
-    p[0] = __bfloat162float(a);
-    const float r = isfinite(p[0]) ? x - p[0] : 0.f;
-    p[1] = __bfloat162float(__float2bfloat16_rn(r));
-    p[2] = __bfloat162float(__float2bfloat16_rn(r - p[1]));
+    return __bfloat162float(a);
+}
+__device__ __forceinline__ float rest_of(float x, float part) { return isfinite(part) ? x - part : 0.f; }
+__device__ __forceinline__ void split3(float x, float (&p)[3]) {
+    p[0] = part_of(x);
+    x = rest_of(x, p[0]);
+    p[1] = part_of(x);
+    p[2] = part_of(rest_of(x, p[1]));
 }
 
 // ------------------------------------------------------------------ epilogues
@@ -157,31 +171,32 @@ __device__ __forceinline__ void store_out(const GemmParams& p, float (&v)[32], i
     const int n = p.N - c0;                                // valid columns from c0 on
     if (p.splits > 1 || p.to_acc) {
         // fp32 sums: of this split, or of the pieces so far.
-        float* dst = p.splits > 1 ? static_cast<float*>(p.out) + ((int64_t)split * p.M + row) * p.N + c0
-                                  : p.acc + (int64_t)row * p.N + c0;
-        if (!live) return;
-        if (n >= 32 && p.N % 4 == 0) {
+        float* dst = p.splits > 1 ? static_cast<float*>(p.out) + ((int64_t)split * p.M + row) * p.lds + c0
+                                  : p.acc + (int64_t)row * p.lds + c0;
+        if (!live || c0 >= p.lds) return;
+        if (p.splits == 1 && p.add) {
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
-                float4 t = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-                if (p.splits == 1 && p.add) {
-                    const float4 o = *reinterpret_cast<const float4*>(dst + i);
-                    t.x += o.x; t.y += o.y; t.z += o.z; t.w += o.w;
-                }
-                *reinterpret_cast<float4*>(dst + i) = t;
+                const float4 o = *reinterpret_cast<const float4*>(dst + i);
+                v[i] += o.x; v[i + 1] += o.y; v[i + 2] += o.z; v[i + 3] += o.w;
             }
-        } else {
+        }
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (i < n) dst[i] = v[i] + (p.splits == 1 && p.add ? dst[i] : 0.f);
+        for (int i = 0; i < 32; i += 8) {
+            uint32_t w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(v[i + j]);
+            st_global_v8(dst + i, w);
         }
         return;
     }
-    if (p.add && live) {
-        const float* o = p.acc + (int64_t)row * p.N + c0;
+    if (p.add && live) {                                   // (the sums' rows are whole chunks)
+        const float* o = p.acc + (int64_t)row * p.lds + c0;
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (i < n) v[i] += o[i];
+        for (int i = 0; i < 32; i += 4) {
+            const float4 t = *reinterpret_cast<const float4*>(o + i);
+            v[i] += t.x; v[i + 1] += t.y; v[i + 2] += t.z; v[i + 3] += t.w;
+        }
     }
     const float s = p.scale ? *p.scale : 1.f;
 #pragma unroll
@@ -191,15 +206,31 @@ __device__ __forceinline__ void store_out(const GemmParams& p, float (&v)[32], i
         if (p.out_f32) {
             float* dst = static_cast<float*>(p.out) + (int64_t)row * p.ldo + c0;
 #pragma unroll
-            for (int i = 0; i < 32; i += 4)
-                *reinterpret_cast<float4*>(dst + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            for (int i = 0; i < 32; i += 8) {
+                uint32_t w[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(v[i + j]);
+                if (p.out_vec == 2) {
+                    st_global_v8(dst + i, w);
+                } else {
+                    *reinterpret_cast<uint4*>(dst + i) = make_uint4(w[0], w[1], w[2], w[3]);
+                    *reinterpret_cast<uint4*>(dst + i + 4) = make_uint4(w[4], w[5], w[6], w[7]);
+                }
+            }
         } else {
             uint16_t* dst = static_cast<uint16_t*>(p.out) + (int64_t)row * p.ldo + c0;
 #pragma unroll
-            for (int i = 0; i < 32; i += 8)
-                *reinterpret_cast<uint4*>(dst + i) =
-                    make_uint4(pack2<BF16>(v[i], v[i + 1]), pack2<BF16>(v[i + 2], v[i + 3]),
-                               pack2<BF16>(v[i + 4], v[i + 5]), pack2<BF16>(v[i + 6], v[i + 7]));
+            for (int i = 0; i < 32; i += 16) {
+                uint32_t w[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j] = pack2<BF16>(v[i + 2 * j], v[i + 2 * j + 1]);
+                if (p.out_vec == 2) {
+                    st_global_v8(dst + i, w);
+                } else {
+                    *reinterpret_cast<uint4*>(dst + i) = make_uint4(w[0], w[1], w[2], w[3]);
+                    *reinterpret_cast<uint4*>(dst + i + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                }
+            }
         }
         return;
     }
@@ -416,7 +447,7 @@ ce_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ Ge
             if constexpr (PAIR) mbar_arrive_cluster(cluster_addr(acce_bar(a), 0));
             else                mbar_arrive(acce_bar(a));
         };
-        int acc = 0;
+        int acc = 0, turn = 0;
         uint32_t acc_phase = 0;
         for (int n_item = first; n_item < jobs.items; n_item += step) {
             int i = n_item;
@@ -437,6 +468,7 @@ ce_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ Ge
                     }
                 }
             }
+            bool lands = true;                                 // EPI_LSE: no wait of this tile ran out
             // PROMOTE: this warp's share of the tile's sums, in registers.
             constexpr int kKept = PROMOTE ? 8 / kGroups : 1;   // 32-column chunks per warp at most
             float sum[kKept][32];
@@ -472,7 +504,8 @@ ce_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ Ge
                     if (lane == 0) emptied(acc);
                     if (++acc == 2) { acc = 0; acc_phase ^= 1; }
                 }
-                if (!got) break;
+                if (EPI != EPI_LSE && !got) break;
+                lands = got;
             } else {
                 if (!__all_sync(0xffffffffu, mbar_wait(accf_bar(acc), acc_phase, abort_flag))) break;
                 tc_fence_after();
@@ -518,22 +551,27 @@ ce_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ Ge
                     }
                     if (live && c0 < p.dz_part) {              // the last tile may end past the piece
                         uint16_t* dst = static_cast<uint16_t*>(p.dz) + (int64_t)row * p.parts * p.dz_part + c0;
-                        if (p.parts == 1) {
+                        // 16 columns of a row are one memory sector (of each part).
 #pragma unroll
-                            for (int j = 0; j < 32; j += 8)
-                                *reinterpret_cast<uint4*>(dst + j) =
-                                    make_uint4(pack2<BF16>(v[j], v[j + 1]), pack2<BF16>(v[j + 2], v[j + 3]),
-                                               pack2<BF16>(v[j + 4], v[j + 5]), pack2<BF16>(v[j + 6], v[j + 7]));
-                        } else {
+                        for (int j = 0; j < 32; j += 16) {
+                            uint32_t u[8];
+                            if (!PROMOTE || p.parts == 1) {
 #pragma unroll
-                            for (int j = 0; j < 32; j += 4) {
-                                float q[4][3];
+                                for (int l = 0; l < 8; ++l) u[l] = pack2<BF16>(v[j + 2 * l], v[j + 2 * l + 1]);
+                                st_global_v8(dst + j, u);
+                            } else {
+                                // Part after part: what a part leaves of v goes on to the next.
 #pragma unroll
-                                for (int l = 0; l < 4; ++l) split3(v[j + l], q[l]);
+                                for (int s = 0; s < 3; ++s) {
 #pragma unroll
-                                for (int s = 0; s < 3; ++s)
-                                    *reinterpret_cast<uint2*>(dst + (int64_t)s * p.dz_part + j) =
-                                        make_uint2(pack2<true>(q[0][s], q[1][s]), pack2<true>(q[2][s], q[3][s]));
+                                    for (int l = 0; l < 8; ++l) {
+                                        const float a = part_of(v[j + 2 * l]), b = part_of(v[j + 2 * l + 1]);
+                                        u[l] = pack2<true>(a, b);
+                                        v[j + 2 * l] = rest_of(v[j + 2 * l], a);
+                                        v[j + 2 * l + 1] = rest_of(v[j + 2 * l + 1], b);
+                                    }
+                                    st_global_v8(dst + (int64_t)s * p.dz_part + j, u);
+                                }
                             }
                         }
                     }
@@ -561,7 +599,20 @@ ce_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ Ge
                 if (++acc == 2) { acc = 0; acc_phase ^= 1; }
             }
             if constexpr (EPI == EPI_LSE) {
-                if (live) p.lse_part[(int64_t)(kGroups * it.n + group) * p.M + row] = make_float2(m_run, s_run);
+                // The groups' pairs of a row become one (two buffers in turn:
+                // the next tile's meeting shows that this one's are read).
+                float2* meet = reinterpret_cast<float2*>(epi_stage) + (turn & 1) * kGroups * 128;
+                ++turn;
+                meet[group * 128 + quarter * 32 + lane] = make_float2(m_run, s_run);
+                if (!named_bar_and(1, kEpiWarps * 32, lands)) break;
+                if (group == 0 && live) {
+#pragma unroll
+                    for (int g = 1; g < kGroups; ++g) {
+                        const float2 o = meet[g * 128 + quarter * 32 + lane];
+                        join(m_run, s_run, o.x, o.y);
+                    }
+                    p.lse_part[(int64_t)it.n * p.M + row] = make_float2(m_run, s_run);
+                }
             }
         }
     }
@@ -581,13 +632,6 @@ ce_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ Ge
 }
 
 // ------------------------------------------------------------------ small kernels
-__device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
-    const float top = fmaxf(m, m2);
-    const float base = top == -INFINITY ? 0.f : top;
-    s = s * exp2_approx((m - base) * kLog2e) + s2 * exp2_approx((m2 - base) * kLog2e);
-    m = top;
-}
-
 // Sum over a block of 256 or 1024 threads, in every thread (fixed order).
 __device__ __forceinline__ float block_sum(float v, float* red) {
     v = lane_sum(v, 32);
@@ -661,12 +705,10 @@ __global__ void __launch_bounds__(1024) ce_reduce_kernel(const float* row_loss, 
 // (|dz| <= 1) and common holds dloss (over their number for the mean).  None:
 // coef is dloss scaled by a power of two, the largest in [2^14, 2^15).  Rows
 // that do not count have coef 0.
-__global__ void __launch_bounds__(1024) ce_coef_kernel(const float* dloss, const int64_t* target, int n, int vocab,
-                                                       int64_t ignore, int per_row, int mean, float* coef,
-                                                       float* common) {
+__device__ __forceinline__ void ce_coef(const float* dloss, const int64_t* target, int n, int vocab, int64_t ignore,
+                                        int per_row, int mean, float* coef, float* common) {
     __shared__ float red[32];
     __shared__ float up_s;
-    pdl_wait();
     float count = 0.f, top = 0.f;
     for (int i = threadIdx.x; i < n; i += blockDim.x) {
         const int64_t t = target[i];
@@ -708,13 +750,12 @@ __global__ void __launch_bounds__(1024) ce_coef_kernel(const float* dloss, const
 // past `cols`, and zero for rows whose target does not count (skip given):
 // their weight in dw is zero, which would not hide a NaN.
 template <typename T, int PARTS>
-__global__ void __launch_bounds__(256) ce_pack_kernel(const T* src, int64_t stride, int64_t rows, int cols, int pitch,
-                                                      int vec, const int64_t* target, int vocab, int64_t ignore,
-                                                      uint16_t* dst) {
-    pdl_wait();
+__device__ __forceinline__ void ce_pack(const T* src, int64_t stride, int64_t rows, int cols, int pitch, int vec,
+                                        const int64_t* target, int vocab, int64_t ignore, uint16_t* dst, int64_t block,
+                                        int64_t blocks) {
     const int per = pitch / 8;
     const int64_t total = rows * per;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
+    for (int64_t i = block * blockDim.x + threadIdx.x; i < total; i += blocks * blockDim.x) {
         const int64_t row = i / per;
         const int c = (int)(i - row * per) * 8;
         bool keep = true;
@@ -751,18 +792,52 @@ __global__ void __launch_bounds__(256) ce_pack_kernel(const T* src, int64_t stri
     }
 }
 
-// out = scale (acc + sum over splits), or acc = that sum unscaled (to_acc).
+template <typename T, int PARTS>
+__global__ void __launch_bounds__(256) ce_pack_kernel(const T* src, int64_t stride, int64_t rows, int cols, int pitch,
+                                                      int vec, uint16_t* dst) {
+    pdl_wait();
+    ce_pack<T, PARTS>(src, stride, rows, cols, pitch, vec, nullptr, 0, 0, dst, blockIdx.x, gridDim.x);
+}
+
+// What the backward pass starts with: block 0 makes coef and common, the others
+// copy h.
+template <typename T, int PARTS>
+__global__ void __launch_bounds__(1024)
+ce_prepare_kernel(const T* h, int64_t stride, int64_t rows, int cols, int pitch, int vec, const float* dloss,
+                  const int64_t* target, int vocab, int64_t ignore, int per_row, int mean, float* coef, float* common,
+                  uint16_t* dst) {
+    pdl_wait();
+    if (blockIdx.x == 0) ce_coef(dloss, target, (int)rows, vocab, ignore, per_row, mean, coef, common);
+    else ce_pack<T, PARTS>(h, stride, rows, cols, pitch, vec, target, vocab, ignore, dst, blockIdx.x - 1, gridDim.x - 1);
+}
+
+// out = scale (acc + sum over splits), or acc = that sum unscaled (to_acc).  The
+// sums' rows are lds wide (a multiple of 64); four columns a thread.
 template <typename T>
-__global__ void __launch_bounds__(256) ce_join_kernel(const float* part, int splits, int64_t count, float* acc, int add,
-                                                      int to_acc, const float* scale, T* out) {
+__global__ void __launch_bounds__(256) ce_join_kernel(const float* part, int splits, int64_t rows, int cols, int64_t lds,
+                                                      float* acc, int add, int to_acc, const float* scale, T* out) {
     pdl_wait();
     const float s = *scale;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < count; i += (int64_t)gridDim.x * blockDim.x) {
-        float v = add ? acc[i] : 0.f;
+    const int per = (cols + 3) / 4;
+    const int64_t total = rows * per, pitch = rows * lds;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t row = i / per;
+        const int c = (int)(i - row * per) * 4;
+        const int64_t at = row * lds + c;
+        float4 v = add ? *reinterpret_cast<const float4*>(acc + at) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-        for (int k = 0; k < splits; ++k) v += part[(int64_t)k * count + i];
-        if (to_acc) acc[i] = v;
-        else out[i] = from_f32<T>(v * s);
+        for (int k = 0; k < splits; ++k) {
+            const float4 t = *reinterpret_cast<const float4*>(part + k * pitch + at);
+            v.x += t.x; v.y += t.y; v.z += t.z; v.w += t.w;
+        }
+        if (to_acc) {
+            *reinterpret_cast<float4*>(acc + at) = v;
+        } else {
+            const float f[4] = {v.x * s, v.y * s, v.z * s, v.w * s};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (c + j < cols) out[row * cols + c + j] = from_f32<T>(f[j]);
+        }
     }
 }
 
@@ -786,8 +861,6 @@ bool make_map(CUtensorMap* map, const void* base, bool bf16, int64_t rows, int64
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// (max, sum) pairs per column tile: one per group of the sixteen epilogue warps.
-constexpr int kPartsPerTile = epi_warps(true) / 4;
 constexpr int64_t kMostPiece = 1LL << 28;      // three parts of a piece keep 32-bit column numbers
 
 
@@ -843,9 +916,6 @@ LaunchPlan plan_gemm(const Product* pr, int n, int step) {
     }
     return best;
 }
-
-// Chunks per accumulation: 256 K elements, 16 steps of the tensor core.
-constexpr int kSegment = 4;
 
 // Lift a kernel's shared-memory limit, once per device and kernel.
 bool allow_smem(const void* kern) {
@@ -919,8 +989,12 @@ conv2d_status launch_gemm(bool bf16, const LaunchPlan& g, const GemmMaps& maps, 
     if (!allow_smem(kern)) return CONV2D_ERR_CUDA;
     const int ctas = g.pair ? 2 : 1;
     jobs.BN = g.BN;
-    jobs.seg = kSegment;
-    jobs.epi_bytes = 0;
+    // Results in fp32: the shortest segment where the tensor cores wait for
+    // memory anyway (few rows).  Emptying an accumulator takes about 1.2 us,
+    // longer than four chunks: large products of fp32 operands take six (dh
+    // of 1000 x 768 x 20011 is 7e-7 off), losses of 16-bit operands sixteen (5e-7).
+    jobs.seg = jobs.job[0].M <= 2 * kBM ? 4 : f32 ? 6 : 16;
+    jobs.epi_bytes = EPI == EPI_LSE ? 2 * epi_warps(true) / 4 * 128 * (int)sizeof(float2) : 0;
     jobs.items0 = jobs.items = 0;
     for (int j = 0; j < n; ++j) {
         GemmParams& p = jobs.job[j];
@@ -987,7 +1061,7 @@ CePlan plan_ce(const linear_ce_desc& d, bool backward) {
     c.z = plan_gemm(&z, 1, backward ? 64 : 32);
     size_t at = 0;
     if (!backward) {
-        take(at, c.part, (size_t)d.tokens * kPartsPerTile * (size_t)(c.pieces * ceil_div(v, c.z.BN)) * sizeof(float2));
+        take(at, c.part, (size_t)d.tokens * (size_t)(c.pieces * ceil_div(v, c.z.BN)) * sizeof(float2));
         take(at, c.z_target, (size_t)d.tokens * 4);
         take(at, c.row_loss, (size_t)d.tokens * 4);
     } else {
@@ -997,28 +1071,43 @@ CePlan plan_ce(const linear_ce_desc& d, bool backward) {
         take(at, c.coef, (size_t)d.tokens * 4);
         take(at, c.common, 4);
         take(at, c.dz, (size_t)d.tokens * (size_t)piece * 2 * c.parts);
-        if (c.pieces > 1) take(at, c.acc, (size_t)d.tokens * d.hidden * 4);
-        if (c.out.splits[0] > 1) take(at, c.sums_h, (size_t)c.out.splits[0] * d.tokens * d.hidden * 4);
-        if (c.out.splits[1] > 1) take(at, c.sums_w, (size_t)c.out.splits[1] * v * d.hidden * 4);
+        if (c.pieces > 1) take(at, c.acc, (size_t)d.tokens * c.dp * 4);
+        if (c.out.splits[0] > 1) take(at, c.sums_h, (size_t)c.out.splits[0] * d.tokens * c.dp * 4);
+        if (c.out.splits[1] > 1) take(at, c.sums_w, (size_t)c.out.splits[1] * v * c.dp * 4);
     }
     if (c.pack_h) take(at, c.hp, (size_t)d.tokens * c.dp * 2 * c.parts);
     if (c.pack_w) take(at, c.wp, (size_t)v * c.dp * 2 * c.parts);
-    c.total = at;
+    c.total = at + 1024;           // the workspace may start at any multiple of 16 bytes
     return c;
 }
 
-cudaError_t pack(const linear_ce_desc& d, const void* src, int64_t stride, int64_t rows, int64_t dp, const int64_t* target,
-                 void* dst, cudaStream_t st) {
+cudaError_t pack(const linear_ce_desc& d, const void* src, int64_t stride, int64_t rows, int64_t dp, void* dst,
+                 cudaStream_t st) {
     const int64_t work = ceil_div(rows * (dp / 8), 256);
     const int64_t most = (int64_t)device_sm_count() * 16;
     const dim3 grid((unsigned)(work < most ? work : most)), block(256);
     if (d.dtype == CONV2D_F32)
         return launch_after(ce_pack_kernel<float, 3>, grid, block, 0, st, static_cast<const float*>(src), stride, rows,
-                            (int)d.hidden, (int)dp, 0, target, (int)d.vocab, d.ignore_index,
-                            static_cast<uint16_t*>(dst));
+                            (int)d.hidden, (int)dp, 0, static_cast<uint16_t*>(dst));
     const int vec = stride % 8 == 0 && aligned_to(src, 16);
     return launch_after(ce_pack_kernel<__half, 1>, grid, block, 0, st, static_cast<const __half*>(src), stride, rows,
-                        (int)d.hidden, (int)dp, vec, target, (int)d.vocab, d.ignore_index, static_cast<uint16_t*>(dst));
+                        (int)d.hidden, (int)dp, vec, static_cast<uint16_t*>(dst));
+}
+
+cudaError_t prepare(const linear_ce_desc& d, const CePlan& c, const void* h, const int64_t* target, const float* dloss,
+                    float* coef, float* common, void* dst, cudaStream_t st) {
+    const int64_t work = ceil_div(d.tokens * (c.dp / 8), 1024);
+    const int64_t most = (int64_t)device_sm_count() * 4;
+    const dim3 grid((unsigned)(work < most ? work : most) + 1), block(1024);
+    const int per_row = d.reduction == HEAD_REDUCE_NONE, mean = d.reduction == HEAD_REDUCE_MEAN;
+    if (d.dtype == CONV2D_F32)
+        return launch_after(ce_prepare_kernel<float, 3>, grid, block, 0, st, static_cast<const float*>(h), d.hs, d.tokens,
+                            (int)d.hidden, (int)c.dp, 0, dloss, target, (int)d.vocab, d.ignore_index, per_row, mean,
+                            coef, common, static_cast<uint16_t*>(dst));
+    const int vec = d.hs % 8 == 0 && aligned_to(h, 16);
+    return launch_after(ce_prepare_kernel<__half, 1>, grid, block, 0, st, static_cast<const __half*>(h), d.hs, d.tokens,
+                        (int)d.hidden, (int)c.dp, vec, dloss, target, (int)d.vocab, d.ignore_index, per_row, mean, coef,
+                        common, static_cast<uint16_t*>(dst));
 }
 
 // h and w as the tensor cores read them: base, columns and row pitch.
@@ -1047,12 +1136,10 @@ conv2d_status gemm_z(const CePlan& c, const linear_ce_desc& d, int epi, const Op
                           : launch_gemm<EPI_DZ>(c.bf16, c.z, maps, jobs, 1, st);
 }
 
-template <typename T>
-cudaError_t join_splits(const float* part, int splits, int64_t count, float* acc, int add, int to_acc,
-                        const float* scale, void* out, cudaStream_t st) {
-    const int64_t work = ceil_div(count, 256), most = (int64_t)device_sm_count() * 16;
-    return launch_after(ce_join_kernel<T>, dim3((unsigned)(work < most ? work : most)), dim3(256), 0, st, part, splits,
-                        count, acc, add, to_acc, scale, static_cast<T*>(out));
+template <typename T> cudaError_t join_splits(const GemmParams& p, const float* sums, void* out, cudaStream_t st) {
+    const int64_t work = ceil_div((int64_t)p.M * ceil_div(p.N, 4), 256), most = (int64_t)device_sm_count() * 16;
+    return launch_after(ce_join_kernel<T>, dim3((unsigned)(work < most ? work : most)), dim3(256), 0, st, sums, p.splits,
+                        (int64_t)p.M, p.N, p.lds, p.acc, p.add, p.to_acc, p.scale, static_cast<T*>(out));
 }
 
 // One of the backward products: out = scale (acc + A B^T), split over K when
@@ -1069,8 +1156,10 @@ GemmParams out_job(const CePlan& c, const linear_ce_desc& d, int splits, bool a_
     p.b_part = (int)b_part;
     p.splits = splits < p.nk * p.pairs ? splits : p.nk * p.pairs;
     p.ldo = d.hidden;
+    p.lds = c.dp;
     p.out_f32 = d.dtype == CONV2D_F32;
-    p.out_vec = d.hidden * (p.out_f32 ? 4 : 2) % 16 == 0 && aligned_to(out, 16);
+    const int64_t row_bytes = d.hidden * (p.out_f32 ? 4 : 2);
+    p.out_vec = row_bytes % 32 == 0 && aligned_to(out, 32) ? 2 : row_bytes % 16 == 0 && aligned_to(out, 16) ? 1 : 0;
     p.add = add;
     p.to_acc = to_acc;
     p.acc = acc;
@@ -1081,12 +1170,15 @@ GemmParams out_job(const CePlan& c, const linear_ce_desc& d, int splits, bool a_
 
 cudaError_t join_job(const linear_ce_desc& d, const GemmParams& p, const float* sums, void* out, cudaStream_t st) {
     if (p.splits == 1) return cudaSuccess;
-    const int64_t count = (int64_t)p.M * d.hidden;
     switch (d.dtype) {
-        case CONV2D_F32: return join_splits<float>(sums, p.splits, count, p.acc, p.add, p.to_acc, p.scale, out, st);
-        case CONV2D_F16: return join_splits<__half>(sums, p.splits, count, p.acc, p.add, p.to_acc, p.scale, out, st);
-        default: return join_splits<__nv_bfloat16>(sums, p.splits, count, p.acc, p.add, p.to_acc, p.scale, out, st);
+        case CONV2D_F32: return join_splits<float>(p, sums, out, st);
+        case CONV2D_F16: return join_splits<__half>(p, sums, out, st);
+        default: return join_splits<__nv_bfloat16>(p, sums, out, st);
     }
+}
+
+uint8_t* aligned_base(void* ws) {
+    return reinterpret_cast<uint8_t*>(align_up(reinterpret_cast<uintptr_t>(ws), 1024));
 }
 
 const void* at_row(const void* base, int64_t row, int64_t stride, size_t e) {
@@ -1105,11 +1197,11 @@ void linear_ce_plan(linear_ce_desc& d) {
 conv2d_status launch_linear_ce_fwd(const linear_ce_desc& d, const void* h, const void* w, const int64_t* target,
                                    float* loss, float* lse, void* ws, cudaStream_t st) {
     const CePlan& c = d.fwd;
-    uint8_t* base = static_cast<uint8_t*>(ws);
+    uint8_t* base = aligned_base(ws);
     const size_t e = elem_bytes(d.dtype);
     Operand ho{h, d.hidden, d.hs};
     if (c.pack_h) {
-        if (pack(d, h, d.hs, d.tokens, c.dp, nullptr, base + c.hp, st) != cudaSuccess) return CONV2D_ERR_CUDA;
+        if (pack(d, h, d.hs, d.tokens, c.dp, base + c.hp, st) != cudaSuccess) return CONV2D_ERR_CUDA;
         ho = Operand{base + c.hp, c.dp * c.parts, c.dp * c.parts};
     }
     GemmParams p{};
@@ -1121,14 +1213,14 @@ conv2d_status launch_linear_ce_fwd(const linear_ce_desc& d, const void* h, const
         const int64_t rows = d.vocab - v0 < c.piece ? d.vocab - v0 : c.piece;
         Operand wo{at_row(w, v0, d.ws, e), d.hidden, d.ws};
         if (c.pack_w) {
-            if (pack(d, wo.base, d.ws, rows, c.dp, nullptr, base + c.wp, st) != cudaSuccess) return CONV2D_ERR_CUDA;
+            if (pack(d, wo.base, d.ws, rows, c.dp, base + c.wp, st) != cudaSuccess) return CONV2D_ERR_CUDA;
             wo = Operand{base + c.wp, c.dp * c.parts, c.dp * c.parts};
         }
         p.col0 = (int)v0;
         p.lse_part = part + (size_t)tiles * d.tokens;
         const conv2d_status s = gemm_z(c, d, EPI_LSE, ho, wo, rows, p, st);
         if (s != CONV2D_OK) return s;
-        tiles += kPartsPerTile * (int)ceil_div(rows, c.z.BN);
+        tiles += (int)ceil_div(rows, c.z.BN);
     }
     float* row_loss = d.reduction == HEAD_REDUCE_NONE ? loss : reinterpret_cast<float*>(base + c.row_loss);
     float* total = d.reduction == HEAD_REDUCE_NONE ? nullptr : loss;
@@ -1151,17 +1243,13 @@ conv2d_status launch_linear_ce_bwd(const linear_ce_desc& d, const void* h, const
                                    const float* lse, const float* dloss, void* dh, void* dw, void* ws,
                                    cudaStream_t st) {
     const CePlan& c = d.bwd;
-    uint8_t* base = static_cast<uint8_t*>(ws);
+    uint8_t* base = aligned_base(ws);
     const size_t e = elem_bytes(d.dtype);
     float* coef = reinterpret_cast<float*>(base + c.coef);
     float* common = reinterpret_cast<float*>(base + c.common);
     float* acc = c.pieces > 1 ? reinterpret_cast<float*>(base + c.acc) : nullptr;
     float *sums_h = reinterpret_cast<float*>(base + c.sums_h), *sums_w = reinterpret_cast<float*>(base + c.sums_w);
-    if (launch_after(ce_coef_kernel, dim3(1), dim3(1024), 0, st, dloss, target, (int)d.tokens, (int)d.vocab,
-                     d.ignore_index, d.reduction == HEAD_REDUCE_NONE ? 1 : 0, d.reduction == HEAD_REDUCE_MEAN ? 1 : 0,
-                     coef, common) != cudaSuccess)
-        return CONV2D_ERR_CUDA;
-    if (pack(d, h, d.hs, d.tokens, c.dp, target, base + c.hp, st) != cudaSuccess) return CONV2D_ERR_CUDA;
+    if (prepare(d, c, h, target, dloss, coef, common, base + c.hp, st) != cudaSuccess) return CONV2D_ERR_CUDA;
     const Operand ho{base + c.hp, c.dp * c.parts, c.dp * c.parts};
     GemmParams p{};
     p.target = target;
@@ -1175,7 +1263,7 @@ conv2d_status launch_linear_ce_bwd(const linear_ce_desc& d, const void* h, const
         const bool first = v0 == 0, last = v0 + rows >= d.vocab;
         Operand wo{at_row(w, v0, d.ws, e), d.hidden, d.ws};
         if (c.pack_w) {
-            if (pack(d, wo.base, d.ws, rows, c.dp, nullptr, base + c.wp, st) != cudaSuccess) return CONV2D_ERR_CUDA;
+            if (pack(d, wo.base, d.ws, rows, c.dp, base + c.wp, st) != cudaSuccess) return CONV2D_ERR_CUDA;
             wo = Operand{base + c.wp, c.dp * c.parts, c.dp * c.parts};
         }
         p.col0 = (int)v0;

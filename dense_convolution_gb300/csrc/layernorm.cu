@@ -466,9 +466,33 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) layernorm_bwd_kernel(
 // exchanges and barrier, and the arithmetic is packed two by two.
 constexpr int kBulkBytes = 1024, kBulkThreads = 512, kBulkElems = 16, kRingBytes = 192 * 1024, kRingMost = 8;
 
-// The lane group that value k of 2 ROWS ends up in when every exchange keeps
-// the lower half of the values in the lower lanes: bit by bit, k itself.
-template <int ROWS> __device__ __forceinline__ constexpr int sum_lane(int k) { return k * (32 / (2 * ROWS)); }
+// N sums (a power of two) over a warp at once: each exchange also halves the
+// values that a lane carries, until lanes k 32 / N on hold sum k.
+template <int N> __device__ __forceinline__ float warp_sums(float (&v)[N]) {
+    const int lane = threadIdx.x & 31;
+    int o = 16;
+#pragma unroll
+    for (int n = N / 2; n > 0; n >>= 1, o >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int k = 0; k < n; ++k)
+            v[k] = (up ? v[k + n] : v[k]) + __shfl_xor_sync(0xffffffffu, up ? v[k] : v[k + n], o);
+    }
+#pragma unroll
+    for (; o > 0; o >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+    return v[0];
+}
+// The group's sums from its warps' (buf[k][warp], written by the first lane of
+// each lane group): sum k in lanes k 32 / N on.
+template <int N> __device__ __forceinline__ float group_sums(const float (*buf)[16], int first, int warps) {
+    constexpr int kSpan = 32 / N;
+    const int lane = threadIdx.x & 31;
+    float w = 0.f;
+    for (int i = lane % kSpan; i < warps; i += kSpan) w += buf[lane / kSpan][first + i];
+#pragma unroll
+    for (int d = kSpan / 2; d > 0; d >>= 1) w += __shfl_xor_sync(0xffffffffu, w, d);
+    return w;
+}
 
 template <typename T, int ROWS>
 __global__ void __launch_bounds__(kBulkThreads, 1) layernorm_bwd_bulk_kernel(const LnParams p, const int ring_rows) {
@@ -570,24 +594,13 @@ __global__ void __launch_bounds__(kBulkThreads, 1) layernorm_bwd_bulk_kernel(con
                 }
             }
         }
-        // 2 ROWS sums over the warp at once: each exchange also halves the
-        // values a lane carries, until lane group k holds sum k.
         float v[2 * ROWS];
 #pragma unroll
         for (int q = 0; q < ROWS; ++q) { v[2 * q] = sum_halves(s1[q]); v[2 * q + 1] = sum_halves(s2[q]); }
-        int o = 16;
-#pragma unroll
-        for (int n = ROWS; n > 0; n >>= 1, o >>= 1) {
-            const bool up = lane & o;
-#pragma unroll
-            for (int k = 0; k < n; ++k)
-                v[k] = (up ? v[k + n] : v[k]) + __shfl_xor_sync(0xffffffffu, up ? v[k] : v[k + n], o);
-        }
-#pragma unroll
-        for (; o > 0; o >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
         constexpr int kSpan = 32 / (2 * ROWS);             // lanes per sum
+        const float part = warp_sums<2 * ROWS>(v);
         float(*buf)[16] = red[turn & 1];                   // two buffers in turn: one barrier a turn is enough
-        if (lane % kSpan == 0) buf[lane / kSpan][warp] = v[0];
+        if (lane % kSpan == 0) buf[lane / kSpan][warp] = part;
         // The group meets once a turn: the sums are there, a wait that ran out
         // stops all of the group, and the previous turn's slots are free.
         ok = named_bar_and(1 + sub, tpr, landed);
@@ -598,16 +611,11 @@ __global__ void __launch_bounds__(kBulkThreads, 1) layernorm_bwd_bulk_kernel(con
         slot += ROWS;
         if (slot == ring_rows) { slot = 0; phase ^= 1; }
         if (p.dx) {
-            const int k = lane % kSpan;
-            float w = 0.f;
-            for (int i = k; i < wpr; i += kSpan) w += buf[lane / kSpan][sub * wpr + i];
-#pragma unroll
-            for (int d = kSpan / 2; d > 0; d >>= 1) w += __shfl_xor_sync(0xffffffffu, w, d);
-            w *= p.inv_cols;
+            const float w = group_sums<2 * ROWS>(buf, sub * wpr, wpr) * p.inv_cols;
 #pragma unroll
             for (int q = 0; q < ROWS; ++q) {
-                const float t1 = __shfl_sync(0xffffffffu, w, sum_lane<ROWS>(2 * q)) * r[q];
-                const float t2 = __shfl_sync(0xffffffffu, w, sum_lane<ROWS>(2 * q + 1)) * r[q] * r[q] * r[q];
+                const float t1 = __shfl_sync(0xffffffffu, w, 2 * q * kSpan) * r[q];
+                const float t2 = __shfl_sync(0xffffffffu, w, (2 * q + 1) * kSpan) * r[q] * r[q] * r[q];
                 if (it + q < mine) {
                     // dx = r a - r mean(a) - (x - mean) r^3 mean(gamma u)
                     const f32x2 nmean = both(-mu[q]), rr = both(r[q]), n1 = both(-t1), n2 = both(-t2);
@@ -659,6 +667,145 @@ __global__ void __launch_bounds__(kBulkThreads, 1) layernorm_bwd_bulk_kernel(con
             }
         }
     }
+}
+
+// Forward of the same rows: a turn's rows go from the ring into registers, so
+// their slots are free again after the first of the two meetings.
+template <typename T, int ROWS>
+__global__ void __launch_bounds__(kBulkThreads, 1) layernorm_fwd_bulk_kernel(const LnParams p, const int ring_rows) {
+    constexpr int V = vec_of<T, WHOLE>(), NV = kBulkElems / V, H = Pairs<T>::N, kSpan = 32 / ROWS;
+    __shared__ float red[2][ROWS][16];
+    __shared__ uint64_t bars[8][kRingMost];
+    __shared__ int abort_word;
+    extern __shared__ __align__(128) uint8_t ring_s[];     // [group][ring_rows][row]
+    volatile int* abort_flag = &abort_word;
+    const int tpr = p.tpr, sub = threadIdx.x / tpr, t = threadIdx.x - sub * tpr, rpb = blockDim.x / tpr;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wpr = tpr >> 5;
+    const int group = blockIdx.x * rpb + sub;
+    const uint32_t row_bytes = (uint32_t)p.cols * sizeof(T);
+    if (t == 0)
+        for (int i = 0; i < ring_rows; ++i) mbar_init(smem_addr(&bars[sub][i]), 1);
+    if (threadIdx.x == 0) abort_word = 0;
+    mbar_fence_init();
+    __syncthreads();
+    pdl_wait();
+    const uint8_t* ring = ring_s + (size_t)sub * ring_rows * row_bytes;
+    const uint32_t bar0 = smem_addr(&bars[sub][0]), ring0 = smem_addr(ring);
+    const int slots = p.cols / V;
+    const int mine = group < p.rows ? (int)((p.rows - group + p.groups - 1) / p.groups) : 0;   // this group's rows
+    const int64_t x_step = (int64_t)p.groups * p.xs, y_step = (int64_t)p.groups * p.ys;
+    const T* x_next = static_cast<const T*>(p.x) + (int64_t)group * p.xs;
+    T* y = static_cast<T*>(p.y) + (int64_t)group * p.ys + t * V;
+    auto issue = [&](int slot) {                           // the next row into its slot (thread 0 of the group)
+        mbar_arrive_expect_tx(bar0 + slot * 8, row_bytes);
+        bulk_load(ring0 + (uint32_t)slot * row_bytes, x_next, row_bytes, bar0 + slot * 8);
+        x_next += x_step;
+    };
+    int issued = 0;
+    if (t == 0)
+        for (; issued < ring_rows && issued < mine; ++issued) issue(issued);
+    f32x2 g[NV][H], b[NV][H];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int s = j * tpr + t;
+        const bool in = s < slots;
+        float f[V], h[V];
+        load_params<T, V>(p.gamma, p.param_f32, s * V, 0, in ? V : 0, p.vec_params && in, 1.f, f);
+        load_params<T, V>(p.beta, p.param_f32, s * V, 0, in ? V : 0, p.vec_params && in, 0.f, h);
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            g[j][i] = pack2f(f[2 * i], f[2 * i + 1]);
+            b[j][i] = pack2f(h[2 * i], h[2 * i + 1]);
+        }
+    }
+    int slot = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int it = 0; it < mine; it += ROWS) {
+        f32x2 f[ROWS][NV][H];
+        float v[ROWS];
+        bool landed = true;
+#pragma unroll
+        for (int q = 0; q < ROWS; ++q) {
+            f32x2 s = 0ull;
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+#pragma unroll
+                for (int i = 0; i < H; ++i) f[q][j][i] = 0ull;
+            if (it + q < mine) {
+                const uint32_t bar = bar0 + (slot + q) * 8;
+                const bool here = mbar_try_wait(bar, phase) || mbar_wait(bar, phase, abort_flag);
+                landed = landed && here;
+                if (here) {
+                    const uint8_t* src = ring + (size_t)(slot + q) * row_bytes + t * 16;
+#pragma unroll
+                    for (int j = 0; j < NV; ++j) {
+                        if (j * tpr + t < slots) {
+                            Pairs<T>::widen(*reinterpret_cast<const uint4*>(src + j * tpr * 16), f[q][j]);
+#pragma unroll
+                            for (int i = 0; i < H; ++i) s = add2(s, f[q][j][i]);
+                        }
+                    }
+                }
+            }
+            v[q] = sum_halves(s);
+        }
+        const float part = warp_sums<ROWS>(v);
+        if (lane % kSpan == 0) red[0][lane / kSpan][warp] = part;
+        ok = named_bar_and(1 + sub, tpr, landed);
+        if (!ok) break;
+        if (t == 0)
+            for (int q = 0; q < ROWS && issued < mine; ++q, ++issued) issue(slot + q);
+        slot += ROWS;
+        if (slot == ring_rows) { slot = 0; phase ^= 1; }
+        const float sum = group_sums<ROWS>(red[0], sub * wpr, wpr) * p.inv_cols;
+        float mean[ROWS];
+#pragma unroll
+        for (int q = 0; q < ROWS; ++q) {
+            mean[q] = __shfl_sync(0xffffffffu, sum, q * kSpan);
+            f32x2 s = 0ull;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                if (j * tpr + t < slots) {
+#pragma unroll
+                    for (int i = 0; i < H; ++i) {
+                        f[q][j][i] = add2(f[q][j][i], both(-mean[q]));
+                        s = fma2(f[q][j][i], f[q][j][i], s);
+                    }
+                }
+            }
+            v[q] = sum_halves(s);
+        }
+        const float part2 = warp_sums<ROWS>(v);
+        if (lane % kSpan == 0) red[1][lane / kSpan][warp] = part2;
+        named_bar_sync(1 + sub, tpr);
+        const float sq = group_sums<ROWS>(red[1], sub * wpr, wpr) * p.inv_cols;
+#pragma unroll
+        for (int q = 0; q < ROWS; ++q) {
+            const float rstd = rsqrtf(__shfl_sync(0xffffffffu, sq, q * kSpan) + p.eps);
+            if (it + q < mine) {
+                if (t == 0) {
+                    const int64_t row = group + (int64_t)(it + q) * p.groups;
+                    if (p.mean) p.mean[row] = mean[q];
+                    if (p.rstd) p.rstd[row] = rstd;
+                }
+#pragma unroll
+                for (int j = 0; j < NV; ++j) {
+                    if (j * tpr + t < slots) {
+                        f32x2 o[H];
+#pragma unroll
+                        for (int i = 0; i < H; ++i) o[i] = fma2(mul2(f[q][j][i], both(rstd)), g[j][i], b[j][i]);
+                        *reinterpret_cast<uint4*>(y + j * tpr * V) = Pairs<T>::narrow(o);
+                    }
+                }
+                y += y_step;
+            }
+        }
+    }
+    // Copies still in flight after a wait that ran out land before the block leaves.
+    if (t == 0 && !ok)
+        for (int i = issued > ring_rows ? issued - ring_rows : 0; i < issued; ++i)
+            mbar_drain_wait(bar0 + (i % ring_rows) * 8, (uint32_t)(i / ring_rows) & 1u);
 }
 
 // Long rows, pass 1: sum a and sum a z of one row's share of columns.
@@ -824,10 +971,42 @@ int cut_of(const void* x, int64_t xs, int64_t cols, size_t e) {
     return whole ? WHOLE : ENDS;
 }
 
+// The ring of a bulk kernel of `rows_held` rows per slot (x; or x and dy): two
+// rows a turn where the ring then still holds two on their way.  False when the
+// call is not for it: rows that are cut or short, or fewer than two a group
+// (there would be nothing to run ahead of).
+struct BulkPlan { int tpr, rpb, rows; bool twice; size_t smem; };
+bool bulk_plan(const LnParams& p, int cut, size_t e, int rows_held, BulkPlan* b) {
+    const int64_t row_bytes = p.cols * (int64_t)e, slots = row_bytes / 16;
+    if (cut != WHOLE || row_bytes < kBulkBytes || p.cols > kBwdCols) return false;
+    b->tpr = threads_for(slots, kBulkElems * (int)e / 16);
+    if (b->tpr < 64) b->tpr = 64;
+    b->rpb = kBulkThreads / b->tpr;
+    if (p.rows < 2 * (int64_t)device_sm_count() * b->rpb) return false;
+    b->rows = (int)(kRingBytes / (b->rpb * rows_held * row_bytes));
+    if (b->rows > kRingMost) b->rows = kRingMost;
+    b->twice = b->rows >= 4;
+    if (b->twice) b->rows &= ~1;
+    b->smem = (size_t)b->rpb * b->rows * rows_held * row_bytes;
+    return true;
+}
+
 template <typename T> cudaError_t fwd_typed(const layernorm_desc& d, LnParams p, cudaStream_t st) {
     const bool scalar = !same_phase(p.x, p.xs, p.y, p.ys, sizeof(T));
     const int cut = scalar ? SINGLE : cut_of(p.x, p.xs, p.cols, sizeof(T));
     const int V = scalar ? 1 : 16 / (int)sizeof(T);
+    BulkPlan bulk;
+    if (p.cols * (int64_t)sizeof(T) >= 2 * kBulkBytes && bulk_plan(p, cut, sizeof(T), 1, &bulk)) {
+        p.tpr = bulk.tpr;
+        p.groups = device_sm_count() * bulk.rpb;
+        auto kern = bulk.rows == 8 ? layernorm_fwd_bulk_kernel<T, 4>
+                    : bulk.twice   ? layernorm_fwd_bulk_kernel<T, 2>
+                                   : layernorm_fwd_bulk_kernel<T, 1>;
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bulk.smem);
+        if (e != cudaSuccess) return e;
+        return launch_after(kern, dim3((unsigned)device_sm_count()), dim3(bulk.rpb * bulk.tpr), bulk.smem, st, p,
+                            bulk.rows);
+    }
     // Vectors of the most unevenly cut row.
     const int shift = scalar                                  ? 0
                       : (p.xs * (int64_t)sizeof(T)) % 16 == 0 ? (int)((reinterpret_cast<uintptr_t>(p.x) & 15u) / sizeof(T))
@@ -905,26 +1084,16 @@ template <typename T> cudaError_t bwd_typed(const layernorm_desc& d, LnParams p,
     const int64_t slots = ceil_div((int64_t)p.cols + most_shift, V);
     const int sms = device_sm_count();
     p.cut_alike = cut_alike;
-    const int64_t row_bytes = (int64_t)p.cols * sizeof(T);
-    if (slots * V <= kBwdCols && cut == WHOLE && row_bytes >= kBulkBytes) {
-        // Bulk copies from two rows a group on (one hides nothing).
-        const int tpr = threads_for(slots, kBulkElems / V) < 64 ? 64 : threads_for(slots, kBulkElems / V);
-        const int rpb = kBulkThreads / tpr;
-        if (p.rows >= 2 * (int64_t)sms * rpb) {
-            p.tpr = tpr;
-            p.groups = sms * rpb;
-            *parts = sms;
-            int rows = (int)(kRingBytes / (rpb * 2 * row_bytes));
-            rows = rows > kRingMost ? kRingMost : rows;
-            const bool twice = rows >= 4;              // two rows a turn, and two on their way
-            if (twice) rows &= ~1;
-            const size_t ring = (size_t)rpb * rows * 2 * row_bytes, sums = 2 * (size_t)p.cols * sizeof(float);
-            const size_t smem = ring > sums ? ring : sums;
-            auto kern = twice ? layernorm_bwd_bulk_kernel<T, 2> : layernorm_bwd_bulk_kernel<T, 1>;
-            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-            if (e != cudaSuccess) return e;
-            return launch_after(kern, dim3((unsigned)sms), dim3(rpb * tpr), smem, st, p, rows);
-        }
+    BulkPlan bulk;
+    if (bulk_plan(p, cut, sizeof(T), 2, &bulk)) {
+        p.tpr = bulk.tpr;
+        p.groups = sms * bulk.rpb;
+        *parts = sms;
+        const size_t sums = 2 * (size_t)p.cols * sizeof(float), smem = bulk.smem > sums ? bulk.smem : sums;
+        auto kern = bulk.twice ? layernorm_bwd_bulk_kernel<T, 2> : layernorm_bwd_bulk_kernel<T, 1>;
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        return launch_after(kern, dim3((unsigned)sms), dim3(bulk.rpb * bulk.tpr), smem, st, p, bulk.rows);
     }
     if (slots * V <= kBwdCols) {
         // As many threads a row as keep one vector each, or eight elements.

@@ -13,7 +13,7 @@
 //
 // Backward: dx needs sum a and sum a z over the channels of a pixel (a = dy
 // gamma, z = (x - mean) rstd); dgamma and dbeta are sums over all pixels.
-// Each warp owns 32 channels of a 512-channel step; their sums over the
+// Each warp owns 32 channels at a time; their sums over the
 // tile's words are transposed-and-added across the half-warp, so one lane ends
 // up with one channel, and collect in shared memory over the block's tiles.
 //
@@ -34,7 +34,8 @@ namespace conv2d_gb300 {
 namespace {
 
 constexpr int kWords = 16, kPitch = 17;     // words of pixels per tile, and their pitch in shared memory
-constexpr int kFwdThreads = 256, kBwdThreads = 512;
+// Threads of a block: few channels make small tiles, and blocks that meet less widely.
+int threads_of(int C) { return C <= 128 ? 128 : 512; }
 
 struct PlaneParams {
     int64_t rows, pixels, ys, tiles;
@@ -88,8 +89,8 @@ template <int PP> struct Spot {
     __device__ __forceinline__ Spot(const PlaneParams& p, int64_t tile, int word) {
         row = (tile * kWords + word) * PP;
         live = row < p.rows;
-        const int64_t n = live ? row / p.pixels : 0;
-        off = live ? n * p.C * p.pixels + (row - n * p.pixels) : 0;
+        const uint32_t n = live ? (uint32_t)row / (uint32_t)p.pixels : 0;      // both below 2^31
+        off = live ? (int64_t)n * p.C * p.pixels + ((uint32_t)row - n * (uint32_t)p.pixels) : 0;
     }
 };
 
@@ -120,10 +121,10 @@ __device__ __forceinline__ void across_halves(float (&v)[PP], int half, int word
     __syncthreads();
 }
 
-template <typename T, int PP>
-__global__ void __launch_bounds__(kFwdThreads, 4) planes_fwd_kernel(const PlaneParams p) {
+template <typename T, int PP, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) planes_fwd_kernel(const PlaneParams p) {
     extern __shared__ uint32_t tile_s[];
-    __shared__ float red[PP][kFwdThreads / 16][kWords + 1];
+    __shared__ float red[PP][THREADS / 16][kWords + 1];
     __shared__ float stat[2][PP][kWords];
     pdl_wait();
     const int half = threadIdx.x >> 4, word = threadIdx.x & 15;
@@ -141,9 +142,9 @@ __global__ void __launch_bounds__(kFwdThreads, 4) planes_fwd_kernel(const PlaneP
             for (int k = 0; k < chunks; ++k) {
                 const int c0 = k * p.chunk, n = min(p.chunk, p.C - c0);
                 // Each thread sums the channels that it loaded itself: no barrier in between.
-                if (chunks > 1 || pass == 0) load_planes<T, PP, kFwdThreads>(p, s, c0, n, half, word, tile_s);
+                if (chunks > 1 || pass == 0) load_planes<T, PP, THREADS>(p, s, c0, n, half, word, tile_s);
 #pragma unroll 4
-                for (int c = half; c < n; c += kFwdThreads / 16) {
+                for (int c = half; c < n; c += THREADS / 16) {
                     float f[PP];
                     Word<T, PP>::widen(tile_s[c * kPitch + word], f);
 #pragma unroll
@@ -153,7 +154,7 @@ __global__ void __launch_bounds__(kFwdThreads, 4) planes_fwd_kernel(const PlaneP
                     }
                 }
             }
-            across_halves<PP, kFwdThreads>(v, half, word, red);
+            across_halves<PP, THREADS>(v, half, word, red);
 #pragma unroll
             for (int i = 0; i < PP; ++i) {
                 if (pass == 0) mean[i] = v[i] * p.inv_c;
@@ -173,7 +174,7 @@ __global__ void __launch_bounds__(kFwdThreads, 4) planes_fwd_kernel(const PlaneP
             const int c0 = k * p.chunk, n = min(p.chunk, p.C - c0);
             if (chunks > 1) {
                 __syncthreads();                       // the previous chunk has been written out
-                load_planes<T, PP, kFwdThreads>(p, s, c0, n, half, word, tile_s);
+                load_planes<T, PP, THREADS>(p, s, c0, n, half, word, tile_s);
             }
             __syncthreads();
             T* y = static_cast<T*>(p.y) + c0;
@@ -186,7 +187,7 @@ __global__ void __launch_bounds__(kFwdThreads, 4) planes_fwd_kernel(const PlaneP
                         b[i] = param_at(p.beta, p.param_f32, is_bf16<T>, c0 + c + i, 0.f);
                     }
 #pragma unroll
-                    for (int w = warp; w < kWords; w += kFwdThreads / 32) {
+                    for (int w = warp; w < kWords; w += THREADS / 32) {
                         const int64_t row = (tile * kWords + w) * PP;
                         if (row >= p.rows) continue;
                         float f[2][PP];
@@ -205,7 +206,7 @@ __global__ void __launch_bounds__(kFwdThreads, 4) planes_fwd_kernel(const PlaneP
                     const float g = param_at(p.gamma, p.param_f32, is_bf16<T>, c0 + c, 1.f);
                     const float b = param_at(p.beta, p.param_f32, is_bf16<T>, c0 + c, 0.f);
 #pragma unroll
-                    for (int w = warp; w < kWords; w += kFwdThreads / 32) {
+                    for (int w = warp; w < kWords; w += THREADS / 32) {
                         const int64_t row = (tile * kWords + w) * PP;
                         if (row >= p.rows) continue;
                         float f[PP];
@@ -223,11 +224,11 @@ __global__ void __launch_bounds__(kFwdThreads, 4) planes_fwd_kernel(const PlaneP
 }
 
 // One chunk of dy, read along channels, into shared memory as [channel][word].
-template <typename T, int PP>
+template <typename T, int PP, int THREADS>
 __device__ __forceinline__ void load_rows(const PlaneParams& p, int64_t tile, int c0, int n, int warp, int lane,
                                           uint32_t* dst) {
     const T* dy = static_cast<const T*>(p.dy) + c0;
-    for (int w = warp; w < kWords; w += kBwdThreads / 32) {
+    for (int w = warp; w < kWords; w += THREADS / 32) {
         const int64_t row = (tile * kWords + w) * PP;
         const bool live = row < p.rows;
         if constexpr (PP == 2) {
@@ -255,10 +256,10 @@ __device__ __forceinline__ void load_rows(const PlaneParams& p, int64_t tile, in
     }
 }
 
-template <typename T, int PP>
-__global__ void __launch_bounds__(kBwdThreads, 2) planes_bwd_kernel(const PlaneParams p) {
+template <typename T, int PP, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) planes_bwd_kernel(const PlaneParams p) {
     extern __shared__ uint32_t smem[];
-    __shared__ float red[PP][kBwdThreads / 16][kWords + 1];
+    __shared__ float red[PP][THREADS / 16][kWords + 1];
     const int chunks = (p.C + p.chunk - 1) / p.chunk;
     uint32_t* xs = smem;                                           // [chunk][17]
     uint32_t* ds = xs + p.chunk * kPitch;                          // [chunk][17]
@@ -267,7 +268,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) planes_bwd_kernel(const PlaneP
     pdl_wait();
     const int half = threadIdx.x >> 4, word = threadIdx.x & 15;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int c = threadIdx.x; c < p.C; c += kBwdThreads) {
+    for (int c = threadIdx.x; c < p.C; c += THREADS) {
         gam[c] = param_at(p.gamma, p.param_f32, is_bf16<T>, c, 1.f);
         acc[c] = acc[p.C + c] = 0.f;
     }
@@ -284,11 +285,11 @@ __global__ void __launch_bounds__(kBwdThreads, 2) planes_bwd_kernel(const PlaneP
         for (int k = 0; k < chunks; ++k) {
             const int c0 = k * p.chunk, n = min(p.chunk, p.C - c0);
             if (k > 0) __syncthreads();
-            load_planes<T, PP, kBwdThreads>(p, s, c0, n, half, word, xs);
-            load_rows<T, PP>(p, tile, c0, n, warp, lane, ds);
+            load_planes<T, PP, THREADS>(p, s, c0, n, half, word, xs);
+            load_rows<T, PP, THREADS>(p, tile, c0, n, warp, lane, ds);
             __syncthreads();
 #pragma unroll 4
-            for (int c = half; c < n; c += kBwdThreads / 16) {
+            for (int c = half; c < n; c += THREADS / 16) {
                 float fx[PP], fd[PP];
                 Word<T, PP>::widen(xs[c * kPitch + word], fx);
                 Word<T, PP>::widen(ds[c * kPitch + word], fd);
@@ -301,8 +302,8 @@ __global__ void __launch_bounds__(kBwdThreads, 2) planes_bwd_kernel(const PlaneP
                 }
             }
         }
-        across_halves<PP, kBwdThreads>(s1, half, word, red);
-        across_halves<PP, kBwdThreads>(s2, half, word, red);
+        across_halves<PP, THREADS>(s1, half, word, red);
+        across_halves<PP, THREADS>(s2, half, word, red);
 #pragma unroll
         for (int i = 0; i < PP; ++i) {
             s1[i] *= p.inv_c;
@@ -312,13 +313,13 @@ __global__ void __launch_bounds__(kBwdThreads, 2) planes_bwd_kernel(const PlaneP
             const int c0 = k * p.chunk, n = min(p.chunk, p.C - c0);
             if (chunks > 1) {
                 __syncthreads();
-                load_planes<T, PP, kBwdThreads>(p, s, c0, n, half, word, xs);
-                load_rows<T, PP>(p, tile, c0, n, warp, lane, ds);
+                load_planes<T, PP, THREADS>(p, s, c0, n, half, word, xs);
+                load_rows<T, PP, THREADS>(p, tile, c0, n, warp, lane, ds);
                 __syncthreads();
             }
             T* dx = static_cast<T*>(p.dx) + s.off + (int64_t)c0 * p.pixels;
             // A warp's 32 channels in 16 steps of two (one per half-warp).
-            for (int cb = warp * 32; cb < n; cb += kBwdThreads) {
+            for (int cb = warp * 32; cb < n; cb += THREADS) {
                 float vg[16], vb[16];
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
@@ -368,7 +369,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) planes_bwd_kernel(const PlaneP
         __syncthreads();
     }
     if (p.want_params)
-        for (int c = threadIdx.x; c < 2 * p.C; c += kBwdThreads) p.part[(int64_t)blockIdx.x * 2 * p.C + c] = acc[c];
+        for (int c = threadIdx.x; c < 2 * p.C; c += THREADS) p.part[(int64_t)blockIdx.x * 2 * p.C + c] = acc[c];
 }
 
 // ------------------------------------------------------------------ 16-bit, 8 x 8 blocks
@@ -793,7 +794,6 @@ planes16_bwd_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_const
 }
 
 constexpr int kSmemMost = 200 * 1024;
-constexpr int kBlocksPerSm = 2;       // backward grid, in blocks per SM
 
 int chunk_of(int C, int tiles_held, int other_bytes) {
     const int64_t most = (kSmemMost - other_bytes) / (tiles_held * kPitch * 4);
@@ -801,29 +801,33 @@ int chunk_of(int C, int tiles_held, int other_bytes) {
     return (int)(most / 32 * 32);
 }
 
-template <typename T, int PP>
-cudaError_t fwd_planes(PlaneParams p, cudaStream_t st) {
+template <typename T, int PP, int THREADS>
+cudaError_t fwd_planes_at(PlaneParams p, cudaStream_t st) {
     p.tiles = (p.rows + kWords * PP - 1) / (kWords * PP);
     p.chunk = chunk_of(p.C, 1, 0);
     const int smem = p.chunk * kPitch * 4;
-    cudaError_t e = cudaFuncSetAttribute(planes_fwd_kernel<T, PP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = cudaFuncSetAttribute(planes_fwd_kernel<T, PP, THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    int64_t grid = (int64_t)device_sm_count() * 8;
+    int64_t grid = (int64_t)device_sm_count() * (2048 / THREADS);
     if (grid > p.tiles) grid = p.tiles;
-    return launch_after(planes_fwd_kernel<T, PP>, dim3((unsigned)grid), dim3(kFwdThreads), smem, st, p);
+    return launch_after(planes_fwd_kernel<T, PP, THREADS>, dim3((unsigned)grid), dim3(THREADS), smem, st, p);
 }
 
-template <typename T, int PP>
-cudaError_t bwd_planes(PlaneParams p, int* parts, cudaStream_t st) {
+template <typename T, int PP> cudaError_t fwd_planes(const PlaneParams& p, cudaStream_t st) {
+    return threads_of(p.C) == 128 ? fwd_planes_at<T, PP, 128>(p, st) : fwd_planes_at<T, PP, 512>(p, st);
+}
+
+template <typename T, int PP, int THREADS>
+cudaError_t bwd_planes_at(PlaneParams p, int* parts, cudaStream_t st) {
     p.tiles = (p.rows + kWords * PP - 1) / (kWords * PP);
     p.chunk = chunk_of(p.C, 2, 3 * p.C * 4);
     const int smem = 2 * p.chunk * kPitch * 4 + 3 * p.C * 4;
-    cudaError_t e = cudaFuncSetAttribute(planes_bwd_kernel<T, PP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = cudaFuncSetAttribute(planes_bwd_kernel<T, PP, THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    int64_t grid = (int64_t)device_sm_count() * kBlocksPerSm;
+    int64_t grid = (int64_t)device_sm_count() * (1024 / THREADS);
     if (grid > p.tiles) grid = p.tiles;
     *parts = (int)grid;
-    return launch_after(planes_bwd_kernel<T, PP>, dim3((unsigned)grid), dim3(kBwdThreads), smem, st, p);
+    return launch_after(planes_bwd_kernel<T, PP, THREADS>, dim3((unsigned)grid), dim3(THREADS), smem, st, p);
 }
 
 // Whether the 16-bit form serves the call: what TMA moves starts and repeats at
@@ -916,6 +920,10 @@ template <typename T> cudaError_t bwd_16(const PlaneParams& p, int* parts, cudaS
     return bwd_fast<T, 2, 2, 2>(p, parts, st);
 }
 
+template <typename T, int PP> cudaError_t bwd_planes(const PlaneParams& p, int* parts, cudaStream_t st) {
+    return threads_of(p.C) == 128 ? bwd_planes_at<T, PP, 128>(p, parts, st) : bwd_planes_at<T, PP, 512>(p, parts, st);
+}
+
 PlaneParams params_of(const layernorm_desc& d) {
     PlaneParams p{};
     p.rows = d.rows; p.pixels = d.pixels; p.ys = d.ys; p.C = (int)d.cols;
@@ -954,7 +962,7 @@ cudaError_t launch_layernorm_planes_fwd(const layernorm_desc& d, const void* x, 
 }
 
 size_t layernorm_planes_bwd_workspace(const layernorm_desc& d) {
-    return (size_t)device_sm_count() * kBlocksPerSm * 2 * (size_t)d.cols * sizeof(float);
+    return (size_t)device_sm_count() * (1024 / threads_of((int)d.cols)) * 2 * (size_t)d.cols * sizeof(float);
 }
 
 cudaError_t launch_layernorm_planes_bwd(const layernorm_desc& d, const void* dy, const void* x, const void* gamma,

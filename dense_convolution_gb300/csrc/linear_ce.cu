@@ -278,6 +278,7 @@ ce_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ Ge
     // full[stages], empty[stages], accumulator full[2], empty[2], drain
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kMaxRing + 5);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    volatile int* copies = abort_flag + 1;                 // PAIR: ring fills that this CTA has issued
     auto full_bar = [&](int i) { return smem_addr(&bars[i]); };
     auto empty_bar = [&](int i) { return smem_addr(&bars[kMaxRing + i]); };
     auto accf_bar = [&](int a) { return smem_addr(&bars[2 * kMaxRing + a]); };
@@ -290,6 +291,7 @@ ce_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ Ge
         for (int a = 0; a < 2; ++a) { mbar_init(accf_bar(a), 1); mbar_init(acce_bar(a), kCtas * kEpiWarps); }
         mbar_init(drain_bar, 1);
         *abort_flag = 0;
+        *copies = 0;
         mbar_fence_init();
         tma_prefetch_desc(&maps.a[0]);
         tma_prefetch_desc(&maps.b[0]);
@@ -364,13 +366,13 @@ ce_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ Ge
                     if (++k == nk) { k = 0; ++pair; }
                 }
             }
+            if constexpr (PAIR) *copies = (int)issued;         // (only the last ring's worth matters below)
             if (!ok) {
-                // Let every copy already issued land before the CTA can exit.
-                // (A pair's first CTA waits for both; the other one meets it at
-                // the end.  If the other has given up too, one limit covers all.)
-                for (int i = 0; i < stages && i < issued && rank == 0; ++i) {
+                // Let every copy already issued land before the CTA can exit (a
+                // pair's CTAs settle this together, below).
+                for (int i = 0; !PAIR && i < stages && i < issued; ++i) {
                     if (--stage < 0) { stage = stages - 1; phase ^= 1; }
-                    if (!mbar_drain_wait(full_bar(stage), phase)) break;
+                    mbar_drain_wait(full_bar(stage), phase);
                 }
             } else if (PAIR) {
                 // Every commit's arrival is in before either CTA can exit.
@@ -619,9 +621,29 @@ ce_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ Ge
 
     tc_fence_before();
     __syncthreads();
-    if constexpr (PAIR) {                                  // both CTAs are done with each other's memory
+    if constexpr (PAIR) {
         __syncwarp();
-        cluster_sync();
+        cluster_sync();                                    // both CTAs are done with each other's memory
+        const uint32_t other = rank ^ 1;
+        const uint32_t stopped = ld_cluster(cluster_addr(smem_addr(const_cast<int*>(abort_flag)), other));
+        if (*abort_flag || stopped) {
+            // A wait ran out.  The two CTAs may have stopped at different fills;
+            // the issuing CTA's barriers count both CTAs' bytes.  It adds what
+            // the one that is behind never sent, or expects what the one ahead
+            // did send, and sees every copy land before either CTA leaves.
+            if (rank == 0 && threadIdx.x == 0) {
+                const int own = *copies, far = (int)ld_cluster(cluster_addr(smem_addr(const_cast<int*>(copies)), other));
+                const int last = own > far ? own : far;
+                for (int c = last > stages ? last - stages : 0; c < last; ++c) {
+                    const uint32_t bar = full_bar(c % stages);
+                    if (c >= far) mbar_complete_tx(bar, (uint32_t)stage_bytes);
+                    else if (c >= own) mbar_arrive_expect_tx(bar, (uint32_t)stage_bytes);
+                    if (!mbar_drain_wait(bar, (uint32_t)(c / stages) & 1u)) break;
+                }
+            }
+            __syncthreads();
+            cluster_sync();
+        }
     }
     if (warp == 1) {
         __syncwarp();
@@ -930,7 +952,7 @@ bool allow_smem(const void* kern) {
     return true;
 }
 
-constexpr int kFixedSmem = 1024 + (2 * kMaxRing + 5) * 8 + 16;
+constexpr int kFixedSmem = 1024 + (2 * kMaxRing + 5) * 8 + 24;
 
 cudaError_t launch_clusters(const void* kern, int grid, int threads, int ctas, int smem, cudaStream_t st, void** args) {
     cudaLaunchConfig_t cfg = {};

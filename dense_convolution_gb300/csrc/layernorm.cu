@@ -318,7 +318,7 @@ template <typename T, int CUT, int NV, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) layernorm_bwd_kernel(const LnParams p) {
     constexpr int V = vec_of<T, CUT>();
     __shared__ float2 red[2][32];
-    extern __shared__ float acc_s[];                   // [2][cols] when several groups share the block
+    extern __shared__ float acc_s[];                   // [group][2][cols] when several groups share the block
     pdl_wait();
     pdl_launch_dependents();                           // one wave: the reduction's blocks wait beside it
     const int tpr = p.tpr, rpb = blockDim.x / tpr, sub = threadIdx.x / tpr, t = threadIdx.x - sub * tpr;
@@ -423,8 +423,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) layernorm_bwd_kernel(
     }
     if (!p.want_params) return;
     float* out = p.part + (int64_t)blockIdx.x * 2 * p.cols;
-    // Groups that share a warp and its cut are added there first.
-    int steps = rpb, mine = sub;
+    // Groups that share a warp and its cut are added there first; the rest lie
+    // side by side in shared memory and are added in order.
+    int held = rpb, mine = sub;
     if (tpr < 32 && p.cut_alike) {
 #pragma unroll
         for (int j = 0; j < NV; ++j)
@@ -434,26 +435,30 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) layernorm_bwd_kernel(
                     dg[j][i] += __shfl_xor_sync(0xffffffffu, dg[j][i], o);
                     db[j][i] += __shfl_xor_sync(0xffffffffu, db[j][i], o);
                 }
-        steps = blockDim.x >> 5;
+        held = blockDim.x >> 5;
         mine = lane < tpr ? warp : -1;
     }
-    for (int k = 0; k < steps; ++k) {
-        if (k > 0) __syncthreads();
-        if (mine == k) {
-            float* dst = k + 1 < steps ? acc_s : out;
+    float* dst = held > 1 ? acc_s + (int64_t)mine * 2 * p.cols : out;
+    if (mine >= 0) {
 #pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int s = j * tpr + t, e0 = s * V - shift;
+        for (int j = 0; j < NV; ++j) {
+            const int s = j * tpr + t, e0 = s * V - shift;
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const int c = e0 + i;
-                    if (s < slots && (CUT != ENDS || (c >= 0 && c < p.cols))) {
-                        dst[c] = dg[j][i] + (k ? acc_s[c] : 0.f);
-                        dst[p.cols + c] = db[j][i] + (k ? acc_s[p.cols + c] : 0.f);
-                    }
+            for (int i = 0; i < V; ++i) {
+                const int c = e0 + i;
+                if (s < slots && (CUT != ENDS || (c >= 0 && c < p.cols))) {
+                    dst[c] = dg[j][i];
+                    dst[p.cols + c] = db[j][i];
                 }
             }
         }
+    }
+    if (held == 1) return;
+    __syncthreads();
+    for (int c = threadIdx.x; c < 2 * p.cols; c += blockDim.x) {
+        float u = acc_s[c];
+        for (int k = 1; k < held; ++k) u += acc_s[k * 2 * p.cols + c];
+        out[c] = u;
     }
 }
 
@@ -462,8 +467,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) layernorm_bwd_kernel(
 // depends on registers, and x and dy are read from shared memory twice (sums,
 // then dx) instead of being kept.  What bounds this kernel is instructions (46
 // an element with eight elements a thread and one row a turn), so a thread
-// takes sixteen elements, a turn ROWS rows whose four sums share their
-// exchanges and barrier, and the arithmetic is packed two by two.
+// takes sixteen elements, a turn ROWS rows whose sums share their exchanges and
+// barrier, the arithmetic is packed two by two, and rows that fill their threads
+// exactly (FULL) get a kernel without the tests for the ones that do not.
 constexpr int kBulkBytes = 1024, kBulkThreads = 512, kBulkElems = 16, kRingBytes = 192 * 1024, kRingMost = 8;
 
 // N sums (a power of two) over a warp at once: each exchange also halves the
@@ -494,13 +500,13 @@ template <int N> __device__ __forceinline__ float group_sums(const float (*buf)[
     return w;
 }
 
-template <typename T, int ROWS>
+template <typename T, int ROWS, bool FULL>
 __global__ void __launch_bounds__(kBulkThreads, 1) layernorm_bwd_bulk_kernel(const LnParams p, const int ring_rows) {
     constexpr int V = vec_of<T, WHOLE>(), NV = kBulkElems / V, H = Pairs<T>::N;
     __shared__ float red[2][2 * ROWS][16];
     __shared__ uint64_t bars[8][kRingMost];                // a group is at least two warps
     __shared__ int abort_word;
-    extern __shared__ __align__(128) uint8_t ring_s[];     // [group][ring_rows][x row, dy row]; then sums [2][cols]
+    extern __shared__ __align__(128) uint8_t ring_s[];     // [group][ring_rows][x row, dy row]; then sums
     volatile int* abort_flag = &abort_word;
     const int tpr = p.tpr, rpb = blockDim.x / tpr, sub = threadIdx.x / tpr, t = threadIdx.x - sub * tpr;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -520,7 +526,7 @@ __global__ void __launch_bounds__(kBulkThreads, 1) layernorm_bwd_bulk_kernel(con
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int s = j * tpr + t;
-        const bool in = s < slots;
+        const bool in = FULL || s < slots;
         float f[V];
         load_params<T, V>(p.gamma, p.param_f32, s * V, 0, in ? V : 0, p.vec_params && in, 1.f, f);
 #pragma unroll
@@ -577,7 +583,7 @@ __global__ void __launch_bounds__(kBulkThreads, 1) layernorm_bwd_bulk_kernel(con
                     const f32x2 nmean = both(-mu[q]), rr = both(r[q]);
 #pragma unroll
                     for (int j = 0; j < NV; ++j) {
-                        if (j * tpr + t < slots) {
+                        if (FULL || j * tpr + t < slots) {
                             f32x2 fx[H], fd[H];
                             Pairs<T>::widen(*reinterpret_cast<const uint4*>(src[q] + j * tpr * 16), fx);
                             Pairs<T>::widen(*reinterpret_cast<const uint4*>(src[q] + row_bytes + j * tpr * 16), fd);
@@ -621,7 +627,7 @@ __global__ void __launch_bounds__(kBulkThreads, 1) layernorm_bwd_bulk_kernel(con
                     const f32x2 nmean = both(-mu[q]), rr = both(r[q]), n1 = both(-t1), n2 = both(-t2);
 #pragma unroll
                     for (int j = 0; j < NV; ++j) {
-                        if (j * tpr + t < slots) {
+                        if (FULL || j * tpr + t < slots) {
                             f32x2 fx[H], fd[H];
                             Pairs<T>::widen(*reinterpret_cast<const uint4*>(src[q] + j * tpr * 16), fx);
                             Pairs<T>::widen(*reinterpret_cast<const uint4*>(src[q] + row_bytes + j * tpr * 16), fd);
@@ -643,35 +649,41 @@ __global__ void __launch_bounds__(kBulkThreads, 1) layernorm_bwd_bulk_kernel(con
         for (int i = issued > ring_rows ? issued - ring_rows : 0; i < issued; ++i)
             mbar_drain_wait(bar0 + (i % ring_rows) * 8, (uint32_t)(i / ring_rows) & 1u);
     if (!p.want_params) return;
-    float* acc_s = reinterpret_cast<float*>(ring_s);       // the ring is done with
-    float* out = p.part + (int64_t)blockIdx.x * 2 * p.cols;
-    for (int k = 0; k < rpb; ++k) {
-        __syncthreads();
-        if (sub == k) {
-            float* dst = k + 1 < rpb ? acc_s : out;
+    // The groups' sums side by side where the ring was, then added in order.
+    float4* acc_s = reinterpret_cast<float4*>(ring_s);     // [group][2][cols]
+    const int quads = p.cols / 4;
+    __syncthreads();
 #pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                if (j * tpr + t < slots) {
+    for (int j = 0; j < NV; ++j) {
+        if (FULL || j * tpr + t < slots) {
 #pragma unroll
-                    for (int i = 0; i < H; ++i) {
-                        const int c = (j * tpr + t) * V + 2 * i;
-                        float a0, a1, b0, b1;
-                        unpack2f(dg[j][i], a0, a1);
-                        unpack2f(db[j][i], b0, b1);
-                        dst[c] = a0 + (k ? acc_s[c] : 0.f);
-                        dst[c + 1] = a1 + (k ? acc_s[c + 1] : 0.f);
-                        dst[p.cols + c] = b0 + (k ? acc_s[p.cols + c] : 0.f);
-                        dst[p.cols + c + 1] = b1 + (k ? acc_s[p.cols + c + 1] : 0.f);
-                    }
-                }
+            for (int i = 0; i < H; i += 2) {
+                const int at = sub * 2 * quads + ((j * tpr + t) * V + 2 * i) / 4;
+                float4 u, w;
+                unpack2f(dg[j][i], u.x, u.y);
+                unpack2f(dg[j][i + 1], u.z, u.w);
+                unpack2f(db[j][i], w.x, w.y);
+                unpack2f(db[j][i + 1], w.z, w.w);
+                acc_s[at] = u;
+                acc_s[at + quads] = w;
             }
         }
+    }
+    __syncthreads();
+    float4* out = reinterpret_cast<float4*>(p.part + (int64_t)blockIdx.x * 2 * p.cols);
+    for (int c = threadIdx.x; c < 2 * quads; c += blockDim.x) {
+        float4 u = acc_s[c];
+        for (int k = 1; k < rpb; ++k) {
+            const float4 w = acc_s[k * 2 * quads + c];
+            u.x += w.x; u.y += w.y; u.z += w.z; u.w += w.w;
+        }
+        out[c] = u;
     }
 }
 
 // Forward of the same rows: a turn's rows go from the ring into registers, so
 // their slots are free again after the first of the two meetings.
-template <typename T, int ROWS>
+template <typename T, int ROWS, bool FULL>
 __global__ void __launch_bounds__(kBulkThreads, 1) layernorm_fwd_bulk_kernel(const LnParams p, const int ring_rows) {
     constexpr int V = vec_of<T, WHOLE>(), NV = kBulkElems / V, H = Pairs<T>::N, kSpan = 32 / ROWS;
     __shared__ float red[2][ROWS][16];
@@ -708,7 +720,7 @@ __global__ void __launch_bounds__(kBulkThreads, 1) layernorm_fwd_bulk_kernel(con
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int s = j * tpr + t;
-        const bool in = s < slots;
+        const bool in = FULL || s < slots;
         float f[V], h[V];
         load_params<T, V>(p.gamma, p.param_f32, s * V, 0, in ? V : 0, p.vec_params && in, 1.f, f);
         load_params<T, V>(p.beta, p.param_f32, s * V, 0, in ? V : 0, p.vec_params && in, 0.f, h);
@@ -728,10 +740,6 @@ __global__ void __launch_bounds__(kBulkThreads, 1) layernorm_fwd_bulk_kernel(con
 #pragma unroll
         for (int q = 0; q < ROWS; ++q) {
             f32x2 s = 0ull;
-#pragma unroll
-            for (int j = 0; j < NV; ++j)
-#pragma unroll
-                for (int i = 0; i < H; ++i) f[q][j][i] = 0ull;
             if (it + q < mine) {
                 const uint32_t bar = bar0 + (slot + q) * 8;
                 const bool here = mbar_try_wait(bar, phase) || mbar_wait(bar, phase, abort_flag);
@@ -740,7 +748,7 @@ __global__ void __launch_bounds__(kBulkThreads, 1) layernorm_fwd_bulk_kernel(con
                     const uint8_t* src = ring + (size_t)(slot + q) * row_bytes + t * 16;
 #pragma unroll
                     for (int j = 0; j < NV; ++j) {
-                        if (j * tpr + t < slots) {
+                        if (FULL || j * tpr + t < slots) {
                             Pairs<T>::widen(*reinterpret_cast<const uint4*>(src + j * tpr * 16), f[q][j]);
 #pragma unroll
                             for (int i = 0; i < H; ++i) s = add2(s, f[q][j][i]);
@@ -766,7 +774,7 @@ __global__ void __launch_bounds__(kBulkThreads, 1) layernorm_fwd_bulk_kernel(con
             f32x2 s = 0ull;
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                if (j * tpr + t < slots) {
+                if (FULL || j * tpr + t < slots) {
 #pragma unroll
                     for (int i = 0; i < H; ++i) {
                         f[q][j][i] = add2(f[q][j][i], both(-mean[q]));
@@ -791,7 +799,7 @@ __global__ void __launch_bounds__(kBulkThreads, 1) layernorm_fwd_bulk_kernel(con
                 }
 #pragma unroll
                 for (int j = 0; j < NV; ++j) {
-                    if (j * tpr + t < slots) {
+                    if (FULL || j * tpr + t < slots) {
                         f32x2 o[H];
 #pragma unroll
                         for (int i = 0; i < H; ++i) o[i] = fma2(mul2(f[q][j][i], both(rstd)), g[j][i], b[j][i]);
@@ -975,12 +983,13 @@ int cut_of(const void* x, int64_t xs, int64_t cols, size_t e) {
 // rows a turn where the ring then still holds two on their way.  False when the
 // call is not for it: rows that are cut or short, or fewer than two a group
 // (there would be nothing to run ahead of).
-struct BulkPlan { int tpr, rpb, rows; bool twice; size_t smem; };
+struct BulkPlan { int tpr, rpb, rows; bool twice, full; size_t smem; };
 bool bulk_plan(const LnParams& p, int cut, size_t e, int rows_held, BulkPlan* b) {
     const int64_t row_bytes = p.cols * (int64_t)e, slots = row_bytes / 16;
     if (cut != WHOLE || row_bytes < kBulkBytes || p.cols > kBwdCols) return false;
     b->tpr = threads_for(slots, kBulkElems * (int)e / 16);
     if (b->tpr < 64) b->tpr = 64;
+    b->full = (int64_t)b->tpr * (kBulkElems * (int)e / 16) == slots;
     b->rpb = kBulkThreads / b->tpr;
     if (p.rows < 2 * (int64_t)device_sm_count() * b->rpb) return false;
     b->rows = (int)(kRingBytes / (b->rpb * rows_held * row_bytes));
@@ -999,9 +1008,12 @@ template <typename T> cudaError_t fwd_typed(const layernorm_desc& d, LnParams p,
     if (p.cols * (int64_t)sizeof(T) >= 2 * kBulkBytes && bulk_plan(p, cut, sizeof(T), 1, &bulk)) {
         p.tpr = bulk.tpr;
         p.groups = device_sm_count() * bulk.rpb;
-        auto kern = bulk.rows == 8 ? layernorm_fwd_bulk_kernel<T, 4>
-                    : bulk.twice   ? layernorm_fwd_bulk_kernel<T, 2>
-                                   : layernorm_fwd_bulk_kernel<T, 1>;
+#define LN_FWD_BULK(FULL)                                          \
+    (bulk.rows == 8 ? layernorm_fwd_bulk_kernel<T, 4, FULL>        \
+     : bulk.twice   ? layernorm_fwd_bulk_kernel<T, 2, FULL>        \
+                    : layernorm_fwd_bulk_kernel<T, 1, FULL>)
+        auto kern = bulk.full ? LN_FWD_BULK(true) : LN_FWD_BULK(false);
+#undef LN_FWD_BULK
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bulk.smem);
         if (e != cudaSuccess) return e;
         return launch_after(kern, dim3((unsigned)device_sm_count()), dim3(bulk.rpb * bulk.tpr), bulk.smem, st, p,
@@ -1089,8 +1101,10 @@ template <typename T> cudaError_t bwd_typed(const layernorm_desc& d, LnParams p,
         p.tpr = bulk.tpr;
         p.groups = sms * bulk.rpb;
         *parts = sms;
-        const size_t sums = 2 * (size_t)p.cols * sizeof(float), smem = bulk.smem > sums ? bulk.smem : sums;
-        auto kern = bulk.twice ? layernorm_bwd_bulk_kernel<T, 2> : layernorm_bwd_bulk_kernel<T, 1>;
+        const size_t sums = (size_t)bulk.rpb * 2 * p.cols * sizeof(float), smem = bulk.smem > sums ? bulk.smem : sums;
+        auto kern = bulk.full ? (bulk.twice ? layernorm_bwd_bulk_kernel<T, 2, true> : layernorm_bwd_bulk_kernel<T, 1, true>)
+                              : (bulk.twice ? layernorm_bwd_bulk_kernel<T, 2, false>
+                                            : layernorm_bwd_bulk_kernel<T, 1, false>);
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
         return launch_after(kern, dim3((unsigned)sms), dim3(bulk.rpb * bulk.tpr), smem, st, p, bulk.rows);
@@ -1108,7 +1122,7 @@ template <typename T> cudaError_t bwd_typed(const layernorm_desc& d, LnParams p,
         if (!cut_alike) grid = ceil_div(grid, V) * V;
         p.groups = (int)grid * rpb;
         *parts = (int)grid;
-        const size_t smem = rpb > 1 && p.want_params ? 2 * (size_t)p.cols * sizeof(float) : 0;
+        const size_t smem = rpb > 1 && p.want_params ? (size_t)rpb * 2 * p.cols * sizeof(float) : 0;   // 32 KB at most
 #define LN_BWD_AT(CUT, NV, TH) launch_after(layernorm_bwd_kernel<T, CUT, NV, TH>, dim3((unsigned)grid), dim3(block), smem, st, p)
 #define LN_BWD(CUT, NV) (block > 512 ? LN_BWD_AT(CUT, NV, 1024) : LN_BWD_AT(CUT, NV, 512))
         if (cut == SINGLE) {

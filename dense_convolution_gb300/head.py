@@ -5,11 +5,10 @@ a loss over a vocabulary and its gradients.  As in ``conv``, PyTorch provides
 device memory and the current stream, every arithmetic step runs in the
 library's kernels, and shapes are checked so that a wrong tensor fails with a
 Python error instead of a bad pointer.  Each class is one problem shape:
-calling it runs the forward pass, ``backward`` the gradients.
+calling it runs the forward pass, ``backward`` the gradients.  With stream= a
+call and the tensors that it allocates belong to that stream.
 """
 from __future__ import annotations
-
-import functools
 
 import torch
 
@@ -22,17 +21,6 @@ _raw_stream = torch._C._cuda_getCurrentRawStream      # the current stream's han
 
 def _stream(t):
     return _raw_stream(t.device.index)
-
-
-def _on_stream(f):
-    """Accept stream=: the call and the tensors that it allocates belong to that stream."""
-    @functools.wraps(f)
-    def call(self, *args, stream=None, **kwargs):
-        if stream is None:
-            return f(self, *args, **kwargs)
-        with torch.cuda.stream(stream):
-            return f(self, *args, **kwargs)
-    return call
 
 
 def _ptr(t):
@@ -48,14 +36,17 @@ class _Rows:
     def check(self, name, t):
         if t.dtype is self.dtype and t.shape == self.shape and t.is_cuda:
             s = t.stride()
+            if s == self.strides:
+                return
             # The stride of a dimension of size one (or of an empty tensor) means nothing.
-            if s == self.strides or ((self.shape[0] <= 1 or s[0] == self.strides[0])
-                                     and (self.shape[1] <= 1 or s[1] == 1)) or t.numel() == 0:
+            if ((self.shape[0] <= 1 or s[0] == self.strides[0]) and (self.shape[1] <= 1 or s[1] == 1)) or t.numel() == 0:
                 return
         raise ValueError(f"{name} must be a CUDA {self.name} tensor of shape {self.shape} with rows "
                          f"{self.strides[0]} elements apart")
 
     def new(self, device):
+        if self.strides[0] == self.shape[1]:
+            return torch.empty(self.shape, dtype=self.dtype, device=device)
         return torch.empty_strided(self.shape, self.strides, dtype=self.dtype, device=device)
 
 
@@ -114,9 +105,11 @@ class LayerNorm(_Op):
         if t is not None:
             _check_flat(name, t, (self.cols,), self._param)
 
-    @_on_stream
-    def __call__(self, x, gamma=None, beta=None, y=None, stats=False):
+    def __call__(self, x, gamma=None, beta=None, y=None, stats=False, stream=None):
         """y, or (y, mean, rstd) with `stats` (what `backward` needs)."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self(x, gamma, beta, y, stats)
         self._check_x(x)
         self._check_param("gamma", gamma)
         self._check_param("beta", beta)
@@ -132,9 +125,11 @@ class LayerNorm(_Op):
                                 _stream(x))
         return (y, mean, rstd) if stats else y
 
-    @_on_stream
-    def backward(self, dy, x, gamma, mean, rstd, need_dx=True, need_params=True, workspace=None):
+    def backward(self, dy, x, gamma, mean, rstd, need_dx=True, need_params=True, workspace=None, stream=None):
         """(dx, dgamma, dbeta); None in the place of what is not needed."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.backward(dy, x, gamma, mean, rstd, need_dx, need_params, workspace)
         self._check_x(x)
         self._y.check("dy", dy)
         self._check_param("gamma", gamma)
@@ -169,9 +164,11 @@ class Dropout(_Op):
         self._x, self._y = _Rows(rows, cols, self.x_stride, dtype), _Rows(rows, cols, self.y_stride, dtype)
         self._residual = _Rows(rows, cols, self.residual_stride, dtype)
 
-    @_on_stream
-    def __call__(self, x, seed, offset=0, residual=None, y=None):
+    def __call__(self, x, seed, offset=0, residual=None, y=None, stream=None):
         """residual + dropped x (y may be x or residual)."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self(x, seed, offset, residual, y)
         self._x.check("x", x)
         if residual is not None:
             self._residual.check("residual", residual)
@@ -182,9 +179,11 @@ class Dropout(_Op):
         head_capi.dropout_fwd(self.desc, x.data_ptr(), _ptr(residual), y.data_ptr(), seed, offset, _stream(x))
         return y
 
-    @_on_stream
-    def backward(self, dy, seed, offset=0, dx=None):
+    def backward(self, dy, seed, offset=0, dx=None, stream=None):
         """dx under the mask of the forward call with the same seed and offset."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.backward(dy, seed, offset, dx)
         self._y.check("dy", dy)
         if dx is None:
             dx = self._x.new(dy.device)
@@ -221,9 +220,11 @@ class LinearCrossEntropy(_Op):
         self._w.check("w", w)
         _check_flat("target", target, (self.tokens,), torch.int64)
 
-    @_on_stream
-    def __call__(self, h, w, target, workspace=None):
+    def __call__(self, h, w, target, workspace=None, stream=None):
         """(loss, lse): lse (log-sum-exp per token) is what `backward` needs."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self(h, w, target, workspace)
         self._check(h, w, target)
         dev = h.device
         loss = torch.empty(self.loss_shape, dtype=torch.float32, device=dev)
@@ -234,9 +235,11 @@ class LinearCrossEntropy(_Op):
                                 lse.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream(h))
         return loss, lse
 
-    @_on_stream
-    def backward(self, h, w, target, lse, dloss, need_dh=True, need_dw=True, workspace=None):
+    def backward(self, h, w, target, lse, dloss, need_dh=True, need_dw=True, workspace=None, stream=None):
         """(dh, dw); None in the place of what is not needed."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.backward(h, w, target, lse, dloss, need_dh, need_dw, workspace)
         self._check(h, w, target)
         _check_flat("lse", lse, (self.tokens,), torch.float32)
         _check_flat("dloss", dloss, self.loss_shape, torch.float32)

@@ -3,7 +3,7 @@
 The training-head operators live in the same shared library as the
 convolution and follow ``capi``'s conventions: each function has the name of
 the C entry point it wraps, raises ``Conv2dError`` on a non-OK status, and takes
-pointers (device addresses) and streams as plain integers, 0 for none.
+pointers (device addresses) and streams as plain integers, 0 for none (NULL).
 """
 from __future__ import annotations
 
@@ -86,14 +86,13 @@ def layernorm_workspace_size(desc: int) -> int:
 
 
 def layernorm_fwd(desc: int, x: int, gamma: int, beta: int, y: int, mean: int = 0, rstd: int = 0, stream: int = 0):
-    _check(load().layernorm_fwd(desc, x or None, gamma or None, beta or None, y or None, mean or None, rstd or None,
-                                stream or None), "layernorm_fwd")
+    _check(load().layernorm_fwd(desc, x, gamma, beta, y, mean, rstd, stream), "layernorm_fwd")
 
 
 def layernorm_bwd(desc: int, dy: int, x: int, gamma: int, mean: int, rstd: int, dx: int, dgamma: int, dbeta: int,
                   workspace: int, workspace_bytes: int, stream: int = 0):
-    _check(load().layernorm_bwd(desc, dy or None, x or None, gamma or None, mean or None, rstd or None, dx or None,
-                                dgamma or None, dbeta or None, workspace or None, workspace_bytes, stream or None),
+    _check(load().layernorm_bwd(desc, dy, x, gamma, mean, rstd, dx,
+                                dgamma, dbeta, workspace, workspace_bytes, stream),
            "layernorm_bwd")
 
 
@@ -113,12 +112,12 @@ def dropout_desc_destroy(desc: int):
 
 
 def dropout_fwd(desc: int, x: int, residual: int, y: int, seed: int, offset: int, stream: int = 0):
-    _check(load().dropout_fwd(desc, x or None, residual or None, y or None, seed, offset, stream or None),
+    _check(load().dropout_fwd(desc, x, residual, y, seed, offset, stream),
            "dropout_fwd")
 
 
 def dropout_bwd(desc: int, dy: int, dx: int, seed: int, offset: int, stream: int = 0):
-    _check(load().dropout_bwd(desc, dy or None, dx or None, seed, offset, stream or None), "dropout_bwd")
+    _check(load().dropout_bwd(desc, dy, dx, seed, offset, stream), "dropout_bwd")
 
 
 def linear_ce_desc_create(tokens, hidden, vocab, dtype="bf16", reduction="mean", ignore_index=-100) -> int:
@@ -150,11 +149,11 @@ def linear_ce_workspace_size(desc: int):
 
 def linear_ce_fwd(desc: int, h: int, w: int, target: int, loss: int, lse: int, workspace: int, workspace_bytes: int,
                   stream: int = 0):
-    _check(load().linear_ce_fwd(desc, h or None, w or None, target or None, loss or None, lse or None,
-                                workspace or None, workspace_bytes, stream or None), "linear_ce_fwd")
+    _check(load().linear_ce_fwd(desc, h, w, target, loss, lse,
+                                workspace, workspace_bytes, stream), "linear_ce_fwd")
 
 
 def linear_ce_bwd(desc: int, h: int, w: int, target: int, lse: int, dloss: int, dh: int, dw: int, workspace: int,
                   workspace_bytes: int, stream: int = 0):
-    _check(load().linear_ce_bwd(desc, h or None, w or None, target or None, lse or None, dloss or None, dh or None,
-                                dw or None, workspace or None, workspace_bytes, stream or None), "linear_ce_bwd")
+    _check(load().linear_ce_bwd(desc, h, w, target, lse, dloss, dh,
+                                dw, workspace, workspace_bytes, stream), "linear_ce_bwd")

@@ -56,7 +56,8 @@ template <typename T, int V> __device__ __forceinline__ void store_part(T* p, co
 
 // Elements [lo, hi) of the V parameters from column e0 on, of type T or fp32
 // (`f32`); `fill` outside, and everywhere when there are none (null).  `vec`
-// says that a whole vector may be read with 16-byte loads.
+// says that a whole vector may be read with 16-byte loads.  Parameters are read
+// as constant data: no store of the kernel holds the loads of the next vector back.
 template <typename T, int V>
 __device__ __forceinline__ void load_params(const void* p, bool f32, int64_t e0, int lo, int hi, bool vec, float fill,
                                             float (&f)[V]) {
@@ -70,19 +71,22 @@ __device__ __forceinline__ void load_params(const void* p, bool f32, int64_t e0,
             if constexpr (V >= 4) {
 #pragma unroll
                 for (int i = 0; i < V; i += 4) {
-                    const float4 t = *reinterpret_cast<const float4*>(q + i);
+                    const float4 t = __ldg(reinterpret_cast<const float4*>(q + i));
                     f[i] = t.x; f[i + 1] = t.y; f[i + 2] = t.z; f[i + 3] = t.w;
                 }
             }
         } else {
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                if (i >= lo && i < hi) f[i] = q[i];
+                if (i >= lo && i < hi) f[i] = __ldg(q + i);
         }
     } else {
         const T* q = static_cast<const T*>(p) + e0;
         if (whole) {
-            widen<T, V>(*reinterpret_cast<const Vec<T, V>*>(q), f);
+            if constexpr (V > 1) {
+                const uint4 t = __ldg(reinterpret_cast<const uint4*>(q));
+                widen<T, V>(*reinterpret_cast<const Vec<T, V>*>(&t), f);
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < V; ++i)

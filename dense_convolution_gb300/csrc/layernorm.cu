@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(1024) layernorm_fwd_kernel(const LnParams p) {
     constexpr int V = vec_of<T, CUT>();
     constexpr bool EARLY = NV == 1;                    // one vector a thread: gamma and beta ride with x's latency
     __shared__ float red[2][32];
-    __shared__ float cl[2];
+    __shared__ float4 share;
     pdl_wait();
     const int rpb = blockDim.x / p.tpr, sub = threadIdx.x / p.tpr, t = threadIdx.x - sub * p.tpr;
     const int rank = p.cs > 1 ? (int)(blockIdx.x % p.cs) : 0;
@@ -191,16 +191,11 @@ __global__ void __launch_bounds__(1024) layernorm_fwd_kernel(const LnParams p) {
             sum += f.sum();
         }
     }
-    float mean = row_sum(sum, p.tpr, red[0]);
-    if (p.cs > 1) {
-        cg::cluster_group cl_g = cg::this_cluster();
-        if (threadIdx.x == 0) cl[0] = mean;
-        cl_g.sync();
-        const int lane = threadIdx.x & 31;
-        mean = lane_sum(lane < p.cs ? *cl_g.map_shared_rank(&cl[0], lane) : 0.f, 32);
-    }
-    mean *= p.inv_cols;
-
+    // Elements of this block's share of the row, their mean, and their squares
+    // about it; a cluster joins its shares from these three.
+    const int from = max(0, rank * p.per_block * V - shift), to = min(p.cols, (rank + 1) * p.per_block * V - shift);
+    const float count = (float)max(0, to - from);
+    float mean = row_sum(sum, p.tpr, red[0]) * (p.cs > 1 ? (count > 0.f ? 1.0f / count : 0.f) : p.inv_cols);
     float sq = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -215,12 +210,15 @@ __global__ void __launch_bounds__(1024) layernorm_fwd_kernel(const LnParams p) {
     }
     sq = row_sum(sq, p.tpr, red[1]);
     if (p.cs > 1) {
+        // sum n_i (m_i - m)^2 + sum s_i: the squares about the row's mean m.
         cg::cluster_group cl_g = cg::this_cluster();
-        if (threadIdx.x == 0) cl[1] = sq;
+        if (threadIdx.x == 0) share = make_float4(mean, sq, count, 0.f);
         cl_g.sync();
         const int lane = threadIdx.x & 31;
-        sq = lane_sum(lane < p.cs ? *cl_g.map_shared_rank(&cl[1], lane) : 0.f, 32);
-        cl_g.sync();                                   // no block leaves while another reads its sums
+        const float4 o = lane < p.cs ? *cl_g.map_shared_rank(&share, lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+        mean = lane_sum(o.x * o.z, 32) * p.inv_cols;
+        sq = lane_sum(o.z > 0.f ? o.y + o.z * (o.x - mean) * (o.x - mean) : 0.f, 32);
+        asm volatile("barrier.cluster.arrive.release;" ::: "memory");     // (waited for before the block leaves)
     }
     const float rstd = rsqrtf(sq * p.inv_cols + p.eps);
     if (live && t == 0 && rank == 0) {
@@ -238,6 +236,8 @@ __global__ void __launch_bounds__(1024) layernorm_fwd_kernel(const LnParams p) {
             store_part<T, V>(y + e0, f.affine(rstd, g, b), slot_first<CUT>(e0), slot_last<CUT, V>(e0, p.cols));
         }
     }
+    // No block leaves while another may still read its share.
+    if (p.cs > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 
 // Rows beyond a cluster's registers: the same three steps, re-reading x.

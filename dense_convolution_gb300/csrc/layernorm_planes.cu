@@ -758,38 +758,47 @@ planes16_bwd_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_const
         bulk_wait_all();
     }
     if (!p.want_params) return;
-    // Add the eight pixels of a matrix, then the warps that share a channel block.
+    // Add the eight pixels of a matrix (every exchange halves the values that a
+    // lane carries: value 4 m + 2 q + e, channel pair m, dgamma or dbeta q, ends
+    // up in the lanes with m in bits 3-4 and q in bit 2), then the warps that
+    // share a channel block.
     __syncthreads();
-    float* acc = reinterpret_cast<float*>(smem);           // [2][channels of the blocks]
-    for (int q = 0; q < PG; q += G) {
-        if (q > 0) __syncthreads();
-        if (sh.group == q) {
+    float* acc = reinterpret_cast<float*>(smem);           // [pixel group share][2][channels of the blocks]
+    const int width = blocks * 32;
 #pragma unroll
-            for (int i = 0; i < NB; ++i) {
-                const int b = sh.share + i * S::kShares;
-                if (b < blocks) {
+    for (int i = 0; i < NB; ++i) {
+        const int b = sh.share + i * S::kShares;
+        float v[16];
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-                        float v[4];
-                        unpack2f(dg[i][m], v[0], v[1]);
-                        unpack2f(db[i][m], v[2], v[3]);
+        for (int m = 0; m < 4; ++m) {
+            unpack2f(dg[i][m], v[4 * m], v[4 * m + 1]);
+            unpack2f(db[i][m], v[4 * m + 2], v[4 * m + 3]);
+        }
+        int o = 16;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
+        for (int n = 8; n > 1; n >>= 1, o >>= 1) {
+            const bool up = lane & o;
 #pragma unroll
-                            for (int o = 4; o < 32; o <<= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-                            const int c = (k >> 1) * blocks * 32 + b * 32 + m * 8 + 2 * (lane & 3) + (k & 1);
-                            if (lane < 4) acc[c] = v[k] + (q ? acc[c] : 0.f);
-                        }
-                    }
-                }
-            }
+            for (int k = 0; k < n; ++k)
+                v[k] = (up ? v[k + n] : v[k]) + __shfl_xor_sync(0xffffffffu, up ? v[k] : v[k + n], o);
+        }
+        if (b < blocks) {
+            const int m = lane >> 3, q = lane >> 2 & 1;
+            float* dst = acc + ((sh.group / G) * 2 + q) * width + b * 32 + m * 8 + 2 * (lane & 3);
+            dst[0] = v[0];
+            dst[1] = v[1];
         }
     }
     __syncthreads();
     float* out = p.part + (int64_t)blockIdx.x * 2 * p.C;
     for (int c = threadIdx.x; c < p.C; c += kThreads16) {
-        out[c] = acc[c];
-        out[p.C + c] = acc[blocks * 32 + c];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            float u = acc[q * width + c];
+#pragma unroll
+            for (int k = 1; k < PG / G; ++k) u += acc[(2 * k + q) * width + c];
+            out[q * p.C + c] = u;
+        }
     }
 }
 

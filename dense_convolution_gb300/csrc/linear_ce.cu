@@ -802,9 +802,17 @@ __device__ __forceinline__ void ce_pack(const T* src, int64_t stride, int64_t ro
             }
             *reinterpret_cast<uint4*>(d) = v;
         } else {
-            float q[8][3];
+            float x[8], q[8][3];
+            if (vec && keep && c + 8 <= cols) {
+                const float4 a = reinterpret_cast<const float4*>(s)[0], b = reinterpret_cast<const float4*>(s)[1];
+                x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+                x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+            } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) split3(keep && c + j < cols ? to_f32(s[j]) : 0.f, q[j]);
+                for (int j = 0; j < 8; ++j) x[j] = keep && c + j < cols ? to_f32(s[j]) : 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) split3(x[j], q[j]);
 #pragma unroll
             for (int k = 0; k < 3; ++k)
                 *reinterpret_cast<uint4*>(d + (int64_t)k * pitch) =
@@ -899,13 +907,13 @@ struct Product { int64_t M, N, chunks; bool may_split; };
 // an item (one tile of one split) adds pipeline fill and its last epilogue;
 // items run in turn over the SMs or pairs, the first product's before the
 // second's; splits add the write and read of their fp32 sums and one launch.
-LaunchPlan plan_gemm(const Product* pr, int n, int step) {
+LaunchPlan plan_gemm(const Product* pr, int n, int step, bool b_mn) {
     LaunchPlan best{256, false, {1, 1}};
     double best_t = -1;
     for (int pair = 0; pair < 2; ++pair) {
         if (pair && pr[0].M <= kBM && (n == 1 || pr[1].M <= kBM)) break;
         const int units = pair ? pair_count() : device_sm_count(), rows = pair ? 2 * kBM : kBM;
-        const int down = pair && step == 64 ? 128 : step;    // half a tile is whole 64-wide boxes
+        const int down = pair && b_mn ? 2 * step : step;     // half a tile is whole 64-wide boxes
         for (int bn = 256; bn >= (pair ? 128 : 64); bn -= down) {
             if (bn - down >= pr[0].N && bn - down >= (pair ? 128 : 64)) continue;      // wider than the output needs
             const double bytes = kABytes + (pair ? bn / 2 : bn) * kBK * 2;
@@ -1080,7 +1088,7 @@ CePlan plan_ce(const linear_ce_desc& d, bool backward) {
     const int64_t v = d.vocab < piece ? d.vocab : piece;
     // dz is read in 64-column chunks, so its tiles write whole ones (zeros past the vocabulary).
     const Product z{d.tokens, v, nk * c.pairs, false};
-    c.z = plan_gemm(&z, 1, backward ? 64 : 32);
+    c.z = plan_gemm(&z, 1, backward ? 64 : 32, false);
     size_t at = 0;
     if (!backward) {
         take(at, c.part, (size_t)d.tokens * (size_t)(c.pieces * ceil_div(v, c.z.BN)) * sizeof(float2));
@@ -1089,7 +1097,7 @@ CePlan plan_ce(const linear_ce_desc& d, bool backward) {
     } else {
         const Product out[2] = {{d.tokens, d.hidden, ceil_div(v, 64) * c.pairs, true},
                                 {v, d.hidden, ceil_div(d.tokens, 64) * c.pairs, true}};
-        c.out = plan_gemm(out, 2, 64);
+        c.out = plan_gemm(out, 2, 64, true);
         take(at, c.coef, (size_t)d.tokens * 4);
         take(at, c.common, 4);
         take(at, c.dz, (size_t)d.tokens * (size_t)piece * 2 * c.parts);
@@ -1110,7 +1118,8 @@ cudaError_t pack(const linear_ce_desc& d, const void* src, int64_t stride, int64
     const dim3 grid((unsigned)(work < most ? work : most)), block(256);
     if (d.dtype == CONV2D_F32)
         return launch_after(ce_pack_kernel<float, 3>, grid, block, 0, st, static_cast<const float*>(src), stride, rows,
-                            (int)d.hidden, (int)dp, 0, static_cast<uint16_t*>(dst));
+                            (int)d.hidden, (int)dp, stride % 4 == 0 && aligned_to(src, 16) ? 1 : 0,
+                            static_cast<uint16_t*>(dst));
     const int vec = stride % 8 == 0 && aligned_to(src, 16);
     return launch_after(ce_pack_kernel<__half, 1>, grid, block, 0, st, static_cast<const __half*>(src), stride, rows,
                         (int)d.hidden, (int)dp, vec, static_cast<uint16_t*>(dst));
@@ -1124,8 +1133,8 @@ cudaError_t prepare(const linear_ce_desc& d, const CePlan& c, const void* h, con
     const int per_row = d.reduction == HEAD_REDUCE_NONE, mean = d.reduction == HEAD_REDUCE_MEAN;
     if (d.dtype == CONV2D_F32)
         return launch_after(ce_prepare_kernel<float, 3>, grid, block, 0, st, static_cast<const float*>(h), d.hs, d.tokens,
-                            (int)d.hidden, (int)c.dp, 0, dloss, target, (int)d.vocab, d.ignore_index, per_row, mean,
-                            coef, common, static_cast<uint16_t*>(dst));
+                            (int)d.hidden, (int)c.dp, d.hs % 4 == 0 && aligned_to(h, 16) ? 1 : 0, dloss, target,
+                            (int)d.vocab, d.ignore_index, per_row, mean, coef, common, static_cast<uint16_t*>(dst));
     const int vec = d.hs % 8 == 0 && aligned_to(h, 16);
     return launch_after(ce_prepare_kernel<__half, 1>, grid, block, 0, st, static_cast<const __half*>(h), d.hs, d.tokens,
                         (int)d.hidden, (int)c.dp, vec, dloss, target, (int)d.vocab, d.ignore_index, per_row, mean, coef,

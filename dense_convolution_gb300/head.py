@@ -19,10 +19,6 @@ from .conv import _NAME, _TORCH_DTYPE
 _raw_stream = torch._C._cuda_getCurrentRawStream      # the current stream's handle by device index
 
 
-def _stream(t):
-    return _raw_stream(t.device.index)
-
-
 def _ptr(t):
     return t.data_ptr() if t is not None else 0
 
@@ -50,9 +46,31 @@ class _Rows:
         return torch.empty_strided(self.shape, self.strides, dtype=self.dtype, device=device)
 
 
-def _check_flat(name, t, shape, dtype):
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError(f"{name} must be a contiguous CUDA tensor of {dtype} and shape {shape}")
+class _Planes:
+    """Contiguous channels-first planes: (images, cols, *pixels)."""
+
+    def __init__(self, rows, cols, pixels, dtype):
+        self.lead, self.count, self.name, self.dtype = (rows // pixels, cols), rows * cols, dtype, _TORCH_DTYPE[dtype]
+        self.pixels = pixels
+
+    def check(self, name, t):
+        if t.dtype is not self.dtype or t.dim() < 3 or t.shape[:2] != self.lead or t.numel() != self.count \
+                or not t.is_contiguous() or not t.is_cuda:
+            raise ValueError(f"{name} must be contiguous CUDA {self.name} planes of shape {self.lead} and {self.pixels} pixels")
+
+
+class _Flat:
+    """The contiguous tensors of one shape and type."""
+
+    def __init__(self, shape, dtype):
+        self.shape, self.dtype = shape, dtype
+
+    def check(self, name, t):
+        if t.dtype is not self.dtype or t.shape != self.shape or not t.is_contiguous() or not t.is_cuda:
+            raise ValueError(f"{name} must be a contiguous CUDA tensor of {self.dtype} and shape {self.shape}")
+
+    def new(self, device):
+        return torch.empty(self.shape, dtype=self.dtype, device=device)
 
 
 class _Op:
@@ -89,40 +107,32 @@ class LayerNorm(_Op):
         if pixels:
             head_capi.layernorm_desc_set_planes(self.desc, pixels)
         self.workspace_bytes = head_capi.layernorm_workspace_size(self.desc)
-        self._x, self._y = _Rows(rows, cols, self.x_stride, dtype), _Rows(rows, cols, self.y_stride, dtype)
-        self._param = _TORCH_DTYPE[self.param_dtype]
-
-    def _check_x(self, x):
-        if not self.pixels:
-            self._x.check("x", x)
-            return
-        want = (self.rows // self.pixels, self.cols)
-        if x.dtype is not self._x.dtype or x.dim() < 3 or x.shape[:2] != want \
-                or x.numel() != self.rows * self.cols or not x.is_contiguous() or not x.is_cuda:
-            raise ValueError(f"x must be contiguous CUDA {self.dtype} planes of shape {want} and {self.pixels} pixels")
-
-    def _check_param(self, name, t):
-        if t is not None:
-            _check_flat(name, t, (self.cols,), self._param)
+        self._x = _Planes(rows, cols, pixels, dtype) if pixels else _Rows(rows, cols, self.x_stride, dtype)
+        self._y = _Rows(rows, cols, self.y_stride, dtype)
+        self._param, self._stat = _Flat((cols,), _TORCH_DTYPE[self.param_dtype]), _Flat((rows,), torch.float32)
 
     def __call__(self, x, gamma=None, beta=None, y=None, stats=False, stream=None):
         """y, or (y, mean, rstd) with `stats` (what `backward` needs)."""
         if stream is not None:
             with torch.cuda.stream(stream):
                 return self(x, gamma, beta, y, stats)
-        self._check_x(x)
-        self._check_param("gamma", gamma)
-        self._check_param("beta", beta)
+        self._x.check("x", x)
+        g = b = mp = rp = 0
+        if gamma is not None:
+            self._param.check("gamma", gamma)
+            g = gamma.data_ptr()
+        if beta is not None:
+            self._param.check("beta", beta)
+            b = beta.data_ptr()
+        dev = x.device
         if y is None:
-            y = self._y.new(x.device)
+            y = self._y.new(dev)
         else:
             self._y.check("y", y)
-        mean = rstd = None
         if stats:
-            mean = torch.empty(self.rows, dtype=torch.float32, device=x.device)
-            rstd = torch.empty(self.rows, dtype=torch.float32, device=x.device)
-        head_capi.layernorm_fwd(self.desc, x.data_ptr(), _ptr(gamma), _ptr(beta), y.data_ptr(), _ptr(mean), _ptr(rstd),
-                                _stream(x))
+            mean, rstd = self._stat.new(dev), self._stat.new(dev)
+            mp, rp = mean.data_ptr(), rstd.data_ptr()
+        head_capi.layernorm_fwd(self.desc, x.data_ptr(), g, b, y.data_ptr(), mp, rp, _raw_stream(dev.index))
         return (y, mean, rstd) if stats else y
 
     def backward(self, dy, x, gamma, mean, rstd, need_dx=True, need_params=True, workspace=None, stream=None):
@@ -130,23 +140,26 @@ class LayerNorm(_Op):
         if stream is not None:
             with torch.cuda.stream(stream):
                 return self.backward(dy, x, gamma, mean, rstd, need_dx, need_params, workspace)
-        self._check_x(x)
+        self._x.check("x", x)
         self._y.check("dy", dy)
-        self._check_param("gamma", gamma)
-        _check_flat("mean", mean, (self.rows,), torch.float32)
-        _check_flat("rstd", rstd, (self.rows,), torch.float32)
+        self._stat.check("mean", mean)
+        self._stat.check("rstd", rstd)
+        g = xp = gp = bp = 0
+        if gamma is not None:
+            self._param.check("gamma", gamma)
+            g = gamma.data_ptr()
         dev = x.device
         dx = dgamma = dbeta = None
         if need_dx:
             dx = torch.empty_like(x) if self.pixels else self._x.new(dev)
+            xp = dx.data_ptr()
         if need_params:
-            dgamma = torch.empty(self.cols, dtype=self._param, device=dev)
-            dbeta = torch.empty(self.cols, dtype=self._param, device=dev)
+            dgamma, dbeta = self._param.new(dev), self._param.new(dev)
+            gp, bp = dgamma.data_ptr(), dbeta.data_ptr()
         if workspace is None:
             workspace = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=dev)
-        head_capi.layernorm_bwd(self.desc, dy.data_ptr(), x.data_ptr(), _ptr(gamma), mean.data_ptr(), rstd.data_ptr(),
-                                _ptr(dx), _ptr(dgamma), _ptr(dbeta), workspace.data_ptr(), workspace.numel(),
-                                _stream(x))
+        head_capi.layernorm_bwd(self.desc, dy.data_ptr(), x.data_ptr(), g, mean.data_ptr(), rstd.data_ptr(), xp, gp, bp,
+                                workspace.data_ptr(), workspace.numel(), _raw_stream(dev.index))
         return dx, dgamma, dbeta
 
 
@@ -176,7 +189,8 @@ class Dropout(_Op):
             y = self._y.new(x.device)
         else:
             self._y.check("y", y)
-        head_capi.dropout_fwd(self.desc, x.data_ptr(), _ptr(residual), y.data_ptr(), seed, offset, _stream(x))
+        head_capi.dropout_fwd(self.desc, x.data_ptr(), _ptr(residual), y.data_ptr(), seed, offset,
+                              _raw_stream(x.device.index))
         return y
 
     def backward(self, dy, seed, offset=0, dx=None, stream=None):
@@ -189,7 +203,7 @@ class Dropout(_Op):
             dx = self._x.new(dy.device)
         else:
             self._x.check("dx", dx)
-        head_capi.dropout_bwd(self.desc, dy.data_ptr(), dx.data_ptr(), seed, offset, _stream(dy))
+        head_capi.dropout_bwd(self.desc, dy.data_ptr(), dx.data_ptr(), seed, offset, _raw_stream(dy.device.index))
         return dx
 
 
@@ -214,11 +228,13 @@ class LinearCrossEntropy(_Op):
         self.workspace_bytes, self.backward_workspace_bytes = head_capi.linear_ce_workspace_size(self.desc)
         self.loss_shape = (tokens,) if reduction == "none" else ()
         self._h, self._w = _Rows(tokens, hidden, self.h_stride, dtype), _Rows(vocab, hidden, self.w_stride, dtype)
+        self._target, self._lse = _Flat((tokens,), torch.int64), _Flat((tokens,), torch.float32)
+        self._loss = _Flat(self.loss_shape, torch.float32)
 
     def _check(self, h, w, target):
         self._h.check("h", h)
         self._w.check("w", w)
-        _check_flat("target", target, (self.tokens,), torch.int64)
+        self._target.check("target", target)
 
     def __call__(self, h, w, target, workspace=None, stream=None):
         """(loss, lse): lse (log-sum-exp per token) is what `backward` needs."""
@@ -227,12 +243,11 @@ class LinearCrossEntropy(_Op):
                 return self(h, w, target, workspace)
         self._check(h, w, target)
         dev = h.device
-        loss = torch.empty(self.loss_shape, dtype=torch.float32, device=dev)
-        lse = torch.empty(self.tokens, dtype=torch.float32, device=dev)
+        loss, lse = self._loss.new(dev), self._lse.new(dev)
         if workspace is None:
             workspace = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=dev)
         head_capi.linear_ce_fwd(self.desc, h.data_ptr(), w.data_ptr(), target.data_ptr(), loss.data_ptr(),
-                                lse.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream(h))
+                                lse.data_ptr(), workspace.data_ptr(), workspace.numel(), _raw_stream(dev.index))
         return loss, lse
 
     def backward(self, h, w, target, lse, dloss, need_dh=True, need_dw=True, workspace=None, stream=None):
@@ -241,8 +256,8 @@ class LinearCrossEntropy(_Op):
             with torch.cuda.stream(stream):
                 return self.backward(h, w, target, lse, dloss, need_dh, need_dw, workspace)
         self._check(h, w, target)
-        _check_flat("lse", lse, (self.tokens,), torch.float32)
-        _check_flat("dloss", dloss, self.loss_shape, torch.float32)
+        self._lse.check("lse", lse)
+        self._loss.check("dloss", dloss)
         dev = h.device
         dh = torch.empty((self.tokens, self.hidden), dtype=h.dtype, device=dev) if need_dh else None
         dw = torch.empty((self.vocab, self.hidden), dtype=w.dtype, device=dev) if need_dw else None
@@ -250,7 +265,7 @@ class LinearCrossEntropy(_Op):
             workspace = torch.empty(self.backward_workspace_bytes, dtype=torch.uint8, device=dev)
         head_capi.linear_ce_bwd(self.desc, h.data_ptr(), w.data_ptr(), target.data_ptr(), lse.data_ptr(),
                                 dloss.data_ptr(), _ptr(dh), _ptr(dw), workspace.data_ptr(), workspace.numel(),
-                                _stream(h))
+                                _raw_stream(dev.index))
         return dh, dw
 
 

@@ -86,7 +86,9 @@ def layernorm_workspace_size(desc: int) -> int:
 
 
 def layernorm_fwd(desc: int, x: int, gamma: int, beta: int, y: int, mean: int = 0, rstd: int = 0, stream: int = 0):
-    _check(load().layernorm_fwd(desc, x, gamma, beta, y, mean, rstd, stream), "layernorm_fwd")
+    s = load().layernorm_fwd(desc, x, gamma, beta, y, mean, rstd, stream)
+    if s:
+        _check(s, "layernorm_fwd")
 
 
 def layernorm_bwd(desc: int, dy: int, x: int, gamma: int, mean: int, rstd: int, dx: int, dgamma: int, dbeta: int,

@@ -215,7 +215,8 @@ CONV2D_API conv2d_status linear_ce_workspace_size(linear_ce_desc_t d, size_t* fw
 namespace {
 
 // h and w are read in place by tensor copies, which need 16-byte alignment,
-// unless they are packed first.
+// unless they are packed first (or there are few tokens: the interface's rule is
+// one for all).
 bool ce_operand_ok(const linear_ce_desc& d, const void* p, int64_t stride) {
     const bool packed = d.dtype == CONV2D_F32 || stride % 8 != 0;
     return aligned_to(p, packed ? elem_bytes(d.dtype) : 16);

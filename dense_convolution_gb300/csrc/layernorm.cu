@@ -472,22 +472,6 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) layernorm_bwd_kernel(
 // exactly (FULL) get a kernel without the tests for the ones that do not.
 constexpr int kBulkBytes = 1024, kBulkThreads = 512, kBulkElems = 16, kRingBytes = 192 * 1024, kRingMost = 8;
 
-// N sums (a power of two) over a warp at once: each exchange also halves the
-// values that a lane carries, until lanes k 32 / N on hold sum k.
-template <int N> __device__ __forceinline__ float warp_sums(float (&v)[N]) {
-    const int lane = threadIdx.x & 31;
-    int o = 16;
-#pragma unroll
-    for (int n = N / 2; n > 0; n >>= 1, o >>= 1) {
-        const bool up = lane & o;
-#pragma unroll
-        for (int k = 0; k < n; ++k)
-            v[k] = (up ? v[k + n] : v[k]) + __shfl_xor_sync(0xffffffffu, up ? v[k] : v[k + n], o);
-    }
-#pragma unroll
-    for (; o > 0; o >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
-    return v[0];
-}
 // The group's sums from its warps' (buf[k][warp], written by the first lane of
 // each lane group): sum k in lanes k 32 / N on.
 template <int N> __device__ __forceinline__ float group_sums(const float (*buf)[16], int first, int warps) {

@@ -37,13 +37,10 @@
 // CTA's copies and shared-memory reads per product are a third less.
 //
 // Few rows by many columns (or a long K by a small output) is split over K and
-// joined by a second kernel in a fixed order, so that all SMs have work.
+// joined by a second kernel in a fixed order, so that all SMs have work.  At most
+// eight tokens go to linear_ce_few.cu instead.
 #include <cuda.h>
 #include <math.h>
-
-#include <mutex>
-#include <set>
-#include <utility>
 
 #include "head_device.cuh"
 #include "head_internal.h"
@@ -947,17 +944,8 @@ LaunchPlan plan_gemm(const Product* pr, int n, int step, bool b_mn) {
     return best;
 }
 
-// Lift a kernel's shared-memory limit, once per device and kernel.
 bool allow_smem(const void* kern) {
-    static std::mutex lock;
-    static std::set<std::pair<int, const void*>> done;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return false;
-    std::lock_guard<std::mutex> hold(lock);
-    if (done.count({dev, kern})) return true;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost) != cudaSuccess) return false;
-    done.insert({dev, kern});
-    return true;
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost) == cudaSuccess;
 }
 
 constexpr int kFixedSmem = 1024 + (2 * kMaxRing + 5) * 8 + 24;
@@ -1061,6 +1049,23 @@ void take(size_t& at, size_t& off, size_t bytes) {
 
 CePlan plan_ce(const linear_ce_desc& d, bool backward) {
     CePlan c{};
+    size_t at = 0;
+    c.few = linear_ce_is_few(d);
+    if (c.few) {
+        c.dp = ceil_div(d.hidden, 64) * 64;
+        if (!backward) {
+            take(at, c.part, (size_t)d.tokens * linear_ce_few_blocks() * sizeof(float2));
+            take(at, c.z_target, (size_t)d.tokens * 4);
+            take(at, c.row_loss, (size_t)d.tokens * 4);
+        } else {
+            take(at, c.common, 4);
+            take(at, c.dz, (size_t)d.tokens * d.vocab * 4);
+            c.out.splits[0] = linear_ce_few_shares(d);
+            take(at, c.sums_h, (size_t)c.out.splits[0] * d.tokens * c.dp * 4);
+        }
+        c.total = at + 1024;
+        return c;
+    }
     const bool f32 = d.dtype == CONV2D_F32;
     c.bf16 = d.dtype != CONV2D_F16;
     c.parts = f32 ? 3 : 1;
@@ -1089,7 +1094,6 @@ CePlan plan_ce(const linear_ce_desc& d, bool backward) {
     // dz is read in 64-column chunks, so its tiles write whole ones (zeros past the vocabulary).
     const Product z{d.tokens, v, nk * c.pairs, false};
     c.z = plan_gemm(&z, 1, backward ? 64 : 32, false);
-    size_t at = 0;
     if (!backward) {
         take(at, c.part, (size_t)d.tokens * (size_t)(c.pieces * ceil_div(v, c.z.BN)) * sizeof(float2));
         take(at, c.z_target, (size_t)d.tokens * 4);
@@ -1230,28 +1234,33 @@ conv2d_status launch_linear_ce_fwd(const linear_ce_desc& d, const void* h, const
     const CePlan& c = d.fwd;
     uint8_t* base = aligned_base(ws);
     const size_t e = elem_bytes(d.dtype);
-    Operand ho{h, d.hidden, d.hs};
-    if (c.pack_h) {
-        if (pack(d, h, d.hs, d.tokens, c.dp, base + c.hp, st) != cudaSuccess) return CONV2D_ERR_CUDA;
-        ho = Operand{base + c.hp, c.dp * c.parts, c.dp * c.parts};
-    }
     GemmParams p{};
     p.target = target;
     p.z_target = reinterpret_cast<float*>(base + c.z_target);
     float2* part = reinterpret_cast<float2*>(base + c.part);
     int tiles = 0;
-    for (int64_t v0 = 0; v0 < d.vocab; v0 += c.piece) {
-        const int64_t rows = d.vocab - v0 < c.piece ? d.vocab - v0 : c.piece;
-        Operand wo{at_row(w, v0, d.ws, e), d.hidden, d.ws};
-        if (c.pack_w) {
-            if (pack(d, wo.base, d.ws, rows, c.dp, base + c.wp, st) != cudaSuccess) return CONV2D_ERR_CUDA;
-            wo = Operand{base + c.wp, c.dp * c.parts, c.dp * c.parts};
+    if (c.few) {
+        if (launch_ce_few_fwd(d, h, w, target, part, p.z_target, st) != cudaSuccess) return CONV2D_ERR_CUDA;
+        tiles = linear_ce_few_blocks();
+    } else {
+        Operand ho{h, d.hidden, d.hs};
+        if (c.pack_h) {
+            if (pack(d, h, d.hs, d.tokens, c.dp, base + c.hp, st) != cudaSuccess) return CONV2D_ERR_CUDA;
+            ho = Operand{base + c.hp, c.dp * c.parts, c.dp * c.parts};
         }
-        p.col0 = (int)v0;
-        p.lse_part = part + (size_t)tiles * d.tokens;
-        const conv2d_status s = gemm_z(c, d, EPI_LSE, ho, wo, rows, p, st);
-        if (s != CONV2D_OK) return s;
-        tiles += (int)ceil_div(rows, c.z.BN);
+        for (int64_t v0 = 0; v0 < d.vocab; v0 += c.piece) {
+            const int64_t rows = d.vocab - v0 < c.piece ? d.vocab - v0 : c.piece;
+            Operand wo{at_row(w, v0, d.ws, e), d.hidden, d.ws};
+            if (c.pack_w) {
+                if (pack(d, wo.base, d.ws, rows, c.dp, base + c.wp, st) != cudaSuccess) return CONV2D_ERR_CUDA;
+                wo = Operand{base + c.wp, c.dp * c.parts, c.dp * c.parts};
+            }
+            p.col0 = (int)v0;
+            p.lse_part = part + (size_t)tiles * d.tokens;
+            const conv2d_status s = gemm_z(c, d, EPI_LSE, ho, wo, rows, p, st);
+            if (s != CONV2D_OK) return s;
+            tiles += (int)ceil_div(rows, c.z.BN);
+        }
     }
     float* row_loss = d.reduction == HEAD_REDUCE_NONE ? loss : reinterpret_cast<float*>(base + c.row_loss);
     float* total = d.reduction == HEAD_REDUCE_NONE ? nullptr : loss;
@@ -1280,6 +1289,19 @@ conv2d_status launch_linear_ce_bwd(const linear_ce_desc& d, const void* h, const
     float* common = reinterpret_cast<float*>(base + c.common);
     float* acc = c.pieces > 1 ? reinterpret_cast<float*>(base + c.acc) : nullptr;
     float *sums_h = reinterpret_cast<float*>(base + c.sums_h), *sums_w = reinterpret_cast<float*>(base + c.sums_w);
+    if (c.few) {
+        if (launch_ce_few_bwd(d, h, w, target, lse, dloss, dw, reinterpret_cast<float*>(base + c.dz), common, dh != nullptr,
+                              sums_h, c.dp, st) != cudaSuccess)
+            return CONV2D_ERR_CUDA;
+        GemmParams p = out_job(c, d, 1, false, d.tokens, 1, 0, dh, nullptr, 0, 0, common, nullptr);
+        p.splits = c.out.splits[0];
+        if (!dh) return CONV2D_OK;
+        if (d.dtype == CONV2D_F32) return join_splits<float>(p, sums_h, dh, st) == cudaSuccess ? CONV2D_OK : CONV2D_ERR_CUDA;
+        return (d.dtype == CONV2D_F16 ? join_splits<__half>(p, sums_h, dh, st)
+                                      : join_splits<__nv_bfloat16>(p, sums_h, dh, st)) == cudaSuccess
+                   ? CONV2D_OK
+                   : CONV2D_ERR_CUDA;
+    }
     if (prepare(d, c, h, target, dloss, coef, common, base + c.hp, st) != cudaSuccess) return CONV2D_ERR_CUDA;
     const Operand ho{base + c.hp, c.dp * c.parts, c.dp * c.parts};
     GemmParams p{};

@@ -7,8 +7,9 @@
  * Conventions are those of conv2d.h: every function returns a conv2d_status
  * and lets no C++ exception out; device pointers belong to the caller; nothing
  * is allocated or retained; `stream` is a cudaStream_t cast to void*, on which
- * all work is queued; descriptors are host memory, made without a CUDA call,
- * and are safe to use from several threads once set up.  Element types are
+ * all work is queued; descriptors are host memory, can be made without a GPU,
+ * and are safe to use from several threads once set up (workspace sizes and
+ * launch plans are those of the device that is current when one is made).  Element types are
  * conv2d_dtype; 16-bit values are widened on load, every sum, mean, norm and
  * softmax is held in fp32, and a result is rounded to nearest even once.
  * Results do not depend on the order in which blocks run: no kernel here
@@ -125,7 +126,8 @@ conv2d_status dropout_bwd(dropout_desc_t d, const void *dy, void *dx, uint64_t s
  * with fp32 accumulation, and dz is rounded to that type for the two products
  * of the backward pass.  fp32 runs on the tensor cores too: each value is the
  * sum of three bf16 parts (8 bits of the significand each), and the six
- * leading products of the parts, exact in fp32, are accumulated. */
+ * leading products of the parts, exact in fp32, are accumulated; an infinity
+ * in h or w makes its logits NaN there (a part of the other factor is zero). */
 
 typedef enum { HEAD_REDUCE_NONE = 0, HEAD_REDUCE_SUM = 1, HEAD_REDUCE_MEAN = 2 } head_reduction;
 

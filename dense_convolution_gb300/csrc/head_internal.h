@@ -31,7 +31,7 @@ struct LaunchPlan { int BN; bool pair; int splits[2]; };
 
 // Sizes and workspace offsets of one pass of the linear cross entropy.
 struct CePlan {
-    bool few;                      // at most eight tokens: linear_ce_few.cu
+    bool few;                      // few tokens: linear_ce_few.cu
     bool bf16, pack_w, pack_h;
     int parts, pairs;              // bf16 parts per value (1, or 3 for fp32) and their products (1 or 6)
     int64_t dp;                    // packed row pitch of one part
@@ -89,14 +89,15 @@ conv2d_status launch_linear_ce_bwd(const linear_ce_desc& d, const void* h, const
                                    const float* lse, const float* dloss, void* dh, void* dw, void* ws,
                                    cudaStream_t st);
 
-// linear_ce_few.cu: at most eight tokens, on the CUDA cores
-bool linear_ce_is_few(const linear_ce_desc& d);
+// linear_ce_few.cu: few tokens, on the CUDA cores
+bool linear_ce_is_few(const linear_ce_desc& d, bool backward);
 int linear_ce_few_blocks();                          // (max, sum) pairs per token of the forward kernel
-int linear_ce_few_shares(const linear_ce_desc& d);   // partial sums of dh
+int64_t linear_ce_few_dz(const linear_ce_desc& d);   // fp32 words of dz and of the partial sums of dh
+int64_t linear_ce_few_sums(const linear_ce_desc& d);
 cudaError_t launch_ce_few_fwd(const linear_ce_desc& d, const void* h, const void* w, const int64_t* target, void* part,
                               float* z_target, cudaStream_t st);
 cudaError_t launch_ce_few_bwd(const linear_ce_desc& d, const void* h, const void* w, const int64_t* target,
-                              const float* lse, const float* dloss, void* dw, float* dz, float* one, bool want_dh,
-                              float* sums, int64_t lds, cudaStream_t st);
+                              const float* lse, const float* dloss, void* dh, void* dw, float* dz, float* sums,
+                              cudaStream_t st);
 
 }  // namespace conv2d_gb300

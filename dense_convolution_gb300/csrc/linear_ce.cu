@@ -37,8 +37,8 @@
 // CTA's copies and shared-memory reads per product are a third less.
 //
 // Few rows by many columns (or a long K by a small output) is split over K and
-// joined by a second kernel in a fixed order, so that all SMs have work.  At most
-// eight tokens go to linear_ce_few.cu instead.
+// joined by a second kernel in a fixed order, so that all SMs have work.  Few
+// tokens go to linear_ce_few.cu instead.
 #include <cuda.h>
 #include <math.h>
 
@@ -1050,18 +1050,15 @@ void take(size_t& at, size_t& off, size_t bytes) {
 CePlan plan_ce(const linear_ce_desc& d, bool backward) {
     CePlan c{};
     size_t at = 0;
-    c.few = linear_ce_is_few(d);
+    c.few = linear_ce_is_few(d, backward);
     if (c.few) {
-        c.dp = ceil_div(d.hidden, 64) * 64;
         if (!backward) {
             take(at, c.part, (size_t)d.tokens * linear_ce_few_blocks() * sizeof(float2));
             take(at, c.z_target, (size_t)d.tokens * 4);
             take(at, c.row_loss, (size_t)d.tokens * 4);
         } else {
-            take(at, c.common, 4);
-            take(at, c.dz, (size_t)d.tokens * d.vocab * 4);
-            c.out.splits[0] = linear_ce_few_shares(d);
-            take(at, c.sums_h, (size_t)c.out.splits[0] * d.tokens * c.dp * 4);
+            take(at, c.dz, (size_t)linear_ce_few_dz(d) * 4);
+            take(at, c.sums_h, (size_t)linear_ce_few_sums(d) * 4);
         }
         c.total = at + 1024;
         return c;
@@ -1289,19 +1286,11 @@ conv2d_status launch_linear_ce_bwd(const linear_ce_desc& d, const void* h, const
     float* common = reinterpret_cast<float*>(base + c.common);
     float* acc = c.pieces > 1 ? reinterpret_cast<float*>(base + c.acc) : nullptr;
     float *sums_h = reinterpret_cast<float*>(base + c.sums_h), *sums_w = reinterpret_cast<float*>(base + c.sums_w);
-    if (c.few) {
-        if (launch_ce_few_bwd(d, h, w, target, lse, dloss, dw, reinterpret_cast<float*>(base + c.dz), common, dh != nullptr,
-                              sums_h, c.dp, st) != cudaSuccess)
-            return CONV2D_ERR_CUDA;
-        GemmParams p = out_job(c, d, 1, false, d.tokens, 1, 0, dh, nullptr, 0, 0, common, nullptr);
-        p.splits = c.out.splits[0];
-        if (!dh) return CONV2D_OK;
-        if (d.dtype == CONV2D_F32) return join_splits<float>(p, sums_h, dh, st) == cudaSuccess ? CONV2D_OK : CONV2D_ERR_CUDA;
-        return (d.dtype == CONV2D_F16 ? join_splits<__half>(p, sums_h, dh, st)
-                                      : join_splits<__nv_bfloat16>(p, sums_h, dh, st)) == cudaSuccess
+    if (c.few)
+        return launch_ce_few_bwd(d, h, w, target, lse, dloss, dh, dw, reinterpret_cast<float*>(base + c.dz), sums_h, st) ==
+                       cudaSuccess
                    ? CONV2D_OK
                    : CONV2D_ERR_CUDA;
-    }
     if (prepare(d, c, h, target, dloss, coef, common, base + c.hp, st) != cudaSuccess) return CONV2D_ERR_CUDA;
     const Operand ho{base + c.hp, c.dp * c.parts, c.dp * c.parts};
     GemmParams p{};

@@ -488,7 +488,7 @@ def _check_ce(h, w, target, dtype, reduction, op, dloss, tag=""):
                                    (129, 72, 257), (300, 509, 1003), (1, 1024, 5000), (64, 256, 20000), (777, 130, 2011),
                                    (1000, 64, 63), (257, 8, 4000), (513, 640, 1537), (5, 4096, 300), (2500, 96, 70),
                                    (2000, 520, 30001), (1500, 1032, 9000), (8, 3801, 1500), (8, 4800, 700), (3, 320, 29888),
-                                   (4, 2487, 2021), (1, 6144, 12345), (2, 31, 3), (6, 1, 9), (8, 1098, 5171)])
+                                   (4, 2487, 2021), (16, 640, 3001), (11, 333, 2000), (1, 6144, 12345), (2, 31, 3), (6, 1, 9), (8, 1098, 5171)])
 def test_linear_ce(dtype, n, d, v):
     import torch
     from dense_convolution_gb300 import head

@@ -152,6 +152,12 @@ template <typename T> struct Values<T, 1> {
     }
 };
 
+// Forward in registers: one read of x, one write of y.  A row takes as few
+// threads as keep every row's threads on the GPU at once, so small calls are
+// bound by one trip to memory and two exchanges (one row of 4096 bf16 2.7 us,
+// 2.0 of them launch), and 65536 x 64 bf16 takes 5.7 us.  A few very long rows
+// go to clusters: 32 x 200704 fp16 12.8 us (2.0 TB/s), where 128 blocks are what
+// 32 rows in clusters of four give.
 template <typename T, int CUT, int NV>
 __global__ void __launch_bounds__(1024) layernorm_fwd_kernel(const LnParams p) {
     constexpr int V = vec_of<T, CUT>();
@@ -313,7 +319,9 @@ __global__ void __launch_bounds__(1024) layernorm_fwd_long_kernel(const LnParams
 // start off the 16-byte boundary, so that all rows of a group are cut alike
 // and a thread's registers keep the same columns.  Eight elements of a row per
 // thread: sums, gamma and two rows in flight fit 64 registers, so 32 warps an
-// SM keep the memory busy; a group meets at a barrier of its own.
+// SM keep the memory busy; a group meets at a barrier of its own.  Short rows
+// leave it bound by latency: 65536 x 64 bf16 8.2 us for dx (3.1 TB/s); 1537 x 771
+// fp32 in a 776-wide buffer, element by element, 12.5 us.
 template <typename T, int CUT, int NV, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) layernorm_bwd_kernel(const LnParams p) {
     constexpr int V = vec_of<T, CUT>();
@@ -470,6 +478,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) layernorm_bwd_kernel(
 // takes sixteen elements, a turn ROWS rows whose sums share their exchanges and
 // barrier, the arithmetic is packed two by two, and rows that fill their threads
 // exactly (FULL) get a kernel without the tests for the ones that do not.
+// 16384 x 2048 bf16: 32.0 us (6.3 TB/s) for dx, dgamma's parts included; 4096 x
+// 8192 32.8 us; 16384 x 1024 fp16 18.0 us (5.6 TB/s).
 constexpr int kBulkBytes = 1024, kBulkThreads = 512, kBulkElems = 16, kRingBytes = 192 * 1024, kRingMost = 8;
 
 // The group's sums from its warps' (buf[k][warp], written by the first lane of
@@ -666,11 +676,16 @@ __global__ void __launch_bounds__(kBulkThreads, 1) layernorm_bwd_bulk_kernel(con
 }
 
 // Forward of the same rows: a turn's rows go from the ring into registers, so
-// their slots are free again after the first of the two meetings.
+// their slots are free again after the turn's one meeting: each warp takes the
+// squares about the mean of its own share, and the shares are joined exactly
+// (a second meeting for the squares cost 2 to 4 us more).  16384 x 2048 bf16 28.9
+// us (4.6 TB/s), 4096 x 8192 29.0, 8192 x 4096 fp32 46.2 (5.8 TB/s), 16384 x 1024
+// fp16 15.5; 16384 x 2040 fp16, whose rows do not fill their threads, 37.2.
 template <typename T, int ROWS, bool FULL>
 __global__ void __launch_bounds__(kBulkThreads, 1) layernorm_fwd_bulk_kernel(const LnParams p, const int ring_rows) {
     constexpr int V = vec_of<T, WHOLE>(), NV = kBulkElems / V, H = Pairs<T>::N, kSpan = 32 / ROWS;
-    __shared__ float red[2][ROWS][16];
+    constexpr int kLook = kSpan < 16 ? 16 / kSpan : 1;     // warps of a group (16 at most) that a lane joins
+    __shared__ float2 red[2][ROWS][16];                    // (mean, squares about it) of each warp's share
     __shared__ uint64_t bars[8][kRingMost];
     __shared__ int abort_word;
     extern __shared__ __align__(128) uint8_t ring_s[];     // [group][ring_rows][row]
@@ -714,7 +729,21 @@ __global__ void __launch_bounds__(kBulkThreads, 1) layernorm_fwd_bulk_kernel(con
             b[j][i] = pack2f(h[2 * i], h[2 * i + 1]);
         }
     }
-    int slot = 0;
+    // Elements of a warp's share of a row, and one over this warp's.
+    auto share_of = [&](int w) {
+        int n = 0;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) n += min(32, max(0, slots - j * tpr - w * 32));
+        return (float)(n * V);
+    };
+    const float own = share_of(warp - sub * wpr), inv_own = own > 0.f ? 1.0f / own : 0.f;
+    float size[kLook];
+#pragma unroll
+    for (int k = 0; k < kLook; ++k) {
+        const int w = lane % kSpan + k * kSpan;
+        size[k] = w < wpr ? share_of(w) : 0.f;
+    }
+    int slot = 0, turn = 0;
     uint32_t phase = 0;
     bool ok = true;
     for (int it = 0; it < mine; it += ROWS) {
@@ -742,36 +771,56 @@ __global__ void __launch_bounds__(kBulkThreads, 1) layernorm_fwd_bulk_kernel(con
             }
             v[q] = sum_halves(s);
         }
-        const float part = warp_sums<ROWS>(v);
-        if (lane % kSpan == 0) red[0][lane / kSpan][warp] = part;
-        ok = named_bar_and(1 + sub, tpr, landed);
-        if (!ok) break;
-        if (t == 0)
-            for (int q = 0; q < ROWS && issued < mine; ++q, ++issued) issue(slot + q);
-        slot += ROWS;
-        if (slot == ring_rows) { slot = 0; phase ^= 1; }
-        const float sum = group_sums<ROWS>(red[0], sub * wpr, wpr) * p.inv_cols;
-        float mean[ROWS];
+        const float warp_mean = warp_sums<ROWS>(v) * inv_own;
 #pragma unroll
         for (int q = 0; q < ROWS; ++q) {
-            mean[q] = __shfl_sync(0xffffffffu, sum, q * kSpan);
+            const f32x2 m = both(-__shfl_sync(0xffffffffu, warp_mean, q * kSpan));
             f32x2 s = 0ull;
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 if (FULL || j * tpr + t < slots) {
 #pragma unroll
                     for (int i = 0; i < H; ++i) {
-                        f[q][j][i] = add2(f[q][j][i], both(-mean[q]));
-                        s = fma2(f[q][j][i], f[q][j][i], s);
+                        const f32x2 d = add2(f[q][j][i], m);
+                        s = fma2(d, d, s);
                     }
                 }
             }
             v[q] = sum_halves(s);
         }
-        const float part2 = warp_sums<ROWS>(v);
-        if (lane % kSpan == 0) red[1][lane / kSpan][warp] = part2;
-        named_bar_sync(1 + sub, tpr);
-        const float sq = group_sums<ROWS>(red[1], sub * wpr, wpr) * p.inv_cols;
+        const float warp_sq = warp_sums<ROWS>(v);
+        if (lane % kSpan == 0) red[turn][lane / kSpan][warp] = make_float2(warp_mean, warp_sq);
+        ok = named_bar_and(1 + sub, tpr, landed);
+        if (!ok) break;
+        if (t == 0)
+            for (int q = 0; q < ROWS && issued < mine; ++q, ++issued) issue(slot + q);
+        slot += ROWS;
+        if (slot == ring_rows) { slot = 0; phase ^= 1; }
+        // The row's mean m, and sum s_i + n_i (m_i - m)^2: the squares about it.
+        float2 o[kLook];
+        float total = 0.f, sq = 0.f;
+#pragma unroll
+        for (int k = 0; k < kLook; ++k) {
+            const int w = lane % kSpan + k * kSpan;
+            o[k] = w < wpr ? red[turn][lane / kSpan][sub * wpr + w] : make_float2(0.f, 0.f);
+            total = fmaf(o[k].x, size[k], total);
+        }
+        turn ^= 1;                                         // (the other half is free: all have met since it was read)
+        total = lane_sum(total, kSpan) * p.inv_cols;
+#pragma unroll
+        for (int k = 0; k < kLook; ++k) sq += fmaf(size[k] * (o[k].x - total), o[k].x - total, o[k].y);
+        sq = lane_sum(sq, kSpan) * p.inv_cols;
+        float mean[ROWS];
+#pragma unroll
+        for (int q = 0; q < ROWS; ++q) {
+            mean[q] = __shfl_sync(0xffffffffu, total, q * kSpan);
+            const f32x2 m = both(-mean[q]);
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+                if (FULL || j * tpr + t < slots)
+#pragma unroll
+                    for (int i = 0; i < H; ++i) f[q][j][i] = add2(f[q][j][i], m);
+        }
 #pragma unroll
         for (int q = 0; q < ROWS; ++q) {
             const float rstd = rsqrtf(__shfl_sync(0xffffffffu, sq, q * kSpan) + p.eps);
@@ -800,7 +849,8 @@ __global__ void __launch_bounds__(kBulkThreads, 1) layernorm_fwd_bulk_kernel(con
             mbar_drain_wait(bar0 + (i % ring_rows) * 8, (uint32_t)(i / ring_rows) & 1u);
 }
 
-// Long rows, pass 1: sum a and sum a z of one row's share of columns.
+// Long rows, pass 1 (both passes of 31 x 99999 fp16 take 12.3 us, of 32 x
+// 200704 21 us; their dgamma and dbeta as much again): sum a and sum a z of one row's share of columns.
 template <typename T, int CUT>
 __global__ void __launch_bounds__(256) layernorm_bwd_sums_kernel(const LnParams p, float2* sums) {
     constexpr int V = vec_of<T, CUT>();
@@ -894,7 +944,8 @@ __global__ void __launch_bounds__(128) layernorm_bwd_cols_kernel(const LnParams 
 // dgamma and dbeta: the parts' columns added in order, SPAN columns by 1024 /
 // SPAN shares of the parts per block (blockIdx.y: dgamma or dbeta).  A few
 // hundred parts of a normal row: 32 shares, about ten loads per thread, all in
-// flight.  A few parts of a long row: one share.
+// flight.  A few parts of a long row: one share.  One trip to memory and the
+// launch are the whole of its 3 to 5 us.
 template <int SPAN>
 __global__ void __launch_bounds__(1024) layernorm_params_kernel(const float* part, int parts, int cols, void* dgamma,
                                                                 void* dbeta, int f32, int bf16) {

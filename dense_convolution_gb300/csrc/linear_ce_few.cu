@@ -6,8 +6,8 @@
 // A warp takes four rows of w at a time, a vector slot a lane; h lies in shared
 // memory, one column block per element of a vector, so that the lanes of a warp
 // read consecutive words whatever the rows' offset from the 16-byte boundary
-// (the four rows are a vector length apart and therefore offset alike; sixteen
-// tokens take two rows).  The 4 x tokens dot products are added over the warp together.
+// (the four rows are a vector length apart and therefore offset alike; a single
+// token, for an even share of short calls, and sixteen take two rows).  The 4 x tokens dot products are added over the warp together.
 //   forward    each lane keeps the running (max, sum) of the products it ends
 //              up with; blocks write one pair per token
 //   backward   dz = g (exp(z - lse) - [v = y]) goes back to all lanes, which
@@ -90,7 +90,7 @@ template <typename T> __device__ __forceinline__ void word_offsets(int shift, in
 
 template <typename T, int NT, bool BACKWARD>
 __global__ void __launch_bounds__(kThreads, 1) ce_few_kernel(const FewParams p) {
-    constexpr int V = kVec<T>, kRows = NT <= 8 ? 4 : 32 / NT;
+    constexpr int V = kVec<T>, kRows = NT == 1 ? 2 : NT <= 8 ? 4 : 32 / NT;
     constexpr int N = kRows * NT, kSpan = 32 / N, kOver = kSpan * NT;   // lanes per product and per row
     constexpr int P = kPair<NT>, NP = NT / P;
     using W = typename Word<P>::T;

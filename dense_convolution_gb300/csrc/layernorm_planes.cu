@@ -23,6 +23,11 @@
 // the way) hand every thread channel pairs of one pixel from either side, for
 // packed arithmetic.  What bounds the general form is instructions (37 an
 // element forward, 68 backward), most of them addresses.
+//
+// Measured, bf16, forward / backward with its sums: 64 images x 512 channels x 784
+// pixels 24.6 / 41.5 us (4.2 / 3.7 TB/s) in the fast form: the tile's way through
+// shared memory and its barriers hold it (issue slots 61 % busy forward, 43 %
+// backward; memory 24 to 37 %).  256 x 512 x 49 pixels, general form, 22.1 / 35.6 us.
 #include <cuda.h>
 
 #include "head_device.cuh"

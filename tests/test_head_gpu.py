@@ -634,7 +634,7 @@ def test_linear_ce_tiny_upstream_gradients(dtype):
         assert torch.equal(a.float()[normal] * 2.0 ** 10, b.float()[normal])
 
 
-@pytest.mark.parametrize("n,d,v", [(40, 32, 150), (300, 520, 1100)])
+@pytest.mark.parametrize("n,d,v", [(40, 32, 150), (300, 520, 1100), (7, 33, 150), (16, 100, 333)])
 def test_linear_ce_gradient_against_differences(n, d, v):
     """fp32: the loss's difference along a direction is the gradient's part of it."""
     import torch
@@ -653,12 +653,13 @@ def test_linear_ce_gradient_against_differences(n, d, v):
     assert abs(float((val(h, w + s * dwdir) - val(h, w - s * dwdir)) / (2 * s) - (dw.double() * dwdir).sum())) < tol
 
 
-def test_linear_ce_is_repeatable_and_keeps_to_its_buffers():
+@pytest.mark.parametrize("n,d,dtype", [(300, 264, "bf16"), (8, 264, "bf16"), (1, 1001, "f16"), (13, 130, "f32")])
+def test_linear_ce_is_repeatable_and_keeps_to_its_buffers(n, d, dtype):
     import torch
     from dense_convolution_gb300 import head, head_capi
-    n, d, v = 300, 264, 3000
-    h, w, target = _ce_inputs(30, n, d, v, "bf16")
-    op = head.LinearCrossEntropy(n, d, v, "bf16", reduction="none", piece=1024)
+    v = 3000
+    h, w, target = _ce_inputs(30, n, d, v, dtype)
+    op = head.LinearCrossEntropy(n, d, v, dtype, reduction="none", piece=1024)
     dloss = torch.rand(n, device="cuda")
     first = None
     for fill in (0x00, 0xFF, 0x7F):                                        # whatever the workspace held
@@ -677,6 +678,42 @@ def test_linear_ce_is_repeatable_and_keeps_to_its_buffers():
     assert none is None and only_w.equal(first[3])
 
 
+@pytest.mark.parametrize("n", [2, 20])
+def test_linear_ce_beyond_32_bit_offsets(n):
+    """A vocabulary whose weights pass 2^32 elements: all zero but for the first and last rows."""
+    import torch
+    from dense_convolution_gb300 import head
+    d, v, k = 4096, 2 ** 20 + 5, 3
+    g = _gen(n)
+    ends = (_randn(g, 2 * k, d) * (2.0 / math.sqrt(d))).to(torch.bfloat16)
+    w = torch.zeros(v, d, device="cuda", dtype=torch.bfloat16)
+    w[:k], w[-k:] = ends[:k], ends[k:]
+    h = (_randn(g, n, d) + 3 * ends[-1].float() / ends[-1].float().norm()).to(torch.bfloat16)
+    target = torch.full((n,), v - 1, device="cuda")
+    target[1] = 1
+    op = head.LinearCrossEntropy(n, d, v, "bf16", reduction="sum")
+    loss, lse = op(h, w, target)
+    dh, dw = op.backward(h, w, target, lse, torch.ones((), device="cuda"))
+    z = h.double() @ ends.double().T
+    want = torch.log((v - 2 * k) + z.exp().sum(1))
+    # v sums of about 1 each in fp32, joined by trees and chains of a few hundred
+    _close(lse, want, 512 * E * want.abs(), "lse")
+    y = torch.full((n,), 2 * k - 1, device="cuda")
+    y[1] = 1
+    _close(loss, (want - z.gather(1, y[:, None])[:, 0]).sum(), n * 512 * E * want.abs().max() + 64 * E * z.abs().max(), "loss")
+    p = torch.exp(z - want[:, None])
+    p[torch.arange(n, device="cuda"), y] -= 1.0
+    dh_want, size = p @ ends.double(), p.abs() @ ends.double().abs()
+    _close(dh, dh_want, U["bf16"] * dh_want.abs() + (U["bf16"] + 1e-4) * size + 1e-30, "dh")
+    dw_want, size = p.T @ h.double(), p.T.abs() @ h.double().abs()
+    got = torch.cat([dw[:k], dw[-k:]])
+    _close(got, dw_want, U["bf16"] * dw_want.abs() + (U["bf16"] + 1e-4) * size + 1e-30, "dw")
+    middle = torch.exp(-want)[:, None].expand(n, 1).T @ h.double()         # every other row: p = exp(-lse)
+    size = torch.exp(-want)[None] @ h.double().abs()
+    for row in (k, v // 2, v - k - 1):
+        _close(dw[row:row + 1], middle, U["bf16"] * middle.abs() + (U["bf16"] + 1e-4) * size + 1e-30, f"dw {row}")
+
+
 def test_linear_ce_no_tokens():
     import torch
     from dense_convolution_gb300 import head
@@ -690,11 +727,12 @@ def test_linear_ce_no_tokens():
 
 
 # ------------------------------------------------------------------ together
-def test_other_stream_and_capture():
+@pytest.mark.parametrize("n", [256, 6])
+def test_other_stream_and_capture(n):
     """The operators on a stream that is not the tensors' own, and in a graph."""
     import torch
     from dense_convolution_gb300 import head
-    n, d, v = 256, 512, 1500
+    d, v = 512, 1500
     h, w, target = _ce_inputs(40, n, d, v, "bf16")
     gamma, beta = torch.ones(d, device="cuda"), torch.zeros(d, device="cuda")
     ln = head.LayerNorm(n, d, "bf16", "f32")

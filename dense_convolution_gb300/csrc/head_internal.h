@@ -34,6 +34,7 @@ struct CePlan {
     bool few;                      // few tokens: linear_ce_few.cu
     bool bf16, pack_w, pack_h;
     int parts, pairs;              // bf16 parts per value (1, or 3 for fp32) and their products (1 or 6)
+    int dz_parts, out_pairs;       // the same for dz and the products that read it (16 bits, few rows: 2 and 2)
     int64_t dp;                    // packed row pitch of one part
     int64_t piece, pieces;         // vocabulary rows per piece
     LaunchPlan z, out;             // the logits; dh and dw together

@@ -7,8 +7,8 @@
 //              target's z, so z never reaches memory.  A second kernel joins
 //              the tiles' pairs: the maximum first, then the rescaled sums.
 //   backward   per piece of the vocabulary: z again, turned by the epilogue
-//              into dz = g (exp(z - lse) - [v = y]) in 16 bits; then
-//              dh += dz w and dw = dz^T h.
+//              into dz = g (exp(z - lse) - [v = y]) in 16 bits (twice 16 for up
+//              to 256 rows); then dh += dz w and dw = dz^T h.
 //
 // All three products run in one kernel (ce_gemm_kernel): C[M][N] = sum_k
 // A[m][k] B[n][k] in 64-wide K chunks, each operand stored either along K
@@ -49,6 +49,8 @@
 #include <cuda.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "head_device.cuh"
 #include "head_internal.h"
 #include "ptx.cuh"
@@ -74,7 +76,7 @@ struct GemmParams {
     int a_mn;                // A is MN-major
     int n_m, n_n;            // tiles
     int group;               // row tiles that share each column tile before the next one is taken
-    int nk, pairs;           // K chunks of one product of parts, and such products (1 or 6)
+    int nk, pairs;           // K chunks of one product of parts, and such products (1, 2 or 6)
     int a_part, b_part;      // column offset from one part to the next
     int splits;
     // EPI_LSE and EPI_DZ
@@ -149,6 +151,10 @@ template <bool BF16> __device__ __forceinline__ uint32_t pack2(float a, float b)
         const __half2 v = __floats2half2_rn(a, b);
         return *reinterpret_cast<const uint32_t*>(&v);
     }
+}
+
+template <bool BF16> __device__ __forceinline__ void unpack2(uint32_t w, float& a, float& b) {
+    unpack2f(widen_pair<std::conditional_t<BF16, __nv_bfloat16, __half>>(w), a, b);
 }
 
 // The bf16 nearest to x (toward zero where that would overflow), and what is
@@ -341,15 +347,17 @@ ce_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ Ge
                 const int k1 = (int)((long long)chunks * (it.split + 1) / p.splits);
                 const int m0 = it.m * kTileM + rank * kBM, n0 = it.n * jobs.BN + rank * bn;
                 const int nk = p.nk, a_mn = p.a_mn, pairs = p.pairs;
-                int pair = k0 / nk, k = k0 - pair * nk;
+                // Six products run one after the other; two in turn, B's chunk read again from the L2.
+                const bool two = pairs == 2;
+                int pair = two ? k0 & 1 : k0 / nk, k = two ? k0 >> 1 : k0 - pair * nk;
                 for (int q = k0; q < k1; ++q) {
                     if (!mbar_wait(empty_bar(stage), phase ^ 1, abort_flag)) { ok = false; break; }
                     // A pair's copies all count on the issuing CTA's barrier.
                     if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), (uint32_t)(kCtas * stage_bytes));
                     const uint32_t bar = PAIR ? cluster_addr(full_bar(stage), 0) : full_bar(stage);
                     const uint32_t a_dst = smem_addr(smem + stage * stage_bytes), b_dst = a_dst + kABytes;
-                    const int ao = pairs > 1 ? kPartA[pair] * p.a_part : 0;
-                    const int bo = pairs > 1 ? kPartB[pair] * p.b_part : 0;
+                    const int ao = two ? (pair ^ 1) * p.a_part : pairs > 1 ? kPartA[pair] * p.a_part : 0;
+                    const int bo = pairs > 2 ? kPartB[pair] * p.b_part : 0;
                     auto load = [&](uint32_t dst, const CUtensorMap* map, int c0, int c1) {
                         if constexpr (PAIR) tma_load_2d_pair(dst, map, bar, c0, c1);
                         else                tma_load_2d(dst, map, bar, c0, c1);
@@ -367,7 +375,13 @@ ce_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ Ge
                     }
                     ++issued;
                     if (++stage == stages) { stage = 0; phase ^= 1; }
-                    if (++k == nk) { k = 0; ++pair; }
+                    if (two) {
+                        k += pair;
+                        pair ^= 1;
+                    } else if (++k == nk) {
+                        k = 0;
+                        ++pair;
+                    }
                 }
             }
             if constexpr (PAIR) *copies = (int)issued;         // (only the last ring's worth matters below)
@@ -561,10 +575,19 @@ ce_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ Ge
 #pragma unroll
                         for (int j = 0; j < 32; j += 16) {
                             uint32_t u[8];
-                            if (!PROMOTE || p.parts == 1) {
+                            if constexpr (!PROMOTE) {
 #pragma unroll
                                 for (int l = 0; l < 8; ++l) u[l] = pack2<BF16>(v[j + 2 * l], v[j + 2 * l + 1]);
                                 st_global_v8(dst + j, u);
+                                if (p.parts == 2) {            // what the rounding left
+#pragma unroll
+                                    for (int l = 0; l < 8; ++l) {
+                                        float a, b;
+                                        unpack2<BF16>(u[l], a, b);
+                                        u[l] = pack2<BF16>(rest_of(v[j + 2 * l], a), rest_of(v[j + 2 * l + 1], b));
+                                    }
+                                    st_global_v8(dst + p.dz_part + j, u);
+                                }
                             } else {
                                 // Part after part: what a part leaves of v goes on to the next.
 #pragma unroll
@@ -1009,7 +1032,7 @@ template <int EPI, bool PAIR> const void* gemm_kernel(bool bf16, bool f32) {
 
 template <int EPI>
 conv2d_status launch_gemm(bool bf16, const LaunchPlan& g, const GemmMaps& maps, GemmJobs& jobs, int n, cudaStream_t st) {
-    const bool f32 = jobs.job[0].pairs > 1, promote = f32 || EPI == EPI_LSE;
+    const bool f32 = jobs.job[0].pairs > 2, promote = f32 || EPI == EPI_LSE;
     const void* kern = g.pair ? gemm_kernel<EPI, true>(bf16, f32) : gemm_kernel<EPI, false>(bf16, f32);
     if (!allow_smem(kern)) return CONV2D_ERR_CUDA;
     const int ctas = g.pair ? 2 : 1;
@@ -1026,7 +1049,7 @@ conv2d_status launch_gemm(bool bf16, const LaunchPlan& g, const GemmMaps& maps, 
         p.n_m = (int)ceil_div(p.M, ctas * kBM);
         p.n_n = (int)ceil_div(p.N, g.BN);
         // Row tiles whose A (read again for every column tile) stays in the L2 beside the streams.
-        const int64_t a_tile = (int64_t)ctas * kBM * p.nk * kBK * 2 * (p.pairs > 1 ? 3 : 1);
+        const int64_t a_tile = (int64_t)ctas * kBM * p.nk * kBK * 2 * (p.pairs > 2 ? 3 : p.pairs);
         const int64_t rows = (24 << 20) / a_tile;
         p.group = (int)(rows < 1 ? 1 : (rows > p.n_m ? p.n_m : rows));
         const int64_t items = (int64_t)p.n_m * p.n_n * p.splits;
@@ -1074,6 +1097,13 @@ CePlan plan_ce(const linear_ce_desc& d, bool backward) {
     c.bf16 = d.dtype != CONV2D_F16;
     c.parts = f32 ? 3 : 1;
     c.pairs = f32 ? 6 : 1;
+    // With few rows the rounding of dz to 16 bits does not average out (one large
+    // element per row: dw of 31 fp16 tokens was off by 3.1e-4, its own rounding is
+    // 2.1e-4): it then keeps what the rounding leaves as a second part.  Backward
+    // with one part and with two, bf16: 64 x 4096 x 65536 329 and 369 us, 256 x 1024
+    // x 32000 94 and 110 us, 256 x 4096 x 65536 460 and 561 us.
+    c.dz_parts = f32 ? 3 : d.tokens <= 2 * kBM ? 2 : 1;
+    c.out_pairs = f32 ? 6 : c.dz_parts;
     c.pack_w = f32 || d.ws % 8 != 0;
     // The backward pass always copies h: ignored rows must be zero in dw's product.
     c.pack_h = backward || f32 || d.hs % 8 != 0;
@@ -1083,7 +1113,7 @@ CePlan plan_ce(const linear_ce_desc& d, bool backward) {
     int64_t piece = ceil_div(d.vocab, 256) * 256;
     if (backward || c.pack_w) {
         int64_t most = budget;
-        if (backward) most = budget / (d.tokens * 2 * c.parts);
+        if (backward) most = budget / (d.tokens * 2 * c.dz_parts);
         if (c.pack_w && budget / (c.dp * 2 * c.parts) < most) most = budget / (c.dp * 2 * c.parts);
         if (d.piece > 0 && backward) most = (d.piece < kMostPiece ? d.piece : kMostPiece) + 255;
         most = most / 256 * 256;
@@ -1103,12 +1133,12 @@ CePlan plan_ce(const linear_ce_desc& d, bool backward) {
         take(at, c.z_target, (size_t)d.tokens * 4);
         take(at, c.row_loss, (size_t)d.tokens * 4);
     } else {
-        const Product out[2] = {{d.tokens, d.hidden, ceil_div(v, 64) * c.pairs, true},
-                                {v, d.hidden, ceil_div(d.tokens, 64) * c.pairs, true}};
+        const Product out[2] = {{d.tokens, d.hidden, ceil_div(v, 64) * c.out_pairs, true},
+                                {v, d.hidden, ceil_div(d.tokens, 64) * c.out_pairs, true}};
         c.out = plan_gemm(out, 2, 64, true);
         take(at, c.coef, (size_t)d.tokens * 4);
         take(at, c.common, 4);
-        take(at, c.dz, (size_t)d.tokens * (size_t)piece * 2 * c.parts);
+        take(at, c.dz, (size_t)d.tokens * (size_t)piece * 2 * c.dz_parts);
         if (c.pieces > 1) take(at, c.acc, (size_t)d.tokens * c.dp * 4);
         if (c.out.splits[0] > 1) take(at, c.sums_h, (size_t)c.out.splits[0] * d.tokens * c.dp * 4);
         if (c.out.splits[1] > 1) take(at, c.sums_w, (size_t)c.out.splits[1] * v * c.dp * 4);
@@ -1190,7 +1220,7 @@ GemmParams out_job(const CePlan& c, const linear_ce_desc& d, int splits, bool a_
     p.N = (int)d.hidden;
     p.a_mn = a_mn;
     p.nk = (int)ceil_div(K, 64);
-    p.pairs = c.pairs;
+    p.pairs = c.out_pairs;
     p.a_part = (int)c.piece;
     p.b_part = (int)b_part;
     p.splits = splits < p.nk * p.pairs ? splits : p.nk * p.pairs;
@@ -1306,7 +1336,7 @@ conv2d_status launch_linear_ce_bwd(const linear_ce_desc& d, const void* h, const
     p.coef = coef;
     p.dz = base + c.dz;
     p.dz_part = (int)c.piece;
-    p.parts = c.parts;
+    p.parts = c.dz_parts;
     for (int64_t v0 = 0; v0 < d.vocab; v0 += c.piece) {
         const int64_t rows = d.vocab - v0 < c.piece ? d.vocab - v0 : c.piece;
         const bool first = v0 == 0, last = v0 + rows >= d.vocab;
@@ -1319,7 +1349,7 @@ conv2d_status launch_linear_ce_bwd(const linear_ce_desc& d, const void* h, const
         conv2d_status s = gemm_z(c, d, EPI_DZ, ho, wo, rows, p, st);
         if (s != CONV2D_OK) return s;
         // dh and dw of the piece in one launch.
-        const int64_t dz_pitch = c.piece * c.parts;
+        const int64_t dz_pitch = c.piece * c.dz_parts;
         GemmMaps maps;
         GemmJobs jobs{};
         int n = 0;

@@ -34,11 +34,12 @@ constexpr int kSmemMost = 200 * 1024;
 
 struct FewParams {
     int tokens, hidden, vocab, reduction;
+    int pitch;               // tokens between the blocks' parts
     int64_t hs, ws, ignore;
     const void *h, *w;
     const int64_t* target;
     // forward
-    float2* part;            // [blocks][tokens]
+    float2* part;            // [blocks][pitch]
     float* z_target;
     // backward
     const float *lse, *dloss;
@@ -273,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1) ce_few_kernel(const FewParams p) 
                 s = s * exp2_of((m - base) * kLog2e) + o.y * exp2_of((o.x - base) * kLog2e);
                 m = top;
             }
-            p.part[(int64_t)blockIdx.x * p.tokens + threadIdx.x] = make_float2(m, s);
+            p.part[(int64_t)blockIdx.x * p.pitch + threadIdx.x] = make_float2(m, s);
         }
     }
 }
@@ -418,36 +419,40 @@ __global__ void __launch_bounds__(256) ce_few_join_kernel(const float* part, int
 
 int nt_of(int64_t tokens) { return tokens <= 1 ? 1 : tokens <= 2 ? 2 : tokens <= 4 ? 4 : tokens <= 8 ? 8 : 16; }
 
-template <typename T> size_t few_smem(const linear_ce_desc& d) {
-    return (size_t)nt_of(d.tokens) * kVec<T> * few_pitch<T>((int)d.hidden) * sizeof(float);
+template <typename T> size_t few_smem(int64_t tokens, int64_t hidden) {
+    return (size_t)nt_of(tokens) * kVec<T> * few_pitch<T>((int)hidden) * sizeof(float);
+}
+bool few_fits(const linear_ce_desc& d, int64_t tokens) {
+    return (d.dtype == CONV2D_F32 ? few_smem<float>(tokens, d.hidden) : few_smem<__half>(tokens, d.hidden)) <=
+           (size_t)kSmemMost;
 }
 
-template <typename T, int NT, bool BACKWARD> cudaError_t few_launch(const linear_ce_desc& d, const FewParams& p, cudaStream_t st) {
-    const size_t smem = few_smem<T>(d);
+template <typename T, int NT, bool BACKWARD> cudaError_t few_launch(const FewParams& p, cudaStream_t st) {
+    const size_t smem = few_smem<T>(NT, p.hidden);
     const cudaError_t e = cudaFuncSetAttribute(ce_few_kernel<T, NT, BACKWARD>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     return launch_after(ce_few_kernel<T, NT, BACKWARD>, dim3((unsigned)linear_ce_few_blocks()), dim3(kThreads), smem, st,
                         p);
 }
-template <typename T, bool BACKWARD> cudaError_t few_tokens(const linear_ce_desc& d, const FewParams& p, cudaStream_t st) {
-    switch (nt_of(d.tokens)) {
-        case 1: return few_launch<T, 1, BACKWARD>(d, p, st);
-        case 2: return few_launch<T, 2, BACKWARD>(d, p, st);
-        case 4: return few_launch<T, 4, BACKWARD>(d, p, st);
-        case 8: return few_launch<T, 8, BACKWARD>(d, p, st);
+template <typename T, bool BACKWARD> cudaError_t few_tokens(const FewParams& p, cudaStream_t st) {
+    switch (nt_of(p.tokens)) {
+        case 1: return few_launch<T, 1, BACKWARD>(p, st);
+        case 2: return few_launch<T, 2, BACKWARD>(p, st);
+        case 4: return few_launch<T, 4, BACKWARD>(p, st);
+        case 8: return few_launch<T, 8, BACKWARD>(p, st);
     }
     if constexpr (sizeof(T) == 4) {
-        return few_launch<T, 16, BACKWARD>(d, p, st);
+        return few_launch<T, 16, BACKWARD>(p, st);
     } else {
         return cudaErrorInvalidValue;
     }
 }
 template <bool BACKWARD> cudaError_t few(const linear_ce_desc& d, const FewParams& p, cudaStream_t st) {
     switch (d.dtype) {
-        case CONV2D_F32: return few_tokens<float, BACKWARD>(d, p, st);
-        case CONV2D_F16: return few_tokens<__half, BACKWARD>(d, p, st);
-        default: return few_tokens<__nv_bfloat16, BACKWARD>(d, p, st);
+        case CONV2D_F32: return few_tokens<float, BACKWARD>(p, st);
+        case CONV2D_F16: return few_tokens<__half, BACKWARD>(p, st);
+        default: return few_tokens<__nv_bfloat16, BACKWARD>(p, st);
     }
 }
 
@@ -494,17 +499,16 @@ int linear_ce_few_blocks() { return device_sm_count(); }
 // Few tokens, whose h fits a block's shared memory.  The products of
 // linear_ce.cu read w at one speed whatever the tokens, but want fp32 split and
 // odd rows copied first.  Forward / backward, this file against that one:
-//   bf16 4096 x 65536, in place   4 tokens  94 / 321 us, 132 / 338;   8 tokens 144 / 447, 109 / 341
+//   bf16 4096 x 65536, in place   4 tokens  94 / 321 us, 132 / 338;   8 tokens 144 / 447, 109 / 406
 //   bf16 2487 x 64640, copied     8 tokens 114 / 327 us, 211 / 465
 //   fp32 2048 x 50000             8 tokens  81 / 249 us, 516 / 825;  16 tokens 131 / 394, 411 / 769
-//   fp32 1024 x 50000            32 tokens 218 / 604 us, 203 / 414
-// (backward of eight 16-bit tokens stays here for its fp32 dz: rounded to fp16,
-// the few large values of dz alone can double the error of dw).
+//   fp32 1024 x 50000            32 tokens 218 / 604 us (a form for 32 at once), 203 / 414
+// Forward of fp32 takes up to 32 tokens in groups, each of which reads w again:
+// 32 x 2048 x 50000 259 us, 411 on the tensor cores; 32 x 1024 x 50000 160, 203.
 bool linear_ce_is_few(const linear_ce_desc& d, bool backward) {
+    if (d.dtype == CONV2D_F32 && !backward) return d.tokens <= 32 && few_fits(d, d.tokens < 8 ? d.tokens : 8);
     const bool copied = d.hs % 8 != 0 || d.ws % 8 != 0;
-    if (d.tokens > (d.dtype == CONV2D_F32 ? 16 : copied || backward ? 8 : 4)) return false;
-    const size_t smem = d.dtype == CONV2D_F32 ? few_smem<float>(d) : few_smem<__half>(d);
-    return smem <= (size_t)kSmemMost;
+    return d.tokens <= (d.dtype == CONV2D_F32 ? 16 : copied ? 8 : 4) && few_fits(d, d.tokens);
 }
 
 // fp32 words of dz and of the partial sums of dh.
@@ -513,13 +517,22 @@ int64_t linear_ce_few_sums(const linear_ce_desc& d) { return (int64_t)dh_plan(d)
 
 cudaError_t launch_ce_few_fwd(const linear_ce_desc& d, const void* h, const void* w, const int64_t* target, void* part,
                               float* z_target, cudaStream_t st) {
-    FewParams p{};
-    p.tokens = (int)d.tokens; p.hidden = (int)d.hidden; p.vocab = (int)d.vocab; p.reduction = d.reduction;
-    p.hs = d.hs; p.ws = d.ws; p.ignore = d.ignore_index;
-    p.h = h; p.w = w; p.target = target;
-    p.part = static_cast<float2*>(part);
-    p.z_target = z_target;
-    return few<false>(d, p, st);
+    const int64_t most = d.tokens <= 8 || !few_fits(d, 16) ? 8 : 16;
+    for (int64_t t = 0; t < d.tokens; t += most) {
+        FewParams p{};
+        p.tokens = (int)(d.tokens - t < most ? d.tokens - t : most);
+        p.pitch = (int)d.tokens;
+        p.hidden = (int)d.hidden; p.vocab = (int)d.vocab; p.reduction = d.reduction;
+        p.hs = d.hs; p.ws = d.ws; p.ignore = d.ignore_index;
+        p.h = static_cast<const uint8_t*>(h) + (size_t)(t * d.hs) * elem_bytes(d.dtype);
+        p.w = w;
+        p.target = target + t;
+        p.part = static_cast<float2*>(part) + t;
+        p.z_target = z_target + t;
+        const cudaError_t e = few<false>(d, p, st);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 cudaError_t launch_ce_few_bwd(const linear_ce_desc& d, const void* h, const void* w, const int64_t* target,

@@ -347,17 +347,24 @@ ce_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ Ge
                 const int k1 = (int)((long long)chunks * (it.split + 1) / p.splits);
                 const int m0 = it.m * kTileM + rank * kBM, n0 = it.n * jobs.BN + rank * bn;
                 const int nk = p.nk, a_mn = p.a_mn, pairs = p.pairs;
-                // Six products run one after the other; two in turn, B's chunk read again from the L2.
-                const bool two = pairs == 2;
-                int pair = two ? k0 & 1 : k0 / nk, k = two ? k0 >> 1 : k0 - pair * nk;
+                // Six products run one after the other; two (never PROMOTE) in turn,
+                // the second part first, B's chunk read again from the L2.
+                const int other = !PROMOTE && pairs == 2 ? p.a_part : 0;
+                int pair = k0 / nk, k = k0 - pair * nk, ao = 0, bo = 0;
+                if (!PROMOTE && pairs == 2) {
+                    k = k0 >> 1;
+                    ao = k0 & 1 ? 0 : other;
+                }
                 for (int q = k0; q < k1; ++q) {
                     if (!mbar_wait(empty_bar(stage), phase ^ 1, abort_flag)) { ok = false; break; }
                     // A pair's copies all count on the issuing CTA's barrier.
                     if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), (uint32_t)(kCtas * stage_bytes));
                     const uint32_t bar = PAIR ? cluster_addr(full_bar(stage), 0) : full_bar(stage);
                     const uint32_t a_dst = smem_addr(smem + stage * stage_bytes), b_dst = a_dst + kABytes;
-                    const int ao = two ? (pair ^ 1) * p.a_part : pairs > 1 ? kPartA[pair] * p.a_part : 0;
-                    const int bo = pairs > 2 ? kPartB[pair] * p.b_part : 0;
+                    if (PROMOTE) {
+                        ao = pairs > 1 ? kPartA[pair] * p.a_part : 0;
+                        bo = pairs > 1 ? kPartB[pair] * p.b_part : 0;
+                    }
                     auto load = [&](uint32_t dst, const CUtensorMap* map, int c0, int c1) {
                         if constexpr (PAIR) tma_load_2d_pair(dst, map, bar, c0, c1);
                         else                tma_load_2d(dst, map, bar, c0, c1);
@@ -375,9 +382,9 @@ ce_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ Ge
                     }
                     ++issued;
                     if (++stage == stages) { stage = 0; phase ^= 1; }
-                    if (two) {
-                        k += pair;
-                        pair ^= 1;
+                    if (!PROMOTE) {
+                        k += ao == 0;
+                        ao = other - ao;
                     } else if (++k == nk) {
                         k = 0;
                         ++pair;

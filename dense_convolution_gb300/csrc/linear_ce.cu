@@ -43,7 +43,7 @@
 // Measured (products counted once): the logits with their reduction 1.51 PFLOP/s
 // at 4096 x 1024 x 65536 bf16 and 1.76 at 16384 x 2048 x 65536, dz 1.40 and 1.55,
 // dh and dw 1.4 to 1.6; large calls run at the power limit (clock 1.5 GHz of
-// 2.07).  fp32 1000 x 768 x 20011: losses 138 us, dz 195 us, dh and dw 300 us (1.3,
+// 2.07).  fp32 1000 x 768 x 20011: losses 140 us, dz 200 us, dh and dw 300 us (1.3,
 // 0.9 and 1.2 PFLOP/s of the six products): dz's three parts leave at each
 // tile's end, longer than two accumulators cover.
 #include <cuda.h>

@@ -1,6 +1,7 @@
 // C ABI of the training-head operators (include/head.h): descriptors, argument
 // checks and workspace sizes.  Host code only; the kernels live in
-// layernorm.cu, dropout.cu and linear_ce.cu.
+// layernorm.cu, layernorm_planes.cu, dropout.cu, linear_ce.cu and
+// linear_ce_few.cu.
 #include <math.h>
 
 #include <new>

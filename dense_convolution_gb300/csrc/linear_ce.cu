@@ -25,11 +25,10 @@
 // matrix, and the K loop runs six times as long.
 //
 // The tensor cores round an accumulator toward zero at every step, a bias that
-// grows with K (4e-5 of dh over 20011 vocabulary rows, measured).  Where the
-// result is kept in fp32 (the losses, and everything of fp32 operands) the
-// accumulator therefore runs for `seg` chunks only and the epilogue adds these
-// partial sums in registers, rounded to nearest, while the next ones are
-// computed (PROMOTE).
+// grows with K.  Where the result is kept in fp32 (the losses, and everything of
+// fp32 operands), and for dz of long 16-bit rows (promote_z), the accumulator
+// therefore runs for `seg` chunks only and the epilogue adds these partial sums
+// in registers, rounded to nearest, while the next ones are computed (PROMOTE).
 //
 // Large products run on CTA pairs (PAIR): the tile is 256 rows by BN columns,
 // each CTA keeps half of the rows of A and half of the columns of B in its
@@ -582,7 +581,7 @@ ce_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ Ge
 #pragma unroll
                         for (int j = 0; j < 32; j += 16) {
                             uint32_t u[8];
-                            if constexpr (!PROMOTE) {
+                            if (!PROMOTE || !BF16 || p.parts < 3) {
 #pragma unroll
                                 for (int l = 0; l < 8; ++l) u[l] = pack2<BF16>(v[j + 2 * l], v[j + 2 * l + 1]);
                                 st_global_v8(dst + j, u);
@@ -1030,21 +1029,37 @@ int pair_count() {
     return n;
 }
 
-template <int EPI, bool PAIR> const void* gemm_kernel(bool bf16, bool f32) {
-    // fp32 operands (six products) are bf16 parts; their results stay in fp32.
-    return f32    ? reinterpret_cast<const void*>(&ce_gemm_kernel<true, EPI, true, PAIR>)
-           : bf16 ? reinterpret_cast<const void*>(&ce_gemm_kernel<true, EPI, EPI == EPI_LSE, PAIR>)
-                  : reinterpret_cast<const void*>(&ce_gemm_kernel<false, EPI, EPI == EPI_LSE, PAIR>);
+// Where the logits of a 16-bit dz are promoted.  What truncation takes from z, which
+// grows with z and the hidden size, is missing from p = exp(z - lse) as a factor,
+// while lse comes from the forward pass's promoted sums: all-positive logits of 2.9 on
+// average lowered dh and dw by 6e-5 at 4096 features, 2.9e-4 at 16384.  One segment of
+// the forward pass is as exact here without; beyond it fp16 promotes, and bf16, whose
+// own rounding is eight times coarser, from eight times that on.  The promoted form
+// costs z 3 to 8 % (bf16 8192 x 2048 x 131072 2.70 and 2.91 ms, fp16 4096 x 4096 x
+// 32768 0.86 and 0.84 ms, 2000 x 520 x 30001 as one segment 0.09 ms).
+bool promote_z(bool bf16, int nk) { return nk > (bf16 ? 128 : 16); }
+
+template <int EPI, bool PAIR> const void* gemm_kernel(bool bf16, bool promote) {
+    if constexpr (EPI == EPI_LSE) {
+        return bf16 ? reinterpret_cast<const void*>(&ce_gemm_kernel<true, EPI, true, PAIR>)
+                    : reinterpret_cast<const void*>(&ce_gemm_kernel<false, EPI, true, PAIR>);
+    } else {
+        if (promote && bf16) return reinterpret_cast<const void*>(&ce_gemm_kernel<true, EPI, true, PAIR>);
+        if constexpr (EPI == EPI_DZ)
+            if (promote) return reinterpret_cast<const void*>(&ce_gemm_kernel<false, EPI, true, PAIR>);
+        return bf16 ? reinterpret_cast<const void*>(&ce_gemm_kernel<true, EPI, false, PAIR>)
+                    : reinterpret_cast<const void*>(&ce_gemm_kernel<false, EPI, false, PAIR>);
+    }
 }
 
 template <int EPI>
 conv2d_status launch_gemm(bool bf16, const LaunchPlan& g, const GemmMaps& maps, GemmJobs& jobs, int n, cudaStream_t st) {
-    const bool f32 = jobs.job[0].pairs > 2, promote = f32 || EPI == EPI_LSE;
-    const void* kern = g.pair ? gemm_kernel<EPI, true>(bf16, f32) : gemm_kernel<EPI, false>(bf16, f32);
+    const bool f32 = jobs.job[0].pairs > 2, promote = f32 || EPI == EPI_LSE || (EPI == EPI_DZ && promote_z(bf16, jobs.job[0].nk));
+    const void* kern = g.pair ? gemm_kernel<EPI, true>(bf16, promote) : gemm_kernel<EPI, false>(bf16, promote);
     if (!allow_smem(kern)) return CONV2D_ERR_CUDA;
     const int ctas = g.pair ? 2 : 1;
     jobs.BN = g.BN;
-    // Results in fp32: the shortest segment where the tensor cores wait for
+    // Promoted sums: the shortest segment where the tensor cores wait for
     // memory anyway (few rows).  Emptying an accumulator takes about 1.2 us,
     // longer than four chunks: large products of fp32 operands take six (dh
     // of 1000 x 768 x 20011 is 7e-7 off), losses of 16-bit operands sixteen (5e-7).

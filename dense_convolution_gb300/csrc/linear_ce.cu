@@ -930,8 +930,8 @@ constexpr int64_t kMostPiece = 1LL << 28;      // three parts of a piece keep 32
 // CTA pairs that run at once (SMs pair up within their cluster hardware).
 int pair_count();
 
-// One product of a launch, for the estimate.
-struct Product { int64_t M, N, chunks; bool may_split; };
+// One product of a launch, for the estimate; at least `least` splits.
+struct Product { int64_t M, N, chunks; bool may_split; int least; };
 
 // Tile width, CTA pairs and K splits of a launch's products by an estimate in SM
 // cycles.  A 64-wide chunk takes its MMAs (2 BN cycles) or its operands' way
@@ -939,7 +939,8 @@ struct Product { int64_t M, N, chunks; bool may_split; };
 // at 78 % of the MMA rate, and any tile narrower than 256), and a fixed cost;
 // an item (one tile of one split) adds pipeline fill and its last epilogue;
 // items run in turn over the SMs or pairs, the first product's before the
-// second's; splits add the write and read of their fp32 sums and one launch.
+// second's; splits add the write and read of their fp32 sums and one launch.  Up
+// to 64 splits are weighed, or the fewest that the product needs.
 LaunchPlan plan_gemm(const Product* pr, int n, int step, bool b_mn) {
     LaunchPlan best{256, false, {1, 1}};
     double best_t = -1;
@@ -951,10 +952,12 @@ LaunchPlan plan_gemm(const Product* pr, int n, int step, bool b_mn) {
             if (bn - down >= pr[0].N && bn - down >= (pair ? 128 : 64)) continue;      // wider than the output needs
             const double bytes = kABytes + (pair ? bn / 2 : bn) * kBK * 2;
             const double chunk = (2.0 * bn > bytes / 75.0 ? 2.0 * bn : bytes / 75.0) + 24.0;
-            for (int s0 = 1; s0 <= 64; s0 = s0 < 4 ? s0 + 1 : s0 + s0 / 2) {
-                if (s0 > 1 && (!pr[0].may_split || s0 > pr[0].chunks)) break;
-                for (int s1 = 1; s1 <= 64; s1 = s1 < 4 ? s1 + 1 : s1 + s1 / 2) {
-                    if (s1 > 1 && (n == 1 || !pr[1].may_split || s1 > pr[1].chunks)) break;
+            const int least[2] = {pr[0].least, n > 1 ? pr[1].least : 1};
+            const int most[2] = {least[0] > 64 ? least[0] : 64, least[1] > 64 ? least[1] : 64};
+            for (int s0 = least[0]; s0 <= most[0]; s0 = s0 < 4 ? s0 + 1 : s0 + s0 / 2) {
+                if (s0 > least[0] && (!pr[0].may_split || s0 > pr[0].chunks)) break;
+                for (int s1 = least[1]; s1 <= most[1]; s1 = s1 < 4 ? s1 + 1 : s1 + s1 / 2) {
+                    if (s1 > least[1] && (n == 1 || !pr[1].may_split || s1 > pr[1].chunks)) break;
                     const int s[2] = {s0, s1};
                     int64_t items[2] = {0, 0};
                     double each[2] = {0, 0}, t = 0;
@@ -1148,15 +1151,21 @@ CePlan plan_ce(const linear_ce_desc& d, bool backward) {
     const int64_t nk = c.dp / 64;
     const int64_t v = d.vocab < piece ? d.vocab : piece;
     // dz is read in 64-column chunks, so its tiles write whole ones (zeros past the vocabulary).
-    const Product z{d.tokens, v, nk * c.pairs, false};
+    const Product z{d.tokens, v, nk * c.pairs, false, 1};
     c.z = plan_gemm(&z, 1, backward ? 64 : 32, false);
     if (!backward) {
         take(at, c.part, (size_t)d.tokens * (size_t)(c.pieces * ceil_div(v, c.z.BN)) * sizeof(float2));
         take(at, c.z_target, (size_t)d.tokens * 4);
         take(at, c.row_loss, (size_t)d.tokens * 4);
     } else {
-        const Product out[2] = {{d.tokens, d.hidden, ceil_div(v, 64) * c.out_pairs, true},
-                                {v, d.hidden, ceil_div(d.tokens, 64) * c.out_pairs, true}};
+        const int64_t kh = ceil_div(v, 64) * c.out_pairs, kw = ceil_div(d.tokens, 64) * c.out_pairs;
+        // Sums of 16-bit operands stay in tensor memory for this many chunks at most,
+        // then go on in fp32.  Terms of one sign lose 6e-9 of their sum with each of
+        // them (fp16 8192 x 512 x 65536 in one piece: dh -3.9e-4; unsplit 1024 x 4608 x
+        // 100000 -6.3e-4): at most a fifth of the result's own rounding.
+        const int64_t most_k = c.bf16 ? 2048 : 256;
+        const Product out[2] = {{d.tokens, d.hidden, kh, true, f32 ? 1 : (int)ceil_div(kh, most_k)},
+                                {v, d.hidden, kw, true, f32 ? 1 : (int)ceil_div(kw, most_k)}};
         c.out = plan_gemm(out, 2, 64, true);
         take(at, c.coef, (size_t)d.tokens * 4);
         take(at, c.common, 4);

@@ -124,7 +124,11 @@ conv2d_status dropout_bwd(dropout_desc_t d, const void *dy, void *dx, uint64_t s
  *   dz_nv = g_n (exp(z_nv - lse_n) - [v = y_n]),  dh = dz w,  dw = dz^T h,
  * with g_n = 0 for ignored targets.  fp16 and bf16 run on the tensor cores
  * with fp32 accumulation, and dz is rounded to that type for the two products
- * of the backward pass.  fp32 runs on the tensor cores too: each value is the
+ * of the backward pass (to two parts of that type, twice its bits, up to 256
+ * tokens).  The tensor cores truncate their fp32 sums: over the 16384 (fp16) or
+ * 131072 (bf16) terms that are summed there at most before the sums go on
+ * rounded to nearest, terms of one sign lose up to a fifth of the result type's
+ * unit roundoff.  fp32 runs on the tensor cores too: each value is the
  * sum of three bf16 parts (8 bits of the significand each), and the six
  * leading products of the parts, exact in fp32, are accumulated; an infinity
  * in h or w makes its logits NaN there (a part of the other factor is zero). */

@@ -25,8 +25,10 @@ def _positive(seed, n, d, v, dtype, scale):
     return h, w, torch.zeros(n, dtype=torch.int64, device="cuda")
 
 
-def _signed_errors(h, w, target, op):
-    """Mean signed relative errors of dh and of dw (without the targets' row), and the mean logit."""
+def _signed_errors(h, w, target, op, rounded=False):
+    """Mean signed relative errors of dh and of dw (without the targets' row), and the
+    mean logit.  `rounded`: against the sums of dz rounded to the operands' type,
+    which has a direction where all of its values lie within one unit in the last place."""
     import torch
     n, v = h.shape[0], w.shape[0]
     _, lse = op(h, w, target)
@@ -38,6 +40,8 @@ def _signed_errors(h, w, target, op):
         mean += float(z.sum()) / (n * v)
         p = torch.exp(z - torch.logsumexp(z, 1, keepdim=True))
         p[:, 0] -= 1.0
+        if rounded:
+            p = (p * 2.0 ** 14).to(h.dtype).double() * 2.0 ** -14
         want_h.append(p @ wd)
         want_w += p.T @ hd[i:i + 4096]
     want_h = torch.cat(want_h)
@@ -56,3 +60,16 @@ def test_dz_takes_its_logits_as_the_losses_do(dtype, n, d, v):
     # steps (twice where dz has two parts); the mean of the outputs' own roundings.
     for bias, k, count in ((bias_h, v, n * d), (bias_w, n, v * d)):
         assert abs(bias) < E * (64 * z + 64 + 2 * k / 16) + 4 * U[dtype] / math.sqrt(count), (bias, z)
+
+
+@pytest.mark.parametrize("dtype,n,d,v,piece", [("f16", 1024, 4608, 100000, None), ("f16", 65536, 64, 19456, 19456),
+                                               ("f16", 8192, 512, 65536, 65536), ("bf16", 1000, 4608, 200000, 200000)])
+def test_long_sums_lose_less_than_their_rounding(dtype, n, d, v, piece):
+    """dh sums over the vocabulary, dw over the tokens: no more than a fifth of the
+    result's unit roundoff goes missing, however long they are."""
+    from dense_convolution_gb300 import head
+    h, w, target = _positive(2, n, d, v, dtype, 0.2)
+    op = head.LinearCrossEntropy(n, d, v, dtype, reduction="sum", piece=piece)
+    bias_h, bias_w, z = _signed_errors(h, w, target, op, rounded=True)
+    for bias, count in ((bias_h, n * d), (bias_w, v * d)):
+        assert abs(bias) < U[dtype] / 5 + E * (64 * z + 64) + 4 * U[dtype] / math.sqrt(count), (bias, z)

@@ -59,6 +59,14 @@ constexpr long long kStripSmemMax = 200 * 1024;   // fp32 im2win transform: stag
 
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
+// Lets launches of `kernel` take up to `most` bytes of dynamic shared memory.  That
+// limit is one figure of the function for the whole process, so every call sets the
+// most that any shape asks of the kernel: one that followed the call's own size would
+// be lowered by another thread's smaller shape between this call and its launch.
+template <typename... KArgs> inline cudaError_t allow_smem(void (*kernel)(KArgs...), int most) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+}
+
 // Launch that may overlap the previous kernel of the stream (programmatic
 // dependent launch): the kernel can start while its predecessor finishes, and
 // must execute griddepcontrol.wait (pdl_wait) before touching that

@@ -1049,7 +1049,7 @@ template <typename T> cudaError_t fwd_typed(const layernorm_desc& d, LnParams p,
                     : layernorm_fwd_bulk_kernel<T, 1, FULL>)
         auto kern = bulk.full ? LN_FWD_BULK(true) : LN_FWD_BULK(false);
 #undef LN_FWD_BULK
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bulk.smem);
+        const cudaError_t e = allow_smem(kern, kRingBytes);
         if (e != cudaSuccess) return e;
         return launch_after(kern, dim3((unsigned)device_sm_count()), dim3(bulk.rpb * bulk.tpr), bulk.smem, st, p,
                             bulk.rows);
@@ -1140,7 +1140,7 @@ template <typename T> cudaError_t bwd_typed(const layernorm_desc& d, LnParams p,
         auto kern = bulk.full ? (bulk.twice ? layernorm_bwd_bulk_kernel<T, 2, true> : layernorm_bwd_bulk_kernel<T, 1, true>)
                               : (bulk.twice ? layernorm_bwd_bulk_kernel<T, 2, false>
                                             : layernorm_bwd_bulk_kernel<T, 1, false>);
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        const cudaError_t e = allow_smem(kern, kRingBytes);        // (the sums take 64 KB at most)
         if (e != cudaSuccess) return e;
         return launch_after(kern, dim3((unsigned)sms), dim3(bulk.rpb * bulk.tpr), smem, st, p, bulk.rows);
     }

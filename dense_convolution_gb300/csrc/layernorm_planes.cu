@@ -807,7 +807,7 @@ planes16_bwd_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_const
     }
 }
 
-constexpr int kSmemMost = 200 * 1024;
+constexpr int kSmemMost = 200 * 1024;     // (no form asks for more: the fast backward with 1024 channels takes 197 KB)
 
 int chunk_of(int C, int tiles_held, int other_bytes) {
     const int64_t most = (kSmemMost - other_bytes) / (tiles_held * kPitch * 4);
@@ -820,7 +820,7 @@ cudaError_t fwd_planes_at(PlaneParams p, cudaStream_t st) {
     p.tiles = (p.rows + kWords * PP - 1) / (kWords * PP);
     p.chunk = chunk_of(p.C, 1, 0);
     const int smem = p.chunk * kPitch * 4;
-    cudaError_t e = cudaFuncSetAttribute(planes_fwd_kernel<T, PP, THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = allow_smem(planes_fwd_kernel<T, PP, THREADS>, kSmemMost);
     if (e != cudaSuccess) return e;
     int64_t grid = (int64_t)device_sm_count() * (2048 / THREADS);
     if (grid > p.tiles) grid = p.tiles;
@@ -836,7 +836,7 @@ cudaError_t bwd_planes_at(PlaneParams p, int* parts, cudaStream_t st) {
     p.tiles = (p.rows + kWords * PP - 1) / (kWords * PP);
     p.chunk = chunk_of(p.C, 2, 3 * p.C * 4);
     const int smem = 2 * p.chunk * kPitch * 4 + 3 * p.C * 4;
-    cudaError_t e = cudaFuncSetAttribute(planes_bwd_kernel<T, PP, THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = allow_smem(planes_bwd_kernel<T, PP, THREADS>, kSmemMost);
     if (e != cudaSuccess) return e;
     int64_t grid = (int64_t)device_sm_count() * (1024 / THREADS);
     if (grid > p.tiles) grid = p.tiles;
@@ -894,8 +894,7 @@ template <typename T, int PG, int G, int NB> cudaError_t fwd_fast(PlaneParams p,
     CUtensorMap xm, ym;
     if (!x_map<PG>(&xm, p, b, p.x, is_bf16<T>) || !y_map<PG>(&ym, p, p.y, is_bf16<T>)) return cudaErrorInvalidValue;
     const int smem = 1024 + 2 * b.x_bytes + b.y_bytes + 2 * p.C * 4;
-    const cudaError_t e =
-        cudaFuncSetAttribute(planes16_fwd_kernel<T, PG, G, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = allow_smem(planes16_fwd_kernel<T, PG, G, NB>, kSmemMost);
     if (e != cudaSuccess) return e;
     int64_t grid = 2 * device_sm_count();
     if (grid > p.tiles) grid = p.tiles;
@@ -910,8 +909,7 @@ template <typename T, int PG, int G, int NB> cudaError_t bwd_fast(PlaneParams p,
         !x_map<PG>(&om, p, b, p.dx ? p.dx : p.x, is_bf16<T>))
         return cudaErrorInvalidValue;
     const int smem = 1024 + 3 * (b.x_bytes + b.y_bytes) + p.C * 4;
-    const cudaError_t e =
-        cudaFuncSetAttribute(planes16_bwd_kernel<T, PG, G, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = allow_smem(planes16_bwd_kernel<T, PG, G, NB>, kSmemMost);
     if (e != cudaSuccess) return e;
     int64_t grid = device_sm_count() * (NB == 1 ? 2 : 1);
     if (grid > p.tiles) grid = p.tiles;

@@ -429,8 +429,7 @@ bool few_fits(const linear_ce_desc& d, int64_t tokens) {
 
 template <typename T, int NT, bool BACKWARD> cudaError_t few_launch(const FewParams& p, cudaStream_t st) {
     const size_t smem = few_smem<T>(NT, p.hidden);
-    const cudaError_t e = cudaFuncSetAttribute(ce_few_kernel<T, NT, BACKWARD>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = allow_smem(ce_few_kernel<T, NT, BACKWARD>, kSmemMost);
     if (e != cudaSuccess) return e;
     return launch_after(ce_few_kernel<T, NT, BACKWARD>, dim3((unsigned)linear_ce_few_blocks()), dim3(kThreads), smem, st,
                         p);

@@ -252,11 +252,13 @@ typedef CUresult (*PFN_encodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_
                                     CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 void* driver_entry(const char* name);   // conv_tc.cu
 
+constexpr int kFp32SmemMost = 220 * 1024;
+
 template <int KW, int S, bool IM2WIN, bool ROWS = false>
 static cudaError_t launch_fp32_inst(const Fp32Params& prm, const CUtensorMap& map, int threads, size_t smem,
                                     long long blocks, cudaStream_t st) {
     auto kern = conv_fp32_kernel<KW, S, IM2WIN, ROWS>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem(kern, kFp32SmemMost);
     if (e != cudaSuccess) return e;
     return launch_after(kern, dim3((unsigned)blocks), dim3(threads), smem, st, prm, map);
 }
@@ -337,7 +339,7 @@ conv2d_status launch_conv_fp32(const conv2d_desc& d, const float* src, const flo
     prm.xs_floats = ((chunk * per_ci_x + slack) + 31) & ~31;
     prm.ws_floats = (chunk * per_ci_w + 31) & ~31;
     const size_t smem = (size_t)2 * (prm.xs_floats + prm.ws_floats) * 4 + 128;
-    if (smem > 220 * 1024) return CONV2D_ERR_UNSUPPORTED;
+    if (smem > kFp32SmemMost) return CONV2D_ERR_UNSUPPORTED;
 
     CUtensorMap map;
     memset(&map, 0, sizeof(map));

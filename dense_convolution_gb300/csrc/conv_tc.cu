@@ -1216,7 +1216,7 @@ static cudaError_t launch_tc_inst(const CUtensorMap& a, const CUtensorMap& b, co
     if constexpr ((MODE == 0 || MODE == 1) && BN % 64 == 0) {
         if (prm.split) kern = conv_tc_kernel<BN, BF16, MODE, true>;
     }
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = allow_smem(kern, kSmemLimit);
     if (e != cudaSuccess) return e;
     const int threads = 32 * (1 + kIssuers + 4 * prm.n_egroups) + (MODE == 4 ? 32 * kTransposerWarps : 0);
     return launch_after(kern, dim3(grid), dim3(threads), smem, st, a, b, y, prm);

@@ -83,8 +83,7 @@ cudaError_t launch_im2win_strips_f32(const float* x, float* xw, const conv2d_des
     const long long blocks = (long long)d.N * d.Ci * n_rb;
     const long long smem = (long long)((rows - 1) * d.s + d.Kh) * d.W * 4;
     if (blocks > 0x7fffffffLL || smem > kStripSmemMax) return cudaErrorInvalidConfiguration;
-    cudaError_t e = cudaFuncSetAttribute(im2win_strips_f32_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
+    cudaError_t e = allow_smem(im2win_strips_f32_kernel, (int)kStripSmemMax);
     if (e != cudaSuccess) return e;
     const int vec_ok = (d.W % 4 == 0 && (reinterpret_cast<uintptr_t>(x) & 15) == 0) ? 1 : 0;
     return launch_chain(pdl, im2win_strips_f32_kernel, dim3((unsigned)blocks), dim3(256), (size_t)smem, st, x,
@@ -531,6 +530,8 @@ __global__ void __launch_bounds__(256) window_cl16_rows_kernel(const uint16_t* _
     pdl_wait();   // complete only after the filter repack launched before us
 }
 
+constexpr int kWinRowSmemMost = 96 * 1024, kWindowSmemMost = 200 * 1024;
+
 cudaError_t launch_window_cl16(const void* x, void* out, int N, int Ci, int H, int W, int Ci8, int Ck, int R,
                                int Wq, int Kh, int s, int p, cudaStream_t st, bool pdl) {
     const uint16_t* xi = static_cast<const uint16_t*>(x);
@@ -539,9 +540,8 @@ cudaError_t launch_window_cl16(const void* x, void* out, int N, int Ci, int H, i
     const int n_xr = (Wq + kWinRowX - 1) / kWinRowX;
     const int n_rb = (R + kWinRowsPerBlock - 1) / kWinRowsPerBlock;
     const long long blocks = (long long)N * n_rb * n_xr;
-    if (Ci8 <= 16 && row_smem <= 96 * 1024 && blocks <= 0x7fffffffLL) {
-        cudaError_t e = cudaFuncSetAttribute(window_cl16_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)row_smem);
+    if (Ci8 <= 16 && row_smem <= kWinRowSmemMost && blocks <= 0x7fffffffLL) {
+        cudaError_t e = allow_smem(window_cl16_rows_kernel, kWinRowSmemMost);
         if (e != cudaSuccess) return e;
         const int vec_ok = (W % 8 == 0 && (reinterpret_cast<uintptr_t>(x) & 15) == 0) ? 1 : 0;
         return launch_chain(pdl, window_cl16_rows_kernel, dim3((unsigned)blocks), dim3(256), (size_t)row_smem, st, xi, o,
@@ -562,12 +562,11 @@ cudaError_t launch_window_cl16(const void* x, void* out, int N, int Ci, int H, i
         if (XT < 1) XT = 1;
         const int XTs = (XT + 7 + 7) / 8 * 8;
         const long long smem = (long long)Kh * Ci8 * XTs * 2 + (long long)XT * Kh * Ci8 * 2 + 16;
-        if (smem > 200 * 1024) return cudaErrorInvalidConfiguration;
+        if (smem > kWindowSmemMost) return cudaErrorInvalidConfiguration;
         const int n_xt = (Wq + XT - 1) / XT;
         const long long blocks = (long long)n_xt * N * R;
         if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-        cudaError_t e = cudaFuncSetAttribute(window_cl16_tiled_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)smem);
+        cudaError_t e = allow_smem(window_cl16_tiled_kernel, kWindowSmemMost);
         if (e != cudaSuccess) return e;
         const bool a16 = (reinterpret_cast<uintptr_t>(x) & 15) == 0;
         const int vec_ok = (W % 8 == 0 && a16) ? 2 : ((W % 4 == 0 && a16) ? 1 : 0);

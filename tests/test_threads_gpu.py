@@ -86,3 +86,29 @@ def _norm(rows, cols, pixels=None, backward=False):
          "rows", "rows_backward"])
 def test_head_shapes_side_by_side(small, large):
     _run([small, large, small, large])
+
+
+def _conv(shape, dtype, algo, tuning=None):
+    def make():
+        import torch
+        from dense_convolution_gb300.conv import Conv2d
+        N, Ci, H, W, Co, K = shape
+        op = Conv2d(N, Ci, H, W, Co, K, K, 1, 0, dtype, algo, tuning=tuning)
+        t = {"f32": torch.float32, "f16": torch.float16}[dtype]
+        x = torch.randn(N, Ci, H, W, device="cuda").to(t)
+        w = torch.randn(Co, Ci, K, K, device="cuda").to(t)
+        ws, y = op.alloc_workspace(), op.alloc_output()
+        want = op(x, w)
+        return (lambda: op(x, w, y=y, workspace=ws)), lambda got: None if got.equal(want) else pytest.fail("another result")
+    return make
+
+
+@pytest.mark.parametrize("small,large", [
+    (_conv((1, 64, 12, 12, 64, 3), "f16", "implicit_tc", {"stages": 2}), _conv((1, 64, 12, 12, 64, 3), "f16", "implicit_tc")),
+    (_conv((1, 4, 12, 12, 16, 3), "f32", "implicit_fp32_cc"), _conv((1, 16, 12, 100, 64, 3), "f32", "implicit_fp32_cc")),
+    (_conv((1, 4, 12, 12, 16, 3), "f32", "im2win_fp32_cc"), _conv((1, 4, 12, 900, 16, 3), "f32", "im2win_fp32_cc")),
+    (_conv((1, 3, 12, 40, 64, 3), "f16", "im2win_tc"), _conv((1, 16, 12, 40, 64, 7), "f16", "im2win_tc")),
+    (_conv((1, 24, 12, 12, 64, 3), "f16", "im2win_tc"), _conv((1, 256, 12, 40, 64, 3), "f16", "im2win_tc"))],
+    ids=["tensor_core", "fp32", "strips", "window_rows", "window_tiles"])
+def test_convolutions_side_by_side(small, large):
+    _run([small, large, small, large])

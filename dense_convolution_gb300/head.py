@@ -3,10 +3,12 @@
 Layer norm, dropout and linear cross entropy take a convolution's features to
 a loss over a vocabulary and its gradients.  As in ``conv``, PyTorch provides
 device memory and the current stream, every arithmetic step runs in the
-library's kernels, and shapes are checked so that a wrong tensor fails with a
-Python error instead of a bad pointer.  Each class is one problem shape:
-calling it runs the forward pass, ``backward`` the gradients.  With stream= a
-call and the tensors that it allocates belong to that stream.
+library's kernels, and shapes and devices are checked so that a wrong tensor
+fails with a Python error instead of a bad pointer.  Each class is one problem
+shape: calling it runs the forward pass, ``backward`` the gradients.  All tensors
+of a call, its workspace among them, are on one GPU, on which it runs whichever
+is current.  With stream= (of that GPU) a call and the tensors that it allocates
+belong to that stream.
 """
 from __future__ import annotations
 
@@ -17,10 +19,27 @@ from .conv import _NAME, _TORCH_DTYPE
 
 
 _raw_stream = torch._C._cuda_getCurrentRawStream      # the current stream's handle by device index
+_current_device = torch._C._cuda_getDevice
 
 
 def _ptr(t):
     return t.data_ptr() if t is not None else 0
+
+
+def _place(dev, stream):
+    """The context in which a call on GPU `dev` belongs: its stream, or that GPU."""
+    if dev < 0:
+        raise ValueError("tensors must be on a GPU")
+    if stream is None:
+        return torch.cuda.device(dev)
+    if stream.device.index != dev:
+        raise ValueError(f"the stream is on GPU {stream.device.index}, the tensors are on GPU {dev}")
+    return torch.cuda.stream(stream)
+
+
+def _check_workspace(t, dev):
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous buffer on GPU {dev}")
 
 
 class _Rows:
@@ -29,8 +48,8 @@ class _Rows:
     def __init__(self, rows, cols, stride, dtype):
         self.shape, self.strides, self.name, self.dtype = (rows, cols), (stride, 1), dtype, _TORCH_DTYPE[dtype]
 
-    def check(self, name, t):
-        if t.dtype is self.dtype and t.shape == self.shape and t.is_cuda:
+    def check(self, name, t, dev):
+        if t.dtype is self.dtype and t.shape == self.shape and t.get_device() == dev:
             s = t.stride()
             if s == self.strides:
                 return
@@ -38,7 +57,7 @@ class _Rows:
             if ((self.shape[0] <= 1 or s[0] == self.strides[0]) and (self.shape[1] <= 1 or s[1] == 1)) or t.numel() == 0:
                 return
         raise ValueError(f"{name} must be a CUDA {self.name} tensor of shape {self.shape} with rows "
-                         f"{self.strides[0]} elements apart")
+                         f"{self.strides[0]} elements apart, on the device of the others")
 
     def new(self, device):
         if self.strides[0] == self.shape[1]:
@@ -53,10 +72,11 @@ class _Planes:
         self.lead, self.count, self.name, self.dtype = (rows // pixels, cols), rows * cols, dtype, _TORCH_DTYPE[dtype]
         self.pixels = pixels
 
-    def check(self, name, t):
+    def check(self, name, t, dev):
         if t.dtype is not self.dtype or t.dim() < 3 or t.shape[:2] != self.lead or t.numel() != self.count \
-                or not t.is_contiguous() or not t.is_cuda:
-            raise ValueError(f"{name} must be contiguous CUDA {self.name} planes of shape {self.lead} and {self.pixels} pixels")
+                or not t.is_contiguous() or t.get_device() != dev:
+            raise ValueError(f"{name} must be contiguous CUDA {self.name} planes of shape {self.lead} and {self.pixels} "
+                             f"pixels, on the device of the others")
 
 
 class _Flat:
@@ -65,9 +85,10 @@ class _Flat:
     def __init__(self, shape, dtype):
         self.shape, self.dtype = shape, dtype
 
-    def check(self, name, t):
-        if t.dtype is not self.dtype or t.shape != self.shape or not t.is_contiguous() or not t.is_cuda:
-            raise ValueError(f"{name} must be a contiguous CUDA tensor of {self.dtype} and shape {self.shape}")
+    def check(self, name, t, dev):
+        if t.dtype is not self.dtype or t.shape != self.shape or not t.is_contiguous() or t.get_device() != dev:
+            raise ValueError(f"{name} must be a contiguous CUDA tensor of {self.dtype} and shape {self.shape}, on the "
+                             f"device of the others")
 
     def new(self, device):
         return torch.empty(self.shape, dtype=self.dtype, device=device)
@@ -113,53 +134,56 @@ class LayerNorm(_Op):
 
     def __call__(self, x, gamma=None, beta=None, y=None, stats=False, stream=None):
         """y, or (y, mean, rstd) with `stats` (what `backward` needs)."""
-        if stream is not None:
-            with torch.cuda.stream(stream):
+        dev = x.get_device()
+        if stream is not None or dev < 0 or dev != _current_device():
+            with _place(dev, stream):
                 return self(x, gamma, beta, y, stats)
-        self._x.check("x", x)
+        self._x.check("x", x, dev)
         g = b = mp = rp = 0
         if gamma is not None:
-            self._param.check("gamma", gamma)
+            self._param.check("gamma", gamma, dev)
             g = gamma.data_ptr()
         if beta is not None:
-            self._param.check("beta", beta)
+            self._param.check("beta", beta, dev)
             b = beta.data_ptr()
-        dev = x.device
         if y is None:
-            y = self._y.new(dev)
+            y = self._y.new(x.device)
         else:
-            self._y.check("y", y)
+            self._y.check("y", y, dev)
         if stats:
-            mean, rstd = self._stat.new(dev), self._stat.new(dev)
+            mean, rstd = self._stat.new(x.device), self._stat.new(x.device)
             mp, rp = mean.data_ptr(), rstd.data_ptr()
-        head_capi.layernorm_fwd(self.desc, x.data_ptr(), g, b, y.data_ptr(), mp, rp, _raw_stream(dev.index))
+        head_capi.layernorm_fwd(self.desc, x.data_ptr(), g, b, y.data_ptr(), mp, rp, _raw_stream(dev))
         return (y, mean, rstd) if stats else y
 
     def backward(self, dy, x, gamma, mean, rstd, need_dx=True, need_params=True, workspace=None, stream=None):
         """(dx, dgamma, dbeta); None in the place of what is not needed."""
-        if stream is not None:
-            with torch.cuda.stream(stream):
+        dev = x.get_device()
+        if stream is not None or dev < 0 or dev != _current_device():
+            with _place(dev, stream):
                 return self.backward(dy, x, gamma, mean, rstd, need_dx, need_params, workspace)
-        self._x.check("x", x)
-        self._y.check("dy", dy)
-        self._stat.check("mean", mean)
-        self._stat.check("rstd", rstd)
+        self._x.check("x", x, dev)
+        self._y.check("dy", dy, dev)
+        self._stat.check("mean", mean, dev)
+        self._stat.check("rstd", rstd, dev)
         g = xp = gp = bp = 0
         if gamma is not None:
-            self._param.check("gamma", gamma)
+            self._param.check("gamma", gamma, dev)
             g = gamma.data_ptr()
-        dev = x.device
+        at = x.device
+        if workspace is None:
+            workspace = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=at)
+        else:
+            _check_workspace(workspace, dev)
         dx = dgamma = dbeta = None
         if need_dx:
-            dx = torch.empty_like(x) if self.pixels else self._x.new(dev)
+            dx = torch.empty_like(x) if self.pixels else self._x.new(at)
             xp = dx.data_ptr()
         if need_params:
-            dgamma, dbeta = self._param.new(dev), self._param.new(dev)
+            dgamma, dbeta = self._param.new(at), self._param.new(at)
             gp, bp = dgamma.data_ptr(), dbeta.data_ptr()
-        if workspace is None:
-            workspace = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=dev)
         head_capi.layernorm_bwd(self.desc, dy.data_ptr(), x.data_ptr(), g, mean.data_ptr(), rstd.data_ptr(), xp, gp, bp,
-                                workspace.data_ptr(), workspace.numel(), _raw_stream(dev.index))
+                                workspace.data_ptr(), workspace.numel(), _raw_stream(dev))
         return dx, dgamma, dbeta
 
 
@@ -179,31 +203,33 @@ class Dropout(_Op):
 
     def __call__(self, x, seed, offset=0, residual=None, y=None, stream=None):
         """residual + dropped x (y may be x or residual)."""
-        if stream is not None:
-            with torch.cuda.stream(stream):
+        dev = x.get_device()
+        if stream is not None or dev < 0 or dev != _current_device():
+            with _place(dev, stream):
                 return self(x, seed, offset, residual, y)
-        self._x.check("x", x)
+        self._x.check("x", x, dev)
         if residual is not None:
-            self._residual.check("residual", residual)
+            self._residual.check("residual", residual, dev)
         if y is None:
             y = self._y.new(x.device)
         else:
-            self._y.check("y", y)
+            self._y.check("y", y, dev)
         head_capi.dropout_fwd(self.desc, x.data_ptr(), _ptr(residual), y.data_ptr(), seed, offset,
-                              _raw_stream(x.device.index))
+                              _raw_stream(dev))
         return y
 
     def backward(self, dy, seed, offset=0, dx=None, stream=None):
         """dx under the mask of the forward call with the same seed and offset."""
-        if stream is not None:
-            with torch.cuda.stream(stream):
+        dev = dy.get_device()
+        if stream is not None or dev < 0 or dev != _current_device():
+            with _place(dev, stream):
                 return self.backward(dy, seed, offset, dx)
-        self._y.check("dy", dy)
+        self._y.check("dy", dy, dev)
         if dx is None:
             dx = self._x.new(dy.device)
         else:
-            self._x.check("dx", dx)
-        head_capi.dropout_bwd(self.desc, dy.data_ptr(), dx.data_ptr(), seed, offset, _raw_stream(dy.device.index))
+            self._x.check("dx", dx, dev)
+        head_capi.dropout_bwd(self.desc, dy.data_ptr(), dx.data_ptr(), seed, offset, _raw_stream(dev))
         return dx
 
 
@@ -231,41 +257,47 @@ class LinearCrossEntropy(_Op):
         self._target, self._lse = _Flat((tokens,), torch.int64), _Flat((tokens,), torch.float32)
         self._loss = _Flat(self.loss_shape, torch.float32)
 
-    def _check(self, h, w, target):
-        self._h.check("h", h)
-        self._w.check("w", w)
-        self._target.check("target", target)
+    def _check(self, h, w, target, dev):
+        self._h.check("h", h, dev)
+        self._w.check("w", w, dev)
+        self._target.check("target", target, dev)
 
     def __call__(self, h, w, target, workspace=None, stream=None):
         """(loss, lse): lse (log-sum-exp per token) is what `backward` needs."""
-        if stream is not None:
-            with torch.cuda.stream(stream):
+        dev = h.get_device()
+        if stream is not None or dev < 0 or dev != _current_device():
+            with _place(dev, stream):
                 return self(h, w, target, workspace)
-        self._check(h, w, target)
-        dev = h.device
-        loss, lse = self._loss.new(dev), self._lse.new(dev)
+        self._check(h, w, target, dev)
+        at = h.device
         if workspace is None:
-            workspace = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=dev)
+            workspace = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=at)
+        else:
+            _check_workspace(workspace, dev)
+        loss, lse = self._loss.new(at), self._lse.new(at)
         head_capi.linear_ce_fwd(self.desc, h.data_ptr(), w.data_ptr(), target.data_ptr(), loss.data_ptr(),
-                                lse.data_ptr(), workspace.data_ptr(), workspace.numel(), _raw_stream(dev.index))
+                                lse.data_ptr(), workspace.data_ptr(), workspace.numel(), _raw_stream(dev))
         return loss, lse
 
     def backward(self, h, w, target, lse, dloss, need_dh=True, need_dw=True, workspace=None, stream=None):
         """(dh, dw); None in the place of what is not needed."""
-        if stream is not None:
-            with torch.cuda.stream(stream):
+        dev = h.get_device()
+        if stream is not None or dev < 0 or dev != _current_device():
+            with _place(dev, stream):
                 return self.backward(h, w, target, lse, dloss, need_dh, need_dw, workspace)
-        self._check(h, w, target)
-        self._lse.check("lse", lse)
-        self._loss.check("dloss", dloss)
-        dev = h.device
-        dh = torch.empty((self.tokens, self.hidden), dtype=h.dtype, device=dev) if need_dh else None
-        dw = torch.empty((self.vocab, self.hidden), dtype=w.dtype, device=dev) if need_dw else None
+        self._check(h, w, target, dev)
+        self._lse.check("lse", lse, dev)
+        self._loss.check("dloss", dloss, dev)
+        at = h.device
         if workspace is None:
-            workspace = torch.empty(self.backward_workspace_bytes, dtype=torch.uint8, device=dev)
+            workspace = torch.empty(self.backward_workspace_bytes, dtype=torch.uint8, device=at)
+        else:
+            _check_workspace(workspace, dev)
+        dh = torch.empty((self.tokens, self.hidden), dtype=h.dtype, device=at) if need_dh else None
+        dw = torch.empty((self.vocab, self.hidden), dtype=w.dtype, device=at) if need_dw else None
         head_capi.linear_ce_bwd(self.desc, h.data_ptr(), w.data_ptr(), target.data_ptr(), lse.data_ptr(),
                                 dloss.data_ptr(), _ptr(dh), _ptr(dw), workspace.data_ptr(), workspace.numel(),
-                                _raw_stream(dev.index))
+                                _raw_stream(dev))
         return dh, dw
 
 

@@ -1,9 +1,10 @@
 """PyTorch-tensor convenience layer over the C ABI.
 
 PyTorch provides device memory (output and workspace tensors) and the current
-stream; every arithmetic step runs in the library's kernels.  Shapes are
-checked here only so that a wrong tensor fails with a Python error instead of
-a bad pointer.
+stream; every arithmetic step runs in the library's kernels.  Shapes and
+devices are checked here only so that a wrong tensor fails with a Python error
+instead of a bad pointer: all tensors of a call are on one GPU, on which it runs
+whichever is current.
 """
 from __future__ import annotations
 
@@ -13,6 +14,19 @@ from . import capi
 
 _TORCH_DTYPE = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
 _NAME = {v: k for k, v in _TORCH_DTYPE.items()}
+
+
+_current_device = torch._C._cuda_getDevice
+
+
+def _device_of(first, others, stream):
+    """The index of the one GPU that all tensors of a call, and its stream, are on."""
+    dev = first.get_device()
+    if dev < 0 or any(t is not None and t.get_device() != dev for t in others):
+        raise ValueError("all tensors of a call must be on one GPU")
+    if stream is not None and stream.device.index != dev:
+        raise ValueError(f"the stream is on GPU {stream.device.index}, the tensors are on GPU {dev}")
+    return dev
 
 
 class Conv2d:
@@ -40,6 +54,10 @@ class Conv2d:
         N, Ci, H, W, Co, Kh, Kw = self.shape[:7]
         if tuple(w.shape) != (Co, Ci, Kh, Kw) or not w.is_contiguous() or w.dtype != _TORCH_DTYPE[self.dtype]:
             raise ValueError(f"w must be a contiguous {self.dtype} tensor of shape {(Co, Ci, Kh, Kw)}")
+        dev = _device_of(w, (), stream)
+        if dev != _current_device():
+            with torch.cuda.device(dev):
+                return self.pack_filter(w, stream)
         wp = torch.empty(capi.conv2d_packed_filter_bytes(self.desc), dtype=torch.uint8, device=w.device)
         st = (stream or torch.cuda.current_stream(w.device)).cuda_stream
         capi.conv2d_pack_filter(self.desc, w.data_ptr(), wp.data_ptr(), st)
@@ -86,6 +104,15 @@ class Conv2d:
             raise ValueError(f"w must be a contiguous {self.dtype} tensor of shape {(Co, Ci, Kh, Kw)}")
         if bias is not None and (tuple(bias.shape) != (Co,) or not bias.is_contiguous() or bias.dtype != x.dtype):
             raise ValueError(f"bias must be a contiguous {self.dtype} tensor of shape {(Co,)}")
+        if y is not None and (not y.is_contiguous()
+                              or y.numel() * y.element_size() < N * Co * self.Ho * self.Wo * _TORCH_DTYPE[self.out_dtype].itemsize):
+            raise ValueError(f"y must be contiguous and hold {self.out_shape} {self.out_dtype} values")
+        if workspace is not None and not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        dev = _device_of(x, (w, bias, y, workspace), stream)
+        if dev != _current_device():
+            with torch.cuda.device(dev):
+                return self(x, w, y, workspace, stream, bias)
         capi.conv2d_desc_set_bias(self.desc, bias.data_ptr() if bias is not None else 0)
         if y is None:
             y = self.alloc_output(x.device)

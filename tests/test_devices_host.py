@@ -33,6 +33,9 @@ class Tensor:
     def numel(self):
         return self.shape.numel()
 
+    def element_size(self):
+        return self.dtype.itemsize
+
     def data_ptr(self):
         return 1 << 20
 
@@ -59,7 +62,8 @@ def lib(monkeypatch):
 
     monkeypatch.setattr(torch.cuda, "device", device)
     monkeypatch.setattr(torch.cuda, "stream", stream)
-    monkeypatch.setattr(head, "_current_device", lambda: seen.current, raising=False)
+    for layer in (head, conv):
+        monkeypatch.setattr(layer, "_current_device", lambda: seen.current, raising=False)
     monkeypatch.setattr(head, "_raw_stream", lambda dev: 100 + dev)
     monkeypatch.setattr(torch, "empty", lambda shape, dtype=None, device=None: Tensor(
         shape if isinstance(shape, (tuple, torch.Size)) else (shape,), dtype, torch.device(device).index))
@@ -132,3 +136,30 @@ def test_a_workspace_that_repeats_itself_is_refused(lib):
     h, w, target = Tensor((4, 8)), Tensor((16, 8)), Tensor((4,), torch.int64)
     with pytest.raises(ValueError):
         ce(h, w, target, workspace=Tensor((1 << 20,), torch.uint8, contiguous=False))
+
+
+@pytest.mark.parametrize("other", [1, -1])
+def test_convolution_tensors_of_another_device_are_refused(lib, other, monkeypatch):
+    capi = lib.conv.capi
+    monkeypatch.setattr(capi, "conv2d_fwd", lambda *a: lib.calls.append(("fwd", lib.current, a[-1])))
+    monkeypatch.setattr(capi, "conv2d_pack_filter", lambda *a: lib.calls.append(("pack", lib.current, a[-1])))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d: types.SimpleNamespace(cuda_stream=100 + d.index))
+    op = lib.conv.Conv2d(1, 4, 8, 8, 16, 3, 3)
+    shapes = {"x": (1, 4, 8, 8), "w": (16, 4, 3, 3), "bias": (16,), "y": (1, 16, 6, 6), "workspace": (1 << 20,)}
+
+    def call(bad, dev=0):
+        t = {k: Tensor(v, torch.uint8 if k == "workspace" else torch.float32, other if k == bad else dev)
+             for k, v in shapes.items()}
+        return op(t["x"], t["w"], y=t["y"], workspace=t["workspace"], bias=t["bias"])
+
+    call(None)
+    call(None, dev=2)
+    assert lib.calls == [("fwd", 0, 100), ("fwd", 2, 102)]
+    for name in shapes:
+        with pytest.raises(ValueError):
+            call(name)
+    with pytest.raises(ValueError):
+        op.pack_filter(Tensor(shapes["w"], dev=-1))
+    with pytest.raises(ValueError):
+        op(Tensor(shapes["x"]), Tensor(shapes["w"]), y=Tensor((1, 16, 6, 5)))
+    assert len(lib.calls) == 2

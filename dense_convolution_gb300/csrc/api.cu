@@ -571,23 +571,14 @@ CONV2D_API conv2d_status conv2d_launches_per_call(conv2d_desc_t d, int* launches
 }
 
 CONV2D_API conv2d_status conv2d_device_status(void* stream, uint32_t* code_out) {
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    uint32_t a = 0, b = 0, c = 0, h = 0, l = 0, n = 0;
-    if (status_read_clear_tc(st, &a) != cudaSuccess || status_read_clear_fp32(st, &b) != cudaSuccess ||
-        status_read_clear_wg(st, &c) != cudaSuccess || status_read_clear_ce(st, &h) != cudaSuccess ||
-        status_read_clear_ln(st, &l) != cudaSuccess || status_read_clear_lp(st, &n) != cudaSuccess)
-        return CONV2D_ERR_CUDA;
-    if (code_out) *code_out = a | b | c | h | l | n;
-    return (a | b | c | h | l | n) ? CONV2D_ERR_DEVICE_TIMEOUT : CONV2D_OK;
+    uint32_t code = 0;
+    if (status_read_clear(static_cast<cudaStream_t>(stream), &code) != cudaSuccess) return CONV2D_ERR_CUDA;
+    if (code_out) *code_out = code;
+    return code ? CONV2D_ERR_DEVICE_TIMEOUT : CONV2D_OK;
 }
 
 CONV2D_API conv2d_status conv2d_set_wait_limit(uint64_t ns, void* stream) {
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (wait_limit_set_tc(st, ns) != cudaSuccess || wait_limit_set_fp32(st, ns) != cudaSuccess ||
-        wait_limit_set_wg(st, ns) != cudaSuccess || wait_limit_set_ce(st, ns) != cudaSuccess ||
-        wait_limit_set_ln(st, ns) != cudaSuccess || wait_limit_set_lp(st, ns) != cudaSuccess)
-        return CONV2D_ERR_CUDA;
-    return CONV2D_OK;
+    return wait_limit_set(static_cast<cudaStream_t>(stream), ns) == cudaSuccess ? CONV2D_OK : CONV2D_ERR_CUDA;
 }
 
 CONV2D_API const char* conv2d_status_string(conv2d_status s) {

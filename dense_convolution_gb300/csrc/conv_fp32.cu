@@ -244,8 +244,8 @@ __global__ void __launch_bounds__(128) conv_fp32_kernel(const Fp32Params prm,
 }
 
 // ---------------------------------------------------------------- host side
-cudaError_t status_read_clear_fp32(cudaStream_t st, uint32_t* out) { return status_read_clear(st, out); }
-cudaError_t wait_limit_set_fp32(cudaStream_t st, uint64_t ns) { return wait_limit_set(st, ns); }
+cudaError_t status_word_fp32(void** p) { return unit_status_word(p); }
+cudaError_t wait_limit_set_fp32(cudaStream_t st, uint64_t ns) { return unit_wait_limit_set(st, ns); }
 
 typedef CUresult (*PFN_encodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                     const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,

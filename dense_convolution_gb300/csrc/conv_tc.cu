@@ -1174,8 +1174,8 @@ void* driver_entry(const char* name) {
     return fn;
 }
 
-cudaError_t status_read_clear_tc(cudaStream_t st, uint32_t* out) { return status_read_clear(st, out); }
-cudaError_t wait_limit_set_tc(cudaStream_t st, uint64_t ns) { return wait_limit_set(st, ns); }
+cudaError_t status_word_tc(void** p) { return unit_status_word(p); }
+cudaError_t wait_limit_set_tc(cudaStream_t st, uint64_t ns) { return unit_wait_limit_set(st, ns); }
 
 // Whether the MODE 4 rings fit for this shape with tile pairs (the larger
 // case): two A stages of the smallest halo (one filter row) and three

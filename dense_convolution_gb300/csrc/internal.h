@@ -126,8 +126,6 @@ size_t winograd_filter_bytes(const conv2d_desc& d);
 cudaError_t launch_winograd_filter(const conv2d_desc& d, const float* w, float* u, cudaStream_t st);
 conv2d_status launch_winograd_main(const conv2d_desc& d, const float* x, const float* u, float* y,
                                    cudaStream_t st);
-cudaError_t status_read_clear_wg(cudaStream_t st, uint32_t* out);
-cudaError_t wait_limit_set_wg(cudaStream_t st, uint64_t ns);
 
 // conv_tc.cu
 conv2d_status launch_conv_tc(const conv2d_desc& d, const void* src, const void* wq, void* y, int amode,
@@ -137,15 +135,22 @@ size_t tc_split_need(const conv2d_desc& d, int n_sm);
 int device_sm_count();
 bool halo_plan_fits(const conv2d_desc& d);
 void* driver_entry(const char* name);
-cudaError_t status_read_clear_tc(cudaStream_t st, uint32_t* out);
-cudaError_t status_read_clear_fp32(cudaStream_t st, uint32_t* out);
-cudaError_t status_read_clear_ce(cudaStream_t st, uint32_t* out);   // linear_ce.cu
-cudaError_t wait_limit_set_ce(cudaStream_t st, uint64_t ns);
-cudaError_t status_read_clear_ln(cudaStream_t st, uint32_t* out);   // layernorm.cu
-cudaError_t wait_limit_set_ln(cudaStream_t st, uint64_t ns);
-cudaError_t status_read_clear_lp(cudaStream_t st, uint32_t* out);   // layernorm_planes.cu
-cudaError_t wait_limit_set_lp(cudaStream_t st, uint64_t ns);
+
+// device_status.cu: all units' status words (read and cleared) and wait limits,
+// synchronising `st`; then each unit's own (ptx.cuh).
+cudaError_t status_read_clear(cudaStream_t st, uint32_t* out);
+cudaError_t wait_limit_set(cudaStream_t st, uint64_t ns);
+cudaError_t status_word_tc(void** p);
+cudaError_t status_word_fp32(void** p);
+cudaError_t status_word_wg(void** p);
+cudaError_t status_word_ce(void** p);
+cudaError_t status_word_ln(void** p);
+cudaError_t status_word_lp(void** p);
 cudaError_t wait_limit_set_tc(cudaStream_t st, uint64_t ns);
 cudaError_t wait_limit_set_fp32(cudaStream_t st, uint64_t ns);
+cudaError_t wait_limit_set_wg(cudaStream_t st, uint64_t ns);
+cudaError_t wait_limit_set_ce(cudaStream_t st, uint64_t ns);
+cudaError_t wait_limit_set_ln(cudaStream_t st, uint64_t ns);
+cudaError_t wait_limit_set_lp(cudaStream_t st, uint64_t ns);
 
 }  // namespace conv2d_gb300

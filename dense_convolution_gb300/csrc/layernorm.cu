@@ -1232,8 +1232,8 @@ size_t layernorm_bwd_workspace(const layernorm_desc& d) {
     return bwd_sums_bytes(d) + parts * 2 * (size_t)d.cols * sizeof(float);
 }
 
-cudaError_t status_read_clear_ln(cudaStream_t st, uint32_t* out) { return status_read_clear(st, out); }
-cudaError_t wait_limit_set_ln(cudaStream_t st, uint64_t ns) { return wait_limit_set(st, ns); }
+cudaError_t status_word_ln(void** p) { return unit_status_word(p); }
+cudaError_t wait_limit_set_ln(cudaStream_t st, uint64_t ns) { return unit_wait_limit_set(st, ns); }
 
 cudaError_t launch_layernorm_params(const float* part, int parts, const layernorm_desc& d, void* dgamma, void* dbeta,
                                     cudaStream_t st) {

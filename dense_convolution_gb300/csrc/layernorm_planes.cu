@@ -955,8 +955,8 @@ bool pair_channels(const layernorm_desc& d, const void* r) {
 
 }  // namespace
 
-cudaError_t status_read_clear_lp(cudaStream_t st, uint32_t* out) { return status_read_clear(st, out); }
-cudaError_t wait_limit_set_lp(cudaStream_t st, uint64_t ns) { return wait_limit_set(st, ns); }
+cudaError_t status_word_lp(void** p) { return unit_status_word(p); }
+cudaError_t wait_limit_set_lp(cudaStream_t st, uint64_t ns) { return unit_wait_limit_set(st, ns); }
 
 cudaError_t launch_layernorm_planes_fwd(const layernorm_desc& d, const void* x, const void* gamma, const void* beta,
                                         void* y, float* mean, float* rstd, cudaStream_t st) {

@@ -1408,7 +1408,7 @@ conv2d_status launch_linear_ce_bwd(const linear_ce_desc& d, const void* h, const
     return CONV2D_OK;
 }
 
-cudaError_t status_read_clear_ce(cudaStream_t st, uint32_t* out) { return status_read_clear(st, out); }
-cudaError_t wait_limit_set_ce(cudaStream_t st, uint64_t ns) { return wait_limit_set(st, ns); }
+cudaError_t status_word_ce(void** p) { return unit_status_word(p); }
+cudaError_t wait_limit_set_ce(cudaStream_t st, uint64_t ns) { return unit_wait_limit_set(st, ns); }
 
 }  // namespace conv2d_gb300

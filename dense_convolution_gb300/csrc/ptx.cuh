@@ -21,34 +21,22 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;   // 2 s per wait, then give up
 static __device__ uint32_t g_device_status = 0;
 
 // Limit of the pipeline waits (mbar_wait), default kWaitLimitNs.  The host can
-// lower it (wait_limit_set) so that a test sees waits give up; the waits that
+// lower it (unit_wait_limit_set) so that a test sees waits give up; the waits that
 // let in-flight copies and MMAs finish before a CTA exits (mbar_drain_wait)
 // always use kWaitLimitNs.
 static __constant__ uint64_t g_wait_limit_ns = kWaitLimitNs;
 
-// Set this translation unit's pipeline-wait limit for kernels launched on
+// Queue this translation unit's pipeline-wait limit for kernels launched on
 // `st` after this call (0, or anything above the default, gives the default:
 // the limit can only be lowered, so every wait stays bounded).
-static inline cudaError_t wait_limit_set(cudaStream_t st, uint64_t ns) {
+static inline cudaError_t unit_wait_limit_set(cudaStream_t st, uint64_t ns) {
     static uint64_t v;   // the copy reads the source when the stream reaches it
     v = (ns == 0 || ns > kWaitLimitNs) ? kWaitLimitNs : ns;
-    cudaError_t e = cudaMemcpyToSymbolAsync(g_wait_limit_ns, &v, sizeof(v), 0, cudaMemcpyHostToDevice, st);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-    return e;
+    return cudaMemcpyToSymbolAsync(g_wait_limit_ns, &v, sizeof(v), 0, cudaMemcpyHostToDevice, st);
 }
 
-// Read and clear this translation unit's status word (synchronises `st`).
-static inline cudaError_t status_read_clear(cudaStream_t st, uint32_t* out) {
-    uint32_t v = 0, z = 0;
-    cudaError_t e = cudaMemcpyFromSymbolAsync(&v, g_device_status, sizeof(v), 0, cudaMemcpyDeviceToHost, st);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-    if (e == cudaSuccess && v != 0) {
-        e = cudaMemcpyToSymbolAsync(g_device_status, &z, sizeof(z), 0, cudaMemcpyHostToDevice, st);
-        if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-    }
-    *out = v;
-    return e;
-}
+// The device address of this translation unit's status word.
+static inline cudaError_t unit_status_word(void** p) { return cudaGetSymbolAddress(p, g_device_status); }
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));

@@ -306,7 +306,7 @@ conv2d_status launch_winograd_main(const conv2d_desc& d, const float* x, const f
     return e == cudaSuccess ? CONV2D_OK : CONV2D_ERR_CUDA;
 }
 
-cudaError_t status_read_clear_wg(cudaStream_t st, uint32_t* out) { return status_read_clear(st, out); }
-cudaError_t wait_limit_set_wg(cudaStream_t st, uint64_t ns) { return wait_limit_set(st, ns); }
+cudaError_t status_word_wg(void** p) { return unit_status_word(p); }
+cudaError_t wait_limit_set_wg(cudaStream_t st, uint64_t ns) { return unit_wait_limit_set(st, ns); }
 
 }  // namespace conv2d_gb300

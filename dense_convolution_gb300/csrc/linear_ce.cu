@@ -119,10 +119,11 @@ __device__ __forceinline__ float exp2_approx(float x) {
     return y;
 }
 
-// Join two (max, sum of exp(z - max)) pairs.
+// Join two (max, sum of exp(z - max)) pairs.  A maximum that is infinite is not taken
+// out: its sum is 0 or infinite as it stands, where inf - inf would make it NaN.
 __device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
     const float top = fmaxf(m, m2);
-    const float base = top == -INFINITY ? 0.f : top;
+    const float base = isinf(top) ? 0.f : top;
     s = s * exp2_approx((m - base) * kLog2e) + s2 * exp2_approx((m2 - base) * kLog2e);
     m = top;
 }
@@ -551,7 +552,7 @@ ce_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ Ge
                     for (int j = 1; j < 32; ++j) top = fmaxf(top, v[j]);
                     const float m_new = fmaxf(m_run, top);
                     // z - max first: a rounded max / ln 2 would scale the whole row.
-                    const float base = m_new == -INFINITY ? 0.f : m_new;
+                    const float base = isinf(m_new) ? 0.f : m_new;
                     float s0 = 0.f, s1 = 0.f;
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) {

@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1) ce_few_kernel(const FewParams p) 
         const int v = v0 + mine_r * V;
         if constexpr (!BACKWARD) {
             if (v < p.vocab) {
-                const float top = fmaxf(m_run, z), base = top == -INFINITY ? 0.f : top;
+                const float top = fmaxf(m_run, z), base = isinf(top) ? 0.f : top;
                 s_run = s_run * exp2_of((m_run - base) * kLog2e) + exp2_of((z - base) * kLog2e);
                 m_run = top;
                 if (v == ty && lane % kSpan == 0) p.z_target[mine_t] = z;
@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1) ce_few_kernel(const FewParams p) 
 #pragma unroll
         for (int o = kOver; o < 32; o <<= 1) {
             const float m2 = __shfl_xor_sync(0xffffffffu, m_run, o), s2 = __shfl_xor_sync(0xffffffffu, s_run, o);
-            const float top = fmaxf(m_run, m2), base = top == -INFINITY ? 0.f : top;
+            const float top = fmaxf(m_run, m2), base = isinf(top) ? 0.f : top;
             s_run = s_run * exp2_of((m_run - base) * kLog2e) + s2 * exp2_of((m2 - base) * kLog2e);
             m_run = top;
         }
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1) ce_few_kernel(const FewParams p) 
             float m = -INFINITY, s = 0.f;
             for (int k = 0; k < kThreads / 32; ++k) {
                 const float2 o = red[k][threadIdx.x];
-                const float top = fmaxf(m, o.x), base = top == -INFINITY ? 0.f : top;
+                const float top = fmaxf(m, o.x), base = isinf(top) ? 0.f : top;
                 s = s * exp2_of((m - base) * kLog2e) + o.y * exp2_of((o.x - base) * kLog2e);
                 m = top;
             }

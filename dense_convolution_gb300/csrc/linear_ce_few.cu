@@ -296,24 +296,21 @@ template <typename T> __device__ __forceinline__ uint4 part_bits(const T* p, int
 }
 
 // Partial dh: a lane owns one vector of columns for all tokens, the warps of a
-// block run down a share of w's rows, every `step`-th of them so that they are
-// offset alike.  Shares are numbered by the grid's y and z together (one block number
-// and a division cost 4 % from eight tokens on, in registers).  The share's dz lies in shared memory; the next
+// block run down a share of w's rows (blockIdx.y), every `step`-th of them so
+// that they are offset alike.  The share's dz lies in shared memory; the next
 // four rows of w are on their way while four are added.  part [share][NT][lds].
 constexpr int kDhThreads = 256, kDhWarps = kDhThreads / 32, kDhWords = 8192;
 template <typename T, int NT>
 __global__ void __launch_bounds__(kDhThreads, NT * kVec<T> <= 8 ? 4 : NT * kVec<T> <= 32 ? 3 : 2)
-ce_few_dh_kernel(const T* w, int64_t ws, const float* dz, int hidden, int vocab, int shares, int step, int per,
-                 float* part, int64_t lds) {
+ce_few_dh_kernel(const T* w, int64_t ws, const float* dz, int hidden, int vocab, int step, int per, float* part,
+                 int64_t lds) {
     constexpr int V = kVec<T>, kDeep = 4, P = kPair<NT>, NP = NT / P;
     using W = typename Word<P>::T;
     __shared__ __align__(16) float dzs[kDhWords];          // [rows of the share][NT]
     __shared__ float red[kDhWarps][32 * V];
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int share = (int)(blockIdx.z * gridDim.y + blockIdx.y);
-    if (share >= shares) return;
-    const int first = share / step * per + share % step, last = min(vocab, (share / step + 1) * per);
+    const int first = blockIdx.y / step * per + blockIdx.y % step, last = min(vocab, (int)(blockIdx.y / step + 1) * per);
     const int rows = last > first ? (last - first + step - 1) / step : 0;
     const int64_t row = (int64_t)step * ws;
     const int shift = phase_of(w + (int64_t)first * ws);
@@ -394,7 +391,7 @@ ce_few_dh_kernel(const T* w, int64_t ws, const float* dz, int hidden, int vocab,
 #pragma unroll
             for (int k = 0; k < kDhWarps; ++k) sum += red[k][(threadIdx.x % V) * 32 + threadIdx.x / V];
             const int64_t e = (int64_t)blockIdx.x * 32 * V + threadIdx.x - shift;
-            if (e >= 0 && e < hidden) part[((int64_t)share * NT + t) * lds + e] = sum;
+            if (e >= 0 && e < hidden) part[((int64_t)blockIdx.y * NT + t) * lds + e] = sum;
         }
     }
 }
@@ -487,12 +484,19 @@ template <typename T> cudaError_t dh_typed(const linear_ce_desc& d, const void* 
     if constexpr (sizeof(T) == 4) {
         if (nt == 16) kern = ce_few_dh_kernel<T, 16>;
     }
-    const int down = (pl.shares + 65534) / 65535;
-    const cudaError_t e =
-        launch_after(kern, dim3((unsigned)pl.columns, (unsigned)((pl.shares + down - 1) / down), (unsigned)down),
-                     dim3(kDhThreads), 0, st, static_cast<const T*>(w), d.ws, dz, (int)d.hidden, (int)d.vocab, pl.shares,
-                     pl.step, pl.per, sums, d.hidden);
-    if (e != cudaSuccess) return e;
+    // As many whole ranges of rows a launch as the grid's y numbers shares of (one
+    // launch up to 33 million rows; share numbers past it would cost the kernel
+    // registers, 1 to 4 %).
+    const int most = 65535 / pl.step * pl.step;
+    for (int s = 0; s < pl.shares; s += most) {
+        const int64_t row = (int64_t)(s / pl.step) * pl.per;
+        const int n = pl.shares - s < most ? pl.shares - s : most;
+        const cudaError_t e = launch_after(kern, dim3((unsigned)pl.columns, (unsigned)n), dim3(kDhThreads), 0, st,
+                                           static_cast<const T*>(w) + row * d.ws, d.ws, dz + row * nt, (int)d.hidden,
+                                           (int)(d.vocab - row), pl.step, pl.per, sums + (int64_t)s * nt * d.hidden,
+                                           d.hidden);
+        if (e != cudaSuccess) return e;
+    }
     return launch_after(ce_few_join_kernel<T>, dim3((unsigned)((d.hidden + 31) / 32), (unsigned)d.tokens), dim3(256), 0, st,
                         sums, pl.shares, nt, (int)d.hidden, d.hidden, static_cast<T*>(dh));
 }

@@ -6,8 +6,9 @@
 // A warp takes four rows of w at a time, a vector slot a lane; h lies in shared
 // memory, one column block per element of a vector, so that the lanes of a warp
 // read consecutive words whatever the rows' offset from the 16-byte boundary
-// (the four rows are a vector length apart and therefore offset alike; a single
-// token, for an even share of short calls, and sixteen take two rows).  The 4 x tokens dot products are added over the warp together.
+// (the four rows are a vector length apart and therefore offset alike; sixteen
+// tokens take two rows, a single one two or four, see one_token_rows).  The 4 x
+// tokens dot products are added over the warp together.
 //   forward    each lane keeps the running (max, sum) of the products it ends
 //              up with; blocks write one pair per token
 //   backward   dz = g (exp(z - lse) - [v = y]) goes back to all lanes, which
@@ -89,9 +90,9 @@ template <typename T> __device__ __forceinline__ void word_offsets(int shift, in
     }
 }
 
-template <typename T, int NT, bool BACKWARD>
+template <typename T, int NT, int kRows, bool BACKWARD>
 __global__ void __launch_bounds__(kThreads, 1) ce_few_kernel(const FewParams p) {
-    constexpr int V = kVec<T>, kRows = NT == 1 ? 2 : NT <= 8 ? 4 : 32 / NT;
+    constexpr int V = kVec<T>;
     constexpr int N = kRows * NT, kSpan = 32 / N, kOver = kSpan * NT;   // lanes per product and per row
     constexpr int P = kPair<NT>, NP = NT / P;
     using W = typename Word<P>::T;
@@ -428,22 +429,42 @@ bool few_fits(const linear_ce_desc& d, int64_t tokens) {
            (size_t)kSmemMost;
 }
 
-template <typename T, int NT, bool BACKWARD> cudaError_t few_launch(const FewParams& p, cudaStream_t st) {
+template <typename T, int NT, int ROWS, bool BACKWARD> cudaError_t few_launch(const FewParams& p, cudaStream_t st) {
     const size_t smem = few_smem<T>(NT, p.hidden);
-    const cudaError_t e = allow_smem(ce_few_kernel<T, NT, BACKWARD>, kSmemMost);
+    const cudaError_t e = allow_smem(ce_few_kernel<T, NT, ROWS, BACKWARD>, kSmemMost);
     if (e != cudaSuccess) return e;
-    return launch_after(ce_few_kernel<T, NT, BACKWARD>, dim3((unsigned)linear_ce_few_blocks()), dim3(kThreads), smem, st,
-                        p);
+    return launch_after(ce_few_kernel<T, NT, ROWS, BACKWARD>, dim3((unsigned)linear_ce_few_blocks()), dim3(kThreads), smem,
+                        st, p);
+}
+
+// Rows of w that a warp takes at a time for a single token: two or four, by the
+// turns of the warp that has most of them.  A turn costs its rows' bytes and, for the
+// trip to memory and the sum over the warp, as much as another 768.  Two rows / four,
+// bf16, forward (dw goes the same way):
+//   256 features    32000 rows 12.4 / 10.4 us, 131072 rows 30.9 / 21.8, 2000 rows 4.7 / 5.0
+//   1024 features   5000 rows 10.4 / 9.7, 10007 rows 12.4 / 16.0, 50257 rows 24.0 / 27.9
+//   2487 features   64640 rows 63.7 / 58.7;   4096   10007 rows 27.3 / 42.5
+// The rule is at most 2.5 % behind the better one at the 36 shapes measured.
+int one_token_rows(int64_t vocab, int64_t row_bytes, int vec) {
+    const int64_t warps = (int64_t)linear_ce_few_blocks() * (kThreads / 32);
+    const auto cost = [&](int64_t rows) {
+        const int64_t groups = (vocab + rows * vec - 1) / (rows * vec) * vec;
+        return (groups + warps - 1) / warps * (rows * row_bytes + 768);
+    };
+    return cost(2) <= cost(4) ? 2 : 4;
 }
 template <typename T, bool BACKWARD> cudaError_t few_tokens(const FewParams& p, cudaStream_t st) {
     switch (nt_of(p.tokens)) {
-        case 1: return few_launch<T, 1, BACKWARD>(p, st);
-        case 2: return few_launch<T, 2, BACKWARD>(p, st);
-        case 4: return few_launch<T, 4, BACKWARD>(p, st);
-        case 8: return few_launch<T, 8, BACKWARD>(p, st);
+        case 1:
+            return one_token_rows(p.vocab, p.hidden * (int64_t)sizeof(T), kVec<T>) == 2
+                       ? few_launch<T, 1, 2, BACKWARD>(p, st)
+                       : few_launch<T, 1, 4, BACKWARD>(p, st);
+        case 2: return few_launch<T, 2, 4, BACKWARD>(p, st);
+        case 4: return few_launch<T, 4, 4, BACKWARD>(p, st);
+        case 8: return few_launch<T, 8, 4, BACKWARD>(p, st);
     }
     if constexpr (sizeof(T) == 4) {
-        return few_launch<T, 16, BACKWARD>(p, st);
+        return few_launch<T, 16, 2, BACKWARD>(p, st);
     } else {
         return cudaErrorInvalidValue;
     }

@@ -39,3 +39,14 @@ def test_few_tokens_of_a_very_large_vocabulary(dtype, n, d, v):
     _close(dh, dh_want, U[dtype] * dh_want.abs() + 1e-4 * size, "dh")
     dw_want, size = p.T @ h.double(), p.T.abs() @ h.double().abs()
     _close(torch.cat([dw[:k], dw[-k:]]), dw_want, U[dtype] * dw_want.abs() + 1e-4 * size, "dw")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("d,v", [(256, 64640), (40, 2000), (1024, 5003), (1024, 20000), (509, 10007), (2487, 9731), (8, 200001)])
+def test_one_token(dtype, d, v):
+    """Either number of rows of w a warp takes, at lengths on both sides of the rule."""
+    import torch
+    from dense_convolution_gb300 import head
+    h, w, target = _ce_inputs(d + v, 1, d, v, dtype, ignored=0.0)
+    op = head.LinearCrossEntropy(1, d, v, dtype, reduction="none")
+    _check_ce(h, w, target, dtype, "none", op, torch.full((1,), 0.7, device="cuda"))

@@ -201,6 +201,15 @@ CONV2D_API conv2d_status linear_ce_desc_set_piece(linear_ce_desc_t d, int64_t vo
     return CONV2D_OK;
 }
 
+CONV2D_API conv2d_status linear_ce_desc_set_dz_parts(linear_ce_desc_t d, int parts) {
+    if (!d) return CONV2D_ERR_NULL_PTR;
+    if (parts < 0 || parts > 2) return CONV2D_ERR_BAD_PARAM;
+    if (parts && d->dtype == CONV2D_F32) return CONV2D_ERR_UNSUPPORTED;
+    d->dz_parts = parts;
+    linear_ce_plan(*d);
+    return CONV2D_OK;
+}
+
 CONV2D_API conv2d_status linear_ce_desc_destroy(linear_ce_desc_t d) {
     delete d;
     return CONV2D_OK;

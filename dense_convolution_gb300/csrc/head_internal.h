@@ -50,6 +50,7 @@ struct linear_ce_desc {
     int64_t ignore_index;
     int64_t hs, ws;      // row strides of h and w
     int64_t piece;       // vocabulary rows per backward piece; 0 = automatic
+    int dz_parts;        // 16-bit parts of dz: 1, 2; 0 = automatic
     conv2d_gb300::CePlan fwd, bwd;
 };
 

@@ -1128,7 +1128,7 @@ CePlan plan_ce(const linear_ce_desc& d, bool backward) {
     // 2.1e-4): it then keeps what the rounding leaves as a second part.  Backward
     // with one part and with two, bf16: 64 x 4096 x 65536 329 and 369 us, 256 x 1024
     // x 32000 94 and 110 us, 256 x 4096 x 65536 460 and 561 us.
-    c.dz_parts = f32 ? 3 : d.tokens <= 2 * kBM ? 2 : 1;
+    c.dz_parts = f32 ? 3 : d.dz_parts ? d.dz_parts : d.tokens <= 2 * kBM ? 2 : 1;
     c.out_pairs = f32 ? 6 : c.dz_parts;
     c.pack_w = f32 || d.ws % 8 != 0;
     // The backward pass always copies h: ignored rows must be zero in dw's product.

@@ -239,11 +239,12 @@ class LinearCrossEntropy(_Op):
     h (tokens, hidden), w (vocab, hidden), target (tokens,) int64
     reduction  "none", "sum" or "mean" (over targets other than ignore_index)
     piece      vocabulary rows per step of the backward pass (None: automatic)
+    dz_parts   16-bit parts of the logits' gradient, 1 or 2 (None: automatic; fp32 has three)
     """
     _destroy = staticmethod(head_capi.linear_ce_desc_destroy)
 
     def __init__(self, tokens, hidden, vocab, dtype="bf16", reduction="mean", ignore_index=-100, h_stride=None,
-                 w_stride=None, piece=None):
+                 w_stride=None, piece=None, dz_parts=None):
         self.tokens, self.hidden, self.vocab, self.dtype, self.reduction = tokens, hidden, vocab, dtype, reduction
         self.h_stride, self.w_stride = h_stride or hidden, w_stride or hidden
         self.desc = head_capi.linear_ce_desc_create(tokens, hidden, vocab, dtype, reduction, ignore_index)
@@ -251,6 +252,8 @@ class LinearCrossEntropy(_Op):
             head_capi.linear_ce_desc_set_row_strides(self.desc, self.h_stride, self.w_stride)
         if piece:
             head_capi.linear_ce_desc_set_piece(self.desc, piece)
+        if dz_parts:
+            head_capi.linear_ce_desc_set_dz_parts(self.desc, dz_parts)
         self.workspace_bytes, self.backward_workspace_bytes = head_capi.linear_ce_workspace_size(self.desc)
         self.loss_shape = (tokens,) if reduction == "none" else ()
         self._h, self._w = _Rows(tokens, hidden, self.h_stride, dtype), _Rows(vocab, hidden, self.w_stride, dtype)

@@ -18,7 +18,7 @@ EXPORTED = ("layernorm_desc_create", "layernorm_desc_set_row_strides", "layernor
             "layernorm_desc_destroy", "layernorm_workspace_size", "layernorm_fwd", "layernorm_bwd",
             "dropout_desc_create", "dropout_desc_set_row_strides", "dropout_desc_destroy", "dropout_fwd", "dropout_bwd",
             "linear_ce_desc_create", "linear_ce_desc_set_row_strides", "linear_ce_desc_set_piece",
-            "linear_ce_desc_destroy", "linear_ce_workspace_size", "linear_ce_fwd", "linear_ce_bwd")
+            "linear_ce_desc_set_dz_parts", "linear_ce_desc_destroy", "linear_ce_workspace_size", "linear_ce_fwd", "linear_ce_bwd")
 
 _lib = None
 
@@ -46,6 +46,7 @@ def load():
     L.linear_ce_desc_create.argtypes = [out, i64, i64, i64, i32, i32, i64]
     L.linear_ce_desc_set_row_strides.argtypes = [vp, i64, i64]
     L.linear_ce_desc_set_piece.argtypes = [vp, i64]
+    L.linear_ce_desc_set_dz_parts.argtypes = [vp, i32]
     L.linear_ce_desc_destroy.argtypes = [vp]
     L.linear_ce_workspace_size.argtypes = [vp, ctypes.POINTER(size), ctypes.POINTER(size)]
     L.linear_ce_fwd.argtypes = [vp] * 7 + [size, vp]
@@ -136,6 +137,10 @@ def linear_ce_desc_set_row_strides(desc: int, h_stride: int, w_stride: int):
 
 def linear_ce_desc_set_piece(desc: int, vocab_rows: int):
     _check(load().linear_ce_desc_set_piece(desc, vocab_rows), "linear_ce_desc_set_piece")
+
+
+def linear_ce_desc_set_dz_parts(desc: int, parts: int):
+    _check(load().linear_ce_desc_set_dz_parts(desc, parts), "linear_ce_desc_set_dz_parts")
 
 
 def linear_ce_desc_destroy(desc: int):

@@ -289,6 +289,7 @@ ce_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ Ge
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kMaxRing + 5);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     volatile int* copies = abort_flag + 1;                 // PAIR: ring fills that this CTA has issued
+    volatile int* peer = copies + 1;                       // PAIR: the other CTA's two words, which it writes here
     auto full_bar = [&](int i) { return smem_addr(&bars[i]); };
     auto empty_bar = [&](int i) { return smem_addr(&bars[kMaxRing + i]); };
     auto accf_bar = [&](int a) { return smem_addr(&bars[2 * kMaxRing + a]); };
@@ -458,7 +459,8 @@ ce_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ Ge
                 }
             }
             if (!ok && issued_any) {
-                commit(drain_bar);
+                if constexpr (PAIR) umma_commit_pair_own(drain_bar);
+                else                umma_commit(drain_bar);
                 mbar_drain_wait(drain_bar, 0);
             }
         }
@@ -656,17 +658,22 @@ ce_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ Ge
     tc_fence_before();
     __syncthreads();
     if constexpr (PAIR) {
+        // Each CTA leaves its state with the other before they meet: after the meeting
+        // the other may be gone, and its memory with it.
+        if (threadIdx.x == 0) {
+            const uint32_t to = cluster_addr(smem_addr(const_cast<int*>(peer)), rank ^ 1);
+            st_cluster(to, (uint32_t)*abort_flag);
+            st_cluster(to + 4, (uint32_t)*copies);
+        }
         __syncwarp();
         cluster_sync();                                    // both CTAs are done with each other's memory
-        const uint32_t other = rank ^ 1;
-        const uint32_t stopped = ld_cluster(cluster_addr(smem_addr(const_cast<int*>(abort_flag)), other));
-        if (*abort_flag || stopped) {
+        if (*abort_flag || peer[0]) {
             // A wait ran out.  The two CTAs may have stopped at different fills;
             // the issuing CTA's barriers count both CTAs' bytes.  It adds what
             // the one that is behind never sent, or expects what the one ahead
             // did send, and sees every copy land before either CTA leaves.
             if (rank == 0 && threadIdx.x == 0) {
-                const int own = *copies, far = (int)ld_cluster(cluster_addr(smem_addr(const_cast<int*>(copies)), other));
+                const int own = *copies, far = peer[1];
                 const int last = own > far ? own : far;
                 for (int c = last > stages ? last - stages : 0; c < last; ++c) {
                     const uint32_t bar = full_bar(c % stages);

@@ -195,11 +195,10 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t a, uint32_t rank) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// 32-bit word at a cluster address.
-__device__ __forceinline__ uint32_t ld_cluster(uint32_t a) {
-    uint32_t v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-    return v;
+// 32-bit word to a cluster address (before a meeting of the cluster: the CTA it
+// belongs to must still be there).
+__device__ __forceinline__ void st_cluster(uint32_t a, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
 // Count `bytes` on a barrier as if a copy had brought them.
 __device__ __forceinline__ void mbar_complete_tx(uint32_t bar, uint32_t bytes) {
@@ -397,6 +396,10 @@ __device__ __forceinline__ void umma_commit_pair(uint32_t bar) {
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
         "h"((uint16_t)3)
         : "memory");
+}
+// The same, arriving at the issuing CTA's barrier alone.
+__device__ __forceinline__ void umma_commit_pair_own(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // Shared-memory matrix descriptor, K-major operand in the 128-byte swizzle

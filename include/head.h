@@ -12,6 +12,9 @@
  * launch plans are those of the device that is current when one is made).  Element types are
  * conv2d_dtype; 16-bit values are widened on load, every sum, mean, norm and
  * softmax is held in fp32, and a result is rounded to nearest even once.
+ * Waits are bounded as conv2d_set_wait_limit says; layer norm's row kernels look
+ * for a copy once, for up to a time slice of the hardware, before the limit
+ * counts.
  * Results do not depend on the order in which blocks run: no kernel here
  * accumulates through floating-point atomics, so a call repeated on the same
  * inputs gives the same bits.

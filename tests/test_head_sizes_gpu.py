@@ -50,3 +50,19 @@ def test_one_token(dtype, d, v):
     h, w, target = _ce_inputs(d + v, 1, d, v, dtype, ignored=0.0)
     op = head.LinearCrossEntropy(1, d, v, dtype, reduction="none")
     _check_ce(h, w, target, dtype, "none", op, torch.full((1,), 0.7, device="cuda"))
+
+
+@pytest.mark.parametrize("n,d,v", [(17, 100, 501), (32, 640, 3001), (31, 33, 700), (11, 4096, 900), (20, 3900, 947),
+                                   (9, 6144, 333), (25, 3168, 600), (32, 8, 40), (24, 5, 9000)])
+def test_fp32_losses_in_groups_of_tokens(n, d, v):
+    """The fp32 forward pass of few tokens in two to four groups, targets ignored in
+    the last one too, with rows of h that are not adjacent."""
+    import torch
+    from dense_convolution_gb300 import head
+    h, w, target = _ce_inputs(n * 7 + d, n, d, v, "f32")
+    target[-2] = -100
+    h, _ = _strided(h, d + 3)
+    for reduction in ("none", "sum", "mean"):
+        op = head.LinearCrossEntropy(n, d, v, "f32", reduction=reduction, h_stride=d + 3)
+        dloss = torch.rand(n, device="cuda") + 0.5 if reduction == "none" else torch.full((), 0.7, device="cuda")
+        _check_ce(h, w, target, "f32", reduction, op, dloss, reduction + " ")

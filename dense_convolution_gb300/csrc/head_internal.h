@@ -51,6 +51,7 @@ struct linear_ce_desc {
     int64_t hs, ws;      // row strides of h and w
     int64_t piece;       // vocabulary rows per backward piece; 0 = automatic
     int dz_parts;        // 16-bit parts of dz: 1, 2; 0 = automatic
+    int sms;             // of the device that the plans are for: the few-token kernels' blocks and shares
     conv2d_gb300::CePlan fwd, bwd;
 };
 
@@ -93,7 +94,7 @@ conv2d_status launch_linear_ce_bwd(const linear_ce_desc& d, const void* h, const
 
 // linear_ce_few.cu: few tokens, on the CUDA cores
 bool linear_ce_is_few(const linear_ce_desc& d, bool backward);
-int linear_ce_few_blocks();                          // (max, sum) pairs per token of the forward kernel
+inline int linear_ce_few_blocks(const linear_ce_desc& d) { return d.sms; }   // (max, sum) pairs per token, forward
 int64_t linear_ce_few_dz(const linear_ce_desc& d);   // fp32 words of dz and of the partial sums of dh
 int64_t linear_ce_few_sums(const linear_ce_desc& d);
 cudaError_t launch_ce_few_fwd(const linear_ce_desc& d, const void* h, const void* w, const int64_t* target, void* part,

@@ -1116,7 +1116,7 @@ CePlan plan_ce(const linear_ce_desc& d, bool backward) {
     c.few = linear_ce_is_few(d, backward);
     if (c.few) {
         if (!backward) {
-            take(at, c.part, (size_t)d.tokens * linear_ce_few_blocks() * sizeof(float2));
+            take(at, c.part, (size_t)d.tokens * linear_ce_few_blocks(d) * sizeof(float2));
             take(at, c.z_target, (size_t)d.tokens * 4);
             take(at, c.row_loss, (size_t)d.tokens * 4);
         } else {
@@ -1298,6 +1298,7 @@ const void* at_row(const void* base, int64_t row, int64_t stride, size_t e) {
 void linear_ce_plan(linear_ce_desc& d) {
     d.fwd = d.bwd = CePlan{};
     if (d.tokens == 0) return;
+    d.sms = device_sm_count();
     d.fwd = plan_ce(d, false);
     d.bwd = plan_ce(d, true);
 }
@@ -1314,7 +1315,7 @@ conv2d_status launch_linear_ce_fwd(const linear_ce_desc& d, const void* h, const
     int tiles = 0;
     if (c.few) {
         if (launch_ce_few_fwd(d, h, w, target, part, p.z_target, st) != cudaSuccess) return CONV2D_ERR_CUDA;
-        tiles = linear_ce_few_blocks();
+        tiles = linear_ce_few_blocks(d);
     } else {
         Operand ho{h, d.hidden, d.hs};
         if (c.pack_h) {

@@ -36,6 +36,7 @@ constexpr int kSmemMost = 200 * 1024;
 struct FewParams {
     int tokens, hidden, vocab, reduction;
     int pitch;               // tokens between the blocks' parts
+    int blocks;
     int64_t hs, ws, ignore;
     const void *h, *w;
     const int64_t* target;
@@ -433,7 +434,7 @@ template <typename T, int NT, int ROWS, bool BACKWARD> cudaError_t few_launch(co
     const size_t smem = few_smem<T>(NT, p.hidden);
     const cudaError_t e = allow_smem(ce_few_kernel<T, NT, ROWS, BACKWARD>, kSmemMost);
     if (e != cudaSuccess) return e;
-    return launch_after(ce_few_kernel<T, NT, ROWS, BACKWARD>, dim3((unsigned)linear_ce_few_blocks()), dim3(kThreads), smem,
+    return launch_after(ce_few_kernel<T, NT, ROWS, BACKWARD>, dim3((unsigned)p.blocks), dim3(kThreads), smem,
                         st, p);
 }
 
@@ -445,8 +446,8 @@ template <typename T, int NT, int ROWS, bool BACKWARD> cudaError_t few_launch(co
 //   1024 features   5000 rows 10.4 / 9.7, 10007 rows 12.4 / 16.0, 50257 rows 24.0 / 27.9
 //   2487 features   64640 rows 63.7 / 58.7;   4096   10007 rows 27.3 / 42.5
 // The rule is at most 2.5 % behind the better one at the 36 shapes measured.
-int one_token_rows(int64_t vocab, int64_t row_bytes, int vec) {
-    const int64_t warps = (int64_t)linear_ce_few_blocks() * (kThreads / 32);
+int one_token_rows(int64_t vocab, int64_t row_bytes, int vec, int blocks) {
+    const int64_t warps = (int64_t)blocks * (kThreads / 32);
     const auto cost = [&](int64_t rows) {
         const int64_t groups = (vocab + rows * vec - 1) / (rows * vec) * vec;
         return (groups + warps - 1) / warps * (rows * row_bytes + 768);
@@ -456,7 +457,7 @@ int one_token_rows(int64_t vocab, int64_t row_bytes, int vec) {
 template <typename T, bool BACKWARD> cudaError_t few_tokens(const FewParams& p, cudaStream_t st) {
     switch (nt_of(p.tokens)) {
         case 1:
-            return one_token_rows(p.vocab, p.hidden * (int64_t)sizeof(T), kVec<T>) == 2
+            return one_token_rows(p.vocab, p.hidden * (int64_t)sizeof(T), kVec<T>, p.blocks) == 2
                        ? few_launch<T, 1, 2, BACKWARD>(p, st)
                        : few_launch<T, 1, 4, BACKWARD>(p, st);
         case 2: return few_launch<T, 2, 4, BACKWARD>(p, st);
@@ -485,7 +486,7 @@ DhPlan dh_plan(const linear_ce_desc& d) {
     const int64_t V = 16 / (int64_t)elem_bytes(d.dtype);
     p.step = d.ws % V == 0 ? 1 : (int)V;
     p.columns = (int)((d.hidden + (V - 1) + 32 * V - 1) / (32 * V));    // rows may begin V - 1 elements into a vector
-    int64_t ranges = (4 * device_sm_count() + p.columns * p.step - 1) / (p.columns * p.step);
+    int64_t ranges = (4 * d.sms + p.columns * p.step - 1) / (p.columns * p.step);
     const int64_t most = (d.vocab + 32 * p.step - 1) / (32 * p.step);
     if (ranges > most) ranges = most;
     const int64_t room = kDhWords / nt_of(d.tokens) * p.step, least = (d.vocab + room - 1) / room;
@@ -524,8 +525,6 @@ template <typename T> cudaError_t dh_typed(const linear_ce_desc& d, const void* 
 
 }  // namespace
 
-int linear_ce_few_blocks() { return device_sm_count(); }
-
 // Few tokens, whose h fits a block's shared memory.  The products of
 // linear_ce.cu read w at one speed whatever the tokens, but want fp32 split and
 // odd rows copied first.  Forward / backward, this file against that one:
@@ -534,7 +533,8 @@ int linear_ce_few_blocks() { return device_sm_count(); }
 //   fp32 2048 x 50000             8 tokens  81 / 249 us, 516 / 825;  16 tokens 131 / 394, 411 / 769
 //   fp32 1024 x 50000            32 tokens 218 / 604 us (a form for 32 at once), 203 / 414
 // Forward of fp32 takes up to 32 tokens in groups, each of which reads w again:
-// 32 x 2048 x 50000 259 us, 411 on the tensor cores; 32 x 1024 x 50000 160, 203.
+// 32 x 2048 x 50000 257 us, 415 on the tensor cores; 20 x 3900 x 9472 116, 195; 32 x
+// 256 x 9472 25, 27; behind only where rows are a tile wide: 32 x 100 x 50000 44, 38.
 bool linear_ce_is_few(const linear_ce_desc& d, bool backward) {
     if (d.dtype == CONV2D_F32 && !backward) return d.tokens <= 32 && few_fits(d, d.tokens < 8 ? d.tokens : 8);
     const bool copied = d.hs % 8 != 0 || d.ws % 8 != 0;
@@ -552,6 +552,7 @@ cudaError_t launch_ce_few_fwd(const linear_ce_desc& d, const void* h, const void
         FewParams p{};
         p.tokens = (int)(d.tokens - t < most ? d.tokens - t : most);
         p.pitch = (int)d.tokens;
+        p.blocks = linear_ce_few_blocks(d);
         p.hidden = (int)d.hidden; p.vocab = (int)d.vocab; p.reduction = d.reduction;
         p.hs = d.hs; p.ws = d.ws; p.ignore = d.ignore_index;
         p.h = static_cast<const uint8_t*>(h) + (size_t)(t * d.hs) * elem_bytes(d.dtype);
@@ -570,6 +571,7 @@ cudaError_t launch_ce_few_bwd(const linear_ce_desc& d, const void* h, const void
                               cudaStream_t st) {
     FewParams p{};
     p.tokens = (int)d.tokens; p.hidden = (int)d.hidden; p.vocab = (int)d.vocab; p.reduction = d.reduction;
+    p.blocks = linear_ce_few_blocks(d);
     p.hs = d.hs; p.ws = d.ws; p.ignore = d.ignore_index;
     p.h = h; p.w = w; p.target = target;
     p.lse = lse; p.dloss = dloss; p.dw = dw;

@@ -66,3 +66,14 @@ def test_fp32_losses_in_groups_of_tokens(n, d, v):
         op = head.LinearCrossEntropy(n, d, v, "f32", reduction=reduction, h_stride=d + 3)
         dloss = torch.rand(n, device="cuda") + 0.5 if reduction == "none" else torch.full((), 0.7, device="cuda")
         _check_ce(h, w, target, "f32", reduction, op, dloss, reduction + " ")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("n,d,v", [(1, 60000, 300), (3, 30001, 200), (9, 25600, 130)])
+def test_few_tokens_too_long_for_shared_memory(dtype, n, d, v):
+    """Few tokens whose h does not fit a block take the tensor cores."""
+    import torch
+    from dense_convolution_gb300 import head
+    h, w, target = _ce_inputs(d, n, d, v, dtype, ignored=0.0)
+    op = head.LinearCrossEntropy(n, d, v, dtype, reduction="sum")
+    _check_ce(h, w, target, dtype, "sum", op, torch.full((), 0.7, device="cuda"))

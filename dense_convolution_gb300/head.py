@@ -8,7 +8,8 @@ fails with a Python error instead of a bad pointer.  Each class is one problem
 shape: calling it runs the forward pass, ``backward`` the gradients.  All tensors
 of a call, its workspace among them, are on one GPU, on which it runs whichever
 is current.  With stream= (of that GPU) a call and the tensors that it allocates
-belong to that stream.
+belong to that stream.  No call records an autograd graph: gradients come from
+``backward``, and results carry none, whatever requires_grad their inputs have.
 """
 from __future__ import annotations
 

@@ -162,7 +162,8 @@ conv2d_status linear_ce_desc_set_piece(linear_ce_desc_t d, int64_t vocab_rows);
 /* 16-bit parts in which dz of fp16 and bf16 operands is kept: 1, or 2 for twice
  * its bits, which leaves dh and dw with little more than their own rounding (dz
  * takes twice the memory, and the two products of the backward pass twice the
- * time).  0 = automatic: 2 up to 256 tokens, where the rounding of dz does not
+ * time; with one part the rounding of dz adds up to as much again as theirs,
+ * where a row's sum is mostly one term).  0 = automatic: 2 up to 256 tokens, where the rounding of dz does not
  * average out, else 1.  Changes the workspace size.  Errors: NULL_PTR;
  * BAD_PARAM; UNSUPPORTED for fp32 (always three parts) unless 0. */
 conv2d_status linear_ce_desc_set_dz_parts(linear_ce_desc_t d, int parts);

@@ -1,0 +1,346 @@
+// AdamW over many tensors at once, in place, with moments of 32 or 8 bits.
+//
+//   m = b1 m + (1 - b1) g,  v = b2 v + (1 - b2) g^2   (g times the gradient scale)
+//   p = p (1 - lr decay) - lr / (1 - b1^t) m / (sqrt(v) / sqrt(1 - b2^t) + eps)
+//
+// and, where wanted, a 16-bit copy of p for the products of the next step.  The
+// tensors' addresses travel as the kernel's parameter, so a step of up to kMany
+// tensors is one launch that needs no workspace and no copy of a table; a block of
+// threads finds its tensor by bisection over the tensors' first blocks.
+//
+// A warp takes 256 adjacent elements, eight a lane: 32-byte loads of fp32 values.
+// They are also the blocks of the 8-bit moments (m e4m3, v e5m2): the block's
+// largest value, found by one reduction over the warp, fixes a power of two that
+// takes it to the type's top binade, and every value goes to one of its two
+// neighbours there, up with the chance that keeps the mean.  Rounding to nearest
+// would leave a moment where it is forever (b2 = 0.999 moves v by a thousandth a step,
+// half a step of e5m2 is a sixteenth); this way it moves as the formula does on
+// average.  With the moments in integers of their bits that is one addition of 16
+// random bits below the kept ones: Philox4x32-10 under key = seed and counter =
+// (element / 4, tensor, step mod 2^32, step div 2^32), one 32-bit word an element, its
+// low half for m, its high half for v.  A positive v never becomes zero: m would
+// be divided by what a single gradient leaves.  The step itself takes the
+// moments before they are rounded.
+//
+// Where p, g or the copy are not aligned for vectors, and at a tensor's end, a
+// warp's elements go through shared memory, so that global memory is read and
+// written along the row all the same.
+#include <math.h>
+
+#include "head_device.cuh"
+#include "head_internal.h"
+#include "ptx.cuh"
+
+namespace conv2d_gb300 {
+
+namespace {
+
+constexpr int kBlock = 256, kLane = 8;                 // elements of a warp and of a lane
+constexpr int kWarps = 8;                              // a block of threads takes kWarps * 256 elements
+constexpr int kFew = 24, kMany = 700;                  // tensors a launch: 1 KB and 31 KB of parameters
+
+struct AdamTensor {
+    float* p;
+    const void* g;
+    void* copy;
+    int64_t n;
+    uint32_t state;          // its first block of 256 in the moments
+    float decay;
+};
+
+struct AdamStep {
+    void *m, *v;
+    uint8_t *ms, *vs;        // 8 bits: the blocks' scales (e8m0)
+    const int64_t* step_at;  // null: `step`, with the corrections below
+    const float* lr_at;      // null: `lr`
+    const float* scale;      // null: 1
+    const float* skip;       // null, or not zero: nothing changes
+    int64_t step;
+    float lr, c1, rc2;       // 1 - b1^t, 1 / sqrt(1 - b2^t)
+    float log_b1, log_b2;
+    float b1, b2, a1, a2, eps;     // a = 1 - b
+    uint32_t k0, k1;
+    uint32_t first_tensor;   // number of the launch's first tensor
+    int copy_bf16, count;
+};
+
+template <int N> struct AdamTable {
+    AdamTensor t[N];
+    uint32_t first[N + 1];   // a tensor's first block of threads
+};
+
+__device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
+    uint32_t r[8];
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "l"(p));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
+    uint32_t r[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = __float_as_uint(f[i]);
+    st_global_v8(p, r);
+}
+template <typename T> __device__ __forceinline__ void load8(const T* p, float (&f)[8]) {
+    widen(*reinterpret_cast<const Vec<T, 8>*>(p), f);
+}
+
+// Eight values in 8 bits, their block's scale 2^(byte - 127): DIGITS bits of the
+// significand after the leading one, the type's smallest normal value 2^LOW.
+template <int DIGITS> __device__ __forceinline__ void from8(uint2 c, uint32_t byte, float (&f)[8]) {
+    constexpr int kBias = DIGITS == 3 ? 7 : 15, kLow = 1 - kBias;
+    // (255 is not a number, 2^-127 not a normal one.)
+    const float scale = __uint_as_float(byte == 255u ? 0x7fffffffu : byte ? byte << 23 : 0x00400000u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t b = (i < 4 ? c.x : c.y) >> (i % 4 * 8), mag = b & 0x7fu;
+        // A code of the lowest binade counts steps of 2^(LOW - DIGITS); of the others, the bits are a float's.
+        const float normal = __uint_as_float((mag << (23 - DIGITS)) + ((127u - kBias) << 23));
+        const float small = (float)mag * __uint_as_float((uint32_t)(127 + kLow - DIGITS) << 23);
+        const float v = mag < (1u << DIGITS) ? small : normal;
+        f[i] = __uint_as_float(__float_as_uint(v * scale) | (b & 0x80u) << 24);
+    }
+}
+
+// The same back.  `most`: the bits of the block's largest magnitude.  KEEP (v): the
+// high halves of the numbers r are its noise, and what is above zero stays there.
+template <int DIGITS, bool KEEP> __device__ __forceinline__ uint2 to8(const float (&f)[8], uint32_t most,
+                                                                     const uint32_t (&r)[8], uint32_t& byte) {
+    constexpr int kBias = DIGITS == 3 ? 7 : 15, kLow = 1 - kBias, kTop = DIGITS == 3 ? 8 : 15, kDrop = 23 - DIGITS;
+    // One binade more where the largest is above 1.75 of its own: what rounding up
+    // makes of it still fits.
+    const int exponent = (int)((most + (1u << 21) - 1u) >> 23) - 127;
+    const int scale = max(exponent - kTop, -127);
+    byte = most >= 0x7f800000u ? 255u : (uint32_t)(scale + 127);
+    const float up = __uint_as_float((uint32_t)(127 - scale) << 23);
+    uint32_t c[2] = {0u, 0u};
+    if (byte != 255u) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t noise = KEEP ? r[i] >> 16 : r[i] & 0xffffu;
+            const float y = fabsf(f[i]) * up;
+            const uint32_t normal = ((__float_as_uint(y) + (noise << (kDrop - 16))) >> kDrop) - ((kLow + 126) << DIGITS);
+            const uint32_t small = (__float2uint_rz(y * __uint_as_float((uint32_t)(127 + DIGITS - kLow + 16) << 23)) + noise) >> 16;
+            uint32_t code = y < __uint_as_float((uint32_t)(127 + kLow) << 23) ? small : normal;
+            if (KEEP && y > 0.f) code = max(code, 1u);
+            code |= __float_as_uint(f[i]) >> 24 & 0x80u;
+            c[i / 4] |= code << (i % 4 * 8);
+        }
+    }
+    return make_uint2(c[0], c[1]);
+}
+
+template <typename G, bool EIGHT, int N>
+__global__ void __launch_bounds__(32 * kWarps) adamw_kernel(const __grid_constant__ AdamTable<N> table,
+                                                            const __grid_constant__ AdamStep s) {
+    __shared__ float stage[kWarps][kBlock + kBlock / 8];
+    // The last tensor whose first block is not past this one.
+    int lo = 0, hi = s.count;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (table.first[mid] <= blockIdx.x) lo = mid;
+        else hi = mid;
+    }
+    const AdamTensor& t = table.t[lo];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t block = (int64_t)(blockIdx.x - table.first[lo]) * kWarps + warp, e0 = block * kBlock;
+    pdl_wait();
+    if (e0 >= t.n || (s.skip && *s.skip != 0.f)) return;
+    const int64_t at = (int64_t)t.state * kBlock + e0;     // in the moments
+    const int left = (int)min((int64_t)kBlock, t.n - e0);
+    float* p = t.p + e0;
+    const G* g = static_cast<const G*>(t.g) + e0;
+    uint16_t* copy = t.copy ? static_cast<uint16_t*>(t.copy) + e0 : nullptr;
+    const bool whole = left == kBlock && (reinterpret_cast<uintptr_t>(p) & 31u) == 0 &&
+                       (reinterpret_cast<uintptr_t>(g) & (sizeof(G) * 8 - 1)) == 0 &&
+                       (reinterpret_cast<uintptr_t>(copy) & 15u) == 0;
+    const int i0 = lane * kLane;
+    float fp[8], fg[8], fm[8], fv[8];
+    // An element's place in the stage: eight in a row, then one to spare.
+    float* const row = stage[warp];
+    const auto place = [](int e) { return e + (e >> 3); };
+    if (whole) {
+        load8(p + i0, fp);
+        load8(g + i0, fg);
+    }
+    uint2 cm, cv;
+    uint32_t bm = 0, bv = 0;
+    if constexpr (EIGHT) {
+        cm = reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(s.m) + at)[lane];
+        cv = reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(s.v) + at)[lane];
+        bm = s.ms[at / kBlock];
+        bv = s.vs[at / kBlock];
+    } else {
+        load8(static_cast<const float*>(s.m) + at + i0, fm);
+        load8(static_cast<const float*>(s.v) + at + i0, fv);
+    }
+    if (!whole) {
+        for (int e = lane; e < kBlock; e += 32) row[place(e)] = e < left ? p[e] : 0.f;
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) fp[i] = row[place(i0 + i)];
+        __syncwarp();
+        for (int e = lane; e < kBlock; e += 32) row[place(e)] = e < left ? to_f32(g[e]) : 0.f;
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) fg[i] = row[place(i0 + i)];
+    }
+    int64_t step = s.step;
+    float c1 = s.c1, rc2 = s.rc2;
+    if (s.step_at) {
+        step = *s.step_at;
+        c1 = -expm1f((float)step * s.log_b1);
+        rc2 = 1.f / sqrtf(-expm1f((float)step * s.log_b2));
+    }
+    const float lr = s.lr_at ? *s.lr_at : s.lr, up = lr / c1, shrink = fmaf(-lr, t.decay, 1.f);
+    if (s.scale) {
+        const float k = *s.scale;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) fg[i] *= k;
+    }
+    if constexpr (EIGHT) {
+        from8<3>(cm, bm, fm);
+        from8<2>(cv, bv, fv);
+    }
+    if (!whole) {                                          // past the end: zero, whatever lies there
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i0 + i >= left) fm[i] = fv[i] = 0.f;
+    }
+    uint32_t top_m = 0, top_v = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        // Each product and sum rounds by itself: the 8-bit codes are then a matter of the formula alone, not of which of
+        // them a compiler joins.
+        fm[i] = __fadd_rn(__fmul_rn(s.b1, fm[i]), __fmul_rn(s.a1, fg[i]));
+        fv[i] = __fadd_rn(__fmul_rn(s.b2, fv[i]), __fmul_rn(__fmul_rn(s.a2, fg[i]), fg[i]));
+        top_m = max(top_m, __float_as_uint(fm[i]) & 0x7fffffffu);
+        top_v = max(top_v, __float_as_uint(fv[i]) & 0x7fffffffu);
+        fp[i] = fmaf(-up, fm[i] / fmaf(sqrtf(fv[i]), rc2, s.eps), fp[i] * shrink);
+    }
+    if (whole) {
+        store8(p + i0, fp);
+        if (copy) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const f32x2 two = pack2f(fp[2 * i], fp[2 * i + 1]);
+                w[i] = s.copy_bf16 ? narrow_pair<__nv_bfloat16>(two) : narrow_pair<__half>(two);
+            }
+            *reinterpret_cast<uint4*>(copy + i0) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    } else {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) row[place(i0 + i)] = fp[i];
+        __syncwarp();
+        for (int e = lane; e < left; e += 32) {
+            const float f = row[place(e)];
+            p[e] = f;
+            if (copy) store_param(copy, false, s.copy_bf16, e, f);
+        }
+    }
+    if constexpr (EIGHT) {
+        uint32_t r[8];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            uint32_t c[4] = {(uint32_t)(e0 / 4) + 2 * lane + k, s.first_tensor + lo, (uint32_t)step, (uint32_t)((uint64_t)step >> 32)};
+            philox(c, s.k0, s.k1);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r[4 * k + i] = c[i];
+        }
+        cm = to8<3, false>(fm, __reduce_max_sync(0xffffffffu, top_m), r, bm);
+        cv = to8<2, true>(fv, __reduce_max_sync(0xffffffffu, top_v), r, bv);
+        reinterpret_cast<uint2*>(static_cast<uint8_t*>(s.m) + at)[lane] = cm;
+        reinterpret_cast<uint2*>(static_cast<uint8_t*>(s.v) + at)[lane] = cv;
+        if (lane == 0) {
+            s.ms[at / kBlock] = (uint8_t)bm;
+            s.vs[at / kBlock] = (uint8_t)bv;
+        }
+    } else {
+        store8(static_cast<float*>(s.m) + at + i0, fm);
+        store8(static_cast<float*>(s.v) + at + i0, fv);
+    }
+}
+
+template <typename G, bool EIGHT, int N>
+cudaError_t launch(const adamw_desc& d, int from, int count, float* const* params, const void* const* grads,
+                   void* const* copies, AdamStep s, cudaStream_t st) {
+    AdamTable<N> table;
+    uint32_t blocks = 0;
+    int k = 0;
+    for (int i = from; i < from + count; ++i) {
+        // (An empty tensor keeps its number and takes no block.)
+        table.t[k] = AdamTensor{params[i], grads[i], copies ? copies[i] : nullptr, d.tensors[i].n,
+                                (uint32_t)(d.tensors[i].offset / kBlock), d.tensors[i].decay};
+        table.first[k++] = blocks;
+        blocks += (uint32_t)((d.tensors[i].n + kBlock * kWarps - 1) / (kBlock * kWarps));
+    }
+    if (!blocks) return cudaSuccess;
+    s.first_tensor = (uint32_t)from;
+    s.count = count;
+    return launch_after(adamw_kernel<G, EIGHT, N>, dim3(blocks), dim3(32 * kWarps), 0, st, table, s);
+}
+
+template <typename G, bool EIGHT>
+cudaError_t run(const adamw_desc& d, float* const* params, const void* const* grads, void* const* copies,
+                const AdamStep& s, cudaStream_t st) {
+    const int count = d.count;
+    for (int from = 0; from < count;) {
+        // As many tensors as a launch's table and its number of blocks take.
+        int n = 0;
+        int64_t blocks = 0;
+        while (from + n < count && n < kMany) {
+            const int64_t more = (d.tensors[from + n].n + kBlock * kWarps - 1) / (kBlock * kWarps);
+            if (n && blocks + more > 0x7fffffffLL) break;
+            blocks += more;
+            ++n;
+        }
+        const cudaError_t e = n <= kFew ? launch<G, EIGHT, kFew>(d, from, n, params, grads, copies, s, st)
+                                        : launch<G, EIGHT, kMany>(d, from, n, params, grads, copies, s, st);
+        if (e != cudaSuccess) return e;
+        from += n;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_adamw(const adamw_desc& d, float* const* params, const void* const* grads, void* const* copies,
+                         void* m, void* v, void* m_scale, void* v_scale, int64_t step, float lr,
+                         const int64_t* step_at, const float* lr_at, const float* grad_scale, const float* skip,
+                         uint64_t seed, cudaStream_t st) {
+    AdamStep s{};
+    s.m = m;
+    s.v = v;
+    s.ms = static_cast<uint8_t*>(m_scale);
+    s.vs = static_cast<uint8_t*>(v_scale);
+    s.step_at = step_at;
+    s.lr_at = lr_at;
+    s.scale = grad_scale;
+    s.skip = skip;
+    s.step = step;
+    s.lr = lr;
+    if (!step_at) {
+        s.c1 = (float)(1.0 - pow(d.beta1, (double)step));
+        s.rc2 = (float)(1.0 / sqrt(1.0 - pow(d.beta2, (double)step)));
+    }
+    s.log_b1 = (float)log(d.beta1);
+    s.log_b2 = (float)log(d.beta2);
+    s.b1 = (float)d.beta1; s.a1 = (float)(1.0 - d.beta1);
+    s.b2 = (float)d.beta2; s.a2 = (float)(1.0 - d.beta2);
+    s.eps = (float)d.eps;
+    s.k0 = (uint32_t)seed;
+    s.k1 = (uint32_t)(seed >> 32);
+    s.copy_bf16 = d.copy == CONV2D_BF16;
+    const bool eight = d.states == ADAMW_STATES_8BIT;
+    switch (d.grad) {
+        case CONV2D_F32: return eight ? run<float, true>(d, params, grads, copies, s, st) : run<float, false>(d, params, grads, copies, s, st);
+        case CONV2D_F16: return eight ? run<__half, true>(d, params, grads, copies, s, st) : run<__half, false>(d, params, grads, copies, s, st);
+        default: return eight ? run<__nv_bfloat16, true>(d, params, grads, copies, s, st) : run<__nv_bfloat16, false>(d, params, grads, copies, s, st);
+    }
+}
+
+}  // namespace conv2d_gb300

@@ -1,7 +1,7 @@
 // C ABI of the training-head operators (include/head.h): descriptors, argument
 // checks and workspace sizes.  Host code only; the kernels live in
-// layernorm.cu, layernorm_planes.cu, dropout.cu, linear_ce.cu and
-// linear_ce_few.cu.
+// layernorm.cu, layernorm_planes.cu, dropout.cu, linear_ce.cu, linear_ce_few.cu
+// and adamw.cu.
 #include <math.h>
 
 #include <new>
@@ -270,4 +270,98 @@ CONV2D_API conv2d_status linear_ce_bwd(linear_ce_desc_t dp, const void* h, const
         return CONV2D_ERR_MISALIGNED;
     if (workspace_bytes < d.bwd.total) return CONV2D_ERR_WORKSPACE_TOO_SMALL;
     return launch_linear_ce_bwd(d, h, w, target, lse, dloss, dh, dw, workspace, st);
+}
+
+// --------------------------------------------------------------------- AdamW
+CONV2D_API conv2d_status adamw_desc_create(adamw_desc_t* out, int64_t count, const int64_t* sizes,
+                                           conv2d_dtype grad_dtype, adamw_states states, conv2d_dtype copy_dtype) {
+    if (!out) return CONV2D_ERR_NULL_PTR;
+    *out = nullptr;
+    if (count < 0 || count > (1LL << 24) || !known(grad_dtype) || !known(copy_dtype)) return CONV2D_ERR_BAD_PARAM;
+    if (states != ADAMW_STATES_F32 && states != ADAMW_STATES_8BIT) return CONV2D_ERR_BAD_PARAM;
+    if (count && !sizes) return CONV2D_ERR_NULL_PTR;
+    adamw_desc d{};
+    d.count = count;
+    d.grad = grad_dtype; d.copy = copy_dtype; d.states = states;
+    d.beta1 = 0.9; d.beta2 = 0.999; d.eps = 1e-8;
+    for (int64_t i = 0; i < count; ++i) {
+        // (The kernel numbers blocks of 256 with 32 bits, and an element's group of four.)
+        if (sizes[i] < 0 || sizes[i] > (1LL << 34)) return CONV2D_ERR_BAD_PARAM;
+        d.elements += (sizes[i] + 255) / 256 * 256;
+        if (d.elements >= (1LL << 40)) return CONV2D_ERR_BAD_PARAM;
+    }
+    d.tensors = new (std::nothrow) adamw_desc::Tensor[count > 0 ? count : 1];
+    if (!d.tensors) return CONV2D_ERR_BAD_PARAM;
+    int64_t at = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        d.tensors[i] = adamw_desc::Tensor{sizes[i], at, 0.f};
+        at += (sizes[i] + 255) / 256 * 256;
+    }
+    const conv2d_status s = give(out, d);
+    if (s != CONV2D_OK) delete[] d.tensors;
+    return s;
+}
+
+CONV2D_API conv2d_status adamw_desc_set_rates(adamw_desc_t d, double beta1, double beta2, double eps) {
+    if (!d) return CONV2D_ERR_NULL_PTR;
+    // As the kernel holds them: 1 - b and eps above zero.
+    if (!(beta1 >= 0.0 && (float)beta1 < 1.f) || !(beta2 >= 0.0 && (float)beta2 < 1.f)) return CONV2D_ERR_BAD_PARAM;
+    if (!((float)eps > 0.f) || !isfinite((float)eps)) return CONV2D_ERR_BAD_PARAM;
+    d->beta1 = beta1;
+    d->beta2 = beta2;
+    d->eps = eps;
+    return CONV2D_OK;
+}
+
+CONV2D_API conv2d_status adamw_desc_set_weight_decay(adamw_desc_t d, const float* decay) {
+    if (!d) return CONV2D_ERR_NULL_PTR;
+    if (d->count && !decay) return CONV2D_ERR_NULL_PTR;
+    for (int64_t i = 0; i < d->count; ++i)
+        if (!isfinite(decay[i])) return CONV2D_ERR_BAD_PARAM;
+    for (int64_t i = 0; i < d->count; ++i) d->tensors[i].decay = decay[i];
+    return CONV2D_OK;
+}
+
+CONV2D_API conv2d_status adamw_desc_destroy(adamw_desc_t d) {
+    if (d) delete[] d->tensors;
+    delete d;
+    return CONV2D_OK;
+}
+
+CONV2D_API conv2d_status adamw_state_elements(adamw_desc_t d, int64_t* elements) {
+    if (!d || !elements) return CONV2D_ERR_NULL_PTR;
+    *elements = d->elements;
+    return CONV2D_OK;
+}
+
+CONV2D_API conv2d_status adamw_state_offset(adamw_desc_t d, int64_t i, int64_t* offset) {
+    if (!d || !offset) return CONV2D_ERR_NULL_PTR;
+    if (i < 0 || i >= d->count) return CONV2D_ERR_BAD_PARAM;
+    *offset = d->tensors[i].offset;
+    return CONV2D_OK;
+}
+
+CONV2D_API conv2d_status adamw_step(adamw_desc_t dp, float* const* params, const void* const* grads,
+                                    void* const* copies, void* m, void* v, void* m_scale, void* v_scale, int64_t step,
+                                    float lr, const int64_t* device_step, const float* device_lr,
+                                    const float* grad_scale, const float* skip, uint64_t seed, void* stream) {
+    if (!dp) return CONV2D_ERR_NULL_PTR;
+    const adamw_desc& d = *dp;
+    if ((!device_step && step < 1) || (!device_lr && !isfinite(lr))) return CONV2D_ERR_BAD_PARAM;
+    if (!aligned_to(device_step, 8) || !aligned_to(device_lr, 4) || !aligned_to(grad_scale, 4) || !aligned_to(skip, 4))
+        return CONV2D_ERR_MISALIGNED;
+    if (d.elements == 0) return CONV2D_OK;
+    const bool eight = d.states == ADAMW_STATES_8BIT, copied = d.copy != CONV2D_F32;
+    if (!params || !grads || (copied && !copies) || !m || !v || (eight && (!m_scale || !v_scale)))
+        return CONV2D_ERR_NULL_PTR;
+    if (!aligned_to(m, 32) || !aligned_to(v, 32)) return CONV2D_ERR_MISALIGNED;
+    const size_t ge = elem_bytes(d.grad);
+    for (int64_t i = 0; i < d.count; ++i) {
+        if (!d.tensors[i].n) continue;
+        if (!params[i] || !grads[i] || (copied && !copies[i])) return CONV2D_ERR_NULL_PTR;
+        if (!aligned_to(params[i], 4) || !aligned_to(grads[i], ge) || (copied && !aligned_to(copies[i], 2)))
+            return CONV2D_ERR_MISALIGNED;
+    }
+    return of(launch_adamw(d, params, grads, copied ? copies : nullptr, m, v, m_scale, v_scale, step, lr, device_step,
+                           device_lr, grad_scale, skip, seed, static_cast<cudaStream_t>(stream)));
 }

@@ -55,6 +55,15 @@ struct linear_ce_desc {
     conv2d_gb300::CePlan fwd, bwd;
 };
 
+struct adamw_desc {
+    struct Tensor { int64_t n, offset; float decay; };
+    int64_t count, elements;             // tensors; elements of each moment
+    conv2d_dtype grad, copy;             // copy F32: none
+    adamw_states states;
+    double beta1, beta2, eps;
+    Tensor* tensors;
+};
+
 namespace conv2d_gb300 {
 
 inline size_t elem_bytes(conv2d_dtype t) { return t == CONV2D_F32 ? 4 : 2; }
@@ -102,5 +111,11 @@ cudaError_t launch_ce_few_fwd(const linear_ce_desc& d, const void* h, const void
 cudaError_t launch_ce_few_bwd(const linear_ce_desc& d, const void* h, const void* w, const int64_t* target,
                               const float* lse, const float* dloss, void* dh, void* dw, float* dz, float* sums,
                               cudaStream_t st);
+
+// adamw.cu
+cudaError_t launch_adamw(const adamw_desc& d, float* const* params, const void* const* grads, void* const* copies,
+                         void* m, void* v, void* m_scale, void* v_scale, int64_t step, float lr,
+                         const int64_t* step_at, const float* lr_at, const float* grad_scale, const float* skip,
+                         uint64_t seed, cudaStream_t st);
 
 }  // namespace conv2d_gb300

@@ -13,6 +13,8 @@ belong to that stream.  No call records an autograd graph: gradients come from
 """
 from __future__ import annotations
 
+import collections
+
 import torch
 
 from . import head_capi
@@ -303,6 +305,95 @@ class LinearCrossEntropy(_Op):
                                 dloss.data_ptr(), _ptr(dh), _ptr(dw), workspace.data_ptr(), workspace.numel(),
                                 _raw_stream(dev))
         return dh, dw
+
+
+AdamWState = collections.namedtuple("AdamWState", "m v m_scale v_scale")
+
+
+class AdamW(_Op):
+    """A step of AdamW over tensors of `sizes` elements at once, in place.
+
+    params fp32, grads of `grad_dtype`, contiguous and of any shape
+    states        "f32", or "8bit": moments in 8 bits with a scale for each 256 elements
+    copy_dtype    "f16" or "bf16": every step also writes the parameters in that type
+    weight_decay  one value, or one for each tensor
+    """
+    _destroy = staticmethod(head_capi.adamw_desc_destroy)
+
+    def __init__(self, sizes, grad_dtype="f32", states="f32", copy_dtype=None, betas=(0.9, 0.999), eps=1e-8,
+                 weight_decay=0.0):
+        self.sizes, self.states, self.grad_dtype, self.copy_dtype = tuple(map(int, sizes)), states, grad_dtype, copy_dtype
+        self.desc = head_capi.adamw_desc_create(self.sizes, grad_dtype, states, copy_dtype or "f32")
+        head_capi.adamw_desc_set_rates(self.desc, *betas, eps)
+        decay = [weight_decay] * len(self.sizes) if isinstance(weight_decay, (int, float)) else list(weight_decay)
+        if len(decay) != len(self.sizes):
+            raise ValueError(f"{len(decay)} weight decays for {len(self.sizes)} tensors")
+        head_capi.adamw_desc_set_weight_decay(self.desc, decay)
+        self.elements = head_capi.adamw_state_elements(self.desc)
+        self._grad, self._copy = _TORCH_DTYPE[grad_dtype], _TORCH_DTYPE[copy_dtype] if copy_dtype else None
+        kinds = (torch.float32,) * 2 if states == "f32" else (torch.float8_e4m3fn, torch.float8_e5m2)
+        self._m, self._v = (_Flat((self.elements,), k) for k in kinds)
+        self._scales = _Flat((self.elements // 256,), torch.float8_e8m0fnu)
+
+    def new_state(self, device="cuda"):
+        """The moments before the first step.  In 8 bits a value is its code times its block's scale."""
+        zeros = [torch.zeros(k.shape, dtype=torch.uint8, device=device).view(k.dtype) if k.dtype.itemsize == 1
+                 else torch.zeros(k.shape, dtype=k.dtype, device=device) for k in (self._m, self._v)]
+        scales = [torch.zeros(self._scales.shape, dtype=torch.uint8, device=device).view(self._scales.dtype)
+                  for _ in range(2)] if self.states != "f32" else [None, None]
+        return AdamWState(*zeros, *scales)
+
+    def offset(self, i):
+        """Where the moments of tensor i begin."""
+        return head_capi.adamw_state_offset(self.desc, i)
+
+    def _addresses(self, name, tensors, dtype, dev):
+        if len(tensors) != len(self.sizes):
+            raise ValueError(f"{len(tensors)} {name} for {len(self.sizes)} tensors")
+        for t, n in zip(tensors, self.sizes):
+            if t.dtype is not dtype or t.numel() != n or not t.is_contiguous() or t.get_device() != dev:
+                raise ValueError(f"{name} must be contiguous CUDA tensors of {dtype} and {n} elements, on the device of "
+                                 f"the state")
+        return [t.data_ptr() for t in tensors]
+
+    def __call__(self, params, grads, state, step, lr, copies=None, grad_scale=None, skip=None, seed=0, stream=None):
+        """Step number `step` (from 1 on).  step and lr are numbers, or tensors of one
+        element on the GPU (int64, fp32) that a captured call reads when it runs.
+        grad_scale and skip: None or such an fp32 tensor; unless skip holds zero,
+        nothing changes.  `seed` draws the roundings of 8-bit states."""
+        dev = state.m.get_device()
+        if stream is not None or dev < 0 or dev != _current_device():
+            with _place(dev, stream):
+                return self(params, grads, state, step, lr, copies, grad_scale, skip, seed)
+        self._m.check("state.m", state.m, dev)
+        self._v.check("state.v", state.v, dev)
+        ms = vs = 0
+        if self.states != "f32":
+            if state.m_scale is None or state.v_scale is None:
+                raise ValueError("8-bit moments need their scales")
+            self._scales.check("state.m_scale", state.m_scale, dev)
+            self._scales.check("state.v_scale", state.v_scale, dev)
+            ms, vs = state.m_scale.data_ptr(), state.v_scale.data_ptr()
+        p = self._addresses("params", params, torch.float32, dev)
+        g = self._addresses("grads", grads, self._grad, dev)
+        if (copies is None) != (self._copy is None):
+            raise ValueError("copies are given where the operator was made with a copy_dtype, and only there")
+        c = self._addresses("copies", copies, self._copy, dev) if copies is not None else None
+        if len(set(p)) != len(p) and len(set(a for a, n in zip(p, self.sizes) if n)) != sum(n > 0 for n in self.sizes):
+            raise ValueError("a tensor is among params twice")
+        at = []
+        for name, t, dtype in (("step", step, torch.int64), ("lr", lr, torch.float32),
+                               ("grad_scale", grad_scale, torch.float32), ("skip", skip, torch.float32)):
+            if isinstance(t, torch.Tensor):
+                if t.dtype is not dtype or t.numel() != 1 or t.get_device() != dev:
+                    raise ValueError(f"{name} must be a CUDA tensor of {dtype} and one element, on the device of the state")
+                at.append(t.data_ptr())
+            else:
+                at.append(0)
+        if (grad_scale is not None and not at[2]) or (skip is not None and not at[3]):
+            raise ValueError("grad_scale and skip are tensors or None")
+        head_capi.adamw_step(self.desc, p, g, c, state.m.data_ptr(), state.v.data_ptr(), ms, vs, 0 if at[0] else step,
+                             0.0 if at[1] else lr, *at, seed, _raw_stream(dev))
 
 
 def layer_norm(x, gamma=None, beta=None, eps=1e-5):

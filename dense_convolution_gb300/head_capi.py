@@ -13,12 +13,15 @@ from . import capi
 from .capi import DTYPES, _check
 
 REDUCTIONS = {"none": 0, "sum": 1, "mean": 2}
+ADAMW_STATES = {"f32": 0, "8bit": 1}
 
 EXPORTED = ("layernorm_desc_create", "layernorm_desc_set_row_strides", "layernorm_desc_set_planes",
             "layernorm_desc_destroy", "layernorm_workspace_size", "layernorm_fwd", "layernorm_bwd",
             "dropout_desc_create", "dropout_desc_set_row_strides", "dropout_desc_destroy", "dropout_fwd", "dropout_bwd",
             "linear_ce_desc_create", "linear_ce_desc_set_row_strides", "linear_ce_desc_set_piece",
-            "linear_ce_desc_set_dz_parts", "linear_ce_desc_destroy", "linear_ce_workspace_size", "linear_ce_fwd", "linear_ce_bwd")
+            "linear_ce_desc_set_dz_parts", "linear_ce_desc_destroy", "linear_ce_workspace_size", "linear_ce_fwd", "linear_ce_bwd",
+            "adamw_desc_create", "adamw_desc_set_rates", "adamw_desc_set_weight_decay", "adamw_desc_destroy",
+            "adamw_state_elements", "adamw_state_offset", "adamw_step")
 
 _lib = None
 
@@ -51,6 +54,14 @@ def load():
     L.linear_ce_workspace_size.argtypes = [vp, ctypes.POINTER(size), ctypes.POINTER(size)]
     L.linear_ce_fwd.argtypes = [vp] * 7 + [size, vp]
     L.linear_ce_bwd.argtypes = [vp] * 9 + [size, vp]
+    f32, f64 = ctypes.c_float, ctypes.c_double
+    L.adamw_desc_create.argtypes = [out, i64, ctypes.POINTER(i64), i32, i32, i32]
+    L.adamw_desc_set_rates.argtypes = [vp, f64, f64, f64]
+    L.adamw_desc_set_weight_decay.argtypes = [vp, ctypes.POINTER(f32)]
+    L.adamw_desc_destroy.argtypes = [vp]
+    L.adamw_state_elements.argtypes = [vp, ctypes.POINTER(i64)]
+    L.adamw_state_offset.argtypes = [vp, i64, ctypes.POINTER(i64)]
+    L.adamw_step.argtypes = [vp] * 8 + [i64, f32] + [vp] * 4 + [u64, vp]
     for f in EXPORTED:
         getattr(L, f).restype = i32
     _lib = L
@@ -164,3 +175,48 @@ def linear_ce_bwd(desc: int, h: int, w: int, target: int, lse: int, dloss: int, 
                   workspace_bytes: int, stream: int = 0):
     _check(load().linear_ce_bwd(desc, h, w, target, lse, dloss, dh,
                                 dw, workspace, workspace_bytes, stream), "linear_ce_bwd")
+
+
+def adamw_desc_create(sizes, grad_dtype="f32", states="f32", copy_dtype="f32") -> int:
+    """copy_dtype "f32": no copies."""
+    d, n = ctypes.c_void_p(), len(sizes)
+    kind = ADAMW_STATES[states] if isinstance(states, str) else int(states)
+    _check(load().adamw_desc_create(ctypes.byref(d), n, (ctypes.c_int64 * n)(*sizes), _dtype(grad_dtype), kind,
+                                    _dtype(copy_dtype)), "adamw_desc_create")
+    return d.value
+
+
+def adamw_desc_set_rates(desc: int, beta1: float, beta2: float, eps: float):
+    _check(load().adamw_desc_set_rates(desc, beta1, beta2, eps), "adamw_desc_set_rates")
+
+
+def adamw_desc_set_weight_decay(desc: int, decay):
+    """One value a tensor of the descriptor."""
+    _check(load().adamw_desc_set_weight_decay(desc, (ctypes.c_float * len(decay))(*decay)), "adamw_desc_set_weight_decay")
+
+
+def adamw_desc_destroy(desc: int):
+    _check(load().adamw_desc_destroy(desc), "adamw_desc_destroy")
+
+
+def adamw_state_elements(desc: int) -> int:
+    n = ctypes.c_int64()
+    _check(load().adamw_state_elements(desc, ctypes.byref(n)), "adamw_state_elements")
+    return n.value
+
+
+def adamw_state_offset(desc: int, i: int) -> int:
+    n = ctypes.c_int64()
+    _check(load().adamw_state_offset(desc, i, ctypes.byref(n)), "adamw_state_offset")
+    return n.value
+
+
+def adamw_step(desc: int, params, grads, copies, m: int, v: int, m_scale: int = 0, v_scale: int = 0, step: int = 1,
+               lr: float = 1e-3, device_step: int = 0, device_lr: int = 0, grad_scale: int = 0, skip: int = 0,
+               seed: int = 0, stream: int = 0):
+    """params, grads and copies (or None): lists of a device address for each tensor of the descriptor."""
+    row = ctypes.c_void_p * len(params)
+    s = load().adamw_step(desc, row(*params), row(*grads), row(*copies) if copies is not None else None, m, v, m_scale,
+                          v_scale, step, lr, device_step, device_lr, grad_scale, skip, seed, stream)
+    if s:
+        _check(s, "adamw_step")

@@ -1,8 +1,9 @@
 /*
  * head.h — C ABI of the training-head operators of the GB300 (sm_103a)
  * convolution library: layer norm, dropout and linear cross entropy, forward
- * and backward.  They take a convolution's output (include/conv2d.h) from
- * feature planes to a loss over a vocabulary and its gradients.
+ * and backward, and AdamW.  They take a convolution's output (include/conv2d.h)
+ * from feature planes to a loss over a vocabulary, its gradients and the next
+ * weights.
  *
  * Conventions are those of conv2d.h: every function returns a conv2d_status
  * and lets no C++ exception out; device pointers belong to the caller; nothing
@@ -31,6 +32,7 @@ extern "C" {
 typedef struct layernorm_desc *layernorm_desc_t;
 typedef struct dropout_desc *dropout_desc_t;
 typedef struct linear_ce_desc *linear_ce_desc_t;
+typedef struct adamw_desc *adamw_desc_t;
 
 /* ---------------------------------------------------------------- layer norm
  * Over each of `rows` rows of `cols` elements:
@@ -192,6 +194,68 @@ conv2d_status linear_ce_fwd(linear_ce_desc_t d, const void *h, const void *w, co
 conv2d_status linear_ce_bwd(linear_ce_desc_t d, const void *h, const void *w, const int64_t *target, const float *lse,
                             const float *dloss, void *dh, void *dw, void *workspace, size_t workspace_bytes,
                             void *stream);
+
+/* --------------------------------------------------------------------- AdamW
+ * A step of `count` tensors at once, in place.  With g the gradient times
+ * *grad_scale, for each element:
+ *   m = b1 m + (1 - b1) g,  v = b2 v + (1 - b2) g^2,
+ *   p = p (1 - lr decay) - lr / (1 - b1^t) m / (sqrt(v) / sqrt(1 - b2^t) + eps),
+ * t the step's number, from 1 on; the copy (fp16 or bf16) is p rounded.  The
+ * parameters are fp32.  The moments of all tensors lie one tensor after the
+ * other in one buffer each, every tensor's in whole blocks of 256
+ * (adamw_state_offset); zero in all their bytes before the first step.
+ * In 8 bits a block's values are its codes (m e4m3, v e5m2, as of the OCP 8-bit
+ * formats) times its scale 2^(byte - 127): the scale takes the largest value to
+ * the type's top binade, at most 1.75 there, and each value goes to one of its
+ * neighbours, up where the bits that are left over and 16 random bits of the
+ * same weight make a carry; v above zero is never stored as zero.  The random
+ * bits of element i of tensor k in step t are the halves (low: m, high: v) of
+ * word i mod 4 of Philox4x32-10 under key = seed and counter = (i div 4, k,
+ * t mod 2^32, t div 2^32).  p takes the moments before they are rounded.  A block
+ * with an infinity or a NaN gets the scale 255: all its values are NaN from
+ * the next step on. */
+
+typedef enum { ADAMW_STATES_F32 = 0, ADAMW_STATES_8BIT = 1 } adamw_states;
+
+/* Create a descriptor of `count` tensors of sizes[i] elements.
+ *   0 <= count <= 2^24, 0 <= sizes[i] <= 2^34, fewer than 2^40 together
+ *   grad_dtype   of all gradients
+ *   copy_dtype   of all copies: CONV2D_F16 or CONV2D_BF16; CONV2D_F32: no copies
+ * b1 = 0.9, b2 = 0.999, eps = 1e-8 and no decay until set.
+ * Errors: NULL_PTR, BAD_PARAM. */
+conv2d_status adamw_desc_create(adamw_desc_t *out, int64_t count, const int64_t *sizes, conv2d_dtype grad_dtype,
+                                adamw_states states, conv2d_dtype copy_dtype);
+
+/* 0 <= beta1, beta2 < 1 and eps > 0 (as fp32).  Errors: NULL_PTR, BAD_PARAM. */
+conv2d_status adamw_desc_set_rates(adamw_desc_t d, double beta1, double beta2, double eps);
+
+/* The decay of each tensor (count values, finite).  Errors: NULL_PTR, BAD_PARAM. */
+conv2d_status adamw_desc_set_weight_decay(adamw_desc_t d, const float *decay);
+
+conv2d_status adamw_desc_destroy(adamw_desc_t d);
+
+/* Elements of each moment's buffer (a multiple of 256; the scales are one byte
+ * for each 256), and the first one of tensor i. */
+conv2d_status adamw_state_elements(adamw_desc_t d, int64_t *elements);
+conv2d_status adamw_state_offset(adamw_desc_t d, int64_t i, int64_t *offset);
+
+/* One step.
+ *   params, grads, copies   host arrays of `count` device addresses (read before
+ *                the call returns; those of empty tensors are ignored); copies is
+ *                NULL where the descriptor has none.  Elements are adjacent and
+ *                need only their own alignment (32-byte aligned ones, 16 of
+ *                16-bit types, run fastest).  No two tensors overlap.
+ *   m, v         the moments, 32-byte aligned; m_scale, v_scale theirs in 8 bits (else ignored)
+ *   step, lr     t >= 1 and a finite rate, unless the device holds them:
+ *   device_step, device_lr   NULL, or addresses that the step reads instead, so
+ *                that a captured call goes on where the program sets them
+ *   grad_scale   NULL, or the address of the factor of all gradients
+ *   skip         NULL, or the address of a float: unless it is 0, nothing changes
+ * Errors: NULL_PTR, BAD_PARAM, MISALIGNED, CUDA. */
+conv2d_status adamw_step(adamw_desc_t d, float *const *params, const void *const *grads, void *const *copies, void *m,
+                         void *v, void *m_scale, void *v_scale, int64_t step, float lr, const int64_t *device_step,
+                         const float *device_lr, const float *grad_scale, const float *skip, uint64_t seed,
+                         void *stream);
 
 #ifdef __cplusplus
 }

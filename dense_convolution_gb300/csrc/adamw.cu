@@ -87,49 +87,62 @@ template <typename T> __device__ __forceinline__ void load8(const T* p, float (&
     widen(*reinterpret_cast<const Vec<T, 8>*>(p), f);
 }
 
-// Eight values in 8 bits, their block's scale 2^(byte - 127): DIGITS bits of the
-// significand after the leading one, the type's smallest normal value 2^LOW.
-template <int DIGITS> __device__ __forceinline__ void from8(uint2 c, uint32_t byte, float (&f)[8]) {
-    constexpr int kBias = DIGITS == 3 ? 7 : 15, kLow = 1 - kBias;
-    // (255 is not a number, 2^-127 not a normal one.)
-    const float scale = __uint_as_float(byte == 255u ? 0x7fffffffu : byte ? byte << 23 : 0x00400000u);
+// Eight values of 8 bits.  An e5m2 code is the high byte of an fp16 value; an e4m3 one,
+// its magnitude moved down by a bit, that of 2^-8 times its own, subnormal values
+// included.  (Conversions from integers run at an eighth of the rate.)
+template <bool E4M3> __device__ __forceinline__ void from8(uint2 c, uint32_t byte, float (&f)[8]) {
+    // The scale 2^(byte - 127): 255 is not a number, 2^-127 no normal value (but 2^-119 is).
+    const uint32_t b = byte + (E4M3 ? 8u : 0u);
+    const float scale = __uint_as_float(byte == 255u ? 0x7fffffffu : b ? b << 23 : 0x00400000u);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t b = (i < 4 ? c.x : c.y) >> (i % 4 * 8), mag = b & 0x7fu;
-        // A code of the lowest binade counts steps of 2^(LOW - DIGITS); of the others, the bits are a float's.
-        const float normal = __uint_as_float((mag << (23 - DIGITS)) + ((127u - kBias) << 23));
-        const float small = (float)mag * __uint_as_float((uint32_t)(127 + kLow - DIGITS) << 23);
-        const float v = mag < (1u << DIGITS) ? small : normal;
-        f[i] = __uint_as_float(__float_as_uint(v * scale) | (b & 0x80u) << 24);
+    for (int i = 0; i < 4; ++i) {
+        uint32_t h = __byte_perm(i < 2 ? c.x : c.y, 0u, i & 1 ? 0x3424 : 0x1404);      // each code in a high byte
+        if (E4M3) h = (h & 0x80008000u) | (h >> 1 & 0x3f803f80u);
+        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        f[2 * i] = v.x * scale;
+        f[2 * i + 1] = v.y * scale;
     }
 }
 
-// The same back.  `most`: the bits of the block's largest magnitude.  KEEP (v): the
-// high halves of the numbers r are its noise, and what is above zero stays there.
-template <int DIGITS, bool KEEP> __device__ __forceinline__ uint2 to8(const float (&f)[8], uint32_t most,
-                                                                     const uint32_t (&r)[8], uint32_t& byte) {
-    constexpr int kBias = DIGITS == 3 ? 7 : 15, kLow = 1 - kBias, kTop = DIGITS == 3 ? 8 : 15, kDrop = 23 - DIGITS;
+// The same back, DIGITS bits of the significand after the leading one.  `most`: the
+// bits of the block's largest magnitude.  r: the elements' numbers, whose low (m) or
+// high (v) half is the noise.  Below the lowest normal value, 2^LOW, that value is added: the
+// bits then count the steps of the subnormal values (the sum is cut, not rounded).
+template <bool E4M3> __device__ __forceinline__ uint2 to8(const float (&f)[8], uint32_t most, const uint32_t (&r)[8],
+                                                          uint32_t& byte) {
+    constexpr int kDigits = E4M3 ? 3 : 2, kLow = E4M3 ? -6 : -14, kTop = E4M3 ? 8 : 15, kDrop = 23 - kDigits;
+    constexpr uint32_t kBase = (uint32_t)(kLow + 126) << kDigits;
+    const float least = __uint_as_float((uint32_t)(127 + kLow) << 23);
     // One binade more where the largest is above 1.75 of its own: what rounding up
     // makes of it still fits.
     const int exponent = (int)((most + (1u << 21) - 1u) >> 23) - 127;
     const int scale = max(exponent - kTop, -127);
     byte = most >= 0x7f800000u ? 255u : (uint32_t)(scale + 127);
     const float up = __uint_as_float((uint32_t)(127 - scale) << 23);
-    uint32_t c[2] = {0u, 0u};
-    if (byte != 255u) {
+    uint32_t code[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t noise = KEEP ? r[i] >> 16 : r[i] & 0xffffu;
-            const float y = fabsf(f[i]) * up;
-            const uint32_t normal = ((__float_as_uint(y) + (noise << (kDrop - 16))) >> kDrop) - ((kLow + 126) << DIGITS);
-            const uint32_t small = (__float2uint_rz(y * __uint_as_float((uint32_t)(127 + DIGITS - kLow + 16) << 23)) + noise) >> 16;
-            uint32_t code = y < __uint_as_float((uint32_t)(127 + kLow) << 23) ? small : normal;
-            if (KEEP && y > 0.f) code = max(code, 1u);
-            code |= __float_as_uint(f[i]) >> 24 & 0x80u;
-            c[i / 4] |= code << (i % 4 * 8);
-        }
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t noise = E4M3 ? (r[i] & 0xffffu) << (kDrop - 16) : r[i] >> 16 << (kDrop - 16);
+        const float y = fabsf(f[i]) * up;
+        const bool small = y < least;
+        const uint32_t bits = __float_as_uint(small ? __fadd_rz(y, least) : y);
+        code[i] = ((bits + noise) >> kDrop) - (small ? kBase + (1u << kDigits) : kBase);
+        if (E4M3) code[i] |= __float_as_uint(f[i]) >> 24 & 0x80u;
+        else code[i] = max(code[i], min(__float_as_uint(y), 1u));      // v: above zero stays above zero
     }
-    return make_uint2(c[0], c[1]);
+    if (byte == 255u) return make_uint2(0u, 0u);
+    const auto four = [&](int i) {
+        return __byte_perm(__byte_perm(code[i], code[i + 1], 0x0040), __byte_perm(code[i + 2], code[i + 3], 0x0040), 0x5410);
+    };
+    return make_uint2(four(0), four(4));
+}
+
+// The root and the quotient of a step's update: off by 2^-23 each at most, a few
+// hundredths of what p's own rounding is of lr times it.
+__device__ __forceinline__ float root(float x) {
+    float y;
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 template <typename G, bool EIGHT, int N>
@@ -201,8 +214,8 @@ __global__ void __launch_bounds__(32 * kWarps) adamw_kernel(const __grid_constan
         for (int i = 0; i < 8; ++i) fg[i] *= k;
     }
     if constexpr (EIGHT) {
-        from8<3>(cm, bm, fm);
-        from8<2>(cv, bv, fv);
+        from8<true>(cm, bm, fm);
+        from8<false>(cv, bv, fv);
     }
     if (!whole) {                                          // past the end: zero, whatever lies there
 #pragma unroll
@@ -218,7 +231,7 @@ __global__ void __launch_bounds__(32 * kWarps) adamw_kernel(const __grid_constan
         fv[i] = __fadd_rn(__fmul_rn(s.b2, fv[i]), __fmul_rn(__fmul_rn(s.a2, fg[i]), fg[i]));
         top_m = max(top_m, __float_as_uint(fm[i]) & 0x7fffffffu);
         top_v = max(top_v, __float_as_uint(fv[i]) & 0x7fffffffu);
-        fp[i] = fmaf(-up, fm[i] / fmaf(sqrtf(fv[i]), rc2, s.eps), fp[i] * shrink);
+        fp[i] = fmaf(-up, __fdividef(fm[i], fmaf(root(fv[i]), rc2, s.eps)), fp[i] * shrink);
     }
     if (whole) {
         store8(p + i0, fp);
@@ -251,8 +264,8 @@ __global__ void __launch_bounds__(32 * kWarps) adamw_kernel(const __grid_constan
 #pragma unroll
             for (int i = 0; i < 4; ++i) r[4 * k + i] = c[i];
         }
-        cm = to8<3, false>(fm, __reduce_max_sync(0xffffffffu, top_m), r, bm);
-        cv = to8<2, true>(fv, __reduce_max_sync(0xffffffffu, top_v), r, bv);
+        cm = to8<true>(fm, __reduce_max_sync(0xffffffffu, top_m), r, bm);
+        cv = to8<false>(fv, __reduce_max_sync(0xffffffffu, top_v), r, bv);
         reinterpret_cast<uint2*>(static_cast<uint8_t*>(s.m) + at)[lane] = cm;
         reinterpret_cast<uint2*>(static_cast<uint8_t*>(s.v) + at)[lane] = cv;
         if (lane == 0) {

@@ -14,6 +14,7 @@ belong to that stream.  No call records an autograd graph: gradients come from
 from __future__ import annotations
 
 import collections
+import operator
 
 import torch
 
@@ -23,6 +24,7 @@ from .conv import _NAME, _TORCH_DTYPE
 
 _raw_stream = torch._C._cuda_getCurrentRawStream      # the current stream's handle by device index
 _current_device = torch._C._cuda_getDevice
+_dtype_of = operator.attrgetter("dtype")
 
 
 def _ptr(t):
@@ -350,11 +352,13 @@ class AdamW(_Op):
     def _addresses(self, name, tensors, dtype, dev):
         if len(tensors) != len(self.sizes):
             raise ValueError(f"{len(tensors)} {name} for {len(self.sizes)} tensors")
-        for t, n in zip(tensors, self.sizes):
-            if t.dtype is not dtype or t.numel() != n or not t.is_contiguous() or t.get_device() != dev:
-                raise ValueError(f"{name} must be contiguous CUDA tensors of {dtype} and {n} elements, on the device of "
-                                 f"the state")
-        return [t.data_ptr() for t in tensors]
+        # (A method at a time over all tensors: a loop over tensors takes a third longer.)
+        if tuple(map(torch.Tensor.numel, tensors)) != self.sizes or not all(map(torch.Tensor.is_contiguous, tensors)) \
+                or (set(map(torch.Tensor.get_device, tensors)) | {dev}) != {dev} \
+                or (set(map(_dtype_of, tensors)) | {dtype}) != {dtype}:
+            raise ValueError(f"{name} must be contiguous CUDA tensors of {dtype} and of the operator's sizes, on the "
+                             f"device of the state")
+        return list(map(torch.Tensor.data_ptr, tensors))
 
     def __call__(self, params, grads, state, step, lr, copies=None, grad_scale=None, skip=None, seed=0, stream=None):
         """Step number `step` (from 1 on).  step and lr are numbers, or tensors of one

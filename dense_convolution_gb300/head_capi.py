@@ -7,6 +7,7 @@ pointers (device addresses) and streams as plain integers, 0 for none (NULL).
 """
 from __future__ import annotations
 
+import array
 import ctypes
 
 from . import capi
@@ -215,8 +216,8 @@ def adamw_step(desc: int, params, grads, copies, m: int, v: int, m_scale: int = 
                lr: float = 1e-3, device_step: int = 0, device_lr: int = 0, grad_scale: int = 0, skip: int = 0,
                seed: int = 0, stream: int = 0):
     """params, grads and copies (or None): lists of a device address for each tensor of the descriptor."""
-    row = ctypes.c_void_p * len(params)
-    s = load().adamw_step(desc, row(*params), row(*grads), row(*copies) if copies is not None else None, m, v, m_scale,
-                          v_scale, step, lr, device_step, device_lr, grad_scale, skip, seed, stream)
+    rows = [array.array("Q", r) if r is not None else None for r in (params, grads, copies)]
+    s = load().adamw_step(desc, *(r.buffer_info()[0] if r is not None else 0 for r in rows), m, v, m_scale, v_scale, step,
+                          lr, device_step, device_lr, grad_scale, skip, seed, stream)
     if s:
         _check(s, "adamw_step")

@@ -36,7 +36,10 @@ namespace conv2d_gb300 {
 namespace {
 
 constexpr int kBlock = 256, kLane = 8;                 // elements of a warp and of a lane
-constexpr int kWarps = 8;                              // a block of threads takes kWarps * 256 elements
+// Warps of a block of threads, each with 256 elements at a time; 8 bits: blocks that a warp has on their way or at work.
+template <bool EIGHT> __host__ __device__ constexpr int warps() { return EIGHT ? 4 : 8; }
+constexpr int kSlots = 3;
+template <typename G> __host__ __device__ constexpr int slot_bytes() { return kBlock * (4 + (int)sizeof(G) + 2); }
 constexpr int kFew = 24, kMany = 700;                  // tensors a launch: 1 KB and 31 KB of parameters
 
 struct AdamTensor {
@@ -62,6 +65,7 @@ struct AdamStep {
     uint32_t k0, k1;
     uint32_t first_tensor;   // number of the launch's first tensor
     int copy_bf16, count;
+    int span;                // blocks of 256 that a warp takes
 };
 
 template <int N> struct AdamTable {
@@ -86,6 +90,15 @@ __device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
 template <typename T> __device__ __forceinline__ void load8(const T* p, float (&f)[8]) {
     widen(*reinterpret_cast<const Vec<T, 8>*>(p), f);
 }
+
+// N bytes to shared memory, behind this thread's back.
+template <int N> __device__ __forceinline__ void copy_async(uint32_t to, const void* from) {
+    if constexpr (N == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(N) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the last N groups have landed.
+template <int N> __device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // Eight values of 8 bits.  An e5m2 code is the high byte of an fp16 value; an e4m3 one,
 // its magnitude moved down by a bit, that of 2^-8 times its own, subnormal values
@@ -126,7 +139,7 @@ template <bool E4M3> __device__ __forceinline__ uint2 to8(const float (&f)[8], u
         const float y = fabsf(f[i]) * up;
         const bool small = y < least;
         const uint32_t bits = __float_as_uint(small ? __fadd_rz(y, least) : y);
-        code[i] = ((bits + noise) >> kDrop) - (small ? kBase + (1u << kDigits) : kBase);
+        code[i] = (bits + noise - (small ? (kBase << kDrop) + (1u << 23) : kBase << kDrop)) >> kDrop;
         if (E4M3) code[i] |= __float_as_uint(f[i]) >> 24 & 0x80u;
         else code[i] = max(code[i], min(__float_as_uint(y), 1u));      // v: above zero stays above zero
     }
@@ -137,18 +150,21 @@ template <bool E4M3> __device__ __forceinline__ uint2 to8(const float (&f)[8], u
     return make_uint2(four(0), four(4));
 }
 
-// The root and the quotient of a step's update: off by 2^-23 each at most, a few
-// hundredths of what p's own rounding is of lr times it.
-__device__ __forceinline__ float root(float x) {
-    float y;
-    asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
+// m / (sqrt(v) k + eps), the root and the reciprocal off by 2^-23 each at most: a few hundredths of what
+// p's own rounding is of lr times it.  They take no subnormal numbers: v below 2^-126 counts as that.
+__device__ __forceinline__ float update(float m, float v, float k, float eps) {
+    float root, inverse;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(root) : "f"(fmaxf(v, 0x1p-126f)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inverse) : "f"(fmaf(root, k, eps)));
+    return m * inverse;
 }
 
 template <typename G, bool EIGHT, int N>
-__global__ void __launch_bounds__(32 * kWarps) adamw_kernel(const __grid_constant__ AdamTable<N> table,
+__global__ void __launch_bounds__(32 * warps<EIGHT>(), EIGHT ? 7 : 4) adamw_kernel(const __grid_constant__ AdamTable<N> table,
                                                             const __grid_constant__ AdamStep s) {
-    __shared__ float stage[kWarps][kBlock + kBlock / 8];
+    constexpr int kWarps = warps<EIGHT>();
+    // A warp's blocks on their way (8 bits), or one block of a tensor's elements on their way between the lanes.
+    __shared__ __align__(16) float stage[kWarps][(EIGHT ? kSlots * slot_bytes<G>() : (kBlock + kBlock / 8) * 4) / 4];
     // The last tensor whose first block is not past this one.
     int lo = 0, hi = s.count;
     while (hi - lo > 1) {
@@ -156,50 +172,13 @@ __global__ void __launch_bounds__(32 * kWarps) adamw_kernel(const __grid_constan
         if (table.first[mid] <= blockIdx.x) lo = mid;
         else hi = mid;
     }
-    const AdamTensor& t = table.t[lo];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t block = (int64_t)(blockIdx.x - table.first[lo]) * kWarps + warp, e0 = block * kBlock;
-    pdl_wait();
-    if (e0 >= t.n || (s.skip && *s.skip != 0.f)) return;
-    const int64_t at = (int64_t)t.state * kBlock + e0;     // in the moments
-    const int left = (int)min((int64_t)kBlock, t.n - e0);
-    float* p = t.p + e0;
-    const G* g = static_cast<const G*>(t.g) + e0;
-    uint16_t* copy = t.copy ? static_cast<uint16_t*>(t.copy) + e0 : nullptr;
-    const bool whole = left == kBlock && (reinterpret_cast<uintptr_t>(p) & 31u) == 0 &&
-                       (reinterpret_cast<uintptr_t>(g) & (sizeof(G) * 8 - 1)) == 0 &&
-                       (reinterpret_cast<uintptr_t>(copy) & 15u) == 0;
-    const int i0 = lane * kLane;
-    float fp[8], fg[8], fm[8], fv[8];
+    const AdamTensor t = table.t[lo];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, i0 = lane * kLane;
     // An element's place in the stage: eight in a row, then one to spare.
     float* const row = stage[warp];
     const auto place = [](int e) { return e + (e >> 3); };
-    if (whole) {
-        load8(p + i0, fp);
-        load8(g + i0, fg);
-    }
-    uint2 cm, cv;
-    uint32_t bm = 0, bv = 0;
-    if constexpr (EIGHT) {
-        cm = reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(s.m) + at)[lane];
-        cv = reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(s.v) + at)[lane];
-        bm = s.ms[at / kBlock];
-        bv = s.vs[at / kBlock];
-    } else {
-        load8(static_cast<const float*>(s.m) + at + i0, fm);
-        load8(static_cast<const float*>(s.v) + at + i0, fv);
-    }
-    if (!whole) {
-        for (int e = lane; e < kBlock; e += 32) row[place(e)] = e < left ? p[e] : 0.f;
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) fp[i] = row[place(i0 + i)];
-        __syncwarp();
-        for (int e = lane; e < kBlock; e += 32) row[place(e)] = e < left ? to_f32(g[e]) : 0.f;
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) fg[i] = row[place(i0 + i)];
-    }
+    pdl_wait();
+    if (s.skip && *s.skip != 0.f) return;
     int64_t step = s.step;
     float c1 = s.c1, rc2 = s.rc2;
     if (s.step_at) {
@@ -208,111 +187,214 @@ __global__ void __launch_bounds__(32 * kWarps) adamw_kernel(const __grid_constan
         rc2 = 1.f / sqrtf(-expm1f((float)step * s.log_b2));
     }
     const float lr = s.lr_at ? *s.lr_at : s.lr, up = lr / c1, shrink = fmaf(-lr, t.decay, 1.f);
-    if (s.scale) {
-        const float k = *s.scale;
+    const float k = s.scale ? *s.scale : 1.f;
+    int64_t e0 = ((int64_t)(blockIdx.x - table.first[lo]) * s.span * kWarps + warp) * kBlock;
+    const bool aligned = (reinterpret_cast<uintptr_t>(t.p) & 31u) == 0 &&
+                         (reinterpret_cast<uintptr_t>(t.g) & (sizeof(G) * 8 - 1)) == 0 &&
+                         (reinterpret_cast<uintptr_t>(t.copy) & 15u) == 0;
+    const auto is_whole = [&](int64_t e) { return aligned && e + kBlock <= t.n; };
+    // In 8 bits a warp has more arithmetic than its own loads can hide: the next two whole blocks are on their way
+    // to shared memory meanwhile, every lane's own values in its own places.
+    constexpr uint32_t kG = kBlock * 4, kM = kG + kBlock * sizeof(G), kV = kM + kBlock;      // p, g, m, v in a slot
+    const auto slot = [&](int j) { return reinterpret_cast<uint8_t*>(row) + j % kSlots * slot_bytes<G>(); };
+    const auto fetch = [&](int j) {
+        const int64_t e = e0 + (int64_t)j * kWarps * kBlock;
+        if (j < s.span && is_whole(e)) {
+            const uint32_t to = smem_addr(slot(j)) + 16 * lane;
+            const int64_t at = (int64_t)t.state * kBlock + e;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) fg[i] *= k;
-    }
+            for (int h = 0; h < 2; ++h) copy_async<16>(to + 512 * h, t.p + e + i0 + 4 * h);
+#pragma unroll
+            for (int h = 0; h < (int)sizeof(G) / 2; ++h)
+                copy_async<16>(to + kG + 512 * h, static_cast<const G*>(t.g) + e + i0 + 4 * h);
+            copy_async<8>(to + kM - 8 * lane, static_cast<const uint8_t*>(s.m) + at + i0);
+            copy_async<8>(to + kV - 8 * lane, static_cast<const uint8_t*>(s.v) + at + i0);
+        }
+        copy_async_commit();
+    };
+    uint32_t scales_m = 0, scales_v = 0;                   // lane j's: those of the warp's block j
     if constexpr (EIGHT) {
-        from8<true>(cm, bm, fm);
-        from8<false>(cv, bv, fv);
+        fetch(0);
+        fetch(1);
+        const int64_t at = (int64_t)t.state + e0 / kBlock + lane * kWarps;
+        if (lane < s.span && e0 + (int64_t)lane * kWarps * kBlock < t.n) {
+            scales_m = s.ms[at];
+            scales_v = s.vs[at];
+        }
     }
-    if (!whole) {                                          // past the end: zero, whatever lies there
+    const int64_t first = e0;
+#pragma unroll 1
+    for (int j = 0; j < (EIGHT ? s.span : 1); ++j) {
+        const int64_t e0 = first + (int64_t)j * kWarps * kBlock;
+        if (e0 >= t.n) break;
+        const int64_t at = (int64_t)t.state * kBlock + e0;     // in the moments
+        const int left = (int)min((int64_t)kBlock, t.n - e0);
+        float* p = t.p + e0;
+        const G* g = static_cast<const G*>(t.g) + e0;
+        uint16_t* copy = t.copy ? static_cast<uint16_t*>(t.copy) + e0 : nullptr;
+        const bool whole = is_whole(e0);
+        float fp[8], fg[8], fm[8], fv[8];
+        uint32_t bm = 0, bv = 0;
+        if constexpr (EIGHT) {
+            bm = __shfl_sync(0xffffffffu, scales_m, j);
+            bv = __shfl_sync(0xffffffffu, scales_v, j);
+            uint2 cm, cv;
+            if (whole) {
+                copy_async_wait<1>();
+                const uint8_t* at = slot(j);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i0 + i >= left) fm[i] = fv[i] = 0.f;
-    }
-    uint32_t top_m = 0, top_v = 0;
+                for (int h = 0; h < 2; ++h) widen(reinterpret_cast<const Vec<float, 4>*>(at + 512 * h)[lane], *reinterpret_cast<float(*)[4]>(fp + 4 * h));
+                if constexpr (sizeof(G) == 4) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        // Each product and sum rounds by itself: the 8-bit codes are then a matter of the formula alone, not of which of
-        // them a compiler joins.
-        fm[i] = __fadd_rn(__fmul_rn(s.b1, fm[i]), __fmul_rn(s.a1, fg[i]));
-        fv[i] = __fadd_rn(__fmul_rn(s.b2, fv[i]), __fmul_rn(__fmul_rn(s.a2, fg[i]), fg[i]));
-        top_m = max(top_m, __float_as_uint(fm[i]) & 0x7fffffffu);
-        top_v = max(top_v, __float_as_uint(fv[i]) & 0x7fffffffu);
-        fp[i] = fmaf(-up, __fdividef(fm[i], fmaf(root(fv[i]), rc2, s.eps)), fp[i] * shrink);
-    }
-    if (whole) {
-        store8(p + i0, fp);
-        if (copy) {
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const f32x2 two = pack2f(fp[2 * i], fp[2 * i + 1]);
-                w[i] = s.copy_bf16 ? narrow_pair<__nv_bfloat16>(two) : narrow_pair<__half>(two);
+                    for (int h = 0; h < 2; ++h) widen(reinterpret_cast<const Vec<float, 4>*>(at + kG + 512 * h)[lane], *reinterpret_cast<float(*)[4]>(fg + 4 * h));
+                } else {
+                    widen(reinterpret_cast<const Vec<G, 8>*>(at + kG)[lane], fg);
+                }
+                cm = reinterpret_cast<const uint2*>(at + kM)[lane];
+                cv = reinterpret_cast<const uint2*>(at + kV)[lane];
+                fetch(j + 2);                              // (where block j - 1 was)
+            } else {
+                cm = reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(s.m) + at)[lane];
+                cv = reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(s.v) + at)[lane];
             }
-            *reinterpret_cast<uint4*>(copy + i0) = make_uint4(w[0], w[1], w[2], w[3]);
+            from8<true>(cm, bm, fm);
+            from8<false>(cv, bv, fv);
+        } else {
+            if (whole) {
+                load8(p + i0, fp);
+                load8(g + i0, fg);
+            }
+            load8(static_cast<const float*>(s.m) + at + i0, fm);
+            load8(static_cast<const float*>(s.v) + at + i0, fv);
         }
-    } else {
-        __syncwarp();
+        const uint32_t nan_m = EIGHT && bm == 255u ? 0x7fffffffu : 0u;
+        if (!whole) {
+            __syncwarp();
+            for (int e = lane; e < kBlock; e += 32) row[place(e)] = e < left ? p[e] : 0.f;
+            __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) row[place(i0 + i)] = fp[i];
-        __syncwarp();
-        for (int e = lane; e < left; e += 32) {
-            const float f = row[place(e)];
-            p[e] = f;
-            if (copy) store_param(copy, false, s.copy_bf16, e, f);
+            for (int i = 0; i < 8; ++i) fp[i] = row[place(i0 + i)];
+            __syncwarp();
+            for (int e = lane; e < kBlock; e += 32) row[place(e)] = e < left ? to_f32(g[e]) : 0.f;
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) fg[i] = row[place(i0 + i)];
+        }
+        if (s.scale) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) fg[i] *= k;
+        }
+        if (!whole) {                                          // past the end: zero, whatever lies there
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i0 + i >= left) fm[i] = fv[i] = 0.f;
+        }
+        float top_m = 0.f;
+        uint32_t top_v = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            // Each product and sum rounds by itself: the 8-bit codes are then a matter of the formula alone, not of which of
+            // them a compiler joins.
+            fm[i] = __fadd_rn(__fmul_rn(s.b1, fm[i]), __fmul_rn(s.a1, fg[i]));
+            fv[i] = __fadd_rn(__fmul_rn(s.b2, fv[i]), __fmul_rn(__fmul_rn(s.a2, fg[i]), fg[i]));
+            top_m = fmaxf(top_m, fabsf(fm[i]));
+            top_v = max(top_v, __float_as_uint(fv[i]));
+            fp[i] = fmaf(-up, update(fm[i], fv[i], rc2, s.eps), fp[i] * shrink);
+        }
+        if (whole) {
+            store8(p + i0, fp);
+            if (copy) {
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const f32x2 two = pack2f(fp[2 * i], fp[2 * i + 1]);
+                    w[i] = s.copy_bf16 ? narrow_pair<__nv_bfloat16>(two) : narrow_pair<__half>(two);
+                }
+                *reinterpret_cast<uint4*>(copy + i0) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        } else {
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) row[place(i0 + i)] = fp[i];
+            __syncwarp();
+            for (int e = lane; e < left; e += 32) {
+                const float f = row[place(e)];
+                p[e] = f;
+                if (copy) store_param(copy, false, s.copy_bf16, e, f);
+            }
+        }
+        if constexpr (EIGHT) {
+            uint32_t r[8];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                uint32_t c[4] = {(uint32_t)(e0 / 4) + 2 * lane + k, s.first_tensor + lo, (uint32_t)step, (uint32_t)((uint64_t)step >> 32)};
+                philox(c, s.k0, s.k1);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) r[4 * k + i] = c[i];
+            }
+            // A NaN, which the maximum of floats passes over, is in m only where it was, or where one in g makes v's.
+            top_v = __reduce_max_sync(0xffffffffu, top_v);
+            const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(top_m));
+            const uint2 cm = to8<true>(fm, top_v > 0x7f800000u ? top_v : max(most, nan_m), r, bm);
+            const uint2 cv = to8<false>(fv, top_v, r, bv);
+            reinterpret_cast<uint2*>(static_cast<uint8_t*>(s.m) + at)[lane] = cm;
+            reinterpret_cast<uint2*>(static_cast<uint8_t*>(s.v) + at)[lane] = cv;
+            if (lane == 0) {
+                s.ms[at / kBlock] = (uint8_t)bm;
+                s.vs[at / kBlock] = (uint8_t)bv;
+            }
+        } else {
+            store8(static_cast<float*>(s.m) + at + i0, fm);
+            store8(static_cast<float*>(s.v) + at + i0, fv);
         }
     }
-    if constexpr (EIGHT) {
-        uint32_t r[8];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            uint32_t c[4] = {(uint32_t)(e0 / 4) + 2 * lane + k, s.first_tensor + lo, (uint32_t)step, (uint32_t)((uint64_t)step >> 32)};
-            philox(c, s.k0, s.k1);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) r[4 * k + i] = c[i];
-        }
-        cm = to8<true>(fm, __reduce_max_sync(0xffffffffu, top_m), r, bm);
-        cv = to8<false>(fv, __reduce_max_sync(0xffffffffu, top_v), r, bv);
-        reinterpret_cast<uint2*>(static_cast<uint8_t*>(s.m) + at)[lane] = cm;
-        reinterpret_cast<uint2*>(static_cast<uint8_t*>(s.v) + at)[lane] = cv;
-        if (lane == 0) {
-            s.ms[at / kBlock] = (uint8_t)bm;
-            s.vs[at / kBlock] = (uint8_t)bv;
-        }
-    } else {
-        store8(static_cast<float*>(s.m) + at + i0, fm);
-        store8(static_cast<float*>(s.v) + at + i0, fv);
-    }
+}
+
+// Blocks of 256 that a warp takes one after the other (at most 32: a lane keeps the scales of one).
+int span_of(const adamw_desc& d) { return d.states == ADAMW_STATES_8BIT && d.elements >= (1 << 24) ? 8 : 1; }
+
+// Blocks of threads for n elements.
+int64_t blocks_of(int64_t n, bool eight, int span) {
+    const int64_t each = (int64_t)kBlock * (eight ? warps<true>() : warps<false>()) * span;
+    return (n + each - 1) / each;
 }
 
 template <typename G, bool EIGHT, int N>
 cudaError_t launch(const adamw_desc& d, int from, int count, float* const* params, const void* const* grads,
-                   void* const* copies, AdamStep s, cudaStream_t st) {
+                   void* const* copies, AdamStep s, int span, cudaStream_t st) {
     AdamTable<N> table;
     uint32_t blocks = 0;
+    s.span = span;
     int k = 0;
     for (int i = from; i < from + count; ++i) {
         // (An empty tensor keeps its number and takes no block.)
         table.t[k] = AdamTensor{params[i], grads[i], copies ? copies[i] : nullptr, d.tensors[i].n,
                                 (uint32_t)(d.tensors[i].offset / kBlock), d.tensors[i].decay};
         table.first[k++] = blocks;
-        blocks += (uint32_t)((d.tensors[i].n + kBlock * kWarps - 1) / (kBlock * kWarps));
+        blocks += (uint32_t)blocks_of(d.tensors[i].n, EIGHT, span);
     }
     if (!blocks) return cudaSuccess;
     s.first_tensor = (uint32_t)from;
     s.count = count;
-    return launch_after(adamw_kernel<G, EIGHT, N>, dim3(blocks), dim3(32 * kWarps), 0, st, table, s);
+    return launch_after(adamw_kernel<G, EIGHT, N>, dim3(blocks), dim3(32 * warps<EIGHT>()), 0, st, table, s);
 }
 
 template <typename G, bool EIGHT>
 cudaError_t run(const adamw_desc& d, float* const* params, const void* const* grads, void* const* copies,
                 const AdamStep& s, cudaStream_t st) {
-    const int count = d.count;
+    const int count = d.count, span = span_of(d);
     for (int from = 0; from < count;) {
         // As many tensors as a launch's table and its number of blocks take.
         int n = 0;
         int64_t blocks = 0;
         while (from + n < count && n < kMany) {
-            const int64_t more = (d.tensors[from + n].n + kBlock * kWarps - 1) / (kBlock * kWarps);
+            const int64_t more = blocks_of(d.tensors[from + n].n, EIGHT, span);
             if (n && blocks + more > 0x7fffffffLL) break;
             blocks += more;
             ++n;
         }
-        const cudaError_t e = n <= kFew ? launch<G, EIGHT, kFew>(d, from, n, params, grads, copies, s, st)
-                                        : launch<G, EIGHT, kMany>(d, from, n, params, grads, copies, s, st);
+        const cudaError_t e = n <= kFew ? launch<G, EIGHT, kFew>(d, from, n, params, grads, copies, s, span, st)
+                                        : launch<G, EIGHT, kMany>(d, from, n, params, grads, copies, s, span, st);
         if (e != cudaSuccess) return e;
         from += n;
     }

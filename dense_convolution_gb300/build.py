@@ -20,7 +20,7 @@ OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libconv2d_gb300.so")
 SOURCES = ["api.cu", "transforms.cu", "conv_fp32.cu", "conv_tc.cu", "winograd.cu", "static_workspace.cu", "device_status.cu",
            "head_api.cu", "layernorm.cu", "layernorm_planes.cu", "dropout.cu", "linear_ce.cu",
-           "linear_ce_few.cu", "adamw.cu"]
+           "linear_ce_few.cu", "gated_ffn.cu", "gated_ffn_few.cu", "adamw.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -9,7 +9,7 @@ namespace conv2d_gb300 {
 
 namespace {
 
-constexpr int kUnits = 6, kSlots = 64;
+constexpr int kUnits = 7, kSlots = 64;
 struct Words { uint32_t* at[kUnits]; };
 __device__ uint32_t g_gathered[kSlots];    // a slot per call in flight
 
@@ -23,8 +23,10 @@ __global__ void gather_status_kernel(const Words w, int slot) {
 
 cudaError_t status_read_clear(cudaStream_t st, uint32_t* out) {
     static std::atomic<unsigned> calls{0};
-    cudaError_t (*const word[kUnits])(void**) = {status_word_tc, status_word_fp32, status_word_wg,
-                                                 status_word_ce, status_word_ln,   status_word_lp};
+    cudaError_t (*const word[])(void**) = {status_word_tc, status_word_fp32, status_word_wg,
+                                                 status_word_ce, status_word_ln,   status_word_lp,
+                                                 status_word_ffn};
+    static_assert(sizeof(word) / sizeof(*word) == kUnits, "a unit is missing");
     Words w;
     for (int i = 0; i < kUnits; ++i) {
         void* p = nullptr;
@@ -41,8 +43,10 @@ cudaError_t status_read_clear(cudaStream_t st, uint32_t* out) {
 }
 
 cudaError_t wait_limit_set(cudaStream_t st, uint64_t ns) {
-    cudaError_t (*const set[kUnits])(cudaStream_t, uint64_t) = {wait_limit_set_tc, wait_limit_set_fp32, wait_limit_set_wg,
-                                                                wait_limit_set_ce, wait_limit_set_ln,   wait_limit_set_lp};
+    cudaError_t (*const set[])(cudaStream_t, uint64_t) = {wait_limit_set_tc, wait_limit_set_fp32, wait_limit_set_wg,
+                                                                wait_limit_set_ce, wait_limit_set_ln,   wait_limit_set_lp,
+                                                                wait_limit_set_ffn};
+    static_assert(sizeof(set) / sizeof(*set) == kUnits, "a unit is missing");
     for (int i = 0; i < kUnits; ++i) {
         const cudaError_t e = set[i](st, ns);
         if (e != cudaSuccess) return e;

@@ -1,0 +1,61 @@
+// The feed-forward block's activations and their slopes.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "../../include/head.h"
+
+namespace conv2d_gb300 {
+
+// act(g) and its slope.  FAST (16-bit results): approximate exponentials and reciprocals,
+// good to 2^-21.
+template <bool FAST> __device__ __forceinline__ float exp_of(float x) {
+    if constexpr (FAST) return __expf(x);
+    else return expf(x);
+}
+template <bool FAST> __device__ __forceinline__ float inverse_of(float x) {
+    if constexpr (FAST) return __fdividef(1.f, x);
+    else return 1.f / x;
+}
+// 1 / (1 + exp(-z)) and what it is from 1, neither by a difference.
+template <bool FAST> __device__ __forceinline__ void sigmoid(float z, float& s, float& q) {
+    const float e = exp_of<FAST>(-fabsf(z)), r = inverse_of<FAST>(1.f + e), er = e * r;
+    s = z >= 0.f ? r : er;
+    q = z >= 0.f ? er : r;
+    if (isnan(z)) s = q = z;
+}
+template <int ACT, bool FAST> __device__ __forceinline__ void activate(float g, float& a, float& slope) {
+    if constexpr (ACT == FFN_SILU) {
+        float s, q;
+        sigmoid<FAST>(g, s, q);
+        a = g * s;
+        slope = s * fmaf(g, q, 1.f);
+    } else if constexpr (ACT == FFN_GELU) {
+        const float phi = fmaf(0.5f, erff(g * 0.70710678118654752f), 0.5f);
+        a = g * phi;
+        slope = fmaf(g * 0.39894228040143268f, exp_of<FAST>(-0.5f * g * g), phi);
+    } else {
+        // 0.5 (1 + tanh z) = 1 / (1 + exp(-2 z)), z = sqrt(2 / pi) (g + 0.044715 g^3).
+        constexpr float k = 1.5957691216057308f, c = 0.044715f;      // 2 sqrt(2 / pi)
+        float s, q;
+        const float gg = g * g;
+        sigmoid<FAST>(k * g * fmaf(c, gg, 1.f), s, q);
+        a = g * s;
+        slope = fmaf(g * k * fmaf(3.f * c, gg, 1.f), s * q, s);
+    }
+}
+// f(a, slope) for each of N pre-activations.
+template <bool FAST, int N, typename F> __device__ __forceinline__ void activate_all(int act, const float (&g)[N], F f) {
+#define FFN_EACH(ACT)                        \
+    _Pragma("unroll") for (int j = 0; j < N; ++j) { \
+        float a, slope;                      \
+        activate<ACT, FAST>(g[j], a, slope); \
+        f(j, a, slope);                      \
+    }
+    if (act == FFN_SILU) { FFN_EACH(FFN_SILU) }
+    else if (act == FFN_GELU) { FFN_EACH(FFN_GELU) }
+    else { FFN_EACH(FFN_GELU_TANH) }
+#undef FFN_EACH
+}
+
+}  // namespace conv2d_gb300

@@ -1,0 +1,279 @@
+// The feed-forward block of few tokens (serving), forward, on the CUDA cores: one pass
+// over the three weights is all there is, so they are read in place, whatever their
+// type, row length or alignment, and nothing is rounded below fp32 on the way.
+//
+//   ffn_few_kernel<GATE>   a team of warps takes two rows of Wg and the same two of Wu at
+//              a time, each warp a share of their columns, a vector a lane; the
+//              tokens' values lie in shared memory (head_few.cuh).  The team's
+//              sums meet in shared memory, and h goes out in fp32.
+//   ffn_few_kernel<!GATE>  the same over four rows of Wd, with h in shared memory.
+//
+// The rows of a quadruple are a vector length apart, so that they are offset alike
+// against the 16-byte boundary.  A team is as many warps as leave each lane two vectors of a
+// row: the rows then spread evenly over the machine (8192 pairs of 2048 bf16 columns
+// are 1.7 rounds of single warps, but 6.7 of teams of four), and a lane has eight loads on
+// their way.  The second kernel fetches its first rows to the L2 before it waits
+// for the first one's h.
+#include "gated_ffn_device.cuh"
+#include "head_device.cuh"
+#include "head_few.cuh"
+#include "head_internal.h"
+#include "ptx.cuh"
+
+namespace conv2d_gb300 {
+
+namespace {
+
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kSmemMost = 200 * 1024;
+
+struct FfnFew {
+    int tokens, cols, rows;      // cols: of the rows that are read; rows: inner, or hidden
+    int team;                    // warps
+    int act;
+    int64_t xs, ys;              // tokens' row strides, in and out (GATE: out is h, `rows` wide)
+    const void *x;               // tokens' values: the operands' type (GATE), or h
+    const void *w, *w2;          // Wg and Wu, or Wd
+    const void* res;
+    float *h, *saved;
+    int64_t fp;                  // pitch of saved's halves
+    void* y;
+};
+
+template <typename T, int NT, bool GATE>
+__global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) ffn_few_kernel(const FfnFew p) {
+    constexpr int V = kVec<T>, kRows = 4, N = kRows * NT, kSpan = 32 / N;
+    constexpr int P = kPair<NT>, NP = NT / P, kStep = GATE ? 2 : 4;          // rows of one matrix
+    using W = typename Word<P>::T;
+    extern __shared__ __align__(16) float hs[];            // [NP][V][pitch][P]
+    const W* words = reinterpret_cast<const W*>(hs);
+    __shared__ float red[2][kWarps][N];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int pitch = few_pitch<T>(p.cols), team = warp / p.team, part = warp - team * p.team;
+    const int teams = gridDim.x * (kWarps / p.team);
+    // Quadruples: a block of kStep V rows and an offset in it below V.
+    const int quads = (int)(((int64_t)p.rows + kStep * V - 1) / (kStep * V)) * V;
+    const int first = blockIdx.x * (kWarps / p.team) + team;
+    const auto row_of = [&](int q) { return q / V * (kStep * V) + q % V; };
+    const auto row_at = [&](int r0, int r) {               // row r of the quadruple, and whether it is there
+        const T* w = static_cast<const T*>(GATE && r >= 2 ? p.w2 : p.w);
+        return w + (int64_t)(r0 + r % kStep * V) * p.cols;
+    };
+    if (!GATE && first < quads) {
+        const int r0 = row_of(first);
+        for (int r = 0; r < kRows; ++r) {
+            if (r0 + r * V >= p.rows) break;
+            const char* at = reinterpret_cast<const char*>(row_at(r0, r));
+            for (int64_t b = (int64_t)(part * 32 + lane) * 128; b < (int64_t)p.cols * (int)sizeof(T); b += (int64_t)p.team * 4096)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(at + b));
+        }
+    }
+    pdl_wait();
+    pdl_launch_dependents();
+    for (int i = threadIdx.x; i < NT * V * pitch; i += kThreads) hs[i] = 0.f;
+    __syncthreads();
+    for (int t = 0; t < p.tokens; ++t) {
+        for (int e = threadIdx.x; e < p.cols; e += kThreads) {
+            const float v = GATE ? to_f32(static_cast<const T*>(p.x)[t * p.xs + e]) : static_cast<const float*>(p.x)[t * p.xs + e];
+            hs[((t / P * V + (e & (V - 1))) * pitch + (e >> shift_bits<T>()) + 1) * P + t % P] = v;
+        }
+    }
+    __syncthreads();
+
+    int turn = 0;
+    for (int q = first; q < quads; q += teams, turn ^= 1) {
+        const int r0 = row_of(q);
+        // (A block's last offsets may have no row at all, the same for the whole team.)
+        if (r0 >= p.rows) continue;
+        W acc[kRows][NP];
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+#pragma unroll
+            for (int t = 0; t < NP; ++t) acc[r][t] = spread<P>(0.f);
+        // Wg's rows and Wu's may be offset unlike each other.
+        constexpr int kSets = GATE ? 2 : 1, kPer = kRows / kSets;
+        const T* base[kSets];
+        int shift[kSets], off[kSets][V];
+#pragma unroll
+        for (int k = 0; k < kSets; ++k) {
+            base[k] = row_at(r0, k * kPer);
+            shift[k] = phase_of(base[k]);
+            word_offsets<T>(shift[k], pitch, off[k]);
+        }
+        const auto add = [&](const Vec<T, V>(&raw)[kRows], int s) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                W f[kRows];
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) f[r] = spread<P>(to_f32(raw[r].v[i]));
+#pragma unroll
+                for (int t = 0; t < NP; ++t) {
+#pragma unroll
+                    for (int k = 0; k < kSets; ++k) {
+                        const W x = words[t * V * pitch + off[k][i] + s];
+#pragma unroll
+                        for (int r = k * kPer; r < (k + 1) * kPer; ++r) acc[r][t] = fma_words(f[r], x, acc[r][t]);
+                    }
+                }
+            }
+        };
+        // This warp's share of the slots; whole vectors of four whole rows without tests.
+        const int most = max(shift[0], shift[kSets - 1]), slots = (p.cols + most + V - 1) >> shift_bits<T>();
+        const int lo = slots * part / p.team, hi = slots * (part + 1) / p.team;
+        const bool four = r0 + (kStep - 1) * V < p.rows;
+        const int wlo = four ? max(lo, (most != 0)) : hi, whi = four ? min(hi, (p.cols + min(shift[0], shift[kSets - 1])) >> shift_bits<T>()) : hi;
+#pragma unroll(NT >= 8 ? 1 : 2)
+        for (int s = wlo + lane; s < whi; s += 32) {
+            Vec<T, V> raw[kRows];
+#pragma unroll
+            for (int r = 0; r < kRows; ++r)
+                raw[r] = *reinterpret_cast<const Vec<T, V>*>(base[r / kPer] + (int64_t)(r % kPer) * V * p.cols + (s * V - shift[r / kPer]));
+            add(raw, s);
+        }
+        // The rows' ends, or all slots of rows at the matrix' end.
+        const auto ends = [&](int s) {
+            Vec<T, V> raw[kRows];
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                const bool in = r0 + r % kStep * V < p.rows;
+                const int e0 = s * V - shift[r / kPer];
+                const int from = max(0, -e0), to = max(from, min(V, p.cols - e0));
+                raw[r] = load_part<T, V>(base[r / kPer] + (in ? (int64_t)(r % kPer) * V * p.cols + e0 : 0), in ? from : V, in ? to : 0);
+            }
+            add(raw, s);
+        };
+        if (four) {
+            if (lo < wlo && lane == 0 && lo < hi) ends(lo);
+            for (int s = max(wlo, whi) + lane; s < hi; s += 32) ends(s);
+        } else {
+            for (int s = lo + lane; s < hi; s += 32) ends(s);
+        }
+        float sums[N];
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+#pragma unroll
+            for (int t = 0; t < NP; ++t) {
+                if constexpr (P == 2) unpack2f(acc[r][t], sums[r * NT + 2 * t], sums[r * NT + 2 * t + 1]);
+                else sums[r] = acc[r][t];
+            }
+        __syncwarp();
+        const float z = warp_sums<N>(sums);
+        if (lane % kSpan == 0) red[turn][warp][lane / kSpan] = z;
+        // (Two buffers in turn: the next meeting shows that this one's are read.)
+        if (p.team > 1) named_bar_sync(1 + team, p.team * 32);
+        else __syncwarp();
+        if (part == 0) {
+            const auto total = [&](int k) {
+                float f = 0.f;
+                for (int i = 0; i < p.team; ++i) f += red[turn][warp + i][k];
+                return f;
+            };
+            if constexpr (GATE) {
+                const int r = lane / NT, t = lane % NT, row = r0 + r * V;
+                if (lane < 2 * NT && t < p.tokens && row < p.rows) {
+                    const float g = total(lane), u = total(lane + 2 * NT);
+                    float h = 0.f;
+                    const float one[1] = {g};
+                    activate_all<false>(p.act, one, [&](int, float a, float) { h = a * u; });
+                    p.h[(int64_t)t * p.ys + row] = h;
+                    if (p.saved) {
+                        p.saved[(int64_t)t * 2 * p.fp + row] = g;
+                        p.saved[((int64_t)t * 2 + 1) * p.fp + row] = u;
+                    }
+                }
+            } else {
+                const int r = lane / NT, t = lane % NT, row = r0 + r * V;
+                if (lane < N && t < p.tokens && row < p.rows) {
+                    float y = total(lane);
+                    if (p.res) y += to_f32(static_cast<const T*>(p.res)[(int64_t)t * p.ys + row]);
+                    static_cast<T*>(p.y)[(int64_t)t * p.ys + row] = from_f32<T>(y);
+                }
+            }
+        }
+    }
+}
+
+int nt_of(int64_t tokens) { return tokens <= 1 ? 1 : tokens <= 2 ? 2 : tokens <= 4 ? 4 : 8; }
+
+template <typename T> size_t few_smem(int nt, int64_t cols) {
+    return (size_t)nt * kVec<T> * few_pitch<T>((int)cols) * sizeof(float);
+}
+
+template <typename T, int NT, bool GATE> cudaError_t few_launch(FfnFew p, int sms, cudaStream_t st) {
+    const cudaError_t e = allow_smem(ffn_few_kernel<T, NT, GATE>, kSmemMost);
+    if (e != cudaSuccess) return e;
+    const int vectors = (p.cols + 32 * kVec<T> - 1) / (32 * kVec<T>);         // of a row, a lane
+    p.team = 1;
+    while (p.team < kWarps && vectors >= 4 * p.team) p.team *= 2;
+    const size_t smem = few_smem<T>(NT, p.cols);
+    const int each = NT <= 2 && smem <= 100 * 1024 ? 2 : 1;
+    return launch_after(ffn_few_kernel<T, NT, GATE>, dim3((unsigned)(sms * each)), dim3(kThreads), smem, st, p);
+}
+template <typename T, bool GATE> cudaError_t few_tokens(const FfnFew& p, int sms, cudaStream_t st) {
+    switch (nt_of(p.tokens)) {
+        case 1: return few_launch<T, 1, GATE>(p, sms, st);
+        case 2: return few_launch<T, 2, GATE>(p, sms, st);
+        case 4: return few_launch<T, 4, GATE>(p, sms, st);
+        default: return few_launch<T, 8, GATE>(p, sms, st);
+    }
+}
+
+// Tokens that go through together.
+constexpr int kGroup = 8;
+
+template <typename T>
+cudaError_t run(const gated_ffn_desc& d, const void* x, const void* wg, const void* wu, const void* wd,
+                const void* residual, void* y, float* saved, float* h, cudaStream_t st) {
+    for (int64_t t = 0; t < d.tokens; t += kGroup) {
+        FfnFew p{};
+        p.tokens = (int)(d.tokens - t < kGroup ? d.tokens - t : kGroup);
+        p.act = d.act;
+        p.cols = (int)d.hidden;
+        p.rows = (int)d.inner;
+        p.xs = d.xs;
+        p.ys = d.inner;
+        p.x = static_cast<const T*>(x) + t * d.xs;
+        p.w = wg;
+        p.w2 = wu;
+        p.h = h;
+        p.fp = (d.inner + 63) / 64 * 64;
+        p.saved = saved ? saved + t * 2 * p.fp : nullptr;
+        cudaError_t e = few_tokens<T, true>(p, d.sms, st);
+        if (e != cudaSuccess) return e;
+        p.cols = (int)d.inner;
+        p.rows = (int)d.hidden;
+        p.xs = d.inner;
+        p.ys = d.ys;
+        p.x = h;
+        p.w = wd;
+        p.res = residual ? static_cast<const T*>(residual) + t * d.ys : nullptr;
+        p.y = static_cast<T*>(y) + t * d.ys;
+        e = few_tokens<T, false>(p, d.sms, st);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace
+
+// Few tokens, whose rows fit a block's shared memory.
+bool gated_ffn_is_few(const gated_ffn_desc& d) {
+    const bool f32 = d.dtype == CONV2D_F32, copied = d.xs % 8 != 0 || d.hidden % 8 != 0 || d.inner % 8 != 0;
+    if (d.tokens > (f32 ? 32 : copied ? 8 : 4)) return false;
+    const int nt = nt_of(d.tokens);
+    const int64_t cols = d.hidden > d.inner ? d.hidden : d.inner;
+    return (f32 ? few_smem<float>(nt, cols) : few_smem<__half>(nt, cols)) <= (size_t)kSmemMost;
+}
+
+int64_t gated_ffn_few_words(const gated_ffn_desc& d) { return (d.tokens < kGroup ? d.tokens : kGroup) * d.inner; }
+
+cudaError_t launch_gated_ffn_few(const gated_ffn_desc& d, const void* x, const void* wg, const void* wu, const void* wd,
+                                 const void* residual, void* y, float* saved, float* h, cudaStream_t st) {
+    switch (d.dtype) {
+        case CONV2D_F32: return run<float>(d, x, wg, wu, wd, residual, y, saved, h, st);
+        case CONV2D_F16: return run<__half>(d, x, wg, wu, wd, residual, y, saved, h, st);
+        default: return run<__nv_bfloat16>(d, x, wg, wu, wd, residual, y, saved, h, st);
+    }
+}
+
+}  // namespace conv2d_gb300

@@ -1,9 +1,10 @@
 // C ABI of the training-head operators (include/head.h): descriptors, argument
 // checks and workspace sizes.  Host code only; the kernels live in
-// layernorm.cu, layernorm_planes.cu, dropout.cu, linear_ce.cu, linear_ce_few.cu
-// and adamw.cu.
+// layernorm.cu, layernorm_planes.cu, dropout.cu, linear_ce.cu, linear_ce_few.cu,
+// gated_ffn.cu, gated_ffn_few.cu and adamw.cu.
 #include <math.h>
 
+#include <initializer_list>
 #include <new>
 
 #include "head_internal.h"
@@ -270,6 +271,101 @@ CONV2D_API conv2d_status linear_ce_bwd(linear_ce_desc_t dp, const void* h, const
         return CONV2D_ERR_MISALIGNED;
     if (workspace_bytes < d.bwd.total) return CONV2D_ERR_WORKSPACE_TOO_SMALL;
     return launch_linear_ce_bwd(d, h, w, target, lse, dloss, dh, dw, workspace, st);
+}
+
+// ------------------------------------------------- gated feed-forward block
+CONV2D_API conv2d_status gated_ffn_desc_create(gated_ffn_desc_t* out, int64_t tokens, int64_t hidden, int64_t inner,
+                                               conv2d_dtype dtype, gated_ffn_act act) {
+    if (!out) return CONV2D_ERR_NULL_PTR;
+    *out = nullptr;
+    // (A sum over `hidden` never leaves tensor memory: 16384 is what fp16 takes there.)
+    if (tokens < 0 || hidden < 1 || inner < 1 || tokens > kMaxGemmSide || hidden > 16384 || inner > (1LL << 20) ||
+        !known(dtype))
+        return CONV2D_ERR_BAD_PARAM;
+    if (((tokens + 127) / 128) * ((inner + 31) / 32) > 0x7fffffffLL) return CONV2D_ERR_BAD_PARAM;
+    if (act != FFN_SILU && act != FFN_GELU && act != FFN_GELU_TANH) return CONV2D_ERR_BAD_PARAM;
+    gated_ffn_desc d{};
+    d.tokens = tokens; d.hidden = hidden; d.inner = inner; d.dtype = dtype; d.act = act;
+    d.xs = d.ys = hidden;
+    gated_ffn_plan(d);
+    return give(out, d);
+}
+
+CONV2D_API conv2d_status gated_ffn_desc_set_row_strides(gated_ffn_desc_t d, int64_t x_stride, int64_t y_stride) {
+    if (!d) return CONV2D_ERR_NULL_PTR;
+    // A tensor map's row pitch is below 2^40 bytes.
+    if (!stride_ok(x_stride, d->hidden) || !stride_ok(y_stride, d->hidden) || x_stride >= kMaxStride / 4 ||
+        y_stride >= kMaxStride / 4)
+        return CONV2D_ERR_BAD_PARAM;
+    d->xs = x_stride;
+    d->ys = y_stride;
+    gated_ffn_plan(*d);
+    return CONV2D_OK;
+}
+
+CONV2D_API conv2d_status gated_ffn_desc_destroy(gated_ffn_desc_t d) {
+    delete d;
+    return CONV2D_OK;
+}
+
+CONV2D_API conv2d_status gated_ffn_workspace_size(gated_ffn_desc_t d, size_t* fwd_bytes, size_t* bwd_bytes,
+                                                  size_t* saved_bytes) {
+    if (!d || (!fwd_bytes && !bwd_bytes && !saved_bytes)) return CONV2D_ERR_NULL_PTR;
+    if (fwd_bytes) *fwd_bytes = d->fwd.total;
+    if (bwd_bytes) *bwd_bytes = d->bwd.total;
+    if (saved_bytes) *saved_bytes = (size_t)d->tokens * 2 * ((d->inner + 63) / 64 * 64) * sizeof(float);
+    return CONV2D_OK;
+}
+
+namespace {
+
+// Operands are read in place by tensor copies, which need 16-byte alignment, unless they are
+// packed first (or there are few tokens: the interface's rule is one for all).
+bool ffn_operands_ok(const gated_ffn_desc& d, const void* x, const void* wg, const void* wu, const void* wd) {
+    const size_t e = elem_bytes(d.dtype);
+    const bool f32 = d.dtype == CONV2D_F32;
+    const size_t ax = f32 || d.xs % 8 ? e : 16, ah = f32 || d.hidden % 8 ? e : 16, ad = f32 || d.inner % 8 ? e : 16;
+    return aligned_to(x, ax) && aligned_to(wg, ah) && aligned_to(wu, ah) && aligned_to(wd, ad);
+}
+
+}  // namespace
+
+CONV2D_API conv2d_status gated_ffn_fwd(gated_ffn_desc_t dp, const void* x, const void* wg, const void* wu,
+                                       const void* wd, const void* residual, void* y, float* saved, void* workspace,
+                                       size_t workspace_bytes, void* stream) {
+    if (!dp) return CONV2D_ERR_NULL_PTR;
+    const gated_ffn_desc& d = *dp;
+    if (d.tokens == 0) return CONV2D_OK;
+    if (!x || !wg || !wu || !wd || !y || !workspace) return CONV2D_ERR_NULL_PTR;
+    const size_t e = elem_bytes(d.dtype);
+    if (!ffn_operands_ok(d, x, wg, wu, wd) || !aligned_to(y, e) || !aligned_to(residual, e) || !aligned_to(saved, 32) ||
+        !aligned_to(workspace, 16))
+        return CONV2D_ERR_MISALIGNED;
+    if (workspace_bytes < d.fwd.total) return CONV2D_ERR_WORKSPACE_TOO_SMALL;
+    return launch_gated_ffn_fwd(d, x, wg, wu, wd, residual, y, saved, workspace, static_cast<cudaStream_t>(stream));
+}
+
+CONV2D_API conv2d_status gated_ffn_bwd(gated_ffn_desc_t dp, const void* dy, const void* x, const void* wg,
+                                       const void* wu, const void* wd, const float* saved, void* dx, void* dwg,
+                                       void* dwu, void* dwd, void* workspace, size_t workspace_bytes, void* stream) {
+    if (!dp) return CONV2D_ERR_NULL_PTR;
+    const gated_ffn_desc& d = *dp;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const size_t e = elem_bytes(d.dtype);
+    if (!dx && !dwg && !dwu && !dwd) return CONV2D_OK;
+    if (!aligned_to(dx, e) || !aligned_to(dwg, e) || !aligned_to(dwu, e) || !aligned_to(dwd, e))
+        return CONV2D_ERR_MISALIGNED;
+    if (d.tokens == 0) {   // no rows: the sums over rows are zero
+        for (void* p : {dwg, dwu, dwd})
+            if (p && cudaMemsetAsync(p, 0, (size_t)d.hidden * d.inner * e, st) != cudaSuccess) return CONV2D_ERR_CUDA;
+        return CONV2D_OK;
+    }
+    if (!dy || !x || !wg || !wu || !wd || !saved || !workspace) return CONV2D_ERR_NULL_PTR;
+    const size_t ay = d.dtype == CONV2D_F32 || d.ys % 8 ? e : 16;
+    if (!ffn_operands_ok(d, x, wg, wu, wd) || !aligned_to(dy, ay) || !aligned_to(saved, 32) || !aligned_to(workspace, 16))
+        return CONV2D_ERR_MISALIGNED;
+    if (workspace_bytes < d.bwd.total) return CONV2D_ERR_WORKSPACE_TOO_SMALL;
+    return launch_gated_ffn_bwd(d, dy, x, wg, wu, wd, saved, dx, dwg, dwu, dwd, workspace, st);
 }
 
 // --------------------------------------------------------------------- AdamW

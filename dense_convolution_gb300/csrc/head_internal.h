@@ -41,6 +41,19 @@ struct CePlan {
     size_t part, z_target, row_loss, coef, common, hp, wp, dz, acc, sums_h, sums_w, total;
 };
 
+// Tile width, CTA pairs and K splits of a launch of the feed-forward block (gated_ffn.cu, plan_tiles).
+struct FfnTile { int BN; bool pair; int splits[4]; };
+
+// Sizes and workspace offsets of one pass of the feed-forward block.
+struct FfnPlan {
+    bool few;                      // few tokens: gated_ffn_few.cu
+    bool bf16, pack_x, pack_wh, pack_wd, pack_dy;      // operands that are copied first: x, Wg and Wu, Wd, dy
+    int parts, pairs;              // bf16 parts per value (1, or 3 for fp32) and their products (1 or 6)
+    int64_t dp, fp;                // row pitch of one part, of `hidden` and of `inner` columns
+    FfnTile first, last;           // h and y; dg and du, and the gradients
+    size_t xp, wgp, wup, wdp, dyp, h, dgu, largest, sums[4], total;
+};
+
 }  // namespace conv2d_gb300
 
 struct linear_ce_desc {
@@ -53,6 +66,15 @@ struct linear_ce_desc {
     int dz_parts;        // 16-bit parts of dz: 1, 2; 0 = automatic
     int sms;             // of the device that the plans are for: the few-token kernels' blocks and shares
     conv2d_gb300::CePlan fwd, bwd;
+};
+
+struct gated_ffn_desc {
+    int64_t tokens, hidden, inner;
+    conv2d_dtype dtype;
+    gated_ffn_act act;
+    int64_t xs, ys;      // row strides of x, and of y, residual and dy
+    int sms;             // of the device that the plans are for
+    conv2d_gb300::FfnPlan fwd, bwd;
 };
 
 struct adamw_desc {
@@ -94,6 +116,7 @@ cudaError_t launch_dropout(const dropout_desc& d, const void* x, int64_t xs, con
                            int64_t ys, uint64_t seed, uint64_t offset, cudaStream_t st);
 
 // linear_ce.cu
+int pair_count();                            // CTA pairs that run at once, one CTA an SM (SMs pair up within their cluster hardware)
 void linear_ce_plan(linear_ce_desc& d);      // sets fwd and bwd from the rest
 conv2d_status launch_linear_ce_fwd(const linear_ce_desc& d, const void* h, const void* w, const int64_t* target,
                                    float* loss, float* lse, void* ws, cudaStream_t st);
@@ -111,6 +134,20 @@ cudaError_t launch_ce_few_fwd(const linear_ce_desc& d, const void* h, const void
 cudaError_t launch_ce_few_bwd(const linear_ce_desc& d, const void* h, const void* w, const int64_t* target,
                               const float* lse, const float* dloss, void* dh, void* dw, float* dz, float* sums,
                               cudaStream_t st);
+
+// gated_ffn.cu
+void gated_ffn_plan(gated_ffn_desc& d);      // sets fwd and bwd from the rest
+conv2d_status launch_gated_ffn_fwd(const gated_ffn_desc& d, const void* x, const void* wg, const void* wu, const void* wd,
+                                   const void* residual, void* y, float* saved, void* ws, cudaStream_t st);
+conv2d_status launch_gated_ffn_bwd(const gated_ffn_desc& d, const void* dy, const void* x, const void* wg, const void* wu,
+                                   const void* wd, const float* saved, void* dx, void* dwg, void* dwu, void* dwd, void* ws,
+                                   cudaStream_t st);
+
+// gated_ffn_few.cu: few tokens, forward, on the CUDA cores
+bool gated_ffn_is_few(const gated_ffn_desc& d);
+int64_t gated_ffn_few_words(const gated_ffn_desc& d);      // fp32 words of h
+cudaError_t launch_gated_ffn_few(const gated_ffn_desc& d, const void* x, const void* wg, const void* wu, const void* wd,
+                                 const void* residual, void* y, float* saved, float* h, cudaStream_t st);
 
 // adamw.cu
 cudaError_t launch_adamw(const adamw_desc& d, float* const* params, const void* const* grads, void* const* copies,

@@ -146,11 +146,13 @@ cudaError_t status_word_wg(void** p);
 cudaError_t status_word_ce(void** p);
 cudaError_t status_word_ln(void** p);
 cudaError_t status_word_lp(void** p);
+cudaError_t status_word_ffn(void** p);
 cudaError_t wait_limit_set_tc(cudaStream_t st, uint64_t ns);
 cudaError_t wait_limit_set_fp32(cudaStream_t st, uint64_t ns);
 cudaError_t wait_limit_set_wg(cudaStream_t st, uint64_t ns);
 cudaError_t wait_limit_set_ce(cudaStream_t st, uint64_t ns);
 cudaError_t wait_limit_set_ln(cudaStream_t st, uint64_t ns);
 cudaError_t wait_limit_set_lp(cudaStream_t st, uint64_t ns);
+cudaError_t wait_limit_set_ffn(cudaStream_t st, uint64_t ns);
 
 }  // namespace conv2d_gb300

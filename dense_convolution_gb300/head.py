@@ -309,6 +309,80 @@ class LinearCrossEntropy(_Op):
         return dh, dw
 
 
+class GatedFeedForward(_Op):
+    """A gated feed-forward block: y = residual + (act(x wg') * x wu') wd'.
+
+    x (tokens, hidden), wg and wu (inner, hidden), wd (hidden, inner), one type
+    act         "silu", "gelu" (by the normal distribution) or "gelu_tanh"
+    x_stride    elements between rows of x
+    y_stride    elements between rows of y, residual and dy
+    """
+    _destroy = staticmethod(head_capi.gated_ffn_desc_destroy)
+
+    def __init__(self, tokens, hidden, inner, dtype="bf16", act="silu", x_stride=None, y_stride=None):
+        self.tokens, self.hidden, self.inner, self.dtype, self.act = tokens, hidden, inner, dtype, act
+        self.x_stride, self.y_stride = x_stride or hidden, y_stride or hidden
+        self.desc = head_capi.gated_ffn_desc_create(tokens, hidden, inner, dtype, act)
+        if self.x_stride != hidden or self.y_stride != hidden:
+            head_capi.gated_ffn_desc_set_row_strides(self.desc, self.x_stride, self.y_stride)
+        self.workspace_bytes, self.backward_workspace_bytes, _ = head_capi.gated_ffn_workspace_size(self.desc)
+        self._x, self._y = _Rows(tokens, hidden, self.x_stride, dtype), _Rows(tokens, hidden, self.y_stride, dtype)
+        self._dx = _Rows(tokens, hidden, hidden, dtype)
+        self._wh, self._wd = _Flat((inner, hidden), _TORCH_DTYPE[dtype]), _Flat((hidden, inner), _TORCH_DTYPE[dtype])
+        self._saved = _Flat((tokens, 2, -(-inner // 64) * 64), torch.float32)
+
+    def _check(self, x, wg, wu, wd, dev):
+        self._x.check("x", x, dev)
+        self._wh.check("wg", wg, dev)
+        self._wh.check("wu", wu, dev)
+        self._wd.check("wd", wd, dev)
+
+    def __call__(self, x, wg, wu, wd, residual=None, y=None, save=False, workspace=None, stream=None):
+        """y, or (y, saved) with `save` (what `backward` needs).  y may be residual,
+        or x where their strides agree."""
+        dev = x.get_device()
+        if stream is not None or dev < 0 or dev != _current_device():
+            with _place(dev, stream):
+                return self(x, wg, wu, wd, residual, y, save, workspace)
+        self._check(x, wg, wu, wd, dev)
+        if residual is not None:
+            self._y.check("residual", residual, dev)
+        at = x.device
+        if y is None:
+            y = self._y.new(at)
+        else:
+            self._y.check("y", y, dev)
+        if workspace is None:
+            workspace = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=at)
+        else:
+            _check_workspace(workspace, dev)
+        saved = self._saved.new(at) if save else None
+        head_capi.gated_ffn_fwd(self.desc, x.data_ptr(), wg.data_ptr(), wu.data_ptr(), wd.data_ptr(), _ptr(residual),
+                                y.data_ptr(), _ptr(saved), workspace.data_ptr(), workspace.numel(), _raw_stream(dev))
+        return (y, saved) if save else y
+
+    def backward(self, dy, x, wg, wu, wd, saved, need_dx=True, need_dw=True, workspace=None, stream=None):
+        """(dx, dwg, dwu, dwd); None in the place of what is not needed."""
+        dev = x.get_device()
+        if stream is not None or dev < 0 or dev != _current_device():
+            with _place(dev, stream):
+                return self.backward(dy, x, wg, wu, wd, saved, need_dx, need_dw, workspace)
+        self._check(x, wg, wu, wd, dev)
+        self._y.check("dy", dy, dev)
+        self._saved.check("saved", saved, dev)
+        at = x.device
+        if workspace is None:
+            workspace = torch.empty(self.backward_workspace_bytes, dtype=torch.uint8, device=at)
+        else:
+            _check_workspace(workspace, dev)
+        dx = self._dx.new(at) if need_dx else None
+        dwg, dwu, dwd = (self._wh.new(at), self._wh.new(at), self._wd.new(at)) if need_dw else (None,) * 3
+        head_capi.gated_ffn_bwd(self.desc, dy.data_ptr(), x.data_ptr(), wg.data_ptr(), wu.data_ptr(), wd.data_ptr(),
+                                saved.data_ptr(), _ptr(dx), _ptr(dwg), _ptr(dwu), _ptr(dwd), workspace.data_ptr(),
+                                workspace.numel(), _raw_stream(dev))
+        return dx, dwg, dwu, dwd
+
+
 AdamWState = collections.namedtuple("AdamWState", "m v m_scale v_scale")
 
 

@@ -14,6 +14,7 @@ from . import capi
 from .capi import DTYPES, _check
 
 REDUCTIONS = {"none": 0, "sum": 1, "mean": 2}
+ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
 ADAMW_STATES = {"f32": 0, "8bit": 1}
 
 EXPORTED = ("layernorm_desc_create", "layernorm_desc_set_row_strides", "layernorm_desc_set_planes",
@@ -21,6 +22,8 @@ EXPORTED = ("layernorm_desc_create", "layernorm_desc_set_row_strides", "layernor
             "dropout_desc_create", "dropout_desc_set_row_strides", "dropout_desc_destroy", "dropout_fwd", "dropout_bwd",
             "linear_ce_desc_create", "linear_ce_desc_set_row_strides", "linear_ce_desc_set_piece",
             "linear_ce_desc_set_dz_parts", "linear_ce_desc_destroy", "linear_ce_workspace_size", "linear_ce_fwd", "linear_ce_bwd",
+            "gated_ffn_desc_create", "gated_ffn_desc_set_row_strides", "gated_ffn_desc_destroy", "gated_ffn_workspace_size",
+            "gated_ffn_fwd", "gated_ffn_bwd",
             "adamw_desc_create", "adamw_desc_set_rates", "adamw_desc_set_weight_decay", "adamw_desc_destroy",
             "adamw_state_elements", "adamw_state_offset", "adamw_step")
 
@@ -55,6 +58,12 @@ def load():
     L.linear_ce_workspace_size.argtypes = [vp, ctypes.POINTER(size), ctypes.POINTER(size)]
     L.linear_ce_fwd.argtypes = [vp] * 7 + [size, vp]
     L.linear_ce_bwd.argtypes = [vp] * 9 + [size, vp]
+    L.gated_ffn_desc_create.argtypes = [out, i64, i64, i64, i32, i32]
+    L.gated_ffn_desc_set_row_strides.argtypes = [vp, i64, i64]
+    L.gated_ffn_desc_destroy.argtypes = [vp]
+    L.gated_ffn_workspace_size.argtypes = [vp] + [ctypes.POINTER(size)] * 3
+    L.gated_ffn_fwd.argtypes = [vp] * 9 + [size, vp]
+    L.gated_ffn_bwd.argtypes = [vp] * 12 + [size, vp]
     f32, f64 = ctypes.c_float, ctypes.c_double
     L.adamw_desc_create.argtypes = [out, i64, ctypes.POINTER(i64), i32, i32, i32]
     L.adamw_desc_set_rates.argtypes = [vp, f64, f64, f64]
@@ -176,6 +185,40 @@ def linear_ce_bwd(desc: int, h: int, w: int, target: int, lse: int, dloss: int, 
                   workspace_bytes: int, stream: int = 0):
     _check(load().linear_ce_bwd(desc, h, w, target, lse, dloss, dh,
                                 dw, workspace, workspace_bytes, stream), "linear_ce_bwd")
+
+
+def gated_ffn_desc_create(tokens, hidden, inner, dtype="bf16", act="silu") -> int:
+    d = ctypes.c_void_p()
+    kind = ACTIVATIONS[act] if isinstance(act, str) else int(act)
+    _check(load().gated_ffn_desc_create(ctypes.byref(d), tokens, hidden, inner, _dtype(dtype), kind), "gated_ffn_desc_create")
+    return d.value
+
+
+def gated_ffn_desc_set_row_strides(desc: int, x_stride: int, y_stride: int):
+    _check(load().gated_ffn_desc_set_row_strides(desc, x_stride, y_stride), "gated_ffn_desc_set_row_strides")
+
+
+def gated_ffn_desc_destroy(desc: int):
+    _check(load().gated_ffn_desc_destroy(desc), "gated_ffn_desc_destroy")
+
+
+def gated_ffn_workspace_size(desc: int):
+    """Workspace bytes of gated_ffn_fwd and gated_ffn_bwd, and bytes of what is saved between them."""
+    b = [ctypes.c_size_t() for _ in range(3)]
+    _check(load().gated_ffn_workspace_size(desc, *map(ctypes.byref, b)), "gated_ffn_workspace_size")
+    return tuple(v.value for v in b)
+
+
+def gated_ffn_fwd(desc: int, x: int, wg: int, wu: int, wd: int, residual: int, y: int, saved: int, workspace: int,
+                  workspace_bytes: int, stream: int = 0):
+    _check(load().gated_ffn_fwd(desc, x, wg, wu, wd, residual, y, saved, workspace, workspace_bytes, stream),
+           "gated_ffn_fwd")
+
+
+def gated_ffn_bwd(desc: int, dy: int, x: int, wg: int, wu: int, wd: int, saved: int, dx: int, dwg: int, dwu: int,
+                  dwd: int, workspace: int, workspace_bytes: int, stream: int = 0):
+    _check(load().gated_ffn_bwd(desc, dy, x, wg, wu, wd, saved, dx, dwg, dwu, dwd, workspace, workspace_bytes, stream),
+           "gated_ffn_bwd")
 
 
 def adamw_desc_create(sizes, grad_dtype="f32", states="f32", copy_dtype="f32") -> int:

@@ -1,7 +1,7 @@
 /*
  * head.h — C ABI of the training-head operators of the GB300 (sm_103a)
- * convolution library: layer norm, dropout and linear cross entropy, forward
- * and backward, and AdamW.  They take a convolution's output (include/conv2d.h)
+ * convolution library: layer norm, dropout, a gated feed-forward block and
+ * linear cross entropy, forward and backward, and AdamW.  They take a convolution's output (include/conv2d.h)
  * from feature planes to a loss over a vocabulary, its gradients and the next
  * weights.
  *
@@ -32,6 +32,7 @@ extern "C" {
 typedef struct layernorm_desc *layernorm_desc_t;
 typedef struct dropout_desc *dropout_desc_t;
 typedef struct linear_ce_desc *linear_ce_desc_t;
+typedef struct gated_ffn_desc *gated_ffn_desc_t;
 typedef struct adamw_desc *adamw_desc_t;
 
 /* ---------------------------------------------------------------- layer norm
@@ -194,6 +195,61 @@ conv2d_status linear_ce_fwd(linear_ce_desc_t d, const void *h, const void *w, co
 conv2d_status linear_ce_bwd(linear_ce_desc_t d, const void *h, const void *w, const int64_t *target, const float *lse,
                             const float *dloss, void *dh, void *dw, void *workspace, size_t workspace_bytes,
                             void *stream);
+
+/* ------------------------------------------------- gated feed-forward block
+ * For each of `tokens` rows of x (`hidden` columns), with Wg and Wu
+ * [inner][hidden] and Wd [hidden][inner]:
+ *   g = x Wg^T,  u = x Wu^T,  h = act(g) u,  y = residual + h Wd^T,
+ * act(g) = g / (1 + exp(-g)) (SILU), g Phi(g) (GELU, Phi the normal
+ * distribution) or g / (1 + exp(-2 sqrt(2/pi) (g + 0.044715 g^3))) (GELU_TANH).
+ * Backward, from dy and the saved g and u:
+ *   dh = dy Wd,  dg = dh u act'(g),  du = dh act(g),  dx = dg Wg + du Wu,
+ *   dWg = dg^T x,  dWu = du^T x,  dWd = dy^T h    (the residual's gradient is dy).
+ * fp16 and bf16 run on the tensor cores with fp32 accumulation; g, u and dh stay
+ * in fp32, while h, dg and du are rounded to the operands' type for the products
+ * that read them (fp16: dg and du held times a power of two that takes the
+ * largest |dy| to [16, 32); an h beyond fp16's range is infinite).  fp32 runs there
+ * too, as three bf16 parts a value and the six leading products of the parts; an
+ * infinity in an operand makes what it enters NaN.  Forward passes of few tokens run
+ * on the CUDA cores and keep h in fp32. */
+
+typedef enum { FFN_SILU = 0, FFN_GELU = 1, FFN_GELU_TANH = 2 } gated_ffn_act;
+
+/* Create a descriptor.
+ *   0 <= tokens <= 2^30, 1 <= hidden <= 16384, 1 <= inner <= 2^20, and fewer than
+ *   2^31 tiles of 128 tokens by 32 inner columns
+ * Errors: NULL_PTR, BAD_PARAM. */
+conv2d_status gated_ffn_desc_create(gated_ffn_desc_t *out, int64_t tokens, int64_t hidden, int64_t inner,
+                                    conv2d_dtype dtype, gated_ffn_act act);
+
+/* Elements from one row to the next of x, and of y, residual and dy (defaults
+ * hidden, at least hidden; dx, the weights and their gradients are contiguous).
+ * Operands whose rows are no multiple of 8 elements apart, and fp32 ones, are first
+ * copied into the workspace in the layout the tensor cores read.  Changes the
+ * workspace sizes. */
+conv2d_status gated_ffn_desc_set_row_strides(gated_ffn_desc_t d, int64_t x_stride, int64_t y_stride);
+
+conv2d_status gated_ffn_desc_destroy(gated_ffn_desc_t d);
+
+/* Workspace bytes of gated_ffn_fwd and gated_ffn_bwd, and bytes of `saved` (each may be NULL). */
+conv2d_status gated_ffn_workspace_size(gated_ffn_desc_t d, size_t *fwd_bytes, size_t *bwd_bytes, size_t *saved_bytes);
+
+/* y from x, the weights and residual (NULL: none).  y may be residual, and x where
+ * their strides agree.  saved (NULL: not wanted) receives g and u for the backward
+ * pass, [tokens][2][inner rounded up to 64] floats, 32-byte aligned.  x and the weights
+ * are 16-byte aligned (those that are copied, and all of fp32: as their elements), the workspace too.
+ * Errors: NULL_PTR, MISALIGNED, WORKSPACE_TOO_SMALL, CUDA; UNSUPPORTED for more
+ * tiles and splits than 2^31; bounded waits that expire are reported by
+ * conv2d_device_status. */
+conv2d_status gated_ffn_fwd(gated_ffn_desc_t d, const void *x, const void *wg, const void *wu, const void *wd,
+                            const void *residual, void *y, float *saved, void *workspace, size_t workspace_bytes,
+                            void *stream);
+
+/* Gradients from dy and what gated_ffn_fwd saved for the same x and weights.  Each of dx
+ * [tokens][hidden], dwg, dwu and dwd may be NULL (not wanted).  Errors as gated_ffn_fwd. */
+conv2d_status gated_ffn_bwd(gated_ffn_desc_t d, const void *dy, const void *x, const void *wg, const void *wu,
+                            const void *wd, const float *saved, void *dx, void *dwg, void *dwu, void *dwd,
+                            void *workspace, size_t workspace_bytes, void *stream);
 
 /* --------------------------------------------------------------------- AdamW
  * A step of `count` tensors at once, in place.  With g the gradient times

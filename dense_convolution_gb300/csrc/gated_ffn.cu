@@ -23,7 +23,8 @@
 // own rounding).  For fp16, whose range gradients leave easily, dg and du are held times a
 // power of two that takes the largest dy to [16, 32).  g and u are saved in fp32:
 // their rounding would pass through act' into every gradient, and the memory is idle
-// beside these products.
+// beside these products.  They lie as the epilogues' lanes, a row each, read them: four columns
+// of 32 rows are 512 bytes in a row.
 //
 // fp32 operands are split into three bf16 parts each and the six products of parts
 // that matter are accumulated, the small ones first; tensor memory then holds a few
@@ -72,7 +73,7 @@ struct FfnJobs {
     int act;
     int inner, fp;           // columns of h, and its pitch
     uint16_t *h, *dgu;       // [M][parts][fp], [M][parts][2][fp]
-    float* saved;            // [M][2][fp], or null
+    float* saved;            // [M / 32][2][fp / 4][32][4]: a warp's rows side by side, or null
     const uint32_t* largest; // maxima of |dy| (fp16), or null
     int maxima;
 };
@@ -225,22 +226,35 @@ __device__ __forceinline__ void store_out(const FfnJobs& jobs, const FfnJob& p, 
 #pragma unroll
         for (int i = 0; i < 16; ++i) stage[lane * 17 + i] = __float_as_uint(v[half * 16 + i]);
         __syncwarp();
-        const int c = half * 16 + (lane & 15);
-        for (int r = lane >> 4; r < rows; r += 2) {
-            if (c < n) {
-                float f = __uint_as_float(stage[r * 17 + (lane & 15)]);
-                if (p.res) f += load_out<BF16>(p.res, f32, (int64_t)(row0 + r) * p.ldr + c0 + c);
-                store_param(p.out, f32, BF16, (int64_t)(row0 + r) * p.ldo + c0 + c, f);
+        const int c = half * 16 + (lane & 15), r0 = lane >> 4;
+        // Eight rows' residuals are on their way together.
+#pragma unroll 1
+        for (int k0 = r0; k0 < 32; k0 += 16) {
+            float f[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                f[k] = p.res && c < n && k0 + 2 * k < rows
+                           ? load_out<BF16>(p.res, f32, (int64_t)(row0 + k0 + 2 * k) * p.ldr + c0 + c) : 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                if (c < n && k0 + 2 * k < rows)
+                    store_param(p.out, f32, BF16, (int64_t)(row0 + k0 + 2 * k) * p.ldo + c0 + c,
+                                f[k] + __uint_as_float(stage[(k0 + 2 * k) * 17 + (lane & 15)]));
             }
         }
     }
 }
 
+// Epilogue warps: sixteen where the activation or the adding of segments keeps them busy.
+__host__ __device__ constexpr int ffn_epi_warps(int product, bool promote) {
+    return epi_warps(promote || product == GATE || product == DGATE);
+}
+
 template <bool BF16, int PRODUCT, bool PROMOTE, bool PAIR>
-__global__ void __launch_bounds__(32 * (2 + epi_warps(PROMOTE)), 1)
+__global__ void __launch_bounds__(32 * (2 + ffn_epi_warps(PRODUCT, PROMOTE)), 1)
 ffn_gemm_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnJobs jobs) {
     constexpr bool B_MN = PRODUCT == DGATE || PRODUCT == GRADS;
-    constexpr int kEpiWarps = epi_warps(PROMOTE), kGroups = kEpiWarps / 4;
+    constexpr int kEpiWarps = ffn_epi_warps(PRODUCT, PROMOTE), kGroups = kEpiWarps / 4;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     constexpr int kTileM = PAIR ? 2 * kBM : kBM, kCtas = PAIR ? 2 : 1;
@@ -455,46 +469,49 @@ ffn_gemm_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ Ff
             const int row0 = it.m * kTileM + rank * kBM + quarter * 32, row = row0 + lane;
             const int n0 = it.n * (PRODUCT == GATE ? jobs.BN / 2 : jobs.BN);
             const bool live = row < p.M;
-            // Sixteen columns from c0 on of h, of dg and du: v is g or dh, w is u.
-            auto half_chunk = [&](int c0, float (&v)[16], float (&w)[16]) {
+            // Sixteen columns from c0 on of what is saved: of g, and jobs.fp * 32 further on of u.
+            auto saved_at = [&](int c0) {
+                return jobs.saved + (int64_t)(row0 / 32) * 64 * jobs.fp + (int64_t)c0 * 32 + lane * 4;
+            };
+            // Sixteen columns from c0 on of h, or of dg, du and h: v is g or dh, w is u (DGATE: g in `q`, u in `w`).
+            auto half_chunk = [&](int c0, float (&v)[16], float (&w)[16], float (&q)[16]) {
                 if (!live || c0 >= jobs.fp) return;
                 const int n = jobs.inner - c0;             // the pitch's last columns are zero
-                const int64_t at = (int64_t)row * 2 * jobs.fp + c0;
                 if constexpr (PRODUCT == GATE) {
                     if (jobs.saved) {
+                        float* at = saved_at(c0);
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            uint32_t r[8];
-#pragma unroll
-                            for (int l = 0; l < 8; ++l) r[l] = __float_as_uint(v[8 * k + l]);
-                            st_global_v8(jobs.saved + at + 8 * k, r);
-#pragma unroll
-                            for (int l = 0; l < 8; ++l) r[l] = __float_as_uint(w[8 * k + l]);
-                            st_global_v8(jobs.saved + at + jobs.fp + 8 * k, r);
+                        for (int k = 0; k < 4; ++k) {
+                            *reinterpret_cast<float4*>(at + k * 128) = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                            *reinterpret_cast<float4*>(at + (int64_t)jobs.fp * 32 + k * 128) =
+                                make_float4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
                         }
                     }
                     activate_all<!PROMOTE>(jobs.act, v, [&](int j, float a, float) { w[j] = j < n ? a * w[j] : 0.f; });
                     store16<BF16, PROMOTE>(jobs.h + (int64_t)row * jobs.parts * jobs.fp + c0, jobs.fp, jobs.parts, w);
                 } else {
-                    float g[16], u[16];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float4 s = reinterpret_cast<const float4*>(jobs.saved + at)[k];
-                        const float4 t = reinterpret_cast<const float4*>(jobs.saved + at + jobs.fp)[k];
-                        g[4 * k] = s.x; g[4 * k + 1] = s.y; g[4 * k + 2] = s.z; g[4 * k + 3] = s.w;
-                        u[4 * k] = t.x; u[4 * k + 1] = t.y; u[4 * k + 2] = t.z; u[4 * k + 3] = t.w;
-                    }
-                    float h[16];
-                    activate_all<!PROMOTE>(jobs.act, g, [&](int j, float a, float slope) {
-                        const float d = v[j] * up;
-                        h[j] = j < n ? a * u[j] : 0.f;
-                        v[j] = j < n ? d * u[j] * slope : 0.f;
+                    activate_all<!PROMOTE>(jobs.act, q, [&](int j, float a, float slope) {
+                        const float d = v[j] * up, u = w[j];
+                        q[j] = j < n ? a * u : 0.f;
+                        v[j] = j < n ? d * u * slope : 0.f;
                         w[j] = j < n ? d * a : 0.f;
                     });
                     uint16_t* dst = jobs.dgu + (int64_t)row * jobs.parts * 2 * jobs.fp + c0;
                     store16<BF16, PROMOTE>(dst, 2 * jobs.fp, jobs.parts, v);
                     store16<BF16, PROMOTE>(dst + jobs.fp, 2 * jobs.fp, jobs.parts, w);
-                    store16<BF16, PROMOTE>(jobs.h + (int64_t)row * jobs.parts * jobs.fp + c0, jobs.fp, jobs.parts, h);
+                    store16<BF16, PROMOTE>(jobs.h + (int64_t)row * jobs.parts * jobs.fp + c0, jobs.fp, jobs.parts, q);
+                }
+            };
+            auto load_saved = [&](int c0, float (&w)[16], float (&q)[16]) {
+                const bool in = live && c0 < jobs.fp;
+                const float* at = saved_at(c0);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+                    const float4 g = in ? *reinterpret_cast<const float4*>(at + k * 128) : z;
+                    const float4 u = in ? *reinterpret_cast<const float4*>(at + (int64_t)jobs.fp * 32 + k * 128) : z;
+                    q[4 * k] = g.x; q[4 * k + 1] = g.y; q[4 * k + 2] = g.z; q[4 * k + 3] = g.w;
+                    w[4 * k] = u.x; w[4 * k + 1] = u.y; w[4 * k + 2] = u.z; w[4 * k + 3] = u.w;
                 }
             };
             if constexpr (PROMOTE) {
@@ -541,19 +558,25 @@ ffn_gemm_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ Ff
                     if constexpr (PRODUCT == GATE || PRODUCT == DGATE) {
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            float v[16], w[16];
+                            float v[16], w[16], q[16];
+                            if constexpr (PRODUCT == DGATE) load_saved(c0 + e * 16, w, q);
 #pragma unroll
                             for (int j = 0; j < 16; ++j) {
                                 v[j] = sum[c][e * 16 + j];
-                                w[j] = PRODUCT == GATE ? sum[1][e * 16 + j] : 0.f;
+                                if (PRODUCT == GATE) w[j] = sum[1][e * 16 + j];
                             }
-                            half_chunk(c0 + e * 16, v, w);
+                            half_chunk(c0 + e * 16, v, w, q);
                         }
                     } else if (p.N > c0) {
                         store_out<BF16>(jobs, p, sum[c], row0, row, c0, it.split, down, stage, lane);
                     }
                 }
             } else {
+                float v[16], w[16], q[16];
+                // The first columns that were saved are on their way while the product is.
+                if constexpr (PRODUCT == DGATE) {
+                    if (c_lo < c_hi) load_saved(n0 + c_lo * 32, w, q);
+                }
                 if (!__all_sync(0xffffffffu, mbar_wait(accf_bar(acc), acc_phase, abort_flag))) break;
                 tc_fence_after();
                 const uint32_t t_row = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * 256);
@@ -564,7 +587,6 @@ ffn_gemm_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ Ff
 #pragma unroll 1
                         for (int e = 0; e < 2; ++e) {
                             uint32_t r[16];
-                            float v[16], w[16];
                             tmem_ld_32x32b_x16(t_row + c * 32 + e * 16, r);
                             if constexpr (PRODUCT == GATE) {
                                 uint32_t s[16];
@@ -573,11 +595,12 @@ ffn_gemm_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ Ff
 #pragma unroll
                                 for (int j = 0; j < 16; ++j) w[j] = __uint_as_float(s[j]);
                             } else {
+                                if (c > c_lo || e) load_saved(c0 + e * 16, w, q);
                                 tmem_ld_wait();
                             }
 #pragma unroll
                             for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
-                            half_chunk(c0 + e * 16, v, w);
+                            half_chunk(c0 + e * 16, v, w, q);
                         }
                     } else {
                         uint32_t r[32];
@@ -808,7 +831,7 @@ conv2d_status launch_gemm(bool bf16, const FfnTile& g, const FfnMaps& maps, FfnJ
         jobs.items += (int)items;
         // Rows that cannot take wide accesses, and ragged last columns, go through shared memory.
         if ((PRODUCT == ROWS || PRODUCT == GRADS) && p.splits == 1 && (!p.out_vec || (p.res && !p.res_vec) || p.N % 32 != 0))
-            jobs.epi_bytes = epi_warps(promote) * kStageWarpBytes;
+            jobs.epi_bytes = ffn_epi_warps(PRODUCT, promote) * kStageWarpBytes;
     }
     const int stage_bytes = kABytes + g.BN / ctas * kBK * 2;
     jobs.stages = (kSmemMost - kFixedSmem - jobs.epi_bytes) / stage_bytes;
@@ -817,7 +840,7 @@ conv2d_status launch_gemm(bool bf16, const FfnTile& g, const FfnMaps& maps, FfnJ
     const int units = g.pair ? pair_count() : device_sm_count();
     const int grid = (jobs.items < units ? jobs.items : units) * ctas;
     void* args[2] = {const_cast<FfnMaps*>(&maps), &jobs};
-    return launch_clusters(kern, grid, 32 * (2 + epi_warps(promote)), ctas, smem, st, args) == cudaSuccess
+    return launch_clusters(kern, grid, 32 * (2 + ffn_epi_warps(PRODUCT, promote)), ctas, smem, st, args) == cudaSuccess
                ? CONV2D_OK
                : CONV2D_ERR_CUDA;
 }

@@ -30,13 +30,14 @@ constexpr int kSmemMost = 200 * 1024;
 struct FfnFew {
     int tokens, cols, rows;      // cols: of the rows that are read; rows: inner, or hidden
     int team;                    // warps
+    int token0;                  // first token's number
     int act;
     int64_t xs, ys;              // tokens' row strides, in and out (GATE: out is h, `rows` wide)
     const void *x;               // tokens' values: the operands' type (GATE), or h
     const void *w, *w2;          // Wg and Wu, or Wd
     const void* res;
     float *h, *saved;
-    int64_t fp;                  // pitch of saved's halves
+    int64_t fp;                  // saved's columns of g
     void* y;
 };
 
@@ -59,13 +60,15 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) ffn_few_kernel(cons
         const T* w = static_cast<const T*>(GATE && r >= 2 ? p.w2 : p.w);
         return w + (int64_t)(r0 + r % kStep * V) * p.cols;
     };
-    if (!GATE && first < quads) {
-        const int r0 = row_of(first);
-        for (int r = 0; r < kRows; ++r) {
-            if (r0 + r * V >= p.rows) break;
-            const char* at = reinterpret_cast<const char*>(row_at(r0, r));
-            for (int64_t b = (int64_t)(part * 32 + lane) * 128; b < (int64_t)p.cols * (int)sizeof(T); b += (int64_t)p.team * 4096)
-                asm volatile("prefetch.global.L2 [%0];" ::"l"(at + b));
+    if (!GATE) {
+        for (int q = first; q < quads; q += teams) {
+            const int r0 = row_of(q);
+            for (int r = 0; r < kRows; ++r) {
+                if (r0 + r * V >= p.rows) break;
+                const char* at = reinterpret_cast<const char*>(row_at(r0, r));
+                for (int64_t b = (int64_t)(part * 32 + lane) * 128; b < (int64_t)p.cols * (int)sizeof(T); b += (int64_t)p.team * 4096)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(at + b));
+            }
         }
     }
     pdl_wait();
@@ -177,8 +180,10 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) ffn_few_kernel(cons
                     activate_all<false>(p.act, one, [&](int, float a, float) { h = a * u; });
                     p.h[(int64_t)t * p.ys + row] = h;
                     if (p.saved) {
-                        p.saved[(int64_t)t * 2 * p.fp + row] = g;
-                        p.saved[((int64_t)t * 2 + 1) * p.fp + row] = u;
+                        // (As gated_ffn.cu lays it out: fewer than 32 tokens are one block of rows.)
+                        float* at = p.saved + (row / 4) * 128 + (p.token0 + t) * 4 + row % 4;
+                        at[0] = g;
+                        at[p.fp * 32] = u;
                     }
                 }
             } else {
@@ -237,7 +242,8 @@ cudaError_t run(const gated_ffn_desc& d, const void* x, const void* wg, const vo
         p.w2 = wu;
         p.h = h;
         p.fp = (d.inner + 63) / 64 * 64;
-        p.saved = saved ? saved + t * 2 * p.fp : nullptr;
+        p.saved = saved;
+        p.token0 = (int)t;
         cudaError_t e = few_tokens<T, true>(p, d.sms, st);
         if (e != cudaSuccess) return e;
         p.cols = (int)d.inner;

@@ -325,11 +325,11 @@ class GatedFeedForward(_Op):
         self.desc = head_capi.gated_ffn_desc_create(tokens, hidden, inner, dtype, act)
         if self.x_stride != hidden or self.y_stride != hidden:
             head_capi.gated_ffn_desc_set_row_strides(self.desc, self.x_stride, self.y_stride)
-        self.workspace_bytes, self.backward_workspace_bytes, _ = head_capi.gated_ffn_workspace_size(self.desc)
+        self.workspace_bytes, self.backward_workspace_bytes, saved = head_capi.gated_ffn_workspace_size(self.desc)
         self._x, self._y = _Rows(tokens, hidden, self.x_stride, dtype), _Rows(tokens, hidden, self.y_stride, dtype)
         self._dx = _Rows(tokens, hidden, hidden, dtype)
         self._wh, self._wd = _Flat((inner, hidden), _TORCH_DTYPE[dtype]), _Flat((hidden, inner), _TORCH_DTYPE[dtype])
-        self._saved = _Flat((tokens, 2, -(-inner // 64) * 64), torch.float32)
+        self._saved = _Flat((saved // 4,), torch.float32)
 
     def _check(self, x, wg, wu, wd, dev):
         self._x.check("x", x, dev)

@@ -236,7 +236,7 @@ conv2d_status gated_ffn_workspace_size(gated_ffn_desc_t d, size_t *fwd_bytes, si
 
 /* y from x, the weights and residual (NULL: none).  y may be residual, and x where
  * their strides agree.  saved (NULL: not wanted) receives g and u for the backward
- * pass, [tokens][2][inner rounded up to 64] floats, 32-byte aligned.  x and the weights
+ * pass in fp32 and an order of its own, 32-byte aligned.  x and the weights
  * are 16-byte aligned (those that are copied, and all of fp32: as their elements), the workspace too.
  * Errors: NULL_PTR, MISALIGNED, WORKSPACE_TOO_SMALL, CUDA; UNSUPPORTED for more
  * tiles and splits than 2^31; bounded waits that expire are reported by

@@ -91,15 +91,6 @@ template <typename T> __device__ __forceinline__ void load8(const T* p, float (&
     widen(*reinterpret_cast<const Vec<T, 8>*>(p), f);
 }
 
-// N bytes to shared memory, behind this thread's back.
-template <int N> __device__ __forceinline__ void copy_async(uint32_t to, const void* from) {
-    if constexpr (N == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
-    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(N) : "memory");
-}
-__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// All but the last N groups have landed.
-template <int N> __device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
 // Eight values of 8 bits.  An e5m2 code is the high byte of an fp16 value; an e4m3 one,
 // its magnitude moved down by a bit, that of 2^-8 times its own, subnormal values
 // included.  (Conversions from integers run at an eighth of the rate.)

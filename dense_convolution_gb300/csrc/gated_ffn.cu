@@ -3,10 +3,10 @@
 //
 //   forward    g = x Wg^T and u = x Wu^T share a tile's accumulator, one half
 //              each; the epilogue turns them into h = act(g) u in 16 bits, so the
-//              pre-activations leave only when the backward pass wants them (fp32,
-//              saved).  Then y = residual + h Wd^T.
+//              pre-activations leave only when the backward pass wants them (saved, in
+//              fp32; h is then kept too).  Then y = residual + h Wd^T.
 //   backward   dh = dy Wd never leaves either: its epilogue reads the saved g and u
-//              and writes dg = dh u act'(g), du = dh act(g) and h again, 16 bits each.
+//              and writes dg = dh u act'(g) and du = dh act(g) in 16 bits.
 //              Then one launch has all products that are left, the long ones first:
 //              dx = [dg du] [Wg; Wu] (one product over both halves of K),
 //              dWg = dg^T x, dWu = du^T x, dWd = dy^T h.
@@ -72,7 +72,7 @@ struct FfnJobs {
     int pairs, parts, f32;
     int act;
     int inner, fp;           // columns of h, and its pitch
-    uint16_t *h, *dgu;       // [M][parts][fp], [M][parts][2][fp]
+    uint16_t *h, *dgu;       // GATE [M][parts][fp], DGATE [M][parts][2][fp]
     float* saved;            // [M / 32][2][fp / 4][32][4]: a warp's rows side by side, or null
     const uint32_t* largest; // maxima of |dy| (fp16), or null
     int maxima;
@@ -244,6 +244,8 @@ __device__ __forceinline__ void store_out(const FfnJobs& jobs, const FfnJob& p, 
         }
     }
 }
+
+constexpr int kSavedWarpBytes = 32 * 16 * 2 * 4;           // DGATE, a warp: sixteen columns of g and u of its rows
 
 // Epilogue warps: sixteen where the activation or the adding of segments keeps them busy.
 __host__ __device__ constexpr int ffn_epi_warps(int product, bool promote) {
@@ -449,17 +451,55 @@ ffn_gemm_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ Ff
         // reads TMEM lanes 32 (q mod 4)..: one output row a lane.  GATE: a chunk is
         // 32 columns of g and the same of u, half a tile further on.
         const int ew = warp - 2, group = ew >> 2, quarter = warp & 3;
-        uint32_t* stage = epi_stage + ew * (kStageWarpBytes / 4);
+        uint32_t* stage = epi_stage + ew * ((PRODUCT == DGATE ? kSavedWarpBytes : kStageWarpBytes) / 4);
         const int nch = jobs.BN / (PRODUCT == GATE ? 64 : 32), c_lo = nch * group / kGroups, c_hi = nch * (group + 1) / kGroups;
         const int u_col = jobs.BN / 2;
         float up = 1.f, down = 1.f;
         if constexpr (PRODUCT == DGATE) up = scale_of(jobs.largest, jobs.maxima, false);
         if constexpr (PRODUCT == GRADS) down = scale_of(jobs.largest, jobs.maxima, true);
-        // An emptied accumulator is reported to the CTA that issues the MMAs.
+        // An accumulator that this warp has read is reported to the CTA that issues the MMAs.
         auto emptied = [&](int a) {
-            if constexpr (PAIR) mbar_arrive_cluster(cluster_addr(acce_bar(a), 0));
-            else                mbar_arrive(acce_bar(a));
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (PAIR) mbar_arrive_cluster_read(cluster_addr(acce_bar(a), 0));
+                else                mbar_arrive(acce_bar(a));
+            }
         };
+        // DGATE: what is saved for the next sixteen columns (part e of chunk c of an item, or of the
+        // warp's next item) is on its way to shared memory while these are worked on, every lane's own
+        // values in its own places.
+        const uint32_t saved_to = smem_addr(stage) + lane * 16;
+        auto fetch_saved = [&](int n_item, int c, int e) {
+            if (c == c_hi) {
+                c = c_lo;
+                n_item += step;
+            }
+            if (n_item < jobs.items && c_lo < c_hi) {
+                const Item it = item_of(jobs.job[0], n_item);
+                const int row0 = it.m * kTileM + rank * kBM + quarter * 32, c0 = it.n * jobs.BN + c * 32 + e * 16;
+                if (row0 + lane < jobs.job[0].M && c0 < jobs.fp) {
+                    const float* at = jobs.saved + (int64_t)(row0 / 32) * 64 * jobs.fp + (int64_t)c0 * 32 + lane * 4;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        copy_async<16>(saved_to + k * 512, at + k * 128);
+                        copy_async<16>(saved_to + 2048 + k * 512, at + (int64_t)jobs.fp * 32 + k * 128);
+                    }
+                }
+            }
+            copy_async_commit();
+        };
+        auto take_saved = [&](float (&w)[16], float (&q)[16]) {
+            copy_async_wait<0>();
+            const float4* at = reinterpret_cast<const float4*>(stage);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float4 g = at[k * 32 + lane], u = at[128 + k * 32 + lane];
+                q[4 * k] = g.x; q[4 * k + 1] = g.y; q[4 * k + 2] = g.z; q[4 * k + 3] = g.w;
+                w[4 * k] = u.x; w[4 * k + 1] = u.y; w[4 * k + 2] = u.z; w[4 * k + 3] = u.w;
+            }
+        };
+        if constexpr (PRODUCT == DGATE) fetch_saved(first, c_lo, 0);
         int acc = 0;
         uint32_t acc_phase = 0;
         for (int n_item = first; n_item < jobs.items; n_item += step) {
@@ -473,7 +513,7 @@ ffn_gemm_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ Ff
             auto saved_at = [&](int c0) {
                 return jobs.saved + (int64_t)(row0 / 32) * 64 * jobs.fp + (int64_t)c0 * 32 + lane * 4;
             };
-            // Sixteen columns from c0 on of h, or of dg, du and h: v is g or dh, w is u (DGATE: g in `q`, u in `w`).
+            // Sixteen columns from c0 on of h, or of dg and du: v is g or dh, w is u, q is g (DGATE).
             auto half_chunk = [&](int c0, float (&v)[16], float (&w)[16], float (&q)[16]) {
                 if (!live || c0 >= jobs.fp) return;
                 const int n = jobs.inner - c0;             // the pitch's last columns are zero
@@ -492,26 +532,12 @@ ffn_gemm_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ Ff
                 } else {
                     activate_all<!PROMOTE>(jobs.act, q, [&](int j, float a, float slope) {
                         const float d = v[j] * up, u = w[j];
-                        q[j] = j < n ? a * u : 0.f;
                         v[j] = j < n ? d * u * slope : 0.f;
                         w[j] = j < n ? d * a : 0.f;
                     });
                     uint16_t* dst = jobs.dgu + (int64_t)row * jobs.parts * 2 * jobs.fp + c0;
                     store16<BF16, PROMOTE>(dst, 2 * jobs.fp, jobs.parts, v);
                     store16<BF16, PROMOTE>(dst + jobs.fp, 2 * jobs.fp, jobs.parts, w);
-                    store16<BF16, PROMOTE>(jobs.h + (int64_t)row * jobs.parts * jobs.fp + c0, jobs.fp, jobs.parts, q);
-                }
-            };
-            auto load_saved = [&](int c0, float (&w)[16], float (&q)[16]) {
-                const bool in = live && c0 < jobs.fp;
-                const float* at = saved_at(c0);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-                    const float4 g = in ? *reinterpret_cast<const float4*>(at + k * 128) : z;
-                    const float4 u = in ? *reinterpret_cast<const float4*>(at + (int64_t)jobs.fp * 32 + k * 128) : z;
-                    q[4 * k] = g.x; q[4 * k + 1] = g.y; q[4 * k + 2] = g.z; q[4 * k + 3] = g.w;
-                    w[4 * k] = u.x; w[4 * k + 1] = u.y; w[4 * k + 2] = u.z; w[4 * k + 3] = u.w;
                 }
             };
             if constexpr (PROMOTE) {
@@ -545,9 +571,7 @@ ffn_gemm_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ Ff
                             }
                         }
                     }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) emptied(acc);
+                    emptied(acc);
                     if (++acc == 2) { acc = 0; acc_phase ^= 1; }
                 }
                 if (!got) break;
@@ -559,7 +583,10 @@ ffn_gemm_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ Ff
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             float v[16], w[16], q[16];
-                            if constexpr (PRODUCT == DGATE) load_saved(c0 + e * 16, w, q);
+                            if constexpr (PRODUCT == DGATE) {
+                                take_saved(w, q);
+                                fetch_saved(n_item, c_lo + c + e, e ^ 1);
+                            }
 #pragma unroll
                             for (int j = 0; j < 16; ++j) {
                                 v[j] = sum[c][e * 16 + j];
@@ -573,10 +600,6 @@ ffn_gemm_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ Ff
                 }
             } else {
                 float v[16], w[16], q[16];
-                // The first columns that were saved are on their way while the product is.
-                if constexpr (PRODUCT == DGATE) {
-                    if (c_lo < c_hi) load_saved(n0 + c_lo * 32, w, q);
-                }
                 if (!__all_sync(0xffffffffu, mbar_wait(accf_bar(acc), acc_phase, abort_flag))) break;
                 tc_fence_after();
                 const uint32_t t_row = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * 256);
@@ -595,9 +618,11 @@ ffn_gemm_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ Ff
 #pragma unroll
                                 for (int j = 0; j < 16; ++j) w[j] = __uint_as_float(s[j]);
                             } else {
-                                if (c > c_lo || e) load_saved(c0 + e * 16, w, q);
+                                take_saved(w, q);
                                 tmem_ld_wait();
+                                fetch_saved(n_item, c + e, e ^ 1);
                             }
+                            if (c + 1 == c_hi && e) emptied(acc);
 #pragma unroll
                             for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
                             half_chunk(c0 + e * 16, v, w, q);
@@ -607,17 +632,17 @@ ffn_gemm_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ Ff
                         float v[32];
                         tmem_ld_32x32b_x32(t_row + c * 32, r);
                         tmem_ld_wait();
+                        if (c + 1 == c_hi) emptied(acc);
 #pragma unroll
                         for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
                         if (p.N > c0) store_out<BF16>(jobs, p, v, row0, row, c0, it.split, down, stage, lane);
                     }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) emptied(acc);
+                if (c_lo == c_hi) emptied(acc);
                 if (++acc == 2) { acc = 0; acc_phase ^= 1; }
             }
         }
+        if constexpr (PRODUCT == DGATE) copy_async_wait<0>();
     }
 
     tc_fence_before();
@@ -830,6 +855,7 @@ conv2d_status launch_gemm(bool bf16, const FfnTile& g, const FfnMaps& maps, FfnJ
         p.items = (int)items;
         jobs.items += (int)items;
         // Rows that cannot take wide accesses, and ragged last columns, go through shared memory.
+        if (PRODUCT == DGATE) jobs.epi_bytes = ffn_epi_warps(PRODUCT, promote) * kSavedWarpBytes;
         if ((PRODUCT == ROWS || PRODUCT == GRADS) && p.splits == 1 && (!p.out_vec || (p.res && !p.res_vec) || p.N % 32 != 0))
             jobs.epi_bytes = ffn_epi_warps(PRODUCT, promote) * kStageWarpBytes;
     }
@@ -968,8 +994,8 @@ void gated_ffn_plan(gated_ffn_desc& d) {
         }
         if (c.pack_wd) take(at, c.wdp, (size_t)D * c.fp * 2 * c.parts);
         if (c.pack_dy) take(at, c.dyp, (size_t)T * c.dp * 2 * c.parts);
-        take(at, c.h, (size_t)T * c.fp * 2 * c.parts);
         if (!pass) {
+            take(at, c.h, (size_t)T * c.fp * 2 * c.parts);
             const Sized gate{T, c.fp, nd * c.pairs, false, 1}, rows{T, D, nf * c.pairs, true, least(nf)};
             c.first = plan_tiles(&gate, 1, GATE);
             c.last = plan_tiles(&rows, 1, ROWS);
@@ -992,6 +1018,15 @@ void gated_ffn_plan(gated_ffn_desc& d) {
     }
 }
 
+// What is saved: g and u, then h as the products read it.
+size_t gated_ffn_saved_bytes(const gated_ffn_desc& d) {
+    const int64_t fp = ceil_div(d.inner, 64) * 64;
+    return (size_t)ceil_div(d.tokens, 32) * 64 * fp * 4 + (size_t)d.tokens * fp * 2 * (d.dtype == CONV2D_F32 ? 3 : 1);
+}
+uint16_t* gated_ffn_saved_h(const gated_ffn_desc& d, const float* saved) {
+    return reinterpret_cast<uint16_t*>(const_cast<float*>(saved) + ceil_div(d.tokens, 32) * 64 * (ceil_div(d.inner, 64) * 64));
+}
+
 conv2d_status launch_gated_ffn_fwd(const gated_ffn_desc& d, const void* x, const void* wg, const void* wu, const void* wd,
                                    const void* residual, void* y, float* saved, void* ws, cudaStream_t st) {
     const FfnPlan& c = d.fwd;
@@ -1008,7 +1043,7 @@ conv2d_status launch_gated_ffn_fwd(const gated_ffn_desc& d, const void* x, const
     FfnMaps maps;
     // h
     FfnJobs jobs = jobs_of(d, c);
-    jobs.h = reinterpret_cast<uint16_t*>(base + c.h);
+    jobs.h = saved ? gated_ffn_saved_h(d, saved) : reinterpret_cast<uint16_t*>(base + c.h);
     jobs.saved = saved;
     FfnJob& p = jobs.job[0];
     p.M = (int)T;
@@ -1050,7 +1085,7 @@ conv2d_status launch_gated_ffn_bwd(const gated_ffn_desc& d, const void* dy, cons
     if (s != CONV2D_OK) return s;
     FfnMaps maps;
     FfnJobs jobs = jobs_of(d, c);
-    jobs.h = reinterpret_cast<uint16_t*>(base + c.h);
+    uint16_t* h = gated_ffn_saved_h(d, saved);
     jobs.dgu = reinterpret_cast<uint16_t*>(base + c.dgu);
     jobs.saved = const_cast<float*>(saved);
     if (d.dtype == CONV2D_F16) {
@@ -1062,7 +1097,7 @@ conv2d_status launch_gated_ffn_bwd(const gated_ffn_desc& d, const void* dy, cons
             return CONV2D_ERR_CUDA;
         jobs.largest = largest;
     }
-    // dg, du and h
+    // dg and du
     FfnJob& p = jobs.job[0];
     p.M = (int)T;
     p.N = (int)c.fp;
@@ -1121,7 +1156,7 @@ conv2d_status launch_gated_ffn_bwd(const gated_ffn_desc& d, const void* dy, cons
         q.b_part = (int)c.fp;
         last.job[j] = q;
         if (!make_map(&maps.a[j], o.dy.base, c.bf16, T, o.dy.cols, o.dy.pitch, 64) ||
-            !make_map(&maps.b[j], jobs.h, c.bf16, T, c.fp * c.parts, c.fp * c.parts, 64))
+            !make_map(&maps.b[j], h, c.bf16, T, c.fp * c.parts, c.fp * c.parts, 64))
             return CONV2D_ERR_CUDA;
     }
     for (int j = last.n; j < 4; ++j) { maps.a[j] = maps.a[0]; maps.b[j] = maps.b[0]; }

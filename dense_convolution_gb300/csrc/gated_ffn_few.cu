@@ -17,6 +17,7 @@
 #include "gated_ffn_device.cuh"
 #include "head_device.cuh"
 #include "head_few.cuh"
+#include "head_parts.cuh"
 #include "head_internal.h"
 #include "ptx.cuh"
 
@@ -37,6 +38,7 @@ struct FfnFew {
     const void *w, *w2;          // Wg and Wu, or Wd
     const void* res;
     float *h, *saved;
+    uint16_t* kept;              // h as it is saved
     int64_t fp;                  // saved's columns of g
     void* y;
 };
@@ -184,6 +186,15 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) ffn_few_kernel(cons
                         float* at = p.saved + (row / 4) * 128 + (p.token0 + t) * 4 + row % 4;
                         at[0] = g;
                         at[p.fp * 32] = u;
+                        uint16_t* kept = p.kept + (int64_t)(p.token0 + t) * p.fp * (sizeof(T) == 4 ? 3 : 1) + row;
+                        if constexpr (sizeof(T) == 4) {
+                            float part[3];
+                            split3(h, part);
+#pragma unroll
+                            for (int k = 0; k < 3; ++k) reinterpret_cast<__nv_bfloat16*>(kept)[k * p.fp] = __float2bfloat16_rn(part[k]);
+                        } else {
+                            *reinterpret_cast<T*>(kept) = from_f32<T>(h);
+                        }
                     }
                 }
             } else {
@@ -243,6 +254,7 @@ cudaError_t run(const gated_ffn_desc& d, const void* x, const void* wg, const vo
         p.h = h;
         p.fp = (d.inner + 63) / 64 * 64;
         p.saved = saved;
+        p.kept = saved ? gated_ffn_saved_h(d, saved) : nullptr;
         p.token0 = (int)t;
         cudaError_t e = few_tokens<T, true>(p, d.sms, st);
         if (e != cudaSuccess) return e;

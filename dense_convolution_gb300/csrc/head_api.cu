@@ -313,7 +313,7 @@ CONV2D_API conv2d_status gated_ffn_workspace_size(gated_ffn_desc_t d, size_t* fw
     if (!d || (!fwd_bytes && !bwd_bytes && !saved_bytes)) return CONV2D_ERR_NULL_PTR;
     if (fwd_bytes) *fwd_bytes = d->fwd.total;
     if (bwd_bytes) *bwd_bytes = d->bwd.total;
-    if (saved_bytes) *saved_bytes = (size_t)((d->tokens + 31) / 32 * 32) * 2 * ((d->inner + 63) / 64 * 64) * sizeof(float);
+    if (saved_bytes) *saved_bytes = gated_ffn_saved_bytes(*d);
     return CONV2D_OK;
 }
 

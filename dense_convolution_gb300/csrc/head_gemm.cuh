@@ -9,6 +9,7 @@
 
 #include "head_device.cuh"
 #include "head_internal.h"
+#include "head_parts.cuh"
 #include "ptx.cuh"
 
 namespace conv2d_gb300 {
@@ -41,21 +42,6 @@ template <bool BF16> __device__ __forceinline__ uint32_t pack2(float a, float b)
 
 template <bool BF16> __device__ __forceinline__ void unpack2(uint32_t w, float& a, float& b) {
     unpack2f(widen_pair<std::conditional_t<BF16, __nv_bfloat16, __half>>(w), a, b);
-}
-
-// The bf16 nearest to x (toward zero where that would overflow), and what is
-// left for the next part: three parts hold all 24 bits of a float.
-__device__ __forceinline__ float part_of(float x) {
-    __nv_bfloat16 a = __float2bfloat16_rn(x);
-    if (__hisinf(a) && !isinf(x)) a = __float2bfloat16_rz(x);
-    return __bfloat162float(a);
-}
-__device__ __forceinline__ float rest_of(float x, float part) { return isfinite(part) ? x - part : 0.f; }
-__device__ __forceinline__ void split3(float x, float (&p)[3]) {
-    p[0] = part_of(x);
-    x = rest_of(x, p[0]);
-    p[1] = part_of(x);
-    p[2] = part_of(rest_of(x, p[1]));
 }
 
 // Rows of T as [rows][parts * pitch] 16-bit values for the tensor cores, zero

@@ -143,6 +143,9 @@ conv2d_status launch_gated_ffn_bwd(const gated_ffn_desc& d, const void* dy, cons
                                    const void* wd, const float* saved, void* dx, void* dwg, void* dwu, void* dwd, void* ws,
                                    cudaStream_t st);
 
+size_t gated_ffn_saved_bytes(const gated_ffn_desc& d);
+uint16_t* gated_ffn_saved_h(const gated_ffn_desc& d, const float* saved);      // [tokens][parts][inner rounded up to 64]
+
 // gated_ffn_few.cu: few tokens, forward, on the CUDA cores
 bool gated_ffn_is_few(const gated_ffn_desc& d);
 int64_t gated_ffn_few_words(const gated_ffn_desc& d);      // fp32 words of h

@@ -195,6 +195,11 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t a, uint32_t rank) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// The same without ordering the thread's global stores first, which takes as long as the last of them:
+// for barriers that say only that tensor memory has been read.
+__device__ __forceinline__ void mbar_arrive_cluster_read(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
 // 32-bit word to a cluster address (before a meeting of the cluster: the CTA it
 // belongs to must still be there).
 __device__ __forceinline__ void st_cluster(uint32_t a, uint32_t v) {
@@ -215,6 +220,16 @@ __device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&v)[8]) {
                  "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                  : "memory");
 }
+
+// ---------------------------------------------------------------- asynchronous copies
+// N bytes (4, 8 or 16, aligned alike) to shared memory; this thread sees them after copy_async_wait.
+template <int N> __device__ __forceinline__ void copy_async(uint32_t to, const void* from) {
+    if constexpr (N == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(N) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the last N groups have landed.
+template <int N> __device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // ---------------------------------------------------------------- TMA
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* map) {

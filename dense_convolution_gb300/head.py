@@ -329,7 +329,7 @@ class GatedFeedForward(_Op):
         self._x, self._y = _Rows(tokens, hidden, self.x_stride, dtype), _Rows(tokens, hidden, self.y_stride, dtype)
         self._dx = _Rows(tokens, hidden, hidden, dtype)
         self._wh, self._wd = _Flat((inner, hidden), _TORCH_DTYPE[dtype]), _Flat((hidden, inner), _TORCH_DTYPE[dtype])
-        self._saved = _Flat((saved // 4,), torch.float32)
+        self._saved = _Flat((saved,), torch.uint8)
 
     def _check(self, x, wg, wu, wd, dev):
         self._x.check("x", x, dev)

@@ -202,7 +202,7 @@ conv2d_status linear_ce_bwd(linear_ce_desc_t d, const void *h, const void *w, co
  *   g = x Wg^T,  u = x Wu^T,  h = act(g) u,  y = residual + h Wd^T,
  * act(g) = g / (1 + exp(-g)) (SILU), g Phi(g) (GELU, Phi the normal
  * distribution) or g / (1 + exp(-2 sqrt(2/pi) (g + 0.044715 g^3))) (GELU_TANH).
- * Backward, from dy and the saved g and u:
+ * Backward, from dy and the saved g, u and h:
  *   dh = dy Wd,  dg = dh u act'(g),  du = dh act(g),  dx = dg Wg + du Wu,
  *   dWg = dg^T x,  dWu = du^T x,  dWd = dy^T h    (the residual's gradient is dy).
  * fp16 and bf16 run on the tensor cores with fp32 accumulation; g, u and dh stay
@@ -235,8 +235,8 @@ conv2d_status gated_ffn_desc_destroy(gated_ffn_desc_t d);
 conv2d_status gated_ffn_workspace_size(gated_ffn_desc_t d, size_t *fwd_bytes, size_t *bwd_bytes, size_t *saved_bytes);
 
 /* y from x, the weights and residual (NULL: none).  y may be residual, and x where
- * their strides agree.  saved (NULL: not wanted) receives g and u for the backward
- * pass in fp32 and an order of its own, 32-byte aligned.  x and the weights
+ * their strides agree.  saved (NULL: not wanted) receives g and u (fp32) and h for the
+ * backward pass, in an order of its own, 32-byte aligned.  x and the weights
  * are 16-byte aligned (those that are copied, and all of fp32: as their elements), the workspace too.
  * Errors: NULL_PTR, MISALIGNED, WORKSPACE_TOO_SMALL, CUDA; UNSUPPORTED for more
  * tiles and splits than 2^31; bounded waits that expire are reported by

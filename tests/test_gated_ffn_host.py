@@ -49,7 +49,7 @@ def test_strides_and_sizes(capi, head):
     for xs, ys in ((63, 64), (64, 63), (1 << 39, 64), (64, 1 << 39)):
         assert _status(capi, head.gated_ffn_desc_set_row_strides, d, xs, ys) == capi.ERR_BAD_PARAM
     f, b, s = head.gated_ffn_workspace_size(d)
-    assert s == 128 * 2 * 256 * 4 and f >= 100 * 256 * 2 and b >= 3 * 100 * 256 * 2
+    assert s == 128 * 2 * 256 * 4 + 100 * 256 * 2 and f >= 100 * 256 * 2 and b >= 2 * 100 * 256 * 2
     head.gated_ffn_desc_set_row_strides(d, 67, 65)                # both are copied now
     f2, b2, s2 = head.gated_ffn_workspace_size(d)
     assert f2 >= f + 100 * 64 * 2 and b2 >= b + 2 * 100 * 64 * 2 and s2 == s

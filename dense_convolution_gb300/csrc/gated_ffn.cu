@@ -34,6 +34,8 @@
 #include <cuda.h>
 #include <math.h>
 
+#include <initializer_list>
+
 #include "gated_ffn_device.cuh"
 #include "head_device.cuh"
 #include "head_gemm.cuh"
@@ -67,6 +69,7 @@ struct FfnJob {
 struct FfnJobs {
     FfnJob job[4];
     int n, items;
+    int extra;               // items of the others that take as long as one of the first
     int BN, stages, seg;     // tile width, ring depth; PROMOTE: chunks per accumulation in tensor memory
     int epi_bytes;           // epilogue staging in shared memory (0: none needed)
     int pairs, parts, f32;
@@ -303,8 +306,21 @@ ffn_gemm_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ Ff
     pdl_wait();
     pdl_launch_dependents();
 
-    // Items are dealt out in turn; every role walks them alike.
-    const int first = blockIdx.x / kCtas, step = gridDim.x / kCtas;
+    // Items are dealt out in turn; every role walks them alike.  Units that get one fewer of the
+    // first, longer product's items get `extra` of the others' before all take turns again.
+    const int unit = blockIdx.x / kCtas, units = gridDim.x / kCtas;
+    const int long_items = jobs.job[0].items, more = long_items % units, in_turn = long_items + jobs.extra * (units - more);
+    auto after = [&](int i) {
+        if (PRODUCT != GRADS || !jobs.extra || i >= in_turn) return i + units;
+        if (i < long_items) {
+            if (i + units < long_items) return i + units;
+            if (unit >= more) return long_items + unit - more;
+        } else if (i + units - more < in_turn) {
+            return i + units - more;
+        }
+        return in_turn + unit;
+    };
+    const int first = PRODUCT != GRADS || unit < long_items ? unit : after(unit - units);
     auto job_of = [&](int& i) {                            // product of item i, which becomes its number there
         int j = 0;
         if constexpr (PRODUCT == GRADS) {
@@ -319,7 +335,7 @@ ffn_gemm_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ Ff
             int stage = 0;
             uint32_t phase = 0;
             long long issued = 0;
-            for (int n_item = first; n_item < jobs.items && ok; n_item += step) {
+            for (int n_item = first; n_item < jobs.items && ok; n_item = after(n_item)) {
                 int i = n_item;
                 const int j = job_of(i);
                 const FfnJob& p = jobs.job[j];
@@ -399,7 +415,7 @@ ffn_gemm_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ Ff
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
             bool ok = true, issued_any = false;
-            for (int n_item = first; n_item < jobs.items && ok; n_item += step) {
+            for (int n_item = first; n_item < jobs.items && ok; n_item = after(n_item)) {
                 int i = n_item;
                 const FfnJob& p = jobs.job[job_of(i)];
                 const int split = i / (p.n_m * p.n_n), chunks = p.nk * jobs.pairs;
@@ -473,7 +489,7 @@ ffn_gemm_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ Ff
         auto fetch_saved = [&](int n_item, int c, int e) {
             if (c == c_hi) {
                 c = c_lo;
-                n_item += step;
+                n_item = after(n_item);
             }
             if (n_item < jobs.items && c_lo < c_hi) {
                 const Item it = item_of(jobs.job[0], n_item);
@@ -502,7 +518,7 @@ ffn_gemm_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ Ff
         if constexpr (PRODUCT == DGATE) fetch_saved(first, c_lo, 0);
         int acc = 0;
         uint32_t acc_phase = 0;
-        for (int n_item = first; n_item < jobs.items; n_item += step) {
+        for (int n_item = first; n_item < jobs.items; n_item = after(n_item)) {
             int i = n_item;
             const FfnJob& p = jobs.job[job_of(i)];
             const Item it = item_of(p, i);
@@ -759,6 +775,12 @@ int64_t most_chunks(bool bf16) { return bf16 ? 2048 : 256; }
 // One product of a launch, for the estimate.
 struct Sized { int64_t M, N, chunks; bool may_split; int64_t least; };
 
+// Items of the other products that take as long as one of the first.
+int extra_turns(double first, double rest) {
+    const int n = (int)(first / rest + 0.5);
+    return n < 1 ? 1 : n;
+}
+
 // Tile width, CTA pairs and K splits of a launch's products by an estimate in SM
 // cycles.  A 64-wide chunk takes its MMAs (2 BN cycles) or its operands' way from
 // the L2 (75 bytes a cycle and SM), and a fixed cost; an item (one tile of one
@@ -802,15 +824,17 @@ FfnTile plan_tiles(const Sized* pr, int n, Product product) {
                     start[j + 1] = start[j] + ceil_div(pr[j].M, rows) * ceil_div(pr[j].N * share, bn) * k;
                     if (k > 1) extra += 4000.0 + (double)k * pr[j].M * pr[j].N * 8.0 / 3500.0;
                 }
-                // The unit with the most work is one where some product's items begin.
+                // The unit with the most work is the first one, or the first of those with one item fewer of the first
+                // product (see the kernel's order).
+                const int64_t more = start[1] % units, total = start[n];
+                double rest = 0;
+                for (int j = 1; j < n; ++j) rest = each[j] > rest ? each[j] : rest;
+                const int64_t turns = n > 1 ? extra_turns(each[0], rest) : 0, in_turn = start[1] + turns * (units - more);
                 double t = 0;
-                for (int b = 0; b < n; ++b) {
-                    const int64_t u = start[b] % units;
-                    double load = 0;
-                    for (int j = 0; j < n; ++j) {
-                        const auto before = [&](int64_t i) { return i > u ? (i - u + units - 1) / units : 0; };
-                        load += (double)(before(start[j + 1]) - before(start[j])) * each[j];
-                    }
+                for (int64_t u : {(int64_t)0, more}) {
+                    const auto count = [&](int64_t from, int64_t to, int64_t by) { return to > from ? (to - from + by - 1) / by : 0; };
+                    double load = (double)count(u, start[1], units) * each[0] + (double)count(in_turn + u, total, units) * rest;
+                    if (u >= more) load += (double)count(start[1] + u - more, in_turn < total ? in_turn : total, units - more) * rest;
                     t = load > t ? load : t;
                 }
                 t += extra;
@@ -818,9 +842,9 @@ FfnTile plan_tiles(const Sized* pr, int n, Product product) {
                     best_t = t;
                     best = tile;
                 }
-                bool more = false;
-                for (int j = 0; j < n; ++j) more = more || pr[j].may_split;
-                if (!more) break;
+                bool splits = false;
+                for (int j = 0; j < n; ++j) splits = splits || pr[j].may_split;
+                if (!splits) break;
             }
         }
     }
@@ -859,6 +883,11 @@ conv2d_status launch_gemm(bool bf16, const FfnTile& g, const FfnMaps& maps, FfnJ
         if ((PRODUCT == ROWS || PRODUCT == GRADS) && p.splits == 1 && (!p.out_vec || (p.res && !p.res_vec) || p.N % 32 != 0))
             jobs.epi_bytes = ffn_epi_warps(PRODUCT, promote) * kStageWarpBytes;
     }
+    // (An item's fixed cost is that of about six chunks.)
+    int rest = 0;
+    const auto length = [&](const FfnJob& p) { return (int)ceil_div((int64_t)p.nk * jobs.pairs, p.splits) + 6; };
+    for (int j = 1; j < jobs.n; ++j) rest = length(jobs.job[j]) > rest ? length(jobs.job[j]) : rest;
+    jobs.extra = jobs.n > 1 ? extra_turns(length(jobs.job[0]), rest) : 0;
     const int stage_bytes = kABytes + g.BN / ctas * kBK * 2;
     jobs.stages = (kSmemMost - kFixedSmem - jobs.epi_bytes) / stage_bytes;
     if (jobs.stages > kMaxRing) jobs.stages = kMaxRing;

@@ -31,9 +31,25 @@ template <int ACT, bool FAST> __device__ __forceinline__ void activate(float g, 
         a = g * s;
         slope = s * fmaf(g, q, 1.f);
     } else if constexpr (ACT == FFN_GELU) {
-        const float phi = fmaf(0.5f, erff(g * 0.70710678118654752f), 0.5f);
+        float phi;
+        const float e = exp_of<FAST>(-0.5f * g * g);
+        if constexpr (FAST) {
+            // erfc by a polynomial in 1 / (1 + p x) times exp(-x^2), x = |g| / sqrt 2, off by 1.5e-7 at most
+            // (Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26): the slope wants that exponential
+            // too, and erff takes three times as long.
+            const float t = inverse_of<true>(fmaf(0.3275911f * 0.70710678118654752f, fabsf(g), 1.f));
+            float q = fmaf(t, 1.061405429f, -1.453152027f);
+            q = fmaf(t, q, 1.421413741f);
+            q = fmaf(t, q, -0.284496736f);
+            q = fmaf(t, q, 0.254829592f);
+            q *= 0.5f * t * e;
+            phi = g > 0.f ? 1.f - q : q;
+            if (isnan(g)) phi = g;
+        } else {
+            phi = fmaf(0.5f, erff(g * 0.70710678118654752f), 0.5f);
+        }
         a = g * phi;
-        slope = fmaf(g * 0.39894228040143268f, exp_of<FAST>(-0.5f * g * g), phi);
+        slope = fmaf(g * 0.39894228040143268f, e, phi);
     } else {
         // 0.5 (1 + tanh z) = 1 / (1 + exp(-2 z)), z = sqrt(2 / pi) (g + 0.044715 g^3).
         constexpr float k = 1.5957691216057308f, c = 0.044715f;      // 2 sqrt(2 / pi)

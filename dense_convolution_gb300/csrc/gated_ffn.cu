@@ -543,7 +543,7 @@ ffn_gemm_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ Ff
                                 make_float4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
                         }
                     }
-                    activate_all<!PROMOTE>(jobs.act, v, [&](int j, float a, float) { w[j] = j < n ? a * w[j] : 0.f; });
+                    activated_all<!PROMOTE>(jobs.act, v, [&](int j, float a) { w[j] = j < n ? a * w[j] : 0.f; });
                     store16<BF16, PROMOTE>(jobs.h + (int64_t)row * jobs.parts * jobs.fp + c0, jobs.fp, jobs.parts, w);
                 } else {
                     activate_all<!PROMOTE>(jobs.act, q, [&](int j, float a, float slope) {
@@ -557,15 +557,17 @@ ffn_gemm_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ Ff
                 }
             };
             if constexpr (PROMOTE) {
-                // This warp's share of the tile's sums, in registers: two chunks, or one of g and one of u.
-                float sum[2][32];
+                // This warp's share of the tile's sums, in registers: two chunks, or one of g and one of u (one of dh, whose
+                // tiles are 128 columns at most: the activation needs the registers).
+                constexpr int kKept = PRODUCT == DGATE ? 1 : 2;
+                float sum[kKept][32];
                 const int col[2] = {c_lo * 32, PRODUCT == GATE ? u_col + c_lo * 32 : c_lo * 32 + 32};
                 const bool has[2] = {c_lo < c_hi, PRODUCT == GATE ? c_lo < c_hi : c_lo + 1 < c_hi};
                 const int chunks = p.nk * jobs.pairs;
                 const int k0 = (int)((long long)chunks * it.split / p.splits);
                 const int k1 = (int)((long long)chunks * (it.split + 1) / p.splits);
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
+                for (int c = 0; c < kKept; ++c)
 #pragma unroll
                     for (int j = 0; j < 32; ++j) sum[c][j] = 0.f;
                 bool got = true;
@@ -575,7 +577,7 @@ ffn_gemm_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ Ff
                     tc_fence_after();
                     const uint32_t t_row = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * 256);
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
+                    for (int c = 0; c < kKept; ++c) {
                         if (has[c]) {
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {      // 16 at a time: the sums leave few registers
@@ -592,7 +594,7 @@ ffn_gemm_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ Ff
                 }
                 if (!got) break;
 #pragma unroll
-                for (int c = 0; c < (PRODUCT == GATE ? 1 : 2); ++c) {
+                for (int c = 0; c < (PRODUCT == ROWS || PRODUCT == GRADS ? 2 : 1); ++c) {
                     if (!has[c]) continue;
                     const int c0 = n0 + (c_lo + c) * 32;
                     if constexpr (PRODUCT == GATE || PRODUCT == DGATE) {
@@ -606,7 +608,7 @@ ffn_gemm_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ Ff
 #pragma unroll
                             for (int j = 0; j < 16; ++j) {
                                 v[j] = sum[c][e * 16 + j];
-                                if (PRODUCT == GATE) w[j] = sum[1][e * 16 + j];
+                                if constexpr (PRODUCT == GATE) w[j] = sum[1][e * 16 + j];
                             }
                             half_chunk(c0 + e * 16, v, w, q);
                         }
@@ -788,7 +790,7 @@ int extra_turns(double first, double rest) {
 // turn, so the load of each follows; splits add the write and read of their fp32 sums
 // and one launch.  All products are split so that their items are about equally
 // long; up to 64 lengths are weighed.
-FfnTile plan_tiles(const Sized* pr, int n, Product product) {
+FfnTile plan_tiles(const Sized* pr, int n, Product product, bool f32) {
     const bool b_mn = product == DGATE || product == GRADS;
     FfnTile best{256, false, {1, 1, 1, 1}};
     double best_t = -1;
@@ -805,7 +807,7 @@ FfnTile plan_tiles(const Sized* pr, int n, Product product) {
         // Boxes of whole 64 columns (MN-major), half tiles of whole chunks of g and of u, half of either for each CTA.
         const int down = b_mn ? (pair ? 128 : 64) : product == GATE ? 64 : 32;
         const int smallest = pair ? 128 : 64;
-        for (int bn = 256; bn >= smallest; bn -= down) {
+        for (int bn = product == DGATE && f32 ? 128 : 256; bn >= smallest; bn -= down) {
             if ((bn - down) / share >= most_n && bn - down >= smallest) continue;      // wider than the output needs
             const double bytes = kABytes + (pair ? bn / 2 : bn) * kBK * 2;
             const double chunk = (2.0 * bn > bytes / 75.0 ? 2.0 * bn : bytes / 75.0) + 24.0;
@@ -1026,19 +1028,19 @@ void gated_ffn_plan(gated_ffn_desc& d) {
         if (!pass) {
             take(at, c.h, (size_t)T * c.fp * 2 * c.parts);
             const Sized gate{T, c.fp, nd * c.pairs, false, 1}, rows{T, D, nf * c.pairs, true, least(nf)};
-            c.first = plan_tiles(&gate, 1, GATE);
-            c.last = plan_tiles(&rows, 1, ROWS);
+            c.first = plan_tiles(&gate, 1, GATE, f32);
+            c.last = plan_tiles(&rows, 1, ROWS, f32);
             if (c.last.splits[0] > 1) take(at, c.sums[0], (size_t)c.last.splits[0] * T * c.dp * 4);
         } else {
             take(at, c.dgu, (size_t)T * 2 * c.fp * 2 * c.parts);
             take(at, c.largest, (size_t)d.sms * 4);
             const Sized dgate{T, c.fp, nd * c.pairs, false, 1};
-            c.first = plan_tiles(&dgate, 1, DGATE);
+            c.first = plan_tiles(&dgate, 1, DGATE, f32);
             const Sized grads[4] = {{T, D, 2 * nf * c.pairs, true, least(2 * nf)},
                                     {F, D, nt * c.pairs, true, least(nt)},
                                     {F, D, nt * c.pairs, true, least(nt)},
                                     {D, F, nt * c.pairs, true, least(nt)}};
-            c.last = plan_tiles(grads, 4, GRADS);
+            c.last = plan_tiles(grads, 4, GRADS, f32);
             const size_t sums[4] = {(size_t)T * c.dp, (size_t)F * c.dp, (size_t)F * c.dp, (size_t)D * c.fp};
             for (int j = 0; j < 4; ++j)
                 if (c.last.splits[j] > 1) take(at, c.sums[j], (size_t)c.last.splits[j] * sums[j] * 4);

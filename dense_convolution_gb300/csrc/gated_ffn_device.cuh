@@ -3,6 +3,8 @@
 
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "../../include/head.h"
 
 namespace conv2d_gb300 {
@@ -60,18 +62,45 @@ template <int ACT, bool FAST> __device__ __forceinline__ void activate(float g, 
         slope = fmaf(g * k * fmaf(3.f * c, gg, 1.f), s * q, s);
     }
 }
+// act(g) alone, where its slope is not wanted: for silu and gelu_tanh an exponential that may overflow is in its
+// place, 1 / (1 + inf) being 0.
+template <int ACT, bool FAST> __device__ __forceinline__ float activated(float g) {
+    if constexpr (FAST && ACT != FFN_GELU) {
+        constexpr float k = 1.5957691216057308f, c = 0.044715f, log2e = 1.4426950408889634f;
+        const float z = ACT == FFN_SILU ? -log2e * g : -log2e * k * g * fmaf(c, g * g, 1.f);
+        float e, r;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+        return g * r;
+    } else {
+        float a, slope;
+        activate<ACT, FAST>(g, a, slope);
+        return a;
+    }
+}
 // f(a, slope) for each of N pre-activations.
 template <bool FAST, int N, typename F> __device__ __forceinline__ void activate_all(int act, const float (&g)[N], F f) {
-#define FFN_EACH(ACT)                        \
-    _Pragma("unroll") for (int j = 0; j < N; ++j) { \
-        float a, slope;                      \
-        activate<ACT, FAST>(g[j], a, slope); \
-        f(j, a, slope);                      \
-    }
-    if (act == FFN_SILU) { FFN_EACH(FFN_SILU) }
-    else if (act == FFN_GELU) { FFN_EACH(FFN_GELU) }
-    else { FFN_EACH(FFN_GELU_TANH) }
-#undef FFN_EACH
+    const auto each = [&](auto kind) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            float a, slope;
+            activate<decltype(kind)::value, FAST>(g[j], a, slope);
+            f(j, a, slope);
+        }
+    };
+    if (act == FFN_SILU) each(std::integral_constant<int, FFN_SILU>{});
+    else if (act == FFN_GELU) each(std::integral_constant<int, FFN_GELU>{});
+    else each(std::integral_constant<int, FFN_GELU_TANH>{});
+}
+// f(a) for each of them.
+template <bool FAST, int N, typename F> __device__ __forceinline__ void activated_all(int act, const float (&g)[N], F f) {
+    const auto each = [&](auto kind) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) f(j, activated<decltype(kind)::value, FAST>(g[j]));
+    };
+    if (act == FFN_SILU) each(std::integral_constant<int, FFN_SILU>{});
+    else if (act == FFN_GELU) each(std::integral_constant<int, FFN_GELU>{});
+    else each(std::integral_constant<int, FFN_GELU_TANH>{});
 }
 
 }  // namespace conv2d_gb300

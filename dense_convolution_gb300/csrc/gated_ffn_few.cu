@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) ffn_few_kernel(cons
                 const float g = total(k), u = total(k + 2 * NT);
                 float h = 0.f;
                 const float one[1] = {g};
-                activate_all<false>(p.act, one, [&](int, float a, float) { h = a * u; });
+                activated_all<false>(p.act, one, [&](int, float a) { h = a * u; });
                 p.h[(int64_t)t * p.ys + row] = h;
                 if (p.saved) {
                     // (As gated_ffn.cu lays it out: up to 32 tokens are one block of rows.)

@@ -9,15 +9,23 @@
 
 namespace conv2d_gb300 {
 
-// act(g) and its slope.  FAST (16-bit results): approximate exponentials and reciprocals,
-// good to 2^-21.
+// act(g) and its slope.  FAST (16-bit results): approximate exponentials and reciprocals, good to
+// 2^-21.  Else the exponential's argument is multiplied by log2 e in two parts, which leaves the approximation's
+// 2^-22, and the reciprocal takes a Newton step: a third of the instructions of expf and a division, which
+// a tile's only pass through the epilogue would wait for.
 template <bool FAST> __device__ __forceinline__ float exp_of(float x) {
     if constexpr (FAST) return __expf(x);
-    else return expf(x);
+    constexpr float hi = 1.4426950216293335f, lo = 1.9259629911e-8f, ln2 = 0.69314718055994531f;
+    const float t = x * hi, rest = fmaf(x, lo, fmaf(x, hi, -t));
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+    return t > -127.f ? fmaf(e, rest * ln2, e) : 0.f;          // (`rest` of an infinity is none)
 }
-template <bool FAST> __device__ __forceinline__ float inverse_of(float x) {
+template <bool FAST> __device__ __forceinline__ float inverse_of(float x) {      // x in [1, 2]
     if constexpr (FAST) return __fdividef(1.f, x);
-    else return 1.f / x;
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return fmaf(r, fmaf(-x, r, 1.f), r);
 }
 // 1 / (1 + exp(-z)) and what it is from 1, neither by a difference.
 template <bool FAST> __device__ __forceinline__ void sigmoid(float z, float& s, float& q) {

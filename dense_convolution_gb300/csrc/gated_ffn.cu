@@ -464,11 +464,12 @@ ffn_gemm_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ Ff
     } else {
         // ------------------------------------------------------------ epilogue
         // Groups of four warps share an accumulator's columns; warp q (mod 4)
-        // reads TMEM lanes 32 (q mod 4)..: one output row a lane.  GATE: a chunk is
-        // 32 columns of g and the same of u, half a tile further on.
+        // reads TMEM lanes 32 (q mod 4)..: one output row a lane.  A chunk is 32 columns; GATE:
+        // 16 (32 for PROMOTE) of g and the same of u, half a tile further on.
         const int ew = warp - 2, group = ew >> 2, quarter = warp & 3;
         uint32_t* stage = epi_stage + ew * ((PRODUCT == DGATE ? kSavedWarpBytes : kStageWarpBytes) / 4);
-        const int nch = jobs.BN / (PRODUCT == GATE ? 64 : 32), c_lo = nch * group / kGroups, c_hi = nch * (group + 1) / kGroups;
+        constexpr int kUnit = PRODUCT == GATE && !PROMOTE ? 16 : 32;
+        const int nch = jobs.BN / kUnit / (PRODUCT == GATE ? 2 : 1), c_lo = nch * group / kGroups, c_hi = nch * (group + 1) / kGroups;
         const int u_col = jobs.BN / 2;
         float up = 1.f, down = 1.f;
         if constexpr (PRODUCT == DGATE) up = scale_of(jobs.largest, jobs.maxima, false);
@@ -623,15 +624,15 @@ ffn_gemm_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ Ff
                 const uint32_t t_row = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * 256);
 #pragma unroll 1
                 for (int c = c_lo; c < c_hi; ++c) {
-                    const int c0 = n0 + c * 32;
+                    const int c0 = n0 + c * kUnit;
                     if constexpr (PRODUCT == GATE || PRODUCT == DGATE) {
 #pragma unroll 1
-                        for (int e = 0; e < 2; ++e) {
+                        for (int e = 0; e < kUnit / 16; ++e) {
                             uint32_t r[16];
-                            tmem_ld_32x32b_x16(t_row + c * 32 + e * 16, r);
+                            tmem_ld_32x32b_x16(t_row + c * kUnit + e * 16, r);
                             if constexpr (PRODUCT == GATE) {
                                 uint32_t s[16];
-                                tmem_ld_32x32b_x16(t_row + u_col + c * 32 + e * 16, s);
+                                tmem_ld_32x32b_x16(t_row + u_col + c * kUnit + e * 16, s);
                                 tmem_ld_wait();
 #pragma unroll
                                 for (int j = 0; j < 16; ++j) w[j] = __uint_as_float(s[j]);
@@ -640,7 +641,7 @@ ffn_gemm_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ Ff
                                 tmem_ld_wait();
                                 fetch_saved(n_item, c + e, e ^ 1);
                             }
-                            if (c + 1 == c_hi && e) emptied(acc);
+                            if (c + 1 == c_hi && e + 1 == kUnit / 16) emptied(acc);
 #pragma unroll
                             for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
                             half_chunk(c0 + e * 16, v, w, q);
@@ -804,8 +805,8 @@ FfnTile plan_tiles(const Sized* pr, int n, Product product, bool f32) {
     for (int pair = 0; pair < 2; ++pair) {
         if (pair && most_m <= kBM) break;
         const int units = pair ? pair_count() : device_sm_count(), rows = pair ? 2 * kBM : kBM;
-        // Boxes of whole 64 columns (MN-major), half tiles of whole chunks of g and of u, half of either for each CTA.
-        const int down = b_mn ? (pair ? 128 : 64) : product == GATE ? 64 : 32;
+        // Boxes of whole 64 columns (MN-major), halves of whole chunks of g and of u, half of either for each CTA.
+        const int down = b_mn ? (pair ? 128 : 64) : product == GATE && f32 ? 64 : 32;
         const int smallest = pair ? 128 : 64;
         for (int bn = product == DGATE && f32 ? 128 : 256; bn >= smallest; bn -= down) {
             if ((bn - down) / share >= most_n && bn - down >= smallest) continue;      // wider than the output needs

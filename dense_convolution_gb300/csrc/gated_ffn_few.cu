@@ -61,11 +61,12 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) ffn_few_kernel(cons
         const T* w = static_cast<const T*>(GATE && r >= 2 ? p.w2 : p.w);
         return w + (int64_t)(r0 + r % kStep * V) * p.cols;
     };
-    pdl_wait();
-    pdl_launch_dependents();
     for (int i = threadIdx.x; i < NT * V * pitch; i += kThreads) hs[i] = 0.f;
     __syncthreads();
+    pdl_wait();
+    pdl_launch_dependents();
     for (int t = 0; t < p.tokens; ++t) {
+#pragma unroll 8
         for (int e = threadIdx.x; e < p.cols; e += kThreads) {
             const float v = GATE ? to_f32(static_cast<const T*>(p.x)[t * p.xs + e]) : static_cast<const float*>(p.x)[t * p.xs + e];
             hs[((t / P * V + (e & (V - 1))) * pitch + (e >> shift_bits<T>()) + 1) * P + t % P] = v;

@@ -246,7 +246,8 @@ conv2d_status gated_ffn_fwd(gated_ffn_desc_t d, const void *x, const void *wg, c
                             void *stream);
 
 /* Gradients from dy and what gated_ffn_fwd saved for the same x and weights.  Each of dx
- * [tokens][hidden], dwg, dwu and dwd may be NULL (not wanted).  Errors as gated_ffn_fwd. */
+ * [tokens][hidden], dwg, dwu and dwd may be NULL (not wanted); none overlaps an operand.
+ * Errors as gated_ffn_fwd. */
 conv2d_status gated_ffn_bwd(gated_ffn_desc_t d, const void *dy, const void *x, const void *wg, const void *wu,
                             const void *wd, const float *saved, void *dx, void *dwg, void *dwu, void *dwd,
                             void *workspace, size_t workspace_bytes, void *stream);

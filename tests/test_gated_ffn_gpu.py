@@ -322,6 +322,60 @@ def test_beyond_32_bit_offsets():
         _close(v, want[k], k, 0.75 * U["bf16"])
 
 
+@pytest.mark.parametrize("dtype,t,d,f", [("bf16", 300, 264, 520), ("f32", 200, 72, 130)])
+def test_each_gradient_alone_has_the_same_bits(dtype, t, d, f):
+    import itertools
+
+    import torch
+    from dense_convolution_gb300 import head, head_capi
+    i = _inputs(9, t, d, f, dtype)
+    op = head.GatedFeedForward(t, d, f, dtype)
+    _, saved = op(i["x"], i["wg"], i["wu"], i["wd"], save=True)
+    want = op.backward(i["dy"], i["x"], i["wg"], i["wu"], i["wd"], saved)
+    ws = torch.empty(op.backward_workspace_bytes, dtype=torch.uint8, device="cuda")
+    for wanted in itertools.product((False, True), repeat=4):
+        out = [torch.full_like(v, float("nan")) for v in want]
+        head_capi.gated_ffn_bwd(op.desc, i["dy"].data_ptr(), i["x"].data_ptr(), i["wg"].data_ptr(), i["wu"].data_ptr(),
+                                i["wd"].data_ptr(), saved.data_ptr(), *(o.data_ptr() if w else 0 for o, w in zip(out, wanted)),
+                                ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream)
+        for o, v, w in zip(out, want, wanted):
+            assert o.equal(v) if w else torch.isnan(o).all(), wanted
+
+
+def test_two_threads_with_shapes_of_their_own():
+    """Calls of one kernel from two threads: what one shape needs of it (its shared memory) takes nothing from the other's."""
+    import threading
+
+    import torch
+    from dense_convolution_gb300 import head
+    start, errors = threading.Barrier(4), []
+
+    def loop(t, d, f, dtype):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                i = _inputs(t, t, d, f, dtype)
+                op = head.GatedFeedForward(t, d, f, dtype)
+                want = _run(op, i)
+                stream.synchronize()
+                start.wait()
+                for _ in range(200):
+                    got = _run(op, i)
+                stream.synchronize()
+                assert all(got[k].equal(want[k]) for k in want)
+        except Exception as e:
+            errors.append(repr(e))
+            start.abort()
+
+    threads = [threading.Thread(target=loop, args=a) for a in ((3, 4096, 64, "bf16"), (3, 64, 96, "bf16"), (300, 512, 512, "bf16"),
+                                                               (140, 33, 47, "bf16"))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+
+
 def test_no_tokens():
     import torch
     from dense_convolution_gb300 import head

@@ -35,6 +35,7 @@
 #include <math.h>
 
 #include <initializer_list>
+#include <utility>
 
 #include "gated_ffn_device.cuh"
 #include "head_device.cuh"
@@ -69,7 +70,7 @@ struct FfnJob {
 struct FfnJobs {
     FfnJob job[4];
     int n, items;
-    int extra;               // items of the others that take as long as one of the first
+    int long_items, extra;   // items of the products with the long ones; as many of the others take as long as one of these
     int BN, stages, seg;     // tile width, ring depth; PROMOTE: chunks per accumulation in tensor memory
     int epi_bytes;           // epilogue staging in shared memory (0: none needed)
     int pairs, parts, f32;
@@ -307,9 +308,9 @@ ffn_gemm_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ Ff
     pdl_launch_dependents();
 
     // Items are dealt out in turn; every role walks them alike.  Units that get one fewer of the
-    // first, longer product's items get `extra` of the others' before all take turns again.
+    // longer items get `extra` of the others before all take turns again.
     const int unit = blockIdx.x / kCtas, units = gridDim.x / kCtas;
-    const int long_items = jobs.job[0].items, more = long_items % units, in_turn = long_items + jobs.extra * (units - more);
+    const int long_items = jobs.long_items, more = long_items % units, in_turn = long_items + jobs.extra * (units - more);
     auto after = [&](int i) {
         if (PRODUCT != GRADS || !jobs.extra || i >= in_turn) return i + units;
         if (i < long_items) {
@@ -744,28 +745,33 @@ __global__ void __launch_bounds__(1024) ffn_largest_kernel(const uint16_t* x, in
     }
 }
 
-// out = scale * (sum over splits) + res.  The sums' rows are lds wide (a multiple of 64); four columns a thread.
-template <typename T>
-__global__ void __launch_bounds__(256) ffn_join_kernel(const float* part, int splits, int64_t rows, int cols, int64_t lds,
-                                                       const uint32_t* largest, int maxima, const T* res, int64_t ldr, T* out, int64_t ldo) {
+// out = scale * (sum over splits) + res for the results that were split, one a blockIdx.y.  The sums' rows are
+// lds wide (a multiple of 64); four columns a thread.
+struct JoinJob { const float* part; const void* res; void* out; int64_t rows, lds, ldr, ldo; int splits, cols, scaled; };
+struct JoinJobs { JoinJob job[4]; const uint32_t* largest; int maxima; };
+template <typename T> __global__ void __launch_bounds__(256) ffn_join_kernel(const JoinJobs jobs) {
     pdl_wait();
-    const float s = scale_of(largest, maxima, true);
-    const int per = (cols + 3) / 4;
-    const int64_t total = rows * per, pitch = rows * lds;
+    const JoinJob& p = jobs.job[blockIdx.y];
+    const float s = scale_of(p.scaled ? jobs.largest : nullptr, jobs.maxima, true);
+    const T* res = static_cast<const T*>(p.res);
+    T* out = static_cast<T*>(p.out);
+    const int per = (p.cols + 3) / 4;
+    const int64_t total = p.rows * per, pitch = p.rows * p.lds;
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
         const int64_t row = i / per;
         const int c = (int)(i - row * per) * 4;
-        const int64_t at = row * lds + c;
+        const int64_t at = row * p.lds + c;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-        for (int k = 0; k < splits; ++k) {
-            const float4 t = *reinterpret_cast<const float4*>(part + k * pitch + at);
+        for (int k = 0; k < p.splits; ++k) {
+            const float4 t = *reinterpret_cast<const float4*>(p.part + k * pitch + at);
             v.x += t.x; v.y += t.y; v.z += t.z; v.w += t.w;
         }
         const float f[4] = {v.x * s, v.y * s, v.z * s, v.w * s};
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (c + j < cols) out[row * ldo + c + j] = from_f32<T>(res ? f[j] + to_f32(res[row * ldr + c + j]) : f[j]);
+            if (c + j < p.cols)
+                out[row * p.ldo + c + j] = from_f32<T>(res ? f[j] + to_f32(res[row * p.ldr + c + j]) : f[j]);
     }
 }
 
@@ -778,10 +784,13 @@ int64_t most_chunks(bool bf16) { return bf16 ? 2048 : 256; }
 // One product of a launch, for the estimate.
 struct Sized { int64_t M, N, chunks; bool may_split; int64_t least; };
 
-// Items of the other products that take as long as one of the first.
-int extra_turns(double first, double rest) {
-    const int n = (int)(first / rest + 0.5);
-    return n < 1 ? 1 : n;
+// Of products in the order of their items' lengths: how many count as long (the first, and those that are
+// nearly so), and how many items of the others take as long as one of these (0: there are none).
+template <typename T> int long_products(const T* length, int n, int* extra) {
+    int k = 1;
+    while (k < n && length[k] * 4 >= length[0] * 3) ++k;
+    *extra = k < n ? (int)((double)length[0] / (double)length[k] + 0.5) : 0;
+    return k;
 }
 
 // Tile width, CTA pairs and K splits of a launch's products by an estimate in SM
@@ -816,28 +825,36 @@ FfnTile plan_tiles(const Sized* pr, int n, Product product, bool f32) {
                 const int64_t longest = ceil_div(most_chunks, s);
                 if (s > 1 && s > most_chunks) break;
                 FfnTile tile{bn, pair != 0, {1, 1, 1, 1}};
-                int64_t start[5] = {0, 0, 0, 0, 0};
+                int64_t start[5] = {0, 0, 0, 0, 0}, items[4];
                 double each[4] = {0, 0, 0, 0}, extra = 0;
                 for (int j = 0; j < n; ++j) {
                     int64_t k = pr[j].may_split ? ceil_div(pr[j].chunks, longest) : 1;
                     if (k < pr[j].least) k = pr[j].least;
                     if (k > pr[j].chunks) k = pr[j].chunks;
                     tile.splits[j] = (int)k;
-                    each[j] = (double)ceil_div(pr[j].chunks, k) * chunk + 3000.0;
-                    start[j + 1] = start[j] + ceil_div(pr[j].M, rows) * ceil_div(pr[j].N * share, bn) * k;
                     if (k > 1) extra += 4000.0 + (double)k * pr[j].M * pr[j].N * 8.0 / 3500.0;
+                    // (Longest items first, as the launch orders them.)
+                    const double length = (double)ceil_div(pr[j].chunks, k) * chunk + 3000.0;
+                    int at = j;
+                    for (; at > 0 && each[at - 1] < length; --at) {
+                        each[at] = each[at - 1];
+                        items[at] = items[at - 1];
+                    }
+                    each[at] = length;
+                    items[at] = ceil_div(pr[j].M, rows) * ceil_div(pr[j].N * share, bn) * k;
                 }
-                // The unit with the most work is the first one, or the first of those with one item fewer of the first
-                // product (see the kernel's order).
-                const int64_t more = start[1] % units, total = start[n];
-                double rest = 0;
-                for (int j = 1; j < n; ++j) rest = each[j] > rest ? each[j] : rest;
-                const int64_t turns = n > 1 ? extra_turns(each[0], rest) : 0, in_turn = start[1] + turns * (units - more);
+                for (int j = 0; j < n; ++j) start[j + 1] = start[j] + items[j];
+                // The unit with the most work is the first one, or the first of those with one long item fewer (see the
+                // kernel's order).
+                int turns = 0;
+                const int k = long_products(each, n, &turns);
+                const int64_t all = start[k], more = all % units, total = start[n], in_turn = all + turns * (units - more);
+                const double rest = k < n ? each[k] : 0;
                 double t = 0;
                 for (int64_t u : {(int64_t)0, more}) {
                     const auto count = [&](int64_t from, int64_t to, int64_t by) { return to > from ? (to - from + by - 1) / by : 0; };
-                    double load = (double)count(u, start[1], units) * each[0] + (double)count(in_turn + u, total, units) * rest;
-                    if (u >= more) load += (double)count(start[1] + u - more, in_turn < total ? in_turn : total, units - more) * rest;
+                    double load = (double)count(u, all, units) * each[0] + (double)count(in_turn + u, total, units) * rest;
+                    if (u >= more) load += (double)count(all + u - more, in_turn < total ? in_turn : total, units - more) * rest;
                     t = load > t ? load : t;
                 }
                 t += extra;
@@ -859,6 +876,9 @@ template <int PRODUCT, bool PAIR> const void* gemm_kernel(bool bf16, bool promot
     return bf16 ? reinterpret_cast<const void*>(&ffn_gemm_kernel<true, PRODUCT, false, PAIR>)
                 : reinterpret_cast<const void*>(&ffn_gemm_kernel<false, PRODUCT, false, PAIR>);
 }
+
+// Chunks of a product's items, and about six more that an item costs beside them.
+int length_of(const FfnJobs& jobs, const FfnJob& p) { return (int)ceil_div((int64_t)p.nk * jobs.pairs, p.splits) + 6; }
 
 template <int PRODUCT>
 conv2d_status launch_gemm(bool bf16, const FfnTile& g, const FfnMaps& maps, FfnJobs& jobs, cudaStream_t st) {
@@ -886,11 +906,11 @@ conv2d_status launch_gemm(bool bf16, const FfnTile& g, const FfnMaps& maps, FfnJ
         if ((PRODUCT == ROWS || PRODUCT == GRADS) && p.splits == 1 && (!p.out_vec || (p.res && !p.res_vec) || p.N % 32 != 0))
             jobs.epi_bytes = ffn_epi_warps(PRODUCT, promote) * kStageWarpBytes;
     }
-    // (An item's fixed cost is that of about six chunks.)
-    int rest = 0;
-    const auto length = [&](const FfnJob& p) { return (int)ceil_div((int64_t)p.nk * jobs.pairs, p.splits) + 6; };
-    for (int j = 1; j < jobs.n; ++j) rest = length(jobs.job[j]) > rest ? length(jobs.job[j]) : rest;
-    jobs.extra = jobs.n > 1 ? extra_turns(length(jobs.job[0]), rest) : 0;
+    int length[4];
+    for (int j = 0; j < jobs.n; ++j) length[j] = length_of(jobs, jobs.job[j]);
+    const int k = long_products(length, jobs.n, &jobs.extra);
+    jobs.long_items = 0;
+    for (int j = 0; j < k; ++j) jobs.long_items += jobs.job[j].items;
     const int stage_bytes = kABytes + g.BN / ctas * kBK * 2;
     jobs.stages = (kSmemMost - kFixedSmem - jobs.epi_bytes) / stage_bytes;
     if (jobs.stages > kMaxRing) jobs.stages = kMaxRing;
@@ -922,19 +942,27 @@ FfnJob out_job(const gated_ffn_desc& d, const FfnPlan& c, int64_t M, int64_t N, 
     return p;
 }
 
-template <typename T>
-cudaError_t join_typed(const FfnJob& p, const FfnJobs& jobs, cudaStream_t st) {
-    const int64_t work = ceil_div((int64_t)p.M * ceil_div(p.N, 4), 256), most = (int64_t)device_sm_count() * 16;
-    return launch_after(ffn_join_kernel<T>, dim3((unsigned)(work < most ? work : most)), dim3(256), 0, st,
-                        static_cast<const float*>(p.sums), p.splits, (int64_t)p.M, p.N, p.lds,
-                        p.scaled ? jobs.largest : nullptr, jobs.maxima, static_cast<const T*>(p.res), p.ldr, static_cast<T*>(p.out), p.ldo);
-}
-cudaError_t join(const gated_ffn_desc& d, const FfnJob& p, const FfnJobs& jobs, cudaStream_t st) {
-    if (p.splits == 1) return cudaSuccess;
+// The results of a launch that were split over K.
+cudaError_t join(const gated_ffn_desc& d, const FfnJobs& jobs, cudaStream_t st) {
+    JoinJobs joins{};
+    joins.largest = jobs.largest;
+    joins.maxima = jobs.maxima;
+    unsigned n = 0;
+    int64_t work = 0;
+    for (int j = 0; j < jobs.n; ++j) {
+        const FfnJob& p = jobs.job[j];
+        if (p.splits == 1) continue;
+        joins.job[n++] = JoinJob{p.sums, p.res, p.out, p.M, p.lds, p.ldr, p.ldo, p.splits, p.N, p.scaled};
+        const int64_t w = ceil_div((int64_t)p.M * ceil_div(p.N, 4), 256);
+        work = w > work ? w : work;
+    }
+    if (!n) return cudaSuccess;
+    const int64_t most = (int64_t)device_sm_count() * 16;
+    const dim3 grid((unsigned)(work < most ? work : most), n), block(256);
     switch (d.dtype) {
-        case CONV2D_F32: return join_typed<float>(p, jobs, st);
-        case CONV2D_F16: return join_typed<__half>(p, jobs, st);
-        default: return join_typed<__nv_bfloat16>(p, jobs, st);
+        case CONV2D_F32: return launch_after(ffn_join_kernel<float>, grid, block, 0, st, joins);
+        case CONV2D_F16: return launch_after(ffn_join_kernel<__half>, grid, block, 0, st, joins);
+        default: return launch_after(ffn_join_kernel<__nv_bfloat16>, grid, block, 0, st, joins);
     }
 }
 
@@ -1103,7 +1131,7 @@ conv2d_status launch_gated_ffn_fwd(const gated_ffn_desc& d, const void* x, const
         return CONV2D_ERR_CUDA;
     s = launch_gemm<ROWS>(c.bf16, c.last, maps, last, st);
     if (s != CONV2D_OK) return s;
-    return join(d, q, last, st) == cudaSuccess ? CONV2D_OK : CONV2D_ERR_CUDA;
+    return join(d, last, st) == cudaSuccess ? CONV2D_OK : CONV2D_ERR_CUDA;
 }
 
 conv2d_status launch_gated_ffn_bwd(const gated_ffn_desc& d, const void* dy, const void* x, const void* wg, const void* wu,
@@ -1191,12 +1219,17 @@ conv2d_status launch_gated_ffn_bwd(const gated_ffn_desc& d, const void* dy, cons
             !make_map(&maps.b[j], h, c.bf16, T, c.fp * c.parts, c.fp * c.parts, 64))
             return CONV2D_ERR_CUDA;
     }
+    // The products with the longest items first.
+    for (int i = 1; i < last.n; ++i)
+        for (int j = i; j > 0 && length_of(last, last.job[j - 1]) < length_of(last, last.job[j]); --j) {
+            std::swap(last.job[j - 1], last.job[j]);
+            std::swap(maps.a[j - 1], maps.a[j]);
+            std::swap(maps.b[j - 1], maps.b[j]);
+        }
     for (int j = last.n; j < 4; ++j) { maps.a[j] = maps.a[0]; maps.b[j] = maps.b[0]; }
     s = launch_gemm<GRADS>(c.bf16, c.last, maps, last, st);
     if (s != CONV2D_OK) return s;
-    for (int j = 0; j < last.n; ++j)
-        if (join(d, last.job[j], last, st) != cudaSuccess) return CONV2D_ERR_CUDA;
-    return CONV2D_OK;
+    return join(d, last, st) == cudaSuccess ? CONV2D_OK : CONV2D_ERR_CUDA;
 }
 
 cudaError_t status_word_ffn(void** p) { return unit_status_word(p); }

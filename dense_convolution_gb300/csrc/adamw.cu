@@ -25,6 +25,12 @@
 // Where p, g or the copy are not aligned for vectors, and at a tensor's end, a
 // warp's elements go through shared memory, so that global memory is read and
 // written along the row all the same.
+//
+// Measured with bf16 gradients and copies, 319 million parameters: fp32 moments 1254 us (7.1 TB/s of 28 bytes a
+// parameter; memory bounds it), 8 bits 927 us (5.5 TB/s of 16).  There instructions bound it, 88 a
+// parameter of which the generator takes some 15: 1364 us at first; codes without conversions between integers and floats,
+// which run at an eighth of the rate, 1172; a warp's next blocks by asynchronous copies, eight blocks a warp, 927 (the
+// same by registers 1479: the loop waits for what it moves).
 #include <math.h>
 
 #include "head_device.cuh"
@@ -141,8 +147,8 @@ template <bool E4M3> __device__ __forceinline__ uint2 to8(const float (&f)[8], u
     return make_uint2(four(0), four(4));
 }
 
-// m / (sqrt(v) k + eps), the root and the reciprocal off by 2^-23 each at most: a few hundredths of what
-// p's own rounding is of lr times it.  They take no subnormal numbers: v below 2^-126 counts as that.
+// m / (sqrt(v) k + eps), the root and the reciprocal off by 2^-23 each at most, which p sees times lr.  They take
+// no subnormal numbers: v below 2^-126 counts as that.
 __device__ __forceinline__ float update(float m, float v, float k, float eps) {
     float root, inverse;
     asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(root) : "f"(fmaxf(v, 0x1p-126f)));

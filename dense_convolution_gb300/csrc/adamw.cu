@@ -148,17 +148,18 @@ template <bool E4M3> __device__ __forceinline__ uint2 to8(const float (&f)[8], u
 }
 
 // m / (sqrt(v) k + eps), the root and the reciprocal off by 2^-23 each at most, which p sees times lr.  They take
-// no subnormal numbers: v below 2^-126 counts as that.
+// no subnormal numbers: v below 2^-126 counts as that (and one that is not a number as it is).
 __device__ __forceinline__ float update(float m, float v, float k, float eps) {
-    float root, inverse;
-    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(root) : "f"(fmaxf(v, 0x1p-126f)));
+    float normal, root, inverse;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(normal) : "f"(v), "f"(0x1p-126f));
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(root) : "f"(normal));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inverse) : "f"(fmaf(root, k, eps)));
     return m * inverse;
 }
 
 template <typename G, bool EIGHT, int N>
-__global__ void __launch_bounds__(32 * warps<EIGHT>(), EIGHT ? 7 : 4) adamw_kernel(const __grid_constant__ AdamTable<N> table,
-                                                            const __grid_constant__ AdamStep s) {
+__global__ void __launch_bounds__(32 * warps<EIGHT>(), EIGHT ? 7 : 4)
+adamw_kernel(const __grid_constant__ AdamTable<N> table, const __grid_constant__ AdamStep s) {
     constexpr int kWarps = warps<EIGHT>();
     // A warp's blocks on their way (8 bits), or one block of a tensor's elements on their way between the lanes.
     __shared__ __align__(16) float stage[kWarps][(EIGHT ? kSlots * slot_bytes<G>() : (kBlock + kBlock / 8) * 4) / 4];

@@ -398,6 +398,8 @@ class AdamW(_Op):
 
     def __init__(self, sizes, grad_dtype="f32", states="f32", copy_dtype=None, betas=(0.9, 0.999), eps=1e-8,
                  weight_decay=0.0):
+        if copy_dtype not in (None, "f16", "bf16"):
+            raise ValueError("copies are f16 or bf16: the parameters are fp32 themselves")
         self.sizes, self.states, self.grad_dtype, self.copy_dtype = tuple(map(int, sizes)), states, grad_dtype, copy_dtype
         self.desc = head_capi.adamw_desc_create(self.sizes, grad_dtype, states, copy_dtype or "f32")
         head_capi.adamw_desc_set_rates(self.desc, *betas, eps)

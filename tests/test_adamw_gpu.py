@@ -248,6 +248,24 @@ def test_blocks_that_are_not_finite_and_zero_gradients():
     assert q.p[0].equal(was) and not q.moments()[0].any() and not q.moments()[1].any()
 
 
+@pytest.mark.parametrize("states", ["f32", "8bit"])
+def test_a_second_moment_that_overflows(states):
+    """v is infinite where the gradient's square is: p stays for the step, as m over infinity says.  In 8 bits the
+    block's v is not a number from then on, and neither is what p takes from it, though m is finite."""
+    import torch
+    q = Problem([1024], "f32", states, decay=[0.0])
+    q.g[0][300] = 1e25
+    was = q.p[0].clone()
+    q.step(1)
+    assert float(q.p[0][300]) == float(was[300]) and torch.isfinite(q.p[0]).all()
+    q.g[0].zero_()
+    q.step(2)
+    if states == "f32":
+        assert torch.isfinite(q.p[0]).all() and float(q.p[0][300]) == float(was[300])
+    else:
+        assert torch.isnan(q.p[0][256:512]).all() and torch.isfinite(q.p[0][:256]).all() and torch.isfinite(q.p[0][512:]).all()
+
+
 def test_8bit_moments_move_as_the_formula_on_average():
     """Without gradients v falls by b2 a step; rounding to nearest would leave it.
     A value's own walk spreads by less than a step of its code in each of a few
@@ -323,6 +341,8 @@ def test_wrong_tensors_are_refused():
         q.op(q.p, q.g, q.state, 0, 0.1, copies=q.c)
     with pytest.raises(ValueError):
         head.AdamW([4, 5], weight_decay=[0.1])
+    with pytest.raises(ValueError):
+        head.AdamW([4], copy_dtype="f32")
     two = head.AdamW([64, 64], "bf16")
     with pytest.raises(ValueError):
         two([q.p[0], q.p[0]], [q.g[0], q.g[0]], two.new_state(), 1, 0.1)

@@ -71,7 +71,6 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) ffn_few_kernel(cons
     pdl_wait();
     pdl_launch_dependents();
     for (int t = 0; t < p.tokens; ++t) {
-#pragma unroll 8
         for (int e = threadIdx.x; e < p.cols; e += kThreads) {
             const float v = GATE ? to_f32(static_cast<const T*>(p.x)[t * p.xs + e]) : static_cast<const float*>(p.x)[t * p.xs + e];
             hs[((t / P * V + (e & (V - 1))) * pitch + (e >> shift_bits<T>()) + 1) * P + t % P] = v;

@@ -241,10 +241,14 @@ adamw_kernel(const __grid_constant__ AdamTable<N> table, const __grid_constant__
                 copy_async_wait<1>();
                 const uint8_t* at = slot(j);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) widen(reinterpret_cast<const Vec<float, 4>*>(at + 512 * h)[lane], *reinterpret_cast<float(*)[4]>(fp + 4 * h));
+                for (int h = 0; h < 2; ++h)
+                    widen(reinterpret_cast<const Vec<float, 4>*>(at + 512 * h)[lane],
+                          *reinterpret_cast<float(*)[4]>(fp + 4 * h));
                 if constexpr (sizeof(G) == 4) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) widen(reinterpret_cast<const Vec<float, 4>*>(at + kG + 512 * h)[lane], *reinterpret_cast<float(*)[4]>(fg + 4 * h));
+                    for (int h = 0; h < 2; ++h)
+                        widen(reinterpret_cast<const Vec<float, 4>*>(at + kG + 512 * h)[lane],
+                              *reinterpret_cast<float(*)[4]>(fg + 4 * h));
                 } else {
                     widen(reinterpret_cast<const Vec<G, 8>*>(at + kG)[lane], fg);
                 }
@@ -325,7 +329,8 @@ adamw_kernel(const __grid_constant__ AdamTable<N> table, const __grid_constant__
             uint32_t r[8];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                uint32_t c[4] = {(uint32_t)(e0 / 4) + 2 * lane + k, s.first_tensor + lo, (uint32_t)step, (uint32_t)((uint64_t)step >> 32)};
+                uint32_t c[4] = {(uint32_t)(e0 / 4) + 2 * lane + k, s.first_tensor + lo, (uint32_t)step,
+                                 (uint32_t)((uint64_t)step >> 32)};
                 philox(c, s.k0, s.k1);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) r[4 * k + i] = c[i];
@@ -430,9 +435,15 @@ cudaError_t launch_adamw(const adamw_desc& d, float* const* params, const void* 
     s.copy_bf16 = d.copy == CONV2D_BF16;
     const bool eight = d.states == ADAMW_STATES_8BIT;
     switch (d.grad) {
-        case CONV2D_F32: return eight ? run<float, true>(d, params, grads, copies, s, st) : run<float, false>(d, params, grads, copies, s, st);
-        case CONV2D_F16: return eight ? run<__half, true>(d, params, grads, copies, s, st) : run<__half, false>(d, params, grads, copies, s, st);
-        default: return eight ? run<__nv_bfloat16, true>(d, params, grads, copies, s, st) : run<__nv_bfloat16, false>(d, params, grads, copies, s, st);
+        case CONV2D_F32:
+            return eight ? run<float, true>(d, params, grads, copies, s, st)
+                         : run<float, false>(d, params, grads, copies, s, st);
+        case CONV2D_F16:
+            return eight ? run<__half, true>(d, params, grads, copies, s, st)
+                         : run<__half, false>(d, params, grads, copies, s, st);
+        default:
+            return eight ? run<__nv_bfloat16, true>(d, params, grads, copies, s, st)
+                         : run<__nv_bfloat16, false>(d, params, grads, copies, s, st);
     }
 }
 

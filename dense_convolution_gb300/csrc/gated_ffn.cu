@@ -941,7 +941,7 @@ int wide(const void* p, int64_t row_bytes) {
 }
 
 // ROWS and GRADS: a result of the final type in rows `ldo` apart.
-FfnJob out_job(const gated_ffn_desc& d, const FfnPlan& c, int64_t M, int64_t N, int64_t nk, int splits, void* out, int64_t ldo, float* sums) {
+FfnJob out_job(const gated_ffn_desc& d, int64_t M, int64_t N, int64_t nk, int splits, void* out, int64_t ldo, float* sums) {
     FfnJob p{};
     p.M = (int)M;
     p.N = (int)N;
@@ -1133,7 +1133,7 @@ conv2d_status launch_gated_ffn_fwd(const gated_ffn_desc& d, const void* x, const
     if (s != CONV2D_OK) return s;
     // y
     FfnJobs last = jobs_of(d, c);
-    last.job[0] = out_job(d, c, T, D, c.fp / 64, c.last.splits[0], y, d.ys, reinterpret_cast<float*>(base + c.sums[0]));
+    last.job[0] = out_job(d, T, D, c.fp / 64, c.last.splits[0], y, d.ys, reinterpret_cast<float*>(base + c.sums[0]));
     FfnJob& q = last.job[0];
     q.a_part = q.b_part = (int)c.fp;
     q.res = residual;
@@ -1195,7 +1195,7 @@ conv2d_status launch_gated_ffn_bwd(const gated_ffn_desc& d, const void* dy, cons
     const int64_t gu = 2 * c.fp * c.parts, nt = ceil_div(T, 64);
     if (dx) {
         const int j = last.n++;
-        FfnJob q = out_job(d, c, T, D, 2 * c.fp / 64, c.last.splits[0], dx, D, sums[0]);
+        FfnJob q = out_job(d, T, D, 2 * c.fp / 64, c.last.splits[0], dx, D, sums[0]);
         q.nk0 = (int)(c.fp / 64);
         q.a_part = (int)(2 * c.fp);
         q.b_part = (int)c.dp;
@@ -1210,7 +1210,7 @@ conv2d_status launch_gated_ffn_bwd(const gated_ffn_desc& d, const void* dy, cons
         void* out = k ? dwu : dwg;
         if (!out) continue;
         const int j = last.n++;
-        FfnJob q = out_job(d, c, F, D, nt, c.last.splits[1 + k], out, D, sums[1 + k]);
+        FfnJob q = out_job(d, F, D, nt, c.last.splits[1 + k], out, D, sums[1 + k]);
         q.a_mn = 1;
         q.a_off = (int)(k * c.fp);
         q.a_part = (int)(2 * c.fp);
@@ -1223,7 +1223,7 @@ conv2d_status launch_gated_ffn_bwd(const gated_ffn_desc& d, const void* dy, cons
     }
     if (dwd) {
         const int j = last.n++;
-        FfnJob q = out_job(d, c, D, F, nt, c.last.splits[3], dwd, F, sums[3]);
+        FfnJob q = out_job(d, D, F, nt, c.last.splits[3], dwd, F, sums[3]);
         q.a_mn = 1;
         q.a_part = (int)c.dp;
         q.b_part = (int)c.fp;

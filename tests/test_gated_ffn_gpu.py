@@ -163,6 +163,23 @@ def test_activations_far_from_zero(act, dtype, t):
         _close(got[k], want[k], k)
 
 
+@pytest.mark.parametrize("t,d,f", [(130, 16384, 64), (20000, 64, 72), (140, 64, 40000)])
+def test_sums_of_one_sign(t, d, f):
+    """All terms positive, in fp16: what the tensor cores cut from long sums stays within the bounds."""
+    from dense_convolution_gb300 import head
+    i = _inputs(12, t, d, f, "f16")
+    for k in ("x", "wg", "wu", "wd", "dy"):
+        i[k].abs_()
+    i["wg"] *= 2 / d ** 0.5                                # pre-activations near one
+    i["wu"] *= 2 / d ** 0.5
+    i["wd"] *= 2 / f ** 0.5
+    i["dy"] *= min(1.0, 100 / t)
+    op = head.GatedFeedForward(t, d, f, "f16", "silu")
+    got, want = _run(op, i), _reference(i, "silu", "f16")
+    for k in want:
+        _close(got[k], want[k], k)
+
+
 def _strided(v, stride, shift):
     """v's values in rows `stride` apart, `shift` elements into a buffer of NaN."""
     import torch
@@ -342,8 +359,8 @@ def test_each_gradient_alone_has_the_same_bits(dtype, t, d, f):
             assert o.equal(v) if w else torch.isnan(o).all(), wanted
 
 
-def test_two_threads_with_shapes_of_their_own():
-    """Calls of one kernel from two threads: what one shape needs of it (its shared memory) takes nothing from the other's."""
+def test_threads_with_shapes_of_their_own():
+    """Calls of one kernel from several threads: what one shape needs of it (its shared memory) takes nothing from another's."""
     import threading
 
     import torch

@@ -46,7 +46,8 @@ constexpr int kBlock = 256, kLane = 8;                 // elements of a warp and
 template <bool EIGHT> __host__ __device__ constexpr int warps() { return EIGHT ? 4 : 8; }
 constexpr int kSlots = 3;
 template <typename G> __host__ __device__ constexpr int slot_bytes() { return kBlock * (4 + (int)sizeof(G) + 2); }
-constexpr int kFew = 24, kMany = 700;                  // tensors a launch: 1 KB and 31 KB of parameters
+// Tensors a launch: 1 KB and 31 KB of parameters (the larger ones cost a launch 0.3 to 0.5 us: 5 k parameters 2.9 and 3.2).
+constexpr int kFew = 24, kMany = 700;
 
 struct AdamTensor {
     float* p;
@@ -353,7 +354,9 @@ adamw_kernel(const __grid_constant__ AdamTable<N> table, const __grid_constant__
     }
 }
 
-// Blocks of 256 that a warp takes one after the other (at most 32: a lane keeps the scales of one).
+// Blocks of 256 that a warp takes one after the other (at most 32: a lane keeps the scales of one).  In 8 bits eight
+// keep the copies going where there are enough of them for the machine: one / eight, 1 M parameters 6.3 / 9.3 us, 4 M 17.3 /
+// 20.0, 16 M 59.5 / 56.8, 64 M 226 / 201, 256 M 892 / 777.
 int span_of(const adamw_desc& d) { return d.states == ADAMW_STATES_8BIT && d.elements >= (1 << 24) ? 8 : 1; }
 
 // Blocks of threads for n elements.

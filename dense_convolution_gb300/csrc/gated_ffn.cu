@@ -96,14 +96,14 @@ struct FfnJobs {
 };
 struct FfnMaps { CUtensorMap a[4], b[4], b2; };
 
-// The power of two that takes the largest |dy| to [16, 32), or its inverse: both normal.  `largest`: the bits of
+// The power of two that takes the largest finite |dy| to [16, 32), or its inverse: both normal.  `largest`: the bits of
 // some maxima (in fp16, as the rows were given), read by a whole warp.
 __device__ __forceinline__ float scale_of(const uint32_t* largest, int count, bool inverse) {
     if (!largest) return 1.f;
     uint32_t top = 0;
     for (int i = threadIdx.x & 31; i < count; i += 32) top = max(top, largest[i]);
     top = __reduce_max_sync(0xffffffffu, top);
-    if (top == 0u || top >= 0x7c00u) return 1.f;           // nothing there, or something that is not finite
+    if (top == 0u) return 1.f;
     const int e = (int)(__float_as_uint(__half2float(__ushort_as_half((unsigned short)top))) >> 23) - 127;     // -24 .. 15
     return __uint_as_float((uint32_t)(127 + (inverse ? e - 4 : 4 - e)) << 23);
 }
@@ -728,11 +728,13 @@ template <typename T, int PARTS> __global__ void __launch_bounds__(256) ffn_pack
                          blockIdx.x, gridDim.x);
 }
 
-// Bits of the largest magnitude of fp16 rows, one value a block (a NaN's are above all).
+// Bits of the largest finite magnitude of fp16 rows, one value a block: a row that is not finite takes no digits from
+// the others.
 __global__ void __launch_bounds__(1024) ffn_largest_kernel(const uint16_t* x, int64_t stride, int64_t rows, int cols, uint32_t* out) {
     __shared__ uint32_t red[32];
     pdl_wait();
     uint32_t top = 0;
+    const auto add = [&](uint32_t bits) { top = max(top, bits < 0x7c00u ? bits : 0u); };
     const int per = (cols + 7) / 8;
     const bool vec = stride % 8 == 0 && (reinterpret_cast<uintptr_t>(x) & 15u) == 0;
 #pragma unroll 4
@@ -744,9 +746,12 @@ __global__ void __launch_bounds__(1024) ffn_largest_kernel(const uint16_t* x, in
             const uint4 v = *reinterpret_cast<const uint4*>(s);
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) top = max(top, max(w[j] & 0x7fffu, w[j] >> 16 & 0x7fffu));
+            for (int j = 0; j < 4; ++j) {
+                add(w[j] & 0x7fffu);
+                add(w[j] >> 16 & 0x7fffu);
+            }
         } else {
-            for (int j = 0; j < 8 && c + j < cols; ++j) top = max(top, (uint32_t)s[j] & 0x7fffu);
+            for (int j = 0; j < 8 && c + j < cols; ++j) add((uint32_t)s[j] & 0x7fffu);
         }
     }
     top = __reduce_max_sync(0xffffffffu, top);

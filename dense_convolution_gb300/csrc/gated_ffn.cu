@@ -21,7 +21,7 @@
 // h, dg and du are rounded to the operands' type: they are the next products'
 // operands, and their errors average out over those sums (a result is off by 1.4 times its
 // own rounding).  For fp16, whose range gradients leave easily, dg and du are held times a
-// power of two that takes the largest dy to [16, 32).  g and u are saved in fp32:
+// power of two that takes the largest of them to [2^10, 2^15) (Held).  g and u are saved in fp32:
 // their rounding would pass through act' into every gradient, and the memory is idle
 // beside these products.  They lie as the epilogues' lanes, a row each, read them: four columns
 // of 32 rows are 512 bytes in a row.
@@ -62,6 +62,18 @@ namespace {
 
 enum Product { GATE = 0, ROWS = 1, DGATE = 2, GRADS = 3 };     // h; y; dg and du; dx and the weights' gradients
 
+// What the scale of fp16's dg and du goes by.  Their largest is wanted in [2^10, 2^15): past 65504 they would be
+// infinite, and what is below 2^-24 of 2^10 loses digits to subnormal numbers.  The first launch of
+// dg and du guesses from dy alone: their largest is 2^-2 to 2^3 of dy's where the weights keep the size of what passes
+// through.  It leaves the largest ones, in fp32 and unscaled, and a second launch does the work again where
+// the guess was off, else returns at once.  A step of 777 x 509 x 1371 takes 75 us with that and 71 without, one of 8192 x
+// 2048 x 8192 1670 where the guess holds and 1950 where it does not (Wd 64 times as large).
+struct Held {
+    const uint32_t* dy;      // maxima of |dy|, as bits of fp16 (finite values only), or null: no scale
+    const uint32_t* dgu;     // maxima of |dg| and |du|, as bits of fp32 (finite values only), or null: not known yet
+    int n_dy, n_dgu;
+};
+
 struct FfnJob {
     int M, N;                // valid extents of the result
     int n_m, n_n;            // tiles
@@ -91,22 +103,32 @@ struct FfnJobs {
     int inner, fp;           // columns of h, and its pitch
     uint16_t *h, *dgu;       // GATE [M][parts][fp], DGATE [M][parts][2][fp]
     float* saved;            // [M / 32][2][fp / 4][32][4]: a warp's rows side by side, or null
-    const uint32_t* largest; // maxima of |dy| (fp16), or null
-    int maxima;
+    Held held;
+    uint32_t* largest;       // DGATE: where a CTA leaves its largest |dg| and |du|, or null
+    int again;               // DGATE: the second launch
+    int ctas;                // of the launch
 };
 struct FfnMaps { CUtensorMap a[4], b[4], b2; };
 
-// The power of two that takes the largest finite |dy| to [16, 32), or its inverse: both normal.  `largest`: the bits of
-// some maxima (in fp16, as the rows were given), read by a whole warp.
-__device__ __forceinline__ float scale_of(const uint32_t* largest, int count, bool inverse) {
-    if (!largest) return 1.f;
-    uint32_t top = 0;
-    for (int i = threadIdx.x & 31; i < count; i += 32) top = max(top, largest[i]);
-    top = __reduce_max_sync(0xffffffffu, top);
-    if (top == 0u) return 1.f;
-    const int e = (int)(__float_as_uint(__half2float(__ushort_as_half((unsigned short)top))) >> 23) - 127;     // -24 .. 15
-    return __uint_as_float((uint32_t)(127 + (inverse ? e - 4 : 4 - e)) << 23);
+// The exponent of that scale, of either sign so that 2^e and 2^-e are normal numbers.  By a whole warp.
+__device__ __forceinline__ int held_exponent(const Held& h) {
+    if (!h.dy) return 0;
+    const auto largest = [](const uint32_t* at, int count) {
+        uint32_t top = 0;
+        for (int i = threadIdx.x & 31; i < count; i += 32) top = max(top, at[i]);
+        return __reduce_max_sync(0xffffffffu, top);
+    };
+    int e = 0;
+    const uint32_t dy = largest(h.dy, h.n_dy);             // (2^-24 .. 2^15, or zero)
+    if (dy) e = 12 + 127 - (int)(__float_as_uint(__half2float(__ushort_as_half((unsigned short)dy))) >> 23);
+    if (h.dgu) {
+        const uint32_t top = largest(h.dgu, h.n_dgu);
+        const int k = (int)(top >> 23) - 127;
+        if (top && (k + e < 10 || k + e > 14)) e = min(14 - k, 126);
+    }
+    return e;
 }
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
 struct Item { int m, n, split; };
 __device__ __forceinline__ Item item_of(const FfnJob& p, int i) {
@@ -272,6 +294,14 @@ __host__ __device__ constexpr int ffn_epi_warps(int product, bool promote) {
 template <bool BF16, int PRODUCT, bool PROMOTE, bool PAIR>
 __global__ void __launch_bounds__(32 * (2 + ffn_epi_warps(PRODUCT, PROMOTE)), 1)
 ffn_gemm_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnJobs jobs) {
+    if constexpr (PRODUCT == DGATE && !BF16) {
+        if (jobs.again) {
+            pdl_wait();
+            Held guess = jobs.held;
+            guess.dgu = nullptr;
+            if (held_exponent(guess) == held_exponent(jobs.held)) return;      // (all CTAs alike)
+        }
+    }
     constexpr bool B_MN = PRODUCT == DGATE || PRODUCT == GRADS;
     constexpr int kEpiWarps = ffn_epi_warps(PRODUCT, PROMOTE), kGroups = kEpiWarps / 4;
     extern __shared__ uint8_t smem_raw[];
@@ -486,8 +516,9 @@ ffn_gemm_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ Ff
         const int nch = jobs.BN / kUnit / (PRODUCT == GATE ? 2 : 1), c_lo = nch * group / kGroups, c_hi = nch * (group + 1) / kGroups;
         const int u_col = jobs.BN / 2;
         float up = 1.f, down = 1.f;
-        if constexpr (PRODUCT == DGATE) up = scale_of(jobs.largest, jobs.maxima, false);
-        if constexpr (PRODUCT == GRADS) down = scale_of(jobs.largest, jobs.maxima, true);
+        if constexpr (PRODUCT == DGATE && !BF16) up = power_of_two(held_exponent(jobs.held));
+        if constexpr (PRODUCT == GRADS && !BF16) down = power_of_two(-held_exponent(jobs.held));
+        float largest = 0.f;                               // DGATE, fp16: of this lane's |dg| and |du|, scaled
         // An accumulator that this warp has read is reported to the CTA that issues the MMAs.
         auto emptied = [&](int a) {
             tc_fence_before();
@@ -566,6 +597,22 @@ ffn_gemm_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ Ff
                         v[j] = j < n ? d * u * slope : 0.f;
                         w[j] = j < n ? d * a : 0.f;
                     });
+                    if constexpr (!BF16) {
+                        if (jobs.largest) {
+                            float top = 0.f;
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) top = fmaxf(top, fmaxf(fabsf(v[j]), fabsf(w[j])));
+                            if (isinf(top)) {              // (a NaN is passed over)
+                                top = 0.f;
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) {
+                                    if (!isinf(v[j])) top = fmaxf(top, fabsf(v[j]));
+                                    if (!isinf(w[j])) top = fmaxf(top, fabsf(w[j]));
+                                }
+                            }
+                            largest = fmaxf(largest, top);
+                        }
+                    }
                     uint16_t* dst = jobs.dgu + (int64_t)row * jobs.parts * 2 * jobs.fp + c0;
                     store16<BF16, PROMOTE>(dst, 2 * jobs.fp, jobs.parts, v);
                     store16<BF16, PROMOTE>(dst + jobs.fp, 2 * jobs.fp, jobs.parts, w);
@@ -676,10 +723,21 @@ ffn_gemm_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ Ff
             }
         }
         if constexpr (PRODUCT == DGATE) copy_async_wait<0>();
+        if constexpr (PRODUCT == DGATE && !BF16) {
+            __syncwarp();
+            const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(largest / up));
+            if (lane == 0) *stage = top;
+        }
     }
 
     tc_fence_before();
     __syncthreads();
+    if constexpr (PRODUCT == DGATE && !BF16) {
+        if (warp == 0 && jobs.largest) {
+            const uint32_t top = __reduce_max_sync(0xffffffffu, lane < kEpiWarps ? epi_stage[lane * (kSavedWarpBytes / 4)] : 0u);
+            if (lane == 0) jobs.largest[blockIdx.x] = top;
+        }
+    }
     if constexpr (PAIR) {
         // Each CTA leaves its state with the other before they meet: after the meeting
         // the other may be gone, and its memory with it.
@@ -766,11 +824,11 @@ __global__ void __launch_bounds__(1024) ffn_largest_kernel(const uint16_t* x, in
 // out = scale * (sum over splits) + res for the results that were split, one a blockIdx.y.  The sums' rows are
 // lds wide (a multiple of 64); four columns a thread.
 struct JoinJob { const float* part; const void* res; void* out; int64_t rows, lds, ldr, ldo; int splits, cols, scaled; };
-struct JoinJobs { JoinJob job[4]; const uint32_t* largest; int maxima; };
+struct JoinJobs { JoinJob job[4]; Held held; };
 template <typename T> __global__ void __launch_bounds__(256) ffn_join_kernel(const JoinJobs jobs) {
     pdl_wait();
     const JoinJob& p = jobs.job[blockIdx.y];
-    const float s = scale_of(p.scaled ? jobs.largest : nullptr, jobs.maxima, true);
+    const float s = p.scaled ? power_of_two(-held_exponent(jobs.held)) : 1.f;
     const T* res = static_cast<const T*>(p.res);
     T* out = static_cast<T*>(p.out);
     const int per = (p.cols + 3) / 4;
@@ -935,6 +993,7 @@ conv2d_status launch_gemm(bool bf16, const FfnTile& g, const FfnMaps& maps, FfnJ
     const int smem = kFixedSmem + jobs.epi_bytes + jobs.stages * stage_bytes;
     const int units = g.pair ? pair_count() : device_sm_count();
     const int grid = (jobs.items < units ? jobs.items : units) * ctas;
+    jobs.ctas = grid;
     void* args[2] = {const_cast<FfnMaps*>(&maps), &jobs};
     return launch_clusters(kern, grid, 32 * (2 + ffn_epi_warps(PRODUCT, promote)), ctas, smem, st, args) == cudaSuccess
                ? CONV2D_OK
@@ -963,8 +1022,7 @@ FfnJob out_job(const gated_ffn_desc& d, int64_t M, int64_t N, int64_t nk, int sp
 // The results of a launch that were split over K.
 cudaError_t join(const gated_ffn_desc& d, const FfnJobs& jobs, cudaStream_t st) {
     JoinJobs joins{};
-    joins.largest = jobs.largest;
-    joins.maxima = jobs.maxima;
+    joins.held = jobs.held;
     unsigned n = 0;
     int64_t work = 0;
     for (int j = 0; j < jobs.n; ++j) {
@@ -1081,6 +1139,7 @@ void gated_ffn_plan(gated_ffn_desc& d) {
         } else {
             take(at, c.dgu, (size_t)T * 2 * c.fp * 2 * c.parts);
             take(at, c.largest, (size_t)d.sms * 4);
+            take(at, c.largest_dgu, (size_t)d.sms * 4);
             const Sized dgate{T, c.fp, nd * c.pairs, false, 1};
             c.first = plan_tiles(&dgate, 1, DGATE, f32);
             const Sized grads[4] = {{T, D, 2 * nf * c.pairs, true, least(2 * nf)},
@@ -1169,11 +1228,12 @@ conv2d_status launch_gated_ffn_bwd(const gated_ffn_desc& d, const void* dy, cons
     if (d.dtype == CONV2D_F16) {
         uint32_t* largest = reinterpret_cast<uint32_t*>(base + c.largest);
         const int64_t work = ceil_div(T * ceil_div(D, 8), 1024);
-        jobs.maxima = (int)(work < d.sms ? work : d.sms);
-        if (launch_after(ffn_largest_kernel, dim3((unsigned)jobs.maxima), dim3(1024), 0, st,
+        jobs.held.n_dy = (int)(work < d.sms ? work : d.sms);
+        if (launch_after(ffn_largest_kernel, dim3((unsigned)jobs.held.n_dy), dim3(1024), 0, st,
                          static_cast<const uint16_t*>(dy), d.ys, T, (int)D, largest) != cudaSuccess)
             return CONV2D_ERR_CUDA;
-        jobs.largest = largest;
+        jobs.held.dy = largest;
+        jobs.largest = reinterpret_cast<uint32_t*>(base + c.largest_dgu);
     }
     // dg and du
     FfnJob& p = jobs.job[0];
@@ -1190,10 +1250,17 @@ conv2d_status launch_gated_ffn_bwd(const gated_ffn_desc& d, const void* dy, cons
     maps.b2 = maps.b[0];
     s = launch_gemm<DGATE>(c.bf16, c.first, maps, jobs, st);
     if (s != CONV2D_OK) return s;
+    if (jobs.largest) {
+        jobs.held.dgu = jobs.largest;
+        jobs.held.n_dgu = jobs.ctas;
+        jobs.largest = nullptr;
+        jobs.again = 1;
+        s = launch_gemm<DGATE>(c.bf16, c.first, maps, jobs, st);
+        if (s != CONV2D_OK) return s;
+    }
     // dx and the weights' gradients
     FfnJobs last = jobs_of(d, c);
-    last.largest = jobs.largest;
-    last.maxima = jobs.maxima;
+    last.held = jobs.held;
     last.n = 0;
     float* sums[4];
     for (int j = 0; j < 4; ++j) sums[j] = reinterpret_cast<float*>(base + c.sums[j]);

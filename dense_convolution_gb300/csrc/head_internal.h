@@ -51,7 +51,7 @@ struct FfnPlan {
     int parts, pairs;              // bf16 parts per value (1, or 3 for fp32) and their products (1 or 6)
     int64_t dp, fp;                // row pitch of one part, of `hidden` and of `inner` columns
     FfnTile first, last;           // h and y; dg and du, and the gradients
-    size_t xp, wgp, wup, wdp, dyp, h, dgu, largest, sums[4], total;
+    size_t xp, wgp, wup, wdp, dyp, h, dgu, largest, largest_dgu, sums[4], total;
 };
 
 }  // namespace conv2d_gb300

@@ -207,8 +207,9 @@ conv2d_status linear_ce_bwd(linear_ce_desc_t d, const void *h, const void *w, co
  *   dWg = dg^T x,  dWu = du^T x,  dWd = dy^T h    (the residual's gradient is dy).
  * fp16 and bf16 run on the tensor cores with fp32 accumulation; g, u and dh stay
  * in fp32, while h, dg and du are rounded to the operands' type for the products
- * that read them (fp16: dg and du held times a power of two that takes the
- * largest finite |dy| to [16, 32); an h beyond fp16's range is infinite).  fp32 runs there
+ * that read them (fp16: dg and du held times a power of two that takes the largest
+ * finite one to [2^10, 2^15), whatever dy's size: only those below 2^-24 of it may lose
+ * digits; an h beyond fp16's range is infinite).  fp32 runs there
  * too, as three bf16 parts a value and the six leading products of the parts; an
  * infinity in an operand makes what it enters NaN.  Forward passes of few tokens run
  * on the CUDA cores and keep h in fp32. */

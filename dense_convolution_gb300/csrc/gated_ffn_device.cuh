@@ -13,15 +13,16 @@ namespace conv2d_gb300 {
 // 2^-21.  Else the exponential's argument is multiplied by log2 e in two parts, which leaves the approximation's
 // 2^-22, and the reciprocal takes a Newton step: a third of the instructions of expf and a division, which
 // a tile's only pass through the epilogue would wait for.
-template <bool FAST> __device__ __forceinline__ float exp_of(float x) {
+// `more`, below 2^-12, is added to x (!FAST).
+template <bool FAST> __device__ __forceinline__ float exp_of(float x, float more = 0.f) {
     if constexpr (FAST) return __expf(x);
     constexpr float hi = 1.4426950216293335f, lo = 1.9259629911e-8f, ln2 = 0.69314718055994531f;
     const float t = x * hi, rest = fmaf(x, lo, fmaf(x, hi, -t));
     float e;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
-    return t > -127.f ? fmaf(e, rest * ln2, e) : 0.f;          // (`rest` of an infinity is none)
+    return t > -127.f ? fmaf(e, fmaf(rest, ln2, more), e) : 0.f;       // (`rest` of an infinity is none)
 }
-template <bool FAST> __device__ __forceinline__ float inverse_of(float x) {      // x in [1, 2]
+template <bool FAST> __device__ __forceinline__ float inverse_of(float x) {      // x in [1, 8]
     if constexpr (FAST) return __fdividef(1.f, x);
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -41,9 +42,9 @@ template <int ACT, bool FAST> __device__ __forceinline__ void activate(float g, 
         a = g * s;
         slope = s * fmaf(g, q, 1.f);
     } else if constexpr (ACT == FFN_GELU) {
-        float phi;
-        const float e = exp_of<FAST>(-0.5f * g * g);
+        float phi, e;
         if constexpr (FAST) {
+            e = exp_of<true>(-0.5f * g * g);
             // erfc by a polynomial in 1 / (1 + p x) times exp(-x^2), x = |g| / sqrt 2, off by 1.5e-7 at most
             // (Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26): the slope wants that exponential
             // too, and erff takes three times as long.
@@ -56,7 +57,22 @@ template <int ACT, bool FAST> __device__ __forceinline__ void activate(float g, 
             phi = g > 0.f ? 1.f - q : q;
             if (isnan(g)) phi = g;
         } else {
-            phi = fmaf(0.5f, erff(g * 0.70710678118654752f), 0.5f);
+            // Half of 1 + erff(g / sqrt 2) would cancel below zero (4 % of it is lost at -5), so the tail comes from a
+            // polynomial here too, fitted for the least relative error over [0, 14.5]: 2^-26, and 2^-21 with its own
+            // roundings.  The square's rounding goes into the exponent.  (Past 20 the exponential is zero.)
+            const float gg = g * g, t = inverse_of<false>(fmaf(0.26516503f, fminf(fabsf(g), 20.f), 1.f));
+            e = exp_of<false>(-0.5f * gg, -0.5f * fmaf(g, g, -gg));
+            float q = fmaf(t, 0.06125977f, -0.286015247f);
+            q = fmaf(t, q, 0.429762213f);
+            q = fmaf(t, q, -0.226484068f);
+            q = fmaf(t, q, 0.271756406f);
+            q = fmaf(t, q, 0.122322229f);
+            q = fmaf(t, q, 0.205109086f);
+            q = fmaf(t, q, 0.210677758f);
+            q = fmaf(t, q, 0.211611851f);
+            q *= 0.5f * t * e;
+            phi = g > 0.f ? 1.f - q : q;
+            if (isnan(g)) phi = g;
         }
         a = g * phi;
         slope = fmaf(g * 0.39894228040143268f, e, phi);

@@ -4,7 +4,9 @@ Hidden columns of g and of one, and weights that are unit vectors, make g and u 
 from dy = 1, dx = (act'(g), act(g)); for one token u = g.  With u the unit roundoff of the type:
   act    fp32 and few tokens: exponentials are good to 2^-22, the normal distribution to 2^-20.7, and products
          round (2^-24 each): 2^-20 for silu, 2^-19 for gelu.  gelu_tanh's argument, up to 36 here, rounds five
-         times: 36 5 2^-24 = 2^-16.5, with the rest 2^-16.
+         times: 36 5 2^-24 = 2^-16.5, with the rest 2^-16.  Long 16-bit ones: gelu_tanh's
+         argument, up to 52 in powers of two, rounds five times for a fast exponential (2^-16); gelu's, up to 36, thrice
+         (2^-17.3), and its tail's polynomial is off by 2^-15: 2^-14.5, beside the roundings of h and of y (u each).
   slope  near its zero (g = -0.75 for gelu) terms cancel: held to the sum of its two terms' magnitudes.
 Values below the type's smallest normal one are held to half a step of the subnormal ones, twice.
 """
@@ -37,7 +39,8 @@ def _functions(act, g):
 
 
 @pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
-@pytest.mark.parametrize("dtype,t", [("bf16", 1), ("f16", 1), ("f32", 1), ("f32", 600)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("t", [1, 600])
 def test_tails_have_digits_of_their_own(act, dtype, t):
     import torch
     from dense_convolution_gb300 import head
@@ -45,7 +48,7 @@ def test_tails_have_digits_of_their_own(act, dtype, t):
     g = torch.linspace(-7, 3, n, device="cuda").to(_dt(dtype))
     one = lambda *shape: torch.ones(*shape, dtype=_dt(dtype), device="cuda")
     few, u = t == 1, U[dtype]
-    rel = {"silu": 2.0 ** -20, "gelu": 2.0 ** -19, "gelu_tanh": 2.0 ** -16}[act]
+    rel = {"silu": 2.0 ** -20, "gelu": 2.0 ** -19, "gelu_tanh": 2.0 ** -16}[act] if few or dtype == "f32" else 2.0 ** -14.5
     a, slope, size = _functions(act, g.double())
     if few:
         # A token for each value would be slow: g lies in the weights, the values in the results of a single hidden column.

@@ -85,7 +85,9 @@ template <int ACT, bool FAST> __device__ __forceinline__ void activate(float g, 
         const float gg = g * g;
         sigmoid<FAST>(k * g * fmaf(c, gg, 1.f), s, q);
         a = g * s;
-        slope = fmaf(g * k * fmaf(3.f * c, gg, 1.f), s * q, s);
+        // (Where s q is zero, the cubic term may have overflowed.)
+        const float sq = s * q;
+        slope = sq > 0.f ? fmaf(g * k * fmaf(3.f * c, gg, 1.f), sq, s) : s;
     }
 }
 // act(g) alone, where its slope is not wanted: for silu and gelu_tanh an exponential that may overflow is in its

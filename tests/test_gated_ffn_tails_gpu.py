@@ -1,4 +1,5 @@
-"""The feed-forward block's activations where they vanish, held relative to their own size.
+"""The feed-forward block's activations where they vanish, held relative to their own size, and where
+their arguments overflow.
 
 Hidden columns of g and of one, and weights that are unit vectors, make g and u = 1 exact, so that y = act(g) and,
 from dy = 1, dx = (act'(g), act(g)); for one token u = g.  With u the unit roundoff of the type:
@@ -73,3 +74,25 @@ def test_tails_have_digits_of_their_own(act, dtype, t):
     for got, want, scale in ((dx[:, 0], slope, size), (dx[:, 1], a, a.abs())):
         off = (got - want).abs() / ((2 * rel) * scale + 2 * u * want.abs() + STEP[dtype])
         assert float(off.max()) <= 1, (float(off.max()), float(g[off.argmax()]))
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("t", [2, 200])
+def test_huge_pre_activations(act, dtype, t):
+    """The slope of a finite pre-activation is 0 or 1 at the ends, whatever its powers overflow to."""
+    import torch
+    from dense_convolution_gb300 import head
+    g = torch.tensor([1.0, -1.0, 1e12, -1e12, 3e13, -3e13, 1e20, -1e20, 1e30, -1e30, 3e38, -3e38], device="cuda").to(_dt(dtype))
+    n = len(g)
+    one = lambda *shape: torch.ones(*shape, dtype=_dt(dtype), device="cuda")
+    x = one(t, 1)
+    wg, wu, wd = g.view(n, 1).clone(), one(n, 1), one(1, n)
+    wd *= 2.0 ** -4
+    op = head.GatedFeedForward(t, 1, n, dtype, act)
+    _, saved = op(x, wg, wu, wd, save=True)
+    _, dwg, dwu, _ = op.backward(one(t, 1), x, wg, wu, wd, saved)
+    slope = _functions(act, g.double())[1]
+    want = t / 16 * torch.where(g.abs() > 2, (g > 0).double(), slope)
+    assert torch.isfinite(dwg).all() and torch.isfinite(dwu[g < 1e38]).all()
+    assert ((dwg[:, 0].double() - want).abs() <= (2 * U[dtype] + 2.0 ** -16) * want.abs() + 1e-30).all(), dwg[:, 0] - want

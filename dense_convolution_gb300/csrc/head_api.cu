@@ -400,9 +400,9 @@ CONV2D_API conv2d_status adamw_desc_create(adamw_desc_t* out, int64_t count, con
 
 CONV2D_API conv2d_status adamw_desc_set_rates(adamw_desc_t d, double beta1, double beta2, double eps) {
     if (!d) return CONV2D_ERR_NULL_PTR;
-    // As the kernel holds them: 1 - b and eps above zero.
+    // As the kernel holds them: 1 - b above zero, eps a normal number.
     if (!(beta1 >= 0.0 && (float)beta1 < 1.f) || !(beta2 >= 0.0 && (float)beta2 < 1.f)) return CONV2D_ERR_BAD_PARAM;
-    if (!((float)eps > 0.f) || !isfinite((float)eps)) return CONV2D_ERR_BAD_PARAM;
+    if (!((float)eps >= 0x1p-126f) || !isfinite((float)eps)) return CONV2D_ERR_BAD_PARAM;
     d->beta1 = beta1;
     d->beta2 = beta2;
     d->eps = eps;

@@ -284,7 +284,7 @@ typedef enum { ADAMW_STATES_F32 = 0, ADAMW_STATES_8BIT = 1 } adamw_states;
 conv2d_status adamw_desc_create(adamw_desc_t *out, int64_t count, const int64_t *sizes, conv2d_dtype grad_dtype,
                                 adamw_states states, conv2d_dtype copy_dtype);
 
-/* 0 <= beta1, beta2 < 1 and eps > 0 (as fp32).  Errors: NULL_PTR, BAD_PARAM. */
+/* 0 <= beta1, beta2 < 1 and eps >= 2^-126 (as fp32).  Errors: NULL_PTR, BAD_PARAM. */
 conv2d_status adamw_desc_set_rates(adamw_desc_t d, double beta1, double beta2, double eps);
 
 /* The decay of each tensor (count values, finite).  Errors: NULL_PTR, BAD_PARAM. */

@@ -141,7 +141,7 @@ template <bool E4M3> __device__ __forceinline__ uint2 to8(const float (&f)[8], u
         const uint32_t bits = __float_as_uint(small ? __fadd_rz(y, least) : y);
         code[i] = (bits + noise - (small ? (kBase << kDrop) + (1u << 23) : kBase << kDrop)) >> kDrop;
         if (E4M3) code[i] |= __float_as_uint(f[i]) >> 24 & 0x80u;
-        else code[i] = max(code[i], min(__float_as_uint(y), 1u));      // v: above zero stays above zero
+        else code[i] = max(code[i], min(__float_as_uint(f[i]), 1u));      // v: above zero stays above zero, also where y does not
     }
     if (byte == 255u) return make_uint2(0u, 0u);
     const auto four = [&](int i) {

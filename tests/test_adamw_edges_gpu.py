@@ -34,3 +34,17 @@ def test_vanishing_second_moments(states, beta2, eps):
     want = -rate * m / den
     off = rate * (m.abs() * (1 / low - 1 / high) + 4 * E * m.abs() / low) + 16 * E * want.abs() + 1e-44
     assert ((p.double() - want).abs() <= off).all(), ((p.double() - want).abs() / off).tolist()
+
+
+def test_blocks_of_widely_different_second_moments():
+    """v above zero is never stored as zero, however far below the block's largest one it is."""
+    import torch
+    from dense_convolution_gb300 import head
+    op = head.AdamW([512], "f32", "8bit", betas=(0.9, 0.95))
+    p, g = torch.zeros(512, device="cuda"), torch.full((512,), 1e-21, device="cuda")
+    g[100], g[300] = 1e15, 0.0
+    state = op.new_state()
+    op([p], [g], state, 1, 1e-3)
+    codes = state.v.view(torch.uint8)
+    live = g != 0
+    assert (codes[live] > 0).all() and codes[300] == 0

@@ -459,8 +459,11 @@ class AdamW(_Op):
         if (copies is None) != (self._copy is None):
             raise ValueError("copies are given where the operator was made with a copy_dtype, and only there")
         c = self._addresses("copies", copies, self._copy, dev) if copies is not None else None
-        if len(set(p)) != len(p) and len(set(a for a, n in zip(p, self.sizes) if n)) != sum(n > 0 for n in self.sizes):
-            raise ValueError("a tensor is among params twice")
+        for name, a in (("params", p), ("copies", c)):
+            # (Empty tensors may share an address.)
+            if a is not None and len(set(a)) != len(a) \
+                    and len(set(k for k, n in zip(a, self.sizes) if n)) != sum(n > 0 for n in self.sizes):
+                raise ValueError(f"a tensor is among {name} twice")
         at = []
         for name, t, dtype in (("step", step, torch.int64), ("lr", lr, torch.float32),
                                ("grad_scale", grad_scale, torch.float32), ("skip", skip, torch.float32)):

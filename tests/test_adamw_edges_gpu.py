@@ -110,3 +110,16 @@ def test_long_8bit_tensors(grad, copy, shift):
                 assert q.c[i].equal(q.p[i].to(q.c[i].dtype)), (t, i)
     for buf, at, n in q.buffers:
         assert torch.isnan(buf[:at]).all() and torch.isnan(buf[at + n:]).all() and not torch.isnan(buf[at:at + n]).any()
+
+
+def test_a_tensor_given_twice_is_refused():
+    import torch
+    from dense_convolution_gb300 import head
+    op = head.AdamW([64, 64, 0, 0], "bf16", "f32", "bf16")
+    z = lambda n, dtype=torch.bfloat16: torch.zeros(n, dtype=dtype, device="cuda")
+    p, g, c = [z(64, torch.float32), z(64, torch.float32), z(0, torch.float32), z(0, torch.float32)], [z(64), z(64), z(0), z(0)], [z(64), z(64), z(0), z(0)]
+    state = op.new_state()
+    op(p, [g[0], g[0], g[2], g[2]], state, 1, 0.1, copies=c)       # a gradient is only read
+    for params, copies in ((p, [c[0], c[0], c[2], c[3]]), ([p[1], p[1], p[2], p[3]], c)):
+        with pytest.raises(ValueError):
+            op(params, g, state, 1, 0.1, copies=copies)

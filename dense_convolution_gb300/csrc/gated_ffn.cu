@@ -34,11 +34,12 @@
 //
 // Measured, one launch at a time (SM clock 1.9 GHz; in a loop the large ones run at the power
 // limit).  bf16 8192 x 2048 x 8192: h 322 us (1.71 PFLOP/s), y 200 (1.37: 256 x 192 tiles are 3.75 rounds
-// of the machine's 76 pairs), dg and du 226 (1.22), the gradients 838 (1.31).  A chunk takes 690
+// of the machine's 76 pairs), dg and du 226 (1.22), the gradients 838 (1.64).  A chunk takes 690
 // cycles of a pair of SMs instead of the MMAs' 512: their reads of shared memory and the copies'
 // writes together are all that it gives.  50176 x 512 x 1408: 156, 53, 172 and 252 us; h and dg, du are bound
-// by memory there (706 MB and 850 MB: 104 and 125 us) and by the epilogue: eight chunks a tile (4100 cycles of
-// MMAs) are shorter than the activation of 128 x 128 values and their stores.
+// by memory there (706 MB and 850 MB: 104 and 125 us) and by the epilogue behind few chunks a tile.  What that takes, forward
+// passes without `saved`, us: 8192 x 1024 x 4096 151 with gelu, 132 with silu, 129 without an activation, 126 without h's
+// stores either; 50176 x 512 x 1408 195, 159 (gelu_tanh 165), 151 and 145.
 // What each step brought at 8192 x 2048 x 8192 / 50176 x 512 x 1408: saved values as the lanes read them, dg and du
 // 339 to 338 / 330 to 273; the accumulator reported free before the stores (an arrival that orders the
 // thread's stores waits for all of them), h 327 to 326 / 190 to 152; saved values through shared memory by asynchronous
@@ -876,6 +877,10 @@ template <typename T> int long_products(const T* length, int n, int* extra) {
 // turn, so the load of each follows; splits add the write and read of their fp32 sums
 // and one launch.  All products are split so that their items are about equally
 // long; up to 64 lengths are weighed.
+// Splits or none, us: y of 16 x 4096 x 16384 fp16 76 / 123 (the whole call), 64 x 2048 x 8192 bf16 34 / 58, 1000 x 768 x 2048
+// fp32 83 / 120, a step of 50176 x 512 x 1408 bf16 650 / 690.  The 3000 cycles of an item and the 4000 of a join are round: half or
+// twice of either leaves twelve calls from 16 to 50176 tokens within 1 %, but for one forward pass (5 % more) and one step (3 %
+// either way).
 FfnTile plan_tiles(const Sized* pr, int n, Product product, bool f32) {
     const bool b_mn = product == DGATE || product == GRADS;
     FfnTile best{256, false, {1, 1, 1, 1}};

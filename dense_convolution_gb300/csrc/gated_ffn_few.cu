@@ -299,6 +299,9 @@ cudaError_t run(const gated_ffn_desc& d, const void* x, const void* wg, const vo
 //   bf16 2047 x 8191, copied        1 token 34 / 72, 4 49 / 72, 8 (two groups) 92 / 71
 //   fp32 2048 x 8192                1 token 41 / 234, 8 (two groups) 88 / 216, 16 (four) 175 / 207
 //   fp32 512 x 1408                 1 token 9 / 43, 8 19 / 43, 32 (four groups) 70 / 43
+//   bf16, fp16 512 x 1408           1 token 9 / 14, 2 12 / 14, 4 12 / 14, 6 16 / 14, 8 18 / 14, 16 (two groups) 35 / 14
+//   bf16 1024 x 4096                1 token 13 / 22, 2 15 / 23, 4 18 / 23, 6 24 / 23, 8 27 / 23
+//   fp16 509 x 1371, copied         1 token 12 / 16, 2 15 / 17, 4 14 / 16, 6 18 / 17
 bool gated_ffn_is_few(const gated_ffn_desc& d) {
     const bool f32 = d.dtype == CONV2D_F32;
     const int group = group_of(d);
